@@ -1,0 +1,216 @@
+// gdr2_layer.h -- shared by the layer operators (convolution, scan, norm):
+// the map from work slots to pieces of sequences, row access in either dtype,
+// the gate functions, and the launchers' declarations.  Not part of the ABI.
+#pragma once
+
+#include "gdr2_device.h"
+#include "gdr2_internal.h"
+
+namespace gdr2 {
+
+// ---- launchers (arguments are validated; they only enqueue work) ----------
+hipError_t launch_conv_forward(const gdr2_conv_args& a, hipStream_t stream);
+hipError_t launch_conv_step(const gdr2_conv_step_args& a, hipStream_t stream);
+hipError_t launch_conv_backward(const gdr2_conv_bwd_args& a, hipStream_t stream);
+size_t conv_backward_workspace_bytes(const gdr2_conv_bwd_args& a);
+int64_t conv_launch_groups(int64_t B, int64_t T, int64_t C, bool packed);
+
+hipError_t launch_scan_forward(const gdr2_scan_args& a, hipStream_t stream);
+hipError_t launch_scan_step(const gdr2_scan_step_args& a, hipStream_t stream);
+hipError_t launch_scan_backward(const gdr2_scan_bwd_args& a, hipStream_t stream);
+size_t scan_workspace_bytes(const gdr2_scan_args& a);
+size_t scan_backward_workspace_bytes(const gdr2_scan_bwd_args& a);
+int64_t scan_launch_groups(const gdr2_scan_args& a);
+
+hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream);
+hipError_t launch_norm_backward(const gdr2_norm_bwd_args& a, hipStream_t stream);
+size_t norm_backward_workspace_bytes(const gdr2_norm_bwd_args& a);
+int64_t norm_launch_groups(const gdr2_norm_args& a);
+
+// Column sums of part [P][M], in an order fixed by P alone.  The columns are
+// cut into up to three outputs (M = their n together); NULL ones are skipped.
+struct ColumnOut {
+    float* p;
+    int64_t n;
+};
+hipError_t launch_column_sum(const float* part, int64_t P, ColumnOut a, ColumnOut b, ColumnOut c, hipStream_t stream);
+
+constexpr int64_t kMaxGroups = (int64_t)1 << 24;   // 256-thread workgroups of one launch, exclusive
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- pieces of sequences ---------------------------------------------------
+// A sequence of `len` rows is cut into pieces of L = 2^lg rows, the last one
+// shorter; an empty sequence still has one (empty) piece 0, which owns its
+// states.  Work slots number the pieces:
+//   dense   slot = s * per + i, per = max(1, ceil(T / L));
+//   packed  slot = offsets[s] / L + s + i.  Sequence s + 1 starts at or after
+//           slot offsets[s]/L + ceil(len/L) + s, so pieces do not collide, and
+//           floor(T/L) + B slots hold them all: the grid is known on the host
+//           without reading the offsets.  Slots no piece maps to are idle.
+struct Pieces {
+    const int64_t* offsets;   // NULL: dense
+    int64_t B, T;
+    int lg;
+
+    __host__ __device__ int64_t per() const { const int64_t n = (T + ((int64_t)1 << lg) - 1) >> lg; return n > 0 ? n : 1; }
+    __host__ __device__ int64_t slots() const { return offsets && B > 0 ? (T >> lg) + B : B * per(); }
+};
+
+struct Piece {
+    int64_t seq;     // -1: an idle slot
+    int64_t index;   // piece number in its sequence
+    int64_t row0;    // first row of the sequence
+    int64_t len;     // rows of the sequence
+    int64_t first;   // first slot of the sequence
+};
+
+__device__ __forceinline__ int64_t clamp_offset(const Pieces& p, int64_t s)
+{
+    const int64_t v = p.offsets[s];
+    return v < 0 ? 0 : (v > p.T ? p.T : v);
+}
+
+// Rows of sequence s and its first slot.
+__device__ __forceinline__ Piece sequence_of(const Pieces& p, int64_t s)
+{
+    Piece r;
+    r.seq = s;
+    r.index = 0;
+    if (!p.offsets) {
+        r.row0 = s * p.T;
+        r.len = p.T;
+        r.first = s * p.per();
+        return r;
+    }
+    r.row0 = clamp_offset(p, s);
+    const int64_t hi = clamp_offset(p, s + 1);
+    r.len = hi > r.row0 ? hi - r.row0 : 0;
+    r.first = (r.row0 >> p.lg) + s;
+    return r;
+}
+
+__device__ __forceinline__ Piece piece_of(const Pieces& p, int64_t slot)
+{
+    if (!p.offsets) {
+        const int64_t per = p.per();
+        int64_t s;
+        if ((slot | per) >> 31)
+            s = slot / per;
+        else
+            s = (uint32_t)slot / (uint32_t)per;
+        Piece r = sequence_of(p, s);
+        r.index = slot - s * per;
+        return r;
+    }
+    // the last sequence whose first slot is not beyond this one
+    int64_t lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if ((clamp_offset(p, mid) >> p.lg) + mid <= slot)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Piece r = sequence_of(p, lo);
+    r.index = slot - r.first;
+    // idle: before the first sequence, or past this one's pieces (the empty
+    // sequence's piece 0 exists)
+    if (r.index < 0 || (r.index > 0 && (r.index << p.lg) >= r.len))
+        r.seq = -1;
+    return r;
+}
+
+// ---- rows ------------------------------------------------------------------
+// V consecutive elements as fp32, one load (V = 1, or 16 bytes when the
+// caller has checked the alignment).
+template <int V> __device__ __forceinline__ void load_row(const float* p, float* v)
+{
+    if constexpr (V == 1) {
+        v[0] = *p;
+    } else {
+        static_assert(V == 4, "16 bytes");
+        const f32x4 x = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = x[i];
+    }
+}
+template <int V> __device__ __forceinline__ void load_row(const bf16* p, float* v)
+{
+    if constexpr (V == 1) {
+        v[0] = (float)*p;
+    } else {
+        static_assert(V == 8, "16 bytes");
+        const bf16x8 x = *reinterpret_cast<const bf16x8*>(p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = (float)x[i];
+    }
+}
+template <int V> __device__ __forceinline__ void store_row(float* p, const float* v)
+{
+    if constexpr (V == 1) {
+        *p = v[0];
+    } else {
+        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    }
+}
+template <int V> __device__ __forceinline__ void store_row(bf16* p, const float* v)
+{
+    if constexpr (V == 1) {
+        *p = (bf16)v[0];
+    } else {
+        bf16x8 x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = (bf16)v[i];
+        *reinterpret_cast<bf16x8*>(p) = x;
+    }
+}
+
+template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
+
+// The same elements unconverted: a load in flight holds half the registers.
+template <typename T, int V> struct Raw {
+    typedef T Type __attribute__((ext_vector_type(V)));
+    static __device__ __forceinline__ Type load(const T* p) { return *reinterpret_cast<const Type*>(p); }
+    static __device__ __forceinline__ Type zero() { Type z; for (int i = 0; i < V; ++i) z[i] = (T)0.f; return z; }
+    static __device__ __forceinline__ void get(Type r, float* v)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = (float)r[i];
+    }
+};
+template <typename T> struct Raw<T, 1> {
+    typedef T Type;
+    static __device__ __forceinline__ Type load(const T* p) { return *p; }
+    static __device__ __forceinline__ Type zero() { return (T)0.f; }
+    static __device__ __forceinline__ void get(Type r, float* v) { v[0] = (float)r; }
+};
+
+// Every row of this matrix starts on 16 bytes and holds whole vectors.
+inline bool rows_aligned(const void* p, int64_t stride, int64_t width, int64_t elt)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * elt) % 16 == 0 && (width * elt) % 16 == 0;
+}
+
+// ---- gate functions --------------------------------------------------------
+// sigmoid on the exp2 and reciprocal units (each within 1 ulp).  Below about
+// -88 the exponential is inf and the reciprocal 0, the right limit.
+__device__ __forceinline__ float sigmoid_f(float x)
+{
+    return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * x));
+}
+// silu(x); -inf gives 0 * -inf = NaN in this form as in the formula's limit
+// taken factor by factor.
+__device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }
+// d silu / dx
+__device__ __forceinline__ float silu_slope_f(float x)
+{
+    const float s = sigmoid_f(x);
+    return s * (1.f + x * (1.f - s));
+}
+
+}  // namespace gdr2

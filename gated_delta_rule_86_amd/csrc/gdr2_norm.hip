@@ -1,0 +1,517 @@
+// gdr2_norm.hip -- layer norm and rms norm of rows, with an optional silu
+// gate, and their gradients.
+//
+//   xh = (x - m) r,  r = (mean((x - m)^2) + eps)^(-1/2),  m = mean or 0
+//   n = xh weight + bias;   y = n, or n silu(z)
+// Gradients, with dn = dy (times silu(z)) and v = dn weight:
+//   dx = r (v - mean(v) [layer only] - xh mean(v xh)),
+//   dz = dy n silu'(z),  dweight = sum_rows dn xh,  dbias = sum_rows dn
+//
+// Memory bounds both.  A row is held in registers by a group of LPR lanes
+// (8 .. 64 of a wave, or a whole workgroup of 256), NV vectors of V elements
+// each, so it is read once; mean and variance are two passes over those
+// registers (no E[x^2] - m^2 cancellation), sums in fp32.
+#include "gdr2_layer.h"
+
+namespace gdr2 {
+
+namespace {
+
+// Sum over the LPR lanes that hold one row; every lane gets it.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, float* s_part)
+{
+    constexpr int W = LPR < 64 ? LPR : 64;
+#pragma unroll
+    for (int off = W / 2; off >= 1; off >>= 1)
+        v += __shfl_xor(v, off);
+    if constexpr (LPR > 64) {
+        __syncthreads();                       // the previous sum has been read
+        if ((threadIdx.x & 63) == 0)
+            s_part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
+    }
+    return v;
+}
+
+// Two sums at once.
+template <int LPR>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* s_part)
+{
+    constexpr int W = LPR < 64 ? LPR : 64;
+#pragma unroll
+    for (int off = W / 2; off >= 1; off >>= 1) {
+        a += __shfl_xor(a, off);
+        b += __shfl_xor(b, off);
+    }
+    if constexpr (LPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) {
+            s_part[threadIdx.x >> 6] = a;
+            s_part[4 + (threadIdx.x >> 6)] = b;
+        }
+        __syncthreads();
+        a = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
+        b = (s_part[4] + s_part[5]) + (s_part[6] + s_part[7]);
+    }
+}
+
+// Mean (0 for rms) and 1/rms of the row in x (elements past C are zero and
+// `in` is false for their vectors).
+template <int LPR, int V, int NV>
+__device__ __forceinline__ void row_stats(const float (&x)[NV][V], const bool (&in)[NV], int64_t C, int kind, float eps,
+                                          float* s_part, float& mean, float& rstd)
+{
+    const float inv = 1.f / (float)C;
+    mean = 0.f;
+    if (kind == GDR2_NORM_LAYER) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                s += x[j][v];
+        mean = row_sum<LPR>(s, s_part) * inv;
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float d = in[j] ? x[j][v] - mean : 0.f;
+            ss = fmaf(d, d, ss);
+        }
+    rstd = 1.f / sqrtf(row_sum<LPR>(ss, s_part) * inv + eps);
+}
+
+template <typename T, int V, int LPR, int NV>
+__global__ __launch_bounds__(256) void norm_forward_kernel(gdr2_norm_args a)
+{
+    __shared__ float s_part[8];
+    constexpr int RPB = 256 / LPR;
+    const int lane = threadIdx.x % LPR;
+    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+    if (row >= a.R)                            // whole groups of lanes; LPR = 256 has one row
+        return;
+    const T* x = (const T*)a.x + row * a.x_stride;
+    float xv[NV][V];
+    bool in[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = ((int64_t)j * LPR + lane) * V;
+        in[j] = c < a.C;
+        if (in[j])
+            load_row<V>(x + c, xv[j]);
+        else
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                xv[j][v] = 0.f;
+    }
+    float mean, rstd;
+    row_stats<LPR, V, NV>(xv, in, a.C, a.kind, a.eps, s_part, mean, rstd);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (!in[j])
+            continue;
+        const int64_t c = ((int64_t)j * LPR + lane) * V;
+        float o[V], z[V];
+        if (a.z)
+            load_row<V>((const T*)a.z + row * a.z_stride + c, z);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float w = a.weight ? a.weight[c + v] : 1.f, b = a.bias ? a.bias[c + v] : 0.f;
+            o[v] = fmaf((xv[j][v] - mean) * rstd, w, b);
+            if (a.z)
+                o[v] *= silu_f(z[v]);
+        }
+        store_row<V>((T*)a.y + row * a.C + c, o);
+    }
+}
+
+// Sums over a whole workgroup, for rows read in passes.
+__device__ __forceinline__ float block_sum(float v, float* s_part) { return row_sum<256>(v, s_part); }
+
+template <typename T>
+__device__ __forceinline__ void looped_stats(const T* x, int64_t C, int kind, float eps, float* s_part, float& mean, float& rstd)
+{
+    const float inv = 1.f / (float)C;
+    mean = 0.f;
+    if (kind == GDR2_NORM_LAYER) {
+        float s = 0.f;
+        for (int64_t c = threadIdx.x; c < C; c += 256)
+            s += to_f32(x[c]);
+        mean = block_sum(s, s_part) * inv;
+    }
+    float ss = 0.f;
+    for (int64_t c = threadIdx.x; c < C; c += 256) {
+        const float d = to_f32(x[c]) - mean;
+        ss = fmaf(d, d, ss);
+    }
+    rstd = 1.f / sqrtf(block_sum(ss, s_part) * inv + eps);
+}
+
+// Rows too long for the registers of a workgroup: passes over the row, which
+// the caches hold.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_forward_long_kernel(gdr2_norm_args a)
+{
+    __shared__ float s_part[8];
+    const int64_t row = blockIdx.x;
+    const T* x = (const T*)a.x + row * a.x_stride;
+    float mean, rstd;
+    looped_stats<T>(x, a.C, a.kind, a.eps, s_part, mean, rstd);
+    for (int64_t c = threadIdx.x; c < a.C; c += 256) {
+        float o = fmaf((to_f32(x[c]) - mean) * rstd, a.weight ? a.weight[c] : 1.f, a.bias ? a.bias[c] : 0.f);
+        if (a.z)
+            o *= silu_f(to_f32(((const T*)a.z)[row * a.z_stride + c]));
+        ((T*)a.y)[row * a.C + c] = from_f32<T>(o);
+    }
+}
+
+// Every group of LPR lanes walks rows g, g + groups, ...; its sums of dweight
+// and dbias stay in registers, are added over the workgroup's groups in LDS
+// (in group order), and leave as one row [2][C] of partial sums.
+template <typename T, int V, int LPR, int NV>
+__global__ __launch_bounds__(256) void norm_backward_kernel(gdr2_norm_bwd_args p, float* part)
+{
+    const gdr2_norm_args& a = p.f;
+    __shared__ float s_part[8];
+    constexpr int RPB = 256 / LPR;
+    __shared__ float s_red[RPB > 1 ? 256 * NV * V : 1];
+    const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const float inv = 1.f / (float)a.C;
+    float dw[NV][V] = {}, db[NV][V] = {};
+    bool in[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        in[j] = ((int64_t)j * LPR + lane) * V < a.C;
+    for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.R; row += (int64_t)gridDim.x * RPB) {
+        const T* x = (const T*)a.x + row * a.x_stride;
+        const T* dy = (const T*)p.dy + row * a.C;
+        float xv[NV][V], dv[NV][V];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = ((int64_t)j * LPR + lane) * V;
+            if (in[j]) {
+                load_row<V>(x + c, xv[j]);
+                load_row<V>(dy + c, dv[j]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    xv[j][v] = dv[j][v] = 0.f;
+            }
+        }
+        float mean, rstd;
+        row_stats<LPR, V, NV>(xv, in, a.C, a.kind, a.eps, s_part, mean, rstd);
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!in[j])
+                continue;
+            const int64_t c = ((int64_t)j * LPR + lane) * V;
+            float z[V], dz[V];
+            if (a.z)
+                load_row<V>((const T*)a.z + row * a.z_stride + c, z);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float w = a.weight ? a.weight[c + v] : 1.f;
+                const float xh = (xv[j][v] - mean) * rstd;
+                float dn = dv[j][v];
+                if (a.z) {
+                    const float b = a.bias ? a.bias[c + v] : 0.f;
+                    dz[v] = dn * fmaf(xh, w, b) * silu_slope_f(z[v]);
+                    dn *= silu_f(z[v]);
+                }
+                dw[j][v] = fmaf(dn, xh, dw[j][v]);
+                db[j][v] += dn;
+                const float g = dn * w;
+                s1 += g;
+                s2 = fmaf(g, xh, s2);
+                xv[j][v] = xh;
+                dv[j][v] = g;
+            }
+            if (a.z)
+                store_row<V>((T*)p.dz + row * a.C + c, dz);
+        }
+        row_sum2<LPR>(s1, s2, s_part);
+        const float m1 = a.kind == GDR2_NORM_LAYER ? s1 * inv : 0.f, m2 = s2 * inv;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!in[j])
+                continue;
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                o[v] = rstd * (dv[j][v] - m1 - xv[j][v] * m2);
+            store_row<V>((T*)p.dx + row * a.C + ((int64_t)j * LPR + lane) * V, o);
+        }
+    }
+    if (!part)
+        return;
+    float* to = part + (int64_t)blockIdx.x * 2 * a.C;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if constexpr (RPB == 1) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (in[j])
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        to[half * a.C + ((int64_t)j * LPR + lane) * V + v] = half ? db[j][v] : dw[j][v];
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    s_red[grp * (LPR * NV * V) + (j * LPR + lane) * V + v] = half ? db[j][v] : dw[j][v];
+            __syncthreads();
+            for (int c = threadIdx.x; c < a.C; c += 256) {
+                float s = 0.f;
+#pragma unroll
+                for (int r = 0; r < RPB; ++r)
+                    s += s_red[r * (LPR * NV * V) + c];
+                to[half * a.C + c] = s;
+            }
+        }
+    }
+}
+
+// Long rows, backwards: one workgroup per row writes dx and dz in passes and
+// leaves the row's mean and 1/rms for the column pass.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_backward_long_kernel(gdr2_norm_bwd_args p, float* stats)
+{
+    const gdr2_norm_args& a = p.f;
+    __shared__ float s_part[8];
+    const int64_t row = blockIdx.x;
+    const float inv = 1.f / (float)a.C;
+    const T* x = (const T*)a.x + row * a.x_stride;
+    const T* dy = (const T*)p.dy + row * a.C;
+    const T* z = a.z ? (const T*)a.z + row * a.z_stride : nullptr;
+    float mean, rstd;
+    looped_stats<T>(x, a.C, a.kind, a.eps, s_part, mean, rstd);
+    if (threadIdx.x == 0) {
+        stats[2 * row] = mean;
+        stats[2 * row + 1] = rstd;
+    }
+    float s1 = 0.f, s2 = 0.f;
+    for (int64_t c = threadIdx.x; c < a.C; c += 256) {
+        const float w = a.weight ? a.weight[c] : 1.f, xh = (to_f32(x[c]) - mean) * rstd;
+        float dn = to_f32(dy[c]);
+        if (z) {
+            const float zc = to_f32(z[c]);
+            ((T*)p.dz)[row * a.C + c] = from_f32<T>(dn * fmaf(xh, w, a.bias ? a.bias[c] : 0.f) * silu_slope_f(zc));
+            dn *= silu_f(zc);
+        }
+        s1 += dn * w;
+        s2 = fmaf(dn * w, xh, s2);
+    }
+    row_sum2<256>(s1, s2, s_part);
+    const float m1 = a.kind == GDR2_NORM_LAYER ? s1 * inv : 0.f, m2 = s2 * inv;
+    for (int64_t c = threadIdx.x; c < a.C; c += 256) {
+        const float w = a.weight ? a.weight[c] : 1.f, xh = (to_f32(x[c]) - mean) * rstd;
+        float dn = to_f32(dy[c]);
+        if (z)
+            dn *= silu_f(to_f32(z[c]));
+        ((T*)p.dx)[row * a.C + c] = from_f32<T>(rstd * (dn * w - m1 - xh * m2));
+    }
+}
+
+// dweight and dbias of long rows: a workgroup sums 64 columns over every
+// gridDim.y-th block of 64 rows.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_backward_columns_kernel(gdr2_norm_bwd_args p, const float* stats, float* part)
+{
+    const gdr2_norm_args& a = p.f;
+    __shared__ float s_red[2][4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float dw = 0.f, db = 0.f;
+    if (c < a.C) {
+        for (int64_t row = (int64_t)blockIdx.y * 4 + wave; row < a.R; row += (int64_t)gridDim.y * 4) {
+            const float xh = (to_f32(((const T*)a.x)[row * a.x_stride + c]) - stats[2 * row]) * stats[2 * row + 1];
+            float dn = to_f32(((const T*)p.dy)[row * a.C + c]);
+            if (a.z)
+                dn *= silu_f(to_f32(((const T*)a.z)[row * a.z_stride + c]));
+            dw = fmaf(dn, xh, dw);
+            db += dn;
+        }
+    }
+    s_red[0][wave][lane] = dw;
+    s_red[1][wave][lane] = db;
+    __syncthreads();
+    if (wave < 2 && c < a.C)
+        part[(int64_t)blockIdx.y * 2 * a.C + wave * a.C + c] =
+            (s_red[wave][0][lane] + s_red[wave][1][lane]) + (s_red[wave][2][lane] + s_red[wave][3][lane]);
+}
+
+// ---- variants --------------------------------------------------------------
+// The narrowest group of lanes whose registers hold the row: a wave (or part
+// of one) up to 32 elements a lane, then a workgroup up to 64 forwards and 32
+// backwards (which also holds dy, dweight and dbias), then passes.
+struct Shape {
+    int lpr, nv;   // lpr == 0: passes
+};
+
+Shape shape_of(int64_t C, int V, bool backward)
+{
+    const int64_t nvec = (C + V - 1) / V;
+    for (int lpr = 8; lpr <= 64; lpr *= 2)
+        if (nvec <= lpr)
+            return {lpr, 1};
+    const int most = backward ? 32 / V : 64 / V;
+    for (int nv = 2; nv * V <= 32; nv *= 2) {
+        // V = 1 keeps a wave to 8 loads before it takes a workgroup
+        if ((V > 1 || nv <= 8) && nvec <= 64 * nv)
+            return {64, nv};
+    }
+    for (int nv = 1; nv <= most && nv <= 32; nv *= 2)
+        if (nvec <= 256 * nv)
+            return {256, nv};
+    return {0, 0};
+}
+
+
+#define GDR2_NORM_CASE(L, N)                                                                     \
+    if (s.lpr == L && s.nv == N) {                                                               \
+        f.template operator()<L, N>();                                                           \
+        return hipGetLastError();                                                                \
+    }
+
+template <typename T, int V> struct ForwardLaunch {
+    const gdr2_norm_args& a;
+    hipStream_t stream;
+    template <int L, int N> void operator()() const
+    {
+        hipLaunchKernelGGL((norm_forward_kernel<T, V, L, N>), dim3((unsigned)ceil_div(a.R, 256 / L)), dim3(256), 0, stream, a);
+    }
+};
+
+template <typename T, int V> struct BackwardLaunch {
+    const gdr2_norm_bwd_args& p;
+    float* part;
+    int64_t groups;
+    hipStream_t stream;
+    template <int L, int N> void operator()() const
+    {
+        if constexpr (N * V <= 32)
+            hipLaunchKernelGGL((norm_backward_kernel<T, V, L, N>), dim3((unsigned)groups), dim3(256), 0, stream, p, part);
+    }
+};
+
+// Exactly the shapes shape_of can return for V.
+template <int V, typename F> hipError_t dispatch(const Shape& s, const F& f)
+{
+    GDR2_NORM_CASE(8, 1) GDR2_NORM_CASE(16, 1) GDR2_NORM_CASE(32, 1) GDR2_NORM_CASE(64, 1)
+    GDR2_NORM_CASE(64, 2) GDR2_NORM_CASE(64, 4)
+    if constexpr (V == 8) {
+        GDR2_NORM_CASE(256, 2) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(256, 8)
+    } else {
+        GDR2_NORM_CASE(64, 8) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(256, 8) GDR2_NORM_CASE(256, 16)
+    }
+    if constexpr (V == 1) {
+        GDR2_NORM_CASE(256, 32)
+    }
+    return hipErrorInvalidValue;
+}
+
+bool norm_vec(const gdr2_norm_args& a)
+{
+    const int64_t e = a.dtype == GDR2_BF16 ? 2 : 4;
+    return rows_aligned(a.x, a.x_stride, a.C, e) && (!a.z || rows_aligned(a.z, a.z_stride, a.C, e));
+}
+
+template <typename T, int V>
+hipError_t forward_v(const gdr2_norm_args& a, hipStream_t stream)
+{
+    const Shape s = shape_of(a.C, V, false);
+    if (s.lpr == 0) {
+        hipLaunchKernelGGL((norm_forward_long_kernel<T>), dim3((unsigned)a.R), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
+    return dispatch<V>(s, ForwardLaunch<T, V>{a, stream});
+}
+
+// Workgroups of the backward: two per compute unit, fewer when there are
+// fewer rows.
+int64_t backward_groups(int64_t R, const Shape& s)
+{
+    return min(ceil_div(R, 256 / s.lpr), (int64_t)device_cu_count() * 2);
+}
+
+int64_t long_row_blocks(int64_t R, int64_t C)
+{
+    return max((int64_t)1, min(ceil_div(R, 4), (int64_t)device_cu_count() * 4 / ceil_div(C, 64)));
+}
+
+template <typename T, int V>
+hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
+{
+    const gdr2_norm_args& a = p.f;
+    const Shape s = shape_of(a.C, V, true);
+    const bool sums = p.dweight || p.dbias;
+    float* part = (float*)p.workspace;
+    int64_t P = 0;
+    if (a.R == 0) {
+        // nothing but the sums' zeros to write
+    } else if (s.lpr != 0) {
+        P = backward_groups(a.R, s);
+        const hipError_t e = dispatch<V>(s, BackwardLaunch<T, V>{p, sums ? part : nullptr, P, stream});
+        if (e != hipSuccess || !sums)
+            return e;
+    } else {
+        float* stats = part;
+        part += 2 * a.R;
+        P = long_row_blocks(a.R, a.C);
+        hipLaunchKernelGGL((norm_backward_long_kernel<T>), dim3((unsigned)a.R), dim3(256), 0, stream, p, stats);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess || !sums)
+            return e;
+        hipLaunchKernelGGL((norm_backward_columns_kernel<T>), dim3((unsigned)ceil_div(a.C, 64), (unsigned)P), dim3(256), 0,
+                           stream, p, stats, part);
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return sums ? launch_column_sum(part, P, {p.dweight, a.C}, {p.dbias, a.C}, {nullptr, 0}, stream) : hipSuccess;
+}
+
+}  // namespace
+
+// Workgroups of the forward's launch (the backward's rows take at most as many).
+int64_t norm_launch_groups(const gdr2_norm_args& a)
+{
+    const Shape s = shape_of(a.C, norm_vec(a) ? (a.dtype == GDR2_BF16 ? 8 : 4) : 1, true);
+    return s.lpr ? ceil_div(a.R, 256 / s.lpr) : a.R;
+}
+
+hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream)
+{
+    if (a.dtype == GDR2_BF16)
+        return norm_vec(a) ? forward_v<bf16, 8>(a, stream) : forward_v<bf16, 1>(a, stream);
+    return norm_vec(a) ? forward_v<float, 4>(a, stream) : forward_v<float, 1>(a, stream);
+}
+
+// The larger of the vector and the scalar variant's needs (the query sees no
+// pointers).
+size_t norm_backward_workspace_bytes(const gdr2_norm_bwd_args& p)
+{
+    const gdr2_norm_args& a = p.f;
+    int64_t floats = 0;
+    for (int V : {1, a.dtype == GDR2_BF16 ? 8 : 4}) {
+        const Shape s = shape_of(a.C, V, true);
+        floats = max(floats, s.lpr ? backward_groups(a.R, s) * 2 * a.C : 2 * a.R + long_row_blocks(a.R, a.C) * 2 * a.C);
+    }
+    return (size_t)floats * sizeof(float);
+}
+
+hipError_t launch_norm_backward(const gdr2_norm_bwd_args& p, hipStream_t stream)
+{
+    if (p.f.dtype == GDR2_BF16)
+        return norm_vec(p.f) ? backward_v<bf16, 8>(p, stream) : backward_v<bf16, 1>(p, stream);
+    return norm_vec(p.f) ? backward_v<float, 4>(p, stream) : backward_v<float, 1>(p, stream);
+}
+
+}  // namespace gdr2

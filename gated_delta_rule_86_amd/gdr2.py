@@ -58,8 +58,12 @@ class BwdArgs(ctypes.Structure):
 # Every symbol include/gdr2.h declares (checked by the tests).
 EXPORTS = ("gdr2_forward_workspace_size", "gdr2_forward_chunked", "gdr2_decode_step",
            "gdr2_backward_workspace_size", "gdr2_backward_chunked",
-           "gdr2_status_string", "gdr2_last_error", "gdr2_abi_version", "gdr2_forward_chunked_noalloc")
-ABI_VERSION = 6
+           "gdr2_status_string", "gdr2_last_error", "gdr2_abi_version", "gdr2_forward_chunked_noalloc",
+           "gdr2_conv_forward", "gdr2_conv_step", "gdr2_conv_backward_workspace_size", "gdr2_conv_backward",
+           "gdr2_scan_chunk_count", "gdr2_scan_workspace_size", "gdr2_scan_forward", "gdr2_scan_step",
+           "gdr2_scan_backward_workspace_size", "gdr2_scan_backward",
+           "gdr2_norm_forward", "gdr2_norm_backward_workspace_size", "gdr2_norm_backward")
+ABI_VERSION = 7
 NOALLOC_SCRATCH_BYTES = 64 << 20
 BWD_CHUNK = 64
 
@@ -104,6 +108,8 @@ def load_library(path: str = LIB_PATH):
         lib.gdr2_abi_version.argtypes = []
         if lib.gdr2_abi_version() != ABI_VERSION:
             raise RuntimeError("libgdr2.so ABI version mismatch")
+        from . import layer
+        layer.declare(lib)
         _lib = lib
         return lib
 

@@ -1,0 +1,482 @@
+"""ctypes binding of the layer operators of ``libgdr2.so`` (include/gdr2.h):
+the short causal convolution, the selective state space scan and the norms
+that stand around the recurrence in a sequence-mixing layer.
+
+Argument marshalling only, as in ``gdr2``.  Common to all functions:
+
+- rows are float32 or bfloat16; weights, biases, A, skip and every state of
+  the scan are float32.  A row input may be a column slice of a wider
+  projection (last dimension dense, equally spaced rows); everything else is
+  contiguous.
+- a batch is dense, ``[B, T, ...]``, or packed: ``[T, ...]`` with ``offsets``,
+  an int64 device tensor of ``B + 1`` ascending row numbers (sequences may be
+  empty; rows of no sequence are not touched: pass ``out`` to keep them).
+- gradients of rows have the rows' dtype, gradients of parameters and states
+  are float32.
+- the call is enqueued on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import gdr2
+from .gdr2 import _c_i32, _c_i64, _check, _dtype_code, _ptr, _req_dev, _req_shape, _vp, load_library
+
+ACTIVATIONS = {None: 0, "silu": 1}
+KINDS = {"layer": 0, "rms": 1}
+SCAN_ALGOS = {n: gdr2.ALGOS[n] for n in ("auto", "staged", "segmented")}
+SCAN_SOFTPLUS = 1
+SCAN_CHUNK = 32
+
+_size = ctypes.c_size_t
+
+
+class ConvArgs(ctypes.Structure):
+    _fields_ = [("B", _c_i64), ("T", _c_i64), ("C", _c_i64), ("x_stride", _c_i64),
+                ("width", _c_i32), ("dtype", _c_i32), ("act", _c_i32), ("reserved", _c_i32),
+                ("x", _vp), ("weight", _vp), ("bias", _vp), ("state0", _vp), ("offsets", _vp),
+                ("y", _vp), ("state_out", _vp)]
+
+
+class ConvStepArgs(ctypes.Structure):
+    _fields_ = [("N", _c_i64), ("C", _c_i64), ("x_stride", _c_i64),
+                ("width", _c_i32), ("dtype", _c_i32), ("act", _c_i32), ("reserved", _c_i32),
+                ("state", _vp), ("x", _vp), ("weight", _vp), ("bias", _vp), ("y", _vp)]
+
+
+class ConvBwdArgs(ctypes.Structure):
+    _fields_ = [("B", _c_i64), ("T", _c_i64), ("C", _c_i64), ("x_stride", _c_i64),
+                ("width", _c_i32), ("dtype", _c_i32), ("act", _c_i32), ("reserved", _c_i32),
+                ("x", _vp), ("weight", _vp), ("bias", _vp), ("state0", _vp), ("offsets", _vp),
+                ("dy", _vp), ("dstate", _vp), ("dx", _vp), ("dweight", _vp), ("dbias", _vp), ("dstate0", _vp),
+                ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [("B", _c_i64), ("T", _c_i64), ("C", _c_i64), ("N", _c_i64), ("G", _c_i64),
+                ("x_stride", _c_i64), ("dt_stride", _c_i64), ("b_stride", _c_i64), ("c_stride", _c_i64),
+                ("z_stride", _c_i64),
+                ("dtype", _c_i32), ("flags", _c_i32), ("algo", _c_i32), ("reserved", _c_i32),
+                ("x", _vp), ("dt", _vp), ("Bt", _vp), ("Ct", _vp), ("z", _vp),
+                ("A", _vp), ("skip", _vp), ("dt_bias", _vp), ("h0", _vp), ("offsets", _vp),
+                ("y", _vp), ("h_out", _vp), ("h_chunks", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class ScanStepArgs(ctypes.Structure):
+    _fields_ = [("s", ScanArgs), ("state", _vp)]
+
+
+class ScanBwdArgs(ctypes.Structure):
+    _fields_ = [("f", ScanArgs), ("dy", _vp), ("dh_out", _vp),
+                ("dx", _vp), ("ddt", _vp), ("dBt", _vp), ("dCt", _vp), ("dz", _vp),
+                ("dA", _vp), ("dskip", _vp), ("ddt_bias", _vp), ("dh0", _vp),
+                ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [("R", _c_i64), ("C", _c_i64), ("x_stride", _c_i64), ("z_stride", _c_i64),
+                ("dtype", _c_i32), ("kind", _c_i32), ("eps", ctypes.c_float), ("reserved", _c_i32),
+                ("x", _vp), ("z", _vp), ("weight", _vp), ("bias", _vp), ("y", _vp)]
+
+
+class NormBwdArgs(ctypes.Structure):
+    _fields_ = [("f", NormArgs), ("dy", _vp), ("dx", _vp), ("dz", _vp), ("dweight", _vp), ("dbias", _vp),
+                ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+# entry point -> its argument struct; size queries of the backward passes
+ENTRIES = {"gdr2_conv_forward": ConvArgs, "gdr2_conv_step": ConvStepArgs, "gdr2_conv_backward": ConvBwdArgs,
+           "gdr2_scan_forward": ScanArgs, "gdr2_scan_step": ScanStepArgs, "gdr2_scan_backward": ScanBwdArgs,
+           "gdr2_norm_forward": NormArgs, "gdr2_norm_backward": NormBwdArgs}
+SIZES = {"gdr2_conv_backward_workspace_size": ConvBwdArgs, "gdr2_scan_workspace_size": ScanArgs,
+         "gdr2_scan_backward_workspace_size": ScanBwdArgs, "gdr2_norm_backward_workspace_size": NormBwdArgs}
+
+
+def declare(lib):
+    """Signatures of the layer operators in a loaded library."""
+    for name, args in ENTRIES.items():
+        f = getattr(lib, name)
+        f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(args), _vp]
+    for name, args in SIZES.items():
+        f = getattr(lib, name)
+        f.restype, f.argtypes = _size, [ctypes.POINTER(args)]
+    lib.gdr2_scan_chunk_count.restype = _c_i64
+    lib.gdr2_scan_chunk_count.argtypes = [_c_i64, _c_i64, ctypes.c_int]
+    return lib
+
+
+# ---- argument checks -------------------------------------------------------
+
+def _row_stride(t: torch.Tensor, name: str, lead: int, width: int) -> int:
+    """Elements between consecutive rows: the first ``lead`` dimensions number
+    the rows, the others hold ``width`` dense elements."""
+    if t.numel() == 0:
+        return width
+    shape, stride = t.shape, t.stride()
+    step = 1
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] != 1:
+            if stride[d] != step:
+                raise ValueError(f"{name}: the elements of a row must be contiguous")
+            step *= shape[d]
+    ld = 0
+    for d in range(lead - 1, -1, -1):
+        if shape[d] == 1:
+            continue
+        if ld == 0:
+            ld, span = stride[d], stride[d] * shape[d]
+        elif stride[d] != span:
+            raise ValueError(f"{name}: rows must be equally spaced")
+        else:
+            span *= shape[d]
+    if ld == 0:
+        return width
+    if ld < width:
+        raise ValueError(f"{name}: rows must not overlap")
+    return ld
+
+
+def _rows_dtype(t: torch.Tensor):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {t.dtype} (float32 or bfloat16)")
+
+
+def _mode(table, value, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"unknown {name} {value!r} ({', '.join(map(repr, table))})")
+    return table[value]
+
+
+def _on(dev, dense=(), rows=()):
+    for n, t in rows:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"{n} must be a device tensor")
+            if t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, expected {dev}")
+    for n, t in dense:
+        if t is not None:
+            _req_dev(t, n, dev)
+
+
+def _offsets(offsets) -> int:
+    """Number of sequences of a packed batch."""
+    _req_shape(offsets, "offsets", torch.int64)
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError(f"offsets must have shape (B + 1,), got {tuple(offsets.shape)}")
+    return offsets.shape[0] - 1
+
+
+def _call(entry: str, args, dev):
+    lib = load_library()
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    f = getattr(lib, entry)
+    if torch.cuda.current_device() == dev.index:
+        _check(lib, f(ctypes.byref(args), stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(lib, f(ctypes.byref(args), stream))
+
+
+def _with_workspace(size: str, args, workspace, dev):
+    """Fills the workspace fields; the size depends on the device's compute
+    units, so it is asked for with that device current."""
+    with torch.cuda.device(dev):
+        need = int(getattr(load_library(), size)(ctypes.byref(args)))
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _empty(t, shape, like):
+    return torch.empty(shape, dtype=like.dtype, device=like.device) if t is None else t
+
+
+# ---- convolution -----------------------------------------------------------
+
+def check_conv_shapes(x, weight, bias=None, state0=None, offsets=None):
+    """Dtypes and shapes of the convolution's inputs; returns (B, T, C, K)."""
+    _rows_dtype(x)
+    if weight.dim() != 2:
+        raise ValueError(f"weight must have shape (C, width), got {tuple(weight.shape)}")
+    C, K = weight.shape
+    _req_shape(weight, "weight", torch.float32)
+    if offsets is None:
+        if x.dim() != 3:
+            raise ValueError(f"x must have shape (B, T, C), got {tuple(x.shape)}")
+        B, T = x.shape[:2]
+    else:
+        if x.dim() != 2:
+            raise ValueError(f"packed x must have shape (T, C), got {tuple(x.shape)}")
+        T = x.shape[0]
+        B = _offsets(offsets)
+    _req_shape(x, "x", None, tuple(x.shape[:-1]) + (C,))
+    if bias is not None:
+        _req_shape(bias, "bias", torch.float32, (C,))
+    if state0 is not None:
+        _req_shape(state0, "state0", x.dtype, (B, K - 1, C))
+    return B, T, C, K
+
+
+def conv_forward(x, weight, bias=None, state0=None, offsets=None, activation="silu", out=None, state_out=None,
+                 final_state: bool = True):
+    """Short causal depthwise convolution.  x [B,T,C] (packed [T,C]); weight
+    float32 [C,K], K in 2..4; bias float32 [C]; state0 [B,K-1,C], the rows
+    before each sequence, oldest first (zero when None).  activation None or
+    'silu'.  Returns (y, state): state [B,K-1,C] is the last K-1 inputs of
+    each sequence, the state0 of its continuation (None when final_state is
+    false and no state_out is given; state_out may be state0)."""
+    B, T, C, K = check_conv_shapes(x, weight, bias, state0, offsets)
+    act = _mode(ACTIVATIONS, activation, "activation")
+    if out is not None:
+        _req_shape(out, "out", x.dtype, tuple(x.shape))
+    if state_out is not None:
+        _req_shape(state_out, "state_out", x.dtype, (B, K - 1, C))
+    ld = _row_stride(x, "x", x.dim() - 1, C)
+    _on(x.device, [("weight", weight), ("bias", bias), ("state0", state0), ("offsets", offsets), ("out", out),
+                   ("state_out", state_out)], [("x", x)])
+    out = _empty(out, x.shape, x)
+    if state_out is None and final_state:
+        state_out = torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=x.device)
+    a = ConvArgs(B, T, C, ld, K, _dtype_code(x), act, 0, x.data_ptr(), weight.data_ptr(), _ptr(bias),
+                 _ptr(state0), _ptr(offsets), out.data_ptr(), _ptr(state_out))
+    _call("gdr2_conv_forward", a, x.device)
+    return out, state_out
+
+
+def conv_step(state, x, weight, bias=None, activation="silu", out=None):
+    """The convolution for one token of each of N sequences, in place on
+    ``state`` [N,K-1,C]; x [N,C].  Returns y [N,C]."""
+    _rows_dtype(x)
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError(f"x and weight must have shapes (N, C) and (C, width), got {tuple(x.shape)} and "
+                         f"{tuple(weight.shape)}")
+    act = _mode(ACTIVATIONS, activation, "activation")
+    C, K = weight.shape
+    N = x.shape[0]
+    _req_shape(x, "x", None, (N, C))
+    _req_shape(weight, "weight", torch.float32)
+    _req_shape(state, "state", x.dtype, (N, K - 1, C))
+    if bias is not None:
+        _req_shape(bias, "bias", torch.float32, (C,))
+    if out is not None:
+        _req_shape(out, "out", x.dtype, (N, C))
+    ld = _row_stride(x, "x", 1, C)
+    _on(x.device, [("state", state), ("weight", weight), ("bias", bias), ("out", out)], [("x", x)])
+    out = _empty(out, (N, C), x)
+    a = ConvStepArgs(N, C, ld, K, _dtype_code(x), act, 0, state.data_ptr(), x.data_ptr(),
+                     weight.data_ptr(), _ptr(bias), out.data_ptr())
+    _call("gdr2_conv_step", a, x.device)
+    return out
+
+
+def conv_backward(x, weight, dy, bias=None, state0=None, offsets=None, activation="silu", dstate=None,
+                  want_dstate0=None, workspace=None):
+    """Gradients of ``conv_forward`` for dL/dy (shaped like y) and optionally
+    dL/dstate ``dstate`` [B,K-1,C].  Returns a dict: dx, dweight, dbias (None
+    without bias), dstate0 (by default when state0 is given)."""
+    B, T, C, K = check_conv_shapes(x, weight, bias, state0, offsets)
+    act = _mode(ACTIVATIONS, activation, "activation")
+    _req_shape(dy, "dy", x.dtype, tuple(x.shape))
+    if dstate is not None:
+        _req_shape(dstate, "dstate", x.dtype, (B, K - 1, C))
+    ld = _row_stride(x, "x", x.dim() - 1, C)
+    dev = x.device
+    _on(dev, [("weight", weight), ("bias", bias), ("state0", state0), ("offsets", offsets), ("dy", dy), ("dstate", dstate),
+              ("workspace", workspace)], [("x", x)])
+    want = state0 is not None if want_dstate0 is None else want_dstate0
+    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
+         "dweight": torch.empty_like(weight),
+         "dbias": None if bias is None else torch.empty_like(bias),
+         "dstate0": torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=dev) if want else None}
+    a = ConvBwdArgs(B, T, C, ld, K, _dtype_code(x), act, 0, x.data_ptr(), weight.data_ptr(), _ptr(bias),
+                    _ptr(state0), _ptr(offsets), dy.data_ptr(), _ptr(dstate), g["dx"].data_ptr(), g["dweight"].data_ptr(),
+                    _ptr(g["dbias"]), _ptr(g["dstate0"]))
+    workspace = _with_workspace("gdr2_conv_backward_workspace_size", a, workspace, dev)
+    _call("gdr2_conv_backward", a, dev)
+    return g
+
+
+# ---- scan ------------------------------------------------------------------
+
+def check_scan_shapes(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, offsets=None, lead=None):
+    """Dtypes and shapes of the scan's inputs; returns (B, T, C, N, G).
+    ``lead``: the number of leading dimensions (a step has one)."""
+    _rows_dtype(x)
+    if A.dim() != 2:
+        raise ValueError(f"A must have shape (C, N), got {tuple(A.shape)}")
+    _req_shape(A, "A", torch.float32)
+    C, N = A.shape
+    nlead = lead if lead is not None else 2 if offsets is None else 1
+    if x.dim() != nlead + 1:
+        raise ValueError(f"x must have {nlead + 1} dimensions, got shape {tuple(x.shape)}")
+    rows = tuple(x.shape[:-1])
+    _req_shape(x, "x", None, rows + (C,))
+    _req_shape(dt, "dt", x.dtype, rows + (C,))
+    if Bt.dim() != nlead + 2:
+        raise ValueError(f"Bt must have shape {rows + ('G', N)}, got {tuple(Bt.shape)}")
+    G = Bt.shape[-2]
+    _req_shape(Bt, "Bt", x.dtype, rows + (G, N))
+    _req_shape(Ct, "Ct", x.dtype, rows + (G, N))
+    if z is not None:
+        _req_shape(z, "z", x.dtype, rows + (C,))
+    for n, t in (("skip", skip), ("dt_bias", dt_bias)):
+        if t is not None:
+            _req_shape(t, n, torch.float32, (C,))
+    if offsets is not None:
+        return _offsets(offsets), rows[0], C, N, G
+    return rows[0], rows[1] if nlead == 2 else 1, C, N, G
+
+
+def scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets=None, algo="auto") -> ScanArgs:
+    lead = x.dim() - 1
+    return ScanArgs(B, T, C, N, G, _row_stride(x, "x", lead, C), _row_stride(dt, "dt", lead, C),
+                    _row_stride(Bt, "Bt", lead, G * N), _row_stride(Ct, "Ct", lead, G * N),
+                    0 if z is None else _row_stride(z, "z", lead, C), _dtype_code(x),
+                    SCAN_SOFTPLUS if softplus else 0, _mode(SCAN_ALGOS, algo, "algo"), 0, x.data_ptr(), dt.data_ptr(), Bt.data_ptr(),
+                    Ct.data_ptr(), _ptr(z), A.data_ptr(), _ptr(skip), _ptr(dt_bias), None, _ptr(offsets))
+
+
+def scan_chunk_count(B: int, T: int, packed: bool = False) -> int:
+    """Rows of h_chunks for B sequences of T tokens (packed: T rows in all)."""
+    return int(load_library().gdr2_scan_chunk_count(B, T, int(packed)))
+
+
+def scan_forward(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, h0=None, offsets=None, softplus: bool = True,
+                 out=None, h_out=None, final_state: bool = True, chunk_states=None, algo: str = "auto", workspace=None):
+    """Selective state space scan.  x, dt, z [B,T,C]; Bt, Ct [B,T,G,N] (packed
+    without B); A float32 [C,N]; skip, dt_bias float32 [C]; h0 float32 [B,C,N].
+    Returns (y, h) or, when chunk_states is True or a float32 tensor
+    [scan_chunk_count,C,N], (y, h, h_chunks): the state before every 32nd
+    token, which ``scan_backward`` takes.  h is the state after each sequence
+    (None when final_state is false and no h_out is given; h_out may be h0)."""
+    B, T, C, N, G = check_scan_shapes(x, dt, A, Bt, Ct, skip, z, dt_bias, offsets)
+    for n, t in (("h0", h0), ("h_out", h_out)):
+        if t is not None:
+            _req_shape(t, n, torch.float32, (B, C, N))
+    if out is not None:
+        _req_shape(out, "out", x.dtype, tuple(x.shape))
+    ck = chunk_states if isinstance(chunk_states, torch.Tensor) else None
+    if ck is not None:
+        _req_shape(ck, "chunk_states", torch.float32, (scan_chunk_count(B, T, offsets is not None), C, N))
+    dev = x.device
+    _on(dev, [("A", A), ("skip", skip), ("dt_bias", dt_bias), ("h0", h0), ("offsets", offsets), ("out", out),
+              ("h_out", h_out), ("chunk_states", ck), ("workspace", workspace)],
+        [("x", x), ("dt", dt), ("Bt", Bt), ("Ct", Ct), ("z", z)])
+    a = scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets, algo)
+    out = _empty(out, x.shape, x)
+    if h_out is None and final_state:
+        h_out = torch.empty((B, C, N), dtype=torch.float32, device=dev)
+    if chunk_states is True:
+        ck = torch.empty((scan_chunk_count(B, T, offsets is not None), C, N), dtype=torch.float32, device=dev)
+    a.h0, a.y, a.h_out, a.h_chunks = _ptr(h0), out.data_ptr(), _ptr(h_out), _ptr(ck)
+    workspace = _with_workspace("gdr2_scan_workspace_size", a, workspace, dev)
+    _call("gdr2_scan_forward", a, dev)
+    return (out, h_out) if ck is None else (out, h_out, ck)
+
+
+def scan_step(state, x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, softplus: bool = True, out=None):
+    """The scan for one token of each of B sequences, in place on ``state``
+    float32 [B,C,N]; x, dt, z [B,C]; Bt, Ct [B,G,N].  Returns y [B,C]."""
+    B, _, C, N, G = check_scan_shapes(x, dt, A, Bt, Ct, skip, z, dt_bias, None, lead=1)
+    _req_shape(state, "state", torch.float32, (B, C, N))
+    if out is not None:
+        _req_shape(out, "out", x.dtype, (B, C))
+    dev = x.device
+    _on(dev, [("state", state), ("A", A), ("skip", skip), ("dt_bias", dt_bias), ("out", out)],
+        [("x", x), ("dt", dt), ("Bt", Bt), ("Ct", Ct), ("z", z)])
+    out = _empty(out, (B, C), x)
+    a = ScanStepArgs(scan_args(B, 1, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus), state.data_ptr())
+    a.s.y = out.data_ptr()
+    _call("gdr2_scan_step", a, dev)
+    return out
+
+
+def scan_backward(x, dt, A, Bt, Ct, dy, h_chunks, skip=None, z=None, dt_bias=None, offsets=None, softplus: bool = True,
+                  dh_out=None, want_dh0: bool = True, algo: str = "auto", workspace=None):
+    """Gradients of ``scan_forward`` for dL/dy and optionally dL/dh ``dh_out``
+    float32 [B,C,N]; h_chunks as the forward of the same inputs returned them.
+    Returns a dict: dx, ddt, dBt, dCt, dz (None without z) in the rows' dtype;
+    dA, dskip, ddt_bias (None without their parameter), dh0 float32."""
+    B, T, C, N, G = check_scan_shapes(x, dt, A, Bt, Ct, skip, z, dt_bias, offsets)
+    _req_shape(dy, "dy", x.dtype, tuple(x.shape))
+    _req_shape(h_chunks, "h_chunks", torch.float32, (scan_chunk_count(B, T, offsets is not None), C, N))
+    if dh_out is not None:
+        _req_shape(dh_out, "dh_out", torch.float32, (B, C, N))
+    dev = x.device
+    _on(dev, [("A", A), ("skip", skip), ("dt_bias", dt_bias), ("offsets", offsets), ("dy", dy), ("h_chunks", h_chunks),
+              ("dh_out", dh_out), ("workspace", workspace)],
+        [("x", x), ("dt", dt), ("Bt", Bt), ("Ct", Ct), ("z", z)])
+    f = scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets, algo)
+    f.h_chunks = h_chunks.data_ptr()
+
+    def rows(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
+
+    g = {"dx": rows(x), "ddt": rows(dt), "dBt": rows(Bt), "dCt": rows(Ct), "dz": rows(z),
+         "dA": torch.empty_like(A), "dskip": rows(skip), "ddt_bias": rows(dt_bias),
+         "dh0": torch.empty((B, C, N), dtype=torch.float32, device=dev) if want_dh0 else None}
+    a = ScanBwdArgs(f, dy.data_ptr(), _ptr(dh_out), *(_ptr(g[n]) for n in ("dx", "ddt", "dBt", "dCt", "dz", "dA", "dskip",
+                                                                          "ddt_bias", "dh0")))
+    workspace = _with_workspace("gdr2_scan_backward_workspace_size", a, workspace, dev)
+    _call("gdr2_scan_backward", a, dev)
+    return g
+
+
+# ---- norm ------------------------------------------------------------------
+
+def check_norm_shapes(x, weight=None, bias=None, z=None):
+    """Dtypes and shapes of the norm's inputs; returns (R, C)."""
+    _rows_dtype(x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must have shape (..., C), got {tuple(x.shape)}")
+    C = x.shape[-1]
+    for n, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _req_shape(t, n, torch.float32, (C,))
+    if z is not None:
+        _req_shape(z, "z", x.dtype, tuple(x.shape))
+    return x.numel() // C, C
+
+
+def norm_args(R, C, x, weight, bias, z, eps, kind) -> NormArgs:
+    lead = x.dim() - 1
+    return NormArgs(R, C, _row_stride(x, "x", lead, C), 0 if z is None else _row_stride(z, "z", lead, C), _dtype_code(x),
+                    _mode(KINDS, kind, "kind"), eps, 0, x.data_ptr(), _ptr(z), _ptr(weight), _ptr(bias))
+
+
+def norm_forward(x, weight=None, bias=None, z=None, eps: float = 1e-5, kind: str = "layer", out=None):
+    """Norm of the last dimension: kind 'layer' (mean taken off) or 'rms';
+    weight, bias float32 [C]; with a gate z (shaped like x) the result is
+    multiplied by silu(z)."""
+    R, C = check_norm_shapes(x, weight, bias, z)
+    if out is not None:
+        _req_shape(out, "out", x.dtype, tuple(x.shape))
+    _on(x.device, [("weight", weight), ("bias", bias), ("out", out)], [("x", x), ("z", z)])
+    a = norm_args(R, C, x, weight, bias, z, eps, kind)
+    out = _empty(out, x.shape, x)
+    a.y = out.data_ptr()
+    _call("gdr2_norm_forward", a, x.device)
+    return out
+
+
+def norm_backward(x, dy, weight=None, bias=None, z=None, eps: float = 1e-5, kind: str = "layer", workspace=None):
+    """Gradients of ``norm_forward`` for dL/dy.  Returns a dict: dx, dz (None
+    without z), dweight and dbias (float32, None without their parameter)."""
+    R, C = check_norm_shapes(x, weight, bias, z)
+    _req_shape(dy, "dy", x.dtype, tuple(x.shape))
+    dev = x.device
+    _on(dev, [("weight", weight), ("bias", bias), ("dy", dy), ("workspace", workspace)], [("x", x), ("z", z)])
+    f = norm_args(R, C, x, weight, bias, z, eps, kind)
+    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
+         "dz": None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev),
+         "dweight": None if weight is None else torch.empty_like(weight),
+         "dbias": None if bias is None else torch.empty_like(bias)}
+    a = NormBwdArgs(f, dy.data_ptr(), g["dx"].data_ptr(), _ptr(g["dz"]), _ptr(g["dweight"]), _ptr(g["dbias"]))
+    workspace = _with_workspace("gdr2_norm_backward_workspace_size", a, workspace, dev)
+    _call("gdr2_norm_backward", a, dev)
+    return g

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define GDR2_ABI_VERSION 6
+#define GDR2_ABI_VERSION 7
 
 typedef enum gdr2_status {
     GDR2_OK = 0,
@@ -303,6 +303,267 @@ gdr2_status gdr2_decode_step(const gdr2_decode_args *args, void *stream);
  * scratch's address is looked up on the first call on each device (a HIP
  * error then returns GDR2_ERR_HIP). */
 gdr2_status gdr2_forward_chunked_noalloc(const gdr2_fwd_args *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the recurrence in a sequence-mixing layer: the short
+ * causal convolution in front of it, the selective state space scan beside
+ * it, and the normalisation before and after it.
+ *
+ * Rules these entry points add to the common rules above
+ *   Rows      : a token row is `C` contiguous elements.  Inputs named with a
+ *               *_stride field may be column slices of a wider matrix: row r
+ *               starts at r * stride elements (stride >= the row's width) and
+ *               the pointer is aligned to its element only.  Every other
+ *               buffer is dense and 16-byte aligned.
+ *   Batches   : offsets == NULL: B sequences of T rows each, row b*T + t.
+ *               offsets != NULL (device, int64 [B+1], ascending, within
+ *               0..T): T rows in all, sequence s owns the rows
+ *               offsets[s] .. offsets[s+1]-1 and may be empty.  Rows of no
+ *               sequence are neither read nor written.  The offsets are read
+ *               on the device only: values out of 0..T are clamped to it and
+ *               a descending pair is an empty sequence; offsets that are
+ *               not ascending give unspecified results, within the buffers.
+ *   Parameters: weights, biases, A, skip are fp32 whatever the dtype of the
+ *               rows, and so are their gradients and the scan's states.
+ *   Gradients : of rows, in the rows' dtype, accumulated in fp32 and rounded
+ *               once at the store.  Every sum runs in a fixed order (no
+ *               atomics): a repeated call gives the same bits.
+ *   Sizes     : all int64; a call that would need 2^24 or more workgroups in
+ *               one launch returns GDR2_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------ */
+
+/* Activation fused behind the convolution. */
+typedef enum gdr2_act {
+    GDR2_ACT_NONE = 0,
+    GDR2_ACT_SILU = 1  /* y = p / (1 + exp(-p)) */
+} gdr2_act;
+
+/*
+ * Short causal depthwise convolution over each sequence:
+ *     p[t, c] = bias[c] + sum_{k < width} weight[c, k] x[t - (width-1) + k, c]
+ *     y = act(p)
+ * Rows before the sequence come from state0 (the width-1 rows before it,
+ * oldest first), or are zero without one.
+ *   x         [.., C]            dtype, rows of x_stride elements
+ *   weight    [C, width] fp32    bias [C] fp32, may be NULL
+ *   state0    [B, width-1, C]    dtype, may be NULL
+ *   offsets   see "Batches"
+ *   y         [.., C]            dtype, dense, written
+ *   state_out [B, width-1, C]    dtype, may be NULL: the last width-1 rows of
+ *             (state0, sequence), the state0 of the sequence's continuation.
+ *             May be the same pointer as state0; no other overlap.
+ * Supported set: width in {2, 3, 4}; C >= 1; dtype F32 or BF16; B, T >= 0.
+ */
+typedef struct gdr2_conv_args {
+    int64_t B, T, C;
+    int64_t x_stride;
+    int32_t width;
+    int32_t dtype;        /* gdr2_dtype */
+    int32_t act;          /* gdr2_act */
+    int32_t reserved;     /* must be 0 */
+    const void *x;
+    const float *weight, *bias;
+    const void *state0;
+    const int64_t *offsets;
+    void *y;
+    void *state_out;
+} gdr2_conv_args;
+
+/*
+ * The convolution for one token of each of N sequences:
+ *   state [N, width-1, C] dtype, the previous inputs oldest first; read, then
+ *         overwritten with its last width-2 rows and x
+ *   x     [N, C] dtype, rows of x_stride elements      y [N, C] dtype, written
+ */
+typedef struct gdr2_conv_step_args {
+    int64_t N, C;
+    int64_t x_stride;
+    int32_t width;
+    int32_t dtype;
+    int32_t act;
+    int32_t reserved;     /* must be 0 */
+    void *state;
+    const void *x;
+    const float *weight, *bias;
+    void *y;
+} gdr2_conv_step_args;
+
+/*
+ * Gradients of the convolution, given dy (dL/dy, dense) and optionally dstate
+ * (dL/dstate_out):
+ *   dx [.., C] dtype, dense     dweight [C, width] fp32    dbias [C] fp32, may
+ *   be NULL                     dstate0 [B, width-1, C] dtype, may be NULL
+ * x, weight, bias, state0, offsets and act as given to the forward.
+ */
+typedef struct gdr2_conv_bwd_args {
+    int64_t B, T, C;
+    int64_t x_stride;
+    int32_t width;
+    int32_t dtype;
+    int32_t act;
+    int32_t reserved;     /* must be 0 */
+    const void *x;
+    const float *weight, *bias;
+    const void *state0;
+    const int64_t *offsets;
+    const void *dy;
+    const void *dstate;
+    void *dx;
+    float *dweight, *dbias;
+    void *dstate0;
+    void *workspace;      /* device, >= gdr2_conv_backward_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_conv_bwd_args;
+
+/* Flags of the scan. */
+typedef enum gdr2_scan_flags {
+    GDR2_SCAN_SOFTPLUS = 1  /* the step is softplus(dt + dt_bias), not dt + dt_bias */
+} gdr2_scan_flags;
+
+/* Tokens between two recorded states of the scan (h_chunks). */
+#define GDR2_SCAN_CHUNK 32
+
+/*
+ * Selective state space scan.  For every sequence and channel c, with the
+ * step d_t = softplus(dt_t + dt_bias) and the group j = c / (C / G):
+ *     h_t[c, n] = exp(d_t A[c, n]) h_{t-1}[c, n] + d_t x_t[c] Bt_t[j, n]
+ *     v_t[c]    = sum_n Ct_t[j, n] h_t[c, n] + skip[c] x_t[c]
+ *     y_t       = v_t, or v_t z_t / (1 + exp(-z_t)) with a gate z
+ * (the erase-free relative of the update above, with a decay of its own for
+ * every state element instead of one per key channel).
+ *   x, dt, z  [.., C]   dtype, rows of x_stride, dt_stride, z_stride elements;
+ *                       z may be NULL
+ *   Bt, Ct    [.., G, N] dtype, rows (of G*N elements) b_stride, c_stride apart
+ *   A         [C, N] fp32 (A <= 0 is expected but not required)
+ *   skip, dt_bias [C] fp32, may be NULL
+ *   h0        [B, C, N] fp32, may be NULL (zero)
+ *   y         [.., C]   dtype, dense, written
+ *   h_out     [B, C, N] fp32, may be NULL: the state after each sequence; may
+ *             be the same pointer as h0
+ *   h_chunks  [gdr2_scan_chunk_count(), C, N] fp32, may be NULL: the state
+ *             before the tokens 0, 32, 64, ... of each sequence, which the
+ *             backward reads.  Token 32*i of sequence s is recorded in slot
+ *             s*ceil(T/32) + i, or with offsets offsets[s]/32 + s + i; other
+ *             slots are left as they were.
+ * Supported set: 1 <= N <= 32; G divides C; dtype F32 or BF16; B, T >= 0.
+ * algo: AUTO, STAGED (one pass over each sequence) or SEGMENTED (sequences
+ * cut into segments that run in parallel: a span pass forms each segment's
+ * total decay and local end state, a fold chains them, and the main pass runs
+ * every segment from its start state).  AUTO takes segments when one pass
+ * would leave much of the GPU idle.
+ */
+typedef struct gdr2_scan_args {
+    int64_t B, T, C, N, G;
+    int64_t x_stride, dt_stride, b_stride, c_stride, z_stride;
+    int32_t dtype;
+    int32_t flags;        /* gdr2_scan_flags bits */
+    int32_t algo;         /* gdr2_algo: AUTO, STAGED or SEGMENTED */
+    int32_t reserved;     /* must be 0 */
+    const void *x, *dt, *Bt, *Ct, *z;
+    const float *A, *skip, *dt_bias, *h0;
+    const int64_t *offsets;
+    void *y;
+    float *h_out, *h_chunks;
+    void *workspace;      /* device, >= gdr2_scan_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_scan_args;
+
+/*
+ * The scan for one token of each of B sequences: state [B, C, N] fp32 is read
+ * and overwritten in place; the rows are [B, C] and [B, G, N].  Uses the
+ * fields of gdr2_scan_args except T (must be 1), offsets, h0, h_out, h_chunks
+ * (must be NULL), algo and workspace (ignored).
+ */
+typedef struct gdr2_scan_step_args {
+    gdr2_scan_args s;
+    float *state;
+} gdr2_scan_step_args;
+
+/*
+ * Gradients of the scan, given dy (dL/dy, dense) and optionally dh_out
+ * (dL/dh_out).  `f` holds the forward's arguments, h_chunks as it wrote them
+ * (the states before every 32nd token; h_chunks is required, h0, h_out, y and
+ * f's workspace are not read).
+ *   dx, ddt, dz [.., C] dtype     dBt, dCt [.., G, N] dtype     all dense
+ *   dA [C, N], dskip, ddt_bias [C] fp32     dh0 [B, C, N] fp32
+ * dskip, ddt_bias and dh0 may be NULL; dz is required with z and refused
+ * without it.  dh0 may be the same pointer as dh_out.
+ */
+typedef struct gdr2_scan_bwd_args {
+    gdr2_scan_args f;
+    const void *dy;
+    const float *dh_out;
+    void *dx, *ddt, *dBt, *dCt, *dz;
+    float *dA, *dskip, *ddt_bias, *dh0;
+    void *workspace;      /* device, >= gdr2_scan_backward_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_scan_bwd_args;
+
+/* Which norm. */
+typedef enum gdr2_norm_kind {
+    GDR2_NORM_LAYER = 0,  /* the row's mean is taken off */
+    GDR2_NORM_RMS = 1
+} gdr2_norm_kind;
+
+/*
+ * Normalisation of R rows of C elements:
+ *     n = (x - m) (mean((x - m)^2) + eps)^(-1/2) weight + bias
+ *     y = n, or n z / (1 + exp(-z)) with a gate z
+ * with m the row's mean (LAYER) or 0 (RMS).
+ *   x, z  [R, C] dtype, rows of x_stride, z_stride elements; z may be NULL
+ *   weight, bias [C] fp32, may be NULL (1 and 0)
+ *   y     [R, C] dtype, dense, written
+ * Supported set: C >= 1, R >= 0; eps >= 0 and finite; dtype F32 or BF16.
+ */
+typedef struct gdr2_norm_args {
+    int64_t R, C;
+    int64_t x_stride, z_stride;
+    int32_t dtype;
+    int32_t kind;         /* gdr2_norm_kind */
+    float eps;
+    int32_t reserved;     /* must be 0 */
+    const void *x, *z;
+    const float *weight, *bias;
+    void *y;
+} gdr2_norm_args;
+
+/*
+ * Gradients of the norm, given dy (dL/dy, dense).  `f` holds the forward's
+ * arguments (y is not read).  The row's statistics are formed again from x,
+ * which the gradient reads in any case.
+ *   dx [R, C] dtype, dense      dz [R, C] dtype, dense; required with z and
+ *                               refused without it
+ *   dweight, dbias [C] fp32, may be NULL
+ */
+typedef struct gdr2_norm_bwd_args {
+    gdr2_norm_args f;
+    const void *dy;
+    void *dx, *dz;
+    float *dweight, *dbias;
+    void *workspace;      /* device, >= gdr2_norm_backward_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_norm_bwd_args;
+
+/* The convolution, its single-token step, its gradients. */
+gdr2_status gdr2_conv_forward(const gdr2_conv_args *args, void *stream);
+gdr2_status gdr2_conv_step(const gdr2_conv_step_args *args, void *stream);
+size_t gdr2_conv_backward_workspace_size(const gdr2_conv_bwd_args *args);
+gdr2_status gdr2_conv_backward(const gdr2_conv_bwd_args *args, void *stream);
+
+/* The scan, its single-token step, its gradients.  The workspace queries read
+ * no pointer but whether offsets, and the optional outputs, are NULL; 0 when
+ * none is needed or the arguments are invalid or unsupported. */
+int64_t gdr2_scan_chunk_count(int64_t B, int64_t T, int packed);
+size_t gdr2_scan_workspace_size(const gdr2_scan_args *args);
+gdr2_status gdr2_scan_forward(const gdr2_scan_args *args, void *stream);
+gdr2_status gdr2_scan_step(const gdr2_scan_step_args *args, void *stream);
+size_t gdr2_scan_backward_workspace_size(const gdr2_scan_bwd_args *args);
+gdr2_status gdr2_scan_backward(const gdr2_scan_bwd_args *args, void *stream);
+
+/* The norm and its gradients. */
+gdr2_status gdr2_norm_forward(const gdr2_norm_args *args, void *stream);
+size_t gdr2_norm_backward_workspace_size(const gdr2_norm_bwd_args *args);
+gdr2_status gdr2_norm_backward(const gdr2_norm_bwd_args *args, void *stream);
 
 /* Static text for a status code (never NULL). */
 const char *gdr2_status_string(gdr2_status status);
