@@ -318,8 +318,6 @@ gdr2_status check_forward_args(const gdr2_fwd_args* a)
     return validate_forward(a, &state_bytes, false);
 }
 
-gdr2_status hip_result(hipError_t e, hipStream_t stream, const char* what) { return hip_check(e, stream, what); }
-
 gdr2_status set_error(gdr2_status s, const char* fmt, ...)
 {
     va_list ap;

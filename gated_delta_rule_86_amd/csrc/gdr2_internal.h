@@ -34,9 +34,6 @@ gdr2_status check_forward_args(const gdr2_fwd_args* a);
 // Records a message for gdr2_last_error() in the calling thread; returns s.
 gdr2_status set_error(gdr2_status s, const char* fmt, ...);
 
-// GDR2_OK, or GDR2_ERR_HIP with the error's text recorded for `what`.
-gdr2_status hip_result(hipError_t e, hipStream_t stream, const char* what);
-
 // Compute units of the current device (256 when it cannot be queried).
 int device_cu_count();
 

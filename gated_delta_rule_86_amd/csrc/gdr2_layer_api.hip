@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "gdr2.h"
 #include "gdr2_layer.h"
@@ -12,6 +13,19 @@
 namespace {
 
 using gdr2::set_error;
+
+// GDR2_OK, or GDR2_ERR_HIP with the error's text; GDR2_DEBUG=1 waits for the
+// work first, as for the recurrence's entry points.
+gdr2_status hip_result(hipError_t e, hipStream_t stream, const char* what)
+{
+    static const bool wait = [] {
+        const char* v = std::getenv("GDR2_DEBUG");
+        return v && v[0] && v[0] != '0';
+    }();
+    if (e == hipSuccess && wait)
+        e = hipStreamSynchronize(stream);
+    return e == hipSuccess ? GDR2_OK : set_error(GDR2_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
 
 constexpr int64_t kHuge = (int64_t)1 << 62;
 
@@ -402,7 +416,7 @@ gdr2_status gdr2_conv_forward(const gdr2_conv_args* a, void* stream)
     GDR2_TRY(validate(a));
     if (a->B == 0)
         return GDR2_OK;
-    return gdr2::hip_result(gdr2::launch_conv_forward(*a, (hipStream_t)stream), (hipStream_t)stream, "convolution");
+    return hip_result(gdr2::launch_conv_forward(*a, (hipStream_t)stream), (hipStream_t)stream, "convolution");
 }
 
 gdr2_status gdr2_conv_step(const gdr2_conv_step_args* a, void* stream)
@@ -410,7 +424,7 @@ gdr2_status gdr2_conv_step(const gdr2_conv_step_args* a, void* stream)
     GDR2_TRY(validate(a));
     if (a->N == 0)
         return GDR2_OK;
-    return gdr2::hip_result(gdr2::launch_conv_step(*a, (hipStream_t)stream), (hipStream_t)stream, "convolution step");
+    return hip_result(gdr2::launch_conv_step(*a, (hipStream_t)stream), (hipStream_t)stream, "convolution step");
 }
 
 size_t gdr2_conv_backward_workspace_size(const gdr2_conv_bwd_args* a)
@@ -421,7 +435,7 @@ size_t gdr2_conv_backward_workspace_size(const gdr2_conv_bwd_args* a)
 gdr2_status gdr2_conv_backward(const gdr2_conv_bwd_args* a, void* stream)
 {
     GDR2_TRY(validate(a));
-    return gdr2::hip_result(gdr2::launch_conv_backward(*a, (hipStream_t)stream), (hipStream_t)stream, "convolution backward");
+    return hip_result(gdr2::launch_conv_backward(*a, (hipStream_t)stream), (hipStream_t)stream, "convolution backward");
 }
 
 int64_t gdr2_scan_chunk_count(int64_t B, int64_t T, int packed)
@@ -441,7 +455,7 @@ gdr2_status gdr2_scan_forward(const gdr2_scan_args* a, void* stream)
     GDR2_TRY(validate(a));
     if (a->B == 0)
         return GDR2_OK;
-    return gdr2::hip_result(gdr2::launch_scan_forward(*a, (hipStream_t)stream), (hipStream_t)stream, "scan");
+    return hip_result(gdr2::launch_scan_forward(*a, (hipStream_t)stream), (hipStream_t)stream, "scan");
 }
 
 gdr2_status gdr2_scan_step(const gdr2_scan_step_args* a, void* stream)
@@ -449,7 +463,7 @@ gdr2_status gdr2_scan_step(const gdr2_scan_step_args* a, void* stream)
     GDR2_TRY(validate(a));
     if (a->s.B == 0)
         return GDR2_OK;
-    return gdr2::hip_result(gdr2::launch_scan_step(*a, (hipStream_t)stream), (hipStream_t)stream, "scan step");
+    return hip_result(gdr2::launch_scan_step(*a, (hipStream_t)stream), (hipStream_t)stream, "scan step");
 }
 
 size_t gdr2_scan_backward_workspace_size(const gdr2_scan_bwd_args* a)
@@ -460,7 +474,7 @@ size_t gdr2_scan_backward_workspace_size(const gdr2_scan_bwd_args* a)
 gdr2_status gdr2_scan_backward(const gdr2_scan_bwd_args* a, void* stream)
 {
     GDR2_TRY(validate(a));
-    return gdr2::hip_result(gdr2::launch_scan_backward(*a, (hipStream_t)stream), (hipStream_t)stream, "scan backward");
+    return hip_result(gdr2::launch_scan_backward(*a, (hipStream_t)stream), (hipStream_t)stream, "scan backward");
 }
 
 gdr2_status gdr2_norm_forward(const gdr2_norm_args* a, void* stream)
@@ -468,7 +482,7 @@ gdr2_status gdr2_norm_forward(const gdr2_norm_args* a, void* stream)
     GDR2_TRY(validate(a));
     if (a->R == 0)
         return GDR2_OK;
-    return gdr2::hip_result(gdr2::launch_norm_forward(*a, (hipStream_t)stream), (hipStream_t)stream, "norm");
+    return hip_result(gdr2::launch_norm_forward(*a, (hipStream_t)stream), (hipStream_t)stream, "norm");
 }
 
 size_t gdr2_norm_backward_workspace_size(const gdr2_norm_bwd_args* a)
@@ -479,7 +493,7 @@ size_t gdr2_norm_backward_workspace_size(const gdr2_norm_bwd_args* a)
 gdr2_status gdr2_norm_backward(const gdr2_norm_bwd_args* a, void* stream)
 {
     GDR2_TRY(validate(a));
-    return gdr2::hip_result(gdr2::launch_norm_backward(*a, (hipStream_t)stream), (hipStream_t)stream, "norm backward");
+    return hip_result(gdr2::launch_norm_backward(*a, (hipStream_t)stream), (hipStream_t)stream, "norm backward");
 }
 
 }  // extern "C"
