@@ -28,6 +28,7 @@ gdr2_status hip_result(hipError_t e, hipStream_t stream, const char* what)
 }
 
 constexpr int64_t kHuge = (int64_t)1 << 62;
+constexpr int64_t kMaxStride = (int64_t)1 << 24;
 
 // One buffer of a call: its bytes from the first to the last element.
 struct Buf {
@@ -106,9 +107,12 @@ gdr2_status check_dtype(int32_t dtype, int32_t reserved)
 
 gdr2_status check_stride(const char* name, int64_t stride, int64_t width)
 {
-    if (stride < width || stride > ((int64_t)1 << 40))
+    if (stride < width)
         return set_error(GDR2_ERR_INVALID_ARG, "%s must be at least the row's %lld elements (got %lld)", name,
                          (long long)width, (long long)stride);
+    // the kernels form offsets within 32 rows in 32 bits of bytes
+    if (stride > kMaxStride)
+        return set_error(GDR2_ERR_UNSUPPORTED, "%s: rows may be at most 2^24 elements apart", name);
     return GDR2_OK;
 }
 
@@ -145,7 +149,7 @@ gdr2_status check_conv(int64_t B, int64_t T, int64_t C, int64_t x_stride, int32_
     if (width < 2 || width > 4)
         return set_error(GDR2_ERR_UNSUPPORTED, "supported widths: 2, 3, 4 (got %d)", width);
     GDR2_TRY(check_stride("x_stride", x_stride, C));
-    if (B > ((int64_t)1 << 40) || T > ((int64_t)1 << 40) || C > ((int64_t)1 << 31) ||
+    if (B > ((int64_t)1 << 40) || T > ((int64_t)1 << 40) ||
         gdr2::conv_launch_groups(B, T, C, packed) >= gdr2::kMaxGroups)
         return too_many();
     return GDR2_OK;
@@ -239,8 +243,6 @@ gdr2_status check_scan(const gdr2_scan_args& a)
     GDR2_TRY(check_stride("dt_stride", a.dt_stride, a.C));
     if (a.z)
         GDR2_TRY(check_stride("z_stride", a.z_stride, a.C));
-    if (a.C > ((int64_t)1 << 31))
-        return too_many();
     GDR2_TRY(check_stride("b_stride", a.b_stride, a.G * a.N));
     GDR2_TRY(check_stride("c_stride", a.c_stride, a.G * a.N));
     const int64_t rows = a.offsets ? a.T : mul(a.B, a.T);
@@ -355,7 +357,7 @@ gdr2_status check_norm(const gdr2_norm_args& a)
     GDR2_TRY(check_stride("x_stride", a.x_stride, a.C));
     if (a.z)
         GDR2_TRY(check_stride("z_stride", a.z_stride, a.C));
-    if (a.C > ((int64_t)1 << 31) || a.R > ((int64_t)1 << 40) || gdr2::norm_launch_groups(a) >= gdr2::kMaxGroups)
+    if (a.R > ((int64_t)1 << 40) || gdr2::norm_launch_groups(a) >= gdr2::kMaxGroups)
         return too_many();
     return GDR2_OK;
 }

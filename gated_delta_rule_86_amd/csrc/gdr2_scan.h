@@ -87,36 +87,137 @@ __device__ __forceinline__ ScanLane scan_lane(const gdr2_scan_args& a, uint32_t 
     return l;
 }
 
-// NS fp32 per lane from / to a row of N states (zero past N).
+// NS fp32 per lane from / to a row of N states (zero past N).  One access per
+// lane when whole lanes are in or out (N a multiple of NS; rows are then
+// aligned to NS elements).
 template <int NS>
-__device__ __forceinline__ void load_states(const float* row, int s, int64_t N, bool on, float (&h)[NS])
+__device__ __forceinline__ void load_states(const float* row, int s, int N, bool on, float (&h)[NS])
 {
+    typedef float Vec __attribute__((ext_vector_type(NS)));
+    if (N % NS == 0) {
+        Vec v;
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-        h[i] = on && s * NS + i < N ? row[s * NS + i] : 0.f;
-}
-template <int NS>
-__device__ __forceinline__ void store_states(float* row, int s, int64_t N, bool on, const float (&h)[NS])
-{
+        for (int i = 0; i < NS; ++i)
+            v[i] = 0.f;
+        if (on && s * NS < N)
+            v = *reinterpret_cast<const Vec*>(row + s * NS);
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-        if (on && s * NS + i < N)
-            row[s * NS + i] = h[i];
-}
-
-// B and / or C of the tokens t .. t + 31 of group j into LDS, fp32 [32][NP],
-// zero past the sequence and past N.
-template <typename T, int NP>
-__device__ __forceinline__ void stage_rows(const void* base, int64_t ld, int64_t row0, int64_t t, int64_t len, int64_t j,
-                                           int64_t N, float (*dst)[NP])
-{
-    for (int e = threadIdx.x; e < kScanChunk * NP; e += 256) {
-        const int r = e / NP, n = e % NP;
-        float v = 0.f;
-        if (t + r < len && n < N)
-            v = to_f32(((const T*)base)[(row0 + t + r) * ld + j * N + n]);
-        dst[r][n] = v;
+        for (int i = 0; i < NS; ++i)
+            h[i] = v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            h[i] = on && s * NS + i < N ? row[s * NS + i] : 0.f;
     }
 }
+template <int NS>
+__device__ __forceinline__ void store_states(float* row, int s, int N, bool on, const float (&h)[NS])
+{
+    typedef float Vec __attribute__((ext_vector_type(NS)));
+    if (N % NS == 0) {
+        Vec v;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            v[i] = h[i];
+        if (on && s * NS < N)
+            *reinterpret_cast<Vec*>(row + s * NS) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (on && s * NS + i < N)
+                row[s * NS + i] = h[i];
+    }
+}
+
+// ---- loads ahead ----------------------------------------------------------
+// A workgroup-uniform value the compiler cannot see to be one (it came through
+// a vector load), kept in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ Piece uniform(const Piece& q)
+{
+    return {uniform(q.seq), uniform(q.index), uniform(q.row0), uniform(q.len), uniform(q.first)};
+}
+
+// Rows are read and written through buffer descriptors: the descriptor's
+// base is the chunk's first row, its length ends behind the last row of the
+// chunk that exists, and an access past the length reads 0 or writes nothing.
+// So the tokens past a sequence cost no compare and no branch, and the lane
+// offsets stay the same from chunk to chunk.
+constexpr int kGroups = kScanChunk / 4;
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset past every length (32 rows, 2^24 elements apart, 4 bytes)
+
+template <typename T> __device__ __forceinline__ auto chunk_buffer(const void* base, int64_t row, int64_t ld, int left)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((T*)base + row * ld), (short)0, (int)(left * (int)ld * (int)sizeof(T)),
+                                             0x00020000);
+}
+template <typename T, typename R> __device__ __forceinline__ T buffer_get(R rsrc, uint32_t off)
+{
+    if constexpr (sizeof(T) == 2)
+        return __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, off, 0, 0));
+    else
+        return __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0));
+}
+template <typename T, typename R> __device__ __forceinline__ void buffer_put(R rsrc, uint32_t off, T v)
+{
+    if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rsrc, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, off, 0, 0);
+}
+
+// One row array of a chunk: this lane's elements are tokens 4 g + s.
+template <typename T> struct TokenRows {
+    uint32_t off[kGroups];
+    __device__ __forceinline__ TokenRows(int64_t ld, int64_t c, int s, bool on)
+    {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            off[g] = on ? (uint32_t)((4 * g + s) * (int)ld + (int)c) * (uint32_t)sizeof(T) : kNowhere;
+    }
+    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t ld, int left, T (&raw)[kGroups]) const
+    {
+        const auto r = chunk_buffer<T>(base, row, ld, left);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            raw[g] = buffer_get<T>(r, off[g]);
+    }
+};
+
+// B or C of a chunk's tokens for group j, on their way to LDS as fp32
+// [32][NP]: zero past the sequence and past N.
+template <typename T, int NP> struct Staged {
+    static constexpr int PER = kScanChunk * NP / 256;
+    uint32_t off[PER];
+    T raw[PER];
+
+    __device__ __forceinline__ Staged(int64_t ld, int64_t j, int N)
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + 256 * i, r = e / NP, n = e % NP;
+            off[i] = n < N ? (uint32_t)(r * (int)ld + (int)j * N + n) * (uint32_t)sizeof(T) : kNowhere;
+        }
+    }
+    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t ld, int left)
+    {
+        const auto r = chunk_buffer<T>(base, row, ld, left);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            raw[i] = buffer_get<T>(r, off[i]);
+    }
+    __device__ __forceinline__ void store(float (*dst)[NP]) const
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = threadIdx.x + 256 * i;
+            dst[e / NP][e % NP] = to_f32(raw[i]);
+        }
+    }
+};
 
 }  // namespace gdr2

@@ -18,32 +18,30 @@ namespace gdr2 {
 
 namespace {
 
-// One token group of four: steps and inputs of this lane's token.
-template <typename T>
-__device__ __forceinline__ void token_step(const gdr2_scan_args& a, int64_t row, int64_t c, bool in, float bias, float& x,
-                                           float& d)
+// The step of a token.
+__device__ __forceinline__ float step_of(float dt, float bias, int flags)
 {
-    x = d = 0.f;
-    if (in) {
-        x = to_f32(((const T*)a.x)[row * a.x_stride + c]);
-        const float raw = to_f32(((const T*)a.dt)[row * a.dt_stride + c]) + bias;
-        d = a.flags & GDR2_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
-    }
+    const float raw = dt + bias;
+    return flags & GDR2_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
 }
 
+// Both passes walk a segment chunk by chunk.  The rows of the next chunk are
+// requested before the current one is computed (there is about one wave per
+// SIMD, so nothing else hides their latency), and B and C alternate between
+// two LDS buffers, so a chunk costs one barrier.
 template <typename T, int NS>
 __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                            const float* starts)
 {
     constexpr int NP = 4 * NS;
-    __shared__ __align__(16) float s_b[kScanChunk][NP], s_c[kScanChunk][NP];
+    __shared__ __align__(16) float s_b[2][kScanChunk][NP], s_c[2][kScanChunk][NP];
     const uint32_t slot = blockIdx.x / ncb;
-    const Piece q = piece_of(seg, slot);
+    const Piece q = uniform(piece_of(seg, slot));
     if (q.seq < 0)
         return;
     const ScanLane l = scan_lane(a, blockIdx.x - slot * ncb, cb_per);
-    const int s = l.s;
-    const int64_t N = a.N, c = l.c;
+    const int s = l.s, N = (int)a.N;
+    const int64_t c = l.c, j = uniform(l.j);
     float A2[NS], h[NS];
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
@@ -56,85 +54,117 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pie
     const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
     const float skip = a.skip && l.on ? a.skip[c] : 0.f;
     const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
-    const int64_t ck0 = sequence_of(ckp, q.seq).first;
+    const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
 
     const int64_t t0 = q.index << seg.lg;
     const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
-    for (int64_t t = t0; t < t1; t += kScanChunk) {
-        __syncthreads();
-        stage_rows<T, NP>(a.Bt, a.b_stride, q.row0, t, t1, l.j, N, s_b);
-        stage_rows<T, NP>(a.Ct, a.c_stride, q.row0, t, t1, l.j, N, s_c);
-        __syncthreads();
+    const TokenRows<T> xs(a.x_stride, c, s, l.on), ts(a.dt_stride, c, s, l.on), zs(a.z_stride, c, s, l.on), ys(a.C, c, s, l.on);
+    T rx[kGroups], rt[kGroups], rz[kGroups] = {};
+    Staged<T, NP> rb(a.b_stride, j, N), rc(a.c_stride, j, N);
+    auto fetch = [&](int64_t t) {
+        const int left = (int)min(t1 - t, (int64_t)kScanChunk);
+        rb.load(a.Bt, q.row0 + t, a.b_stride, left);
+        rc.load(a.Ct, q.row0 + t, a.c_stride, left);
+        ts.load(a.dt, q.row0 + t, a.dt_stride, left, rt);
+        xs.load(a.x, q.row0 + t, a.x_stride, left, rx);
+        if (a.z)
+            zs.load(a.z, q.row0 + t, a.z_stride, left, rz);
+    };
+    if (t0 < t1)
+        fetch(t0);
+    int buf = 0;
+    for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
+        const int left = (int)min(t1 - t, (int64_t)kScanChunk);
+        float x[kGroups], d[kGroups], z[kGroups];
+        rb.store(s_b[buf]);
+        rc.store(s_c[buf]);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            x[g] = to_f32(rx[g]);
+            d[g] = 4 * g + s < left ? step_of(to_f32(rt[g]), bias, a.flags) : 0.f;
+            z[g] = to_f32(rz[g]);
+        }
+        if (t + kScanChunk < t1)
+            fetch(t + kScanChunk);
         if (a.h_chunks)
             store_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * a.C + c) * N, s, N, l.on, h);
-#pragma unroll 1
-        for (int tt = 0; tt < kScanChunk; tt += 4) {
-            const int64_t mt = t + tt + s;
-            const bool in = l.on && mt < t1;
-            const int64_t row = q.row0 + mt;
-            float x, d;
-            token_step<T>(a, row, c, in, bias, x, d);
-            const float u = d * x;
+        __syncthreads();
+        const auto yb = chunk_buffer<T>(a.y, q.row0 + t, a.C, left);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const float u = d[g] * x[g];
             float p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float dk = quad_bcast_k(d, k), uk = quad_bcast_k(u, k);
+                const float dk = quad_bcast_k(d[g], k), uk = quad_bcast_k(u, k);
                 p[k] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * s_b[tt + k][s * NS + i]);
-                    p[k] = fmaf(s_c[tt + k][s * NS + i], h[i], p[k]);
+                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * s_b[buf][4 * g + k][s * NS + i]);
+                    p[k] = fmaf(s_c[buf][4 * g + k][s * NS + i], h[i], p[k]);
                 }
             }
-            float y = fmaf(skip, x, quad_sum_transposed(p, s));
-            if (in) {
-                if (a.z)
-                    y *= silu_f(to_f32(((const T*)a.z)[row * a.z_stride + c]));
-                ((T*)a.y)[row * a.C + c] = from_f32<T>(y);
-            }
+            float y = fmaf(skip, x[g], quad_sum_transposed(p, s));
+            if (a.z)
+                y *= silu_f(z[g]);
+            buffer_put<T>(yb, ys.off[g], from_f32<T>(y));
         }
     }
     if (a.h_out && t1 == q.len)
         store_states<NS>(a.h_out + (q.seq * a.C + c) * N, s, N, l.on, h);
 }
 
-// (sum d, E) of every segment but the last of its sequence.
+// (sum d, E) of every segment but the last of its sequence: whole segments.
 template <typename T, int NS>
 __global__ __launch_bounds__(256) void scan_span_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                         float* states, float* sums)
 {
     constexpr int NP = 4 * NS;
-    __shared__ __align__(16) float s_b[kScanChunk][NP];
+    __shared__ __align__(16) float s_b[2][kScanChunk][NP];
     const uint32_t slot = blockIdx.x / ncb;
-    const Piece q = piece_of(seg, slot);
+    const Piece q = uniform(piece_of(seg, slot));
     const int64_t t0 = q.index << seg.lg, t1 = t0 + ((int64_t)1 << seg.lg);
     if (q.seq < 0 || t1 >= q.len)
         return;
     const ScanLane l = scan_lane(a, blockIdx.x - slot * ncb, cb_per);
-    const int s = l.s;
-    const int64_t N = a.N, c = l.c;
+    const int s = l.s, N = (int)a.N;
+    const int64_t c = l.c, j = uniform(l.j);
     float A2[NS], h[NS] = {}, sum = 0.f;
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
         A2[i] *= kLog2e;
     const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
-    for (int64_t t = t0; t < t1; t += kScanChunk) {
+    const TokenRows<T> xs(a.x_stride, c, s, l.on), ts(a.dt_stride, c, s, l.on);
+    T rx[kGroups], rt[kGroups];
+    Staged<T, NP> rb(a.b_stride, j, N);
+    auto fetch = [&](int64_t t) {
+        rb.load(a.Bt, q.row0 + t, a.b_stride, kScanChunk);
+        ts.load(a.dt, q.row0 + t, a.dt_stride, kScanChunk, rt);
+        xs.load(a.x, q.row0 + t, a.x_stride, kScanChunk, rx);
+    };
+    fetch(t0);
+    int buf = 0;
+    for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
+        float u[kGroups], d[kGroups];
+        rb.store(s_b[buf]);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            d[g] = step_of(to_f32(rt[g]), bias, a.flags);
+            u[g] = d[g] * to_f32(rx[g]);
+        }
+        if (t + kScanChunk < t1)
+            fetch(t + kScanChunk);
         __syncthreads();
-        stage_rows<T, NP>(a.Bt, a.b_stride, q.row0, t, t1, l.j, N, s_b);
-        __syncthreads();
-#pragma unroll 1
-        for (int tt = 0; tt < kScanChunk; tt += 4) {
-            float x, d;
-            token_step<T>(a, q.row0 + t + tt + s, c, l.on, bias, x, d);
-            const float u = d * x;
-            sum += d;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            sum += d[g];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float dk = quad_bcast_k(d, k), uk = quad_bcast_k(u, k);
+                const float dk = quad_bcast_k(d[g], k), uk = quad_bcast_k(u[g], k);
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
-                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * s_b[tt + k][s * NS + i]);
+                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * s_b[buf][4 * g + k][s * NS + i]);
             }
         }
     }
@@ -191,8 +221,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p)
         Bv[i] = in ? to_f32(Bt[s * 4 + i]) : 0.f;
         Cv[i] = in ? to_f32(Ct[s * 4 + i]) : 0.f;
     }
-    float x = 0.f, d = 0.f;
-    token_step<T>(a, b, c, on, a.dt_bias ? a.dt_bias[c] : 0.f, x, d);
+    const float x = on ? to_f32(((const T*)a.x)[b * a.x_stride + c]) : 0.f;
+    const float d = on ? step_of(to_f32(((const T*)a.dt)[b * a.dt_stride + c]), a.dt_bias ? a.dt_bias[c] : 0.f, a.flags) : 0.f;
     float y = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

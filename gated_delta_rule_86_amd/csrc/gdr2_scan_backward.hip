@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void scan_backward_kernel(gdr2_scan_bwd_args p
     __shared__ __align__(16) float s_b[kScanChunk][NP], s_c[kScanChunk][NP];
     __shared__ __align__(16) float s_red[2][4][SUB][NP];
     const uint32_t slot = blockIdx.x / ncb, cb = blockIdx.x - slot * ncb;
-    const Piece q = piece_of(seg, slot);
+    const Piece q = uniform(piece_of(seg, slot));
     const ScanLane l = scan_lane(a, cb, cb_per);
     const int s = l.s, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t N = a.N, C = a.C, c = l.c;
@@ -81,8 +81,12 @@ __global__ __launch_bounds__(256) void scan_backward_kernel(gdr2_scan_bwd_args p
         const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
         for (int64_t t = t0 + ((t1 - t0 - 1) >> kScanLg << kScanLg); t1 > t0 && t >= t0; t -= kScanChunk) {
             __syncthreads();
-            stage_rows<T, NP>(a.Bt, a.b_stride, q.row0, t, t1, l.j, N, s_b);
-            stage_rows<T, NP>(a.Ct, a.c_stride, q.row0, t, t1, l.j, N, s_c);
+            const int left = (int)min(t1 - t, (int64_t)kScanChunk);
+            Staged<T, NP> rb(a.b_stride, l.j, (int)N), rc(a.c_stride, l.j, (int)N);
+            rb.load(a.Bt, q.row0 + t, a.b_stride, left);
+            rc.load(a.Ct, q.row0 + t, a.c_stride, left);
+            rb.store(s_b);
+            rc.store(s_c);
             float xs[NG], raws[NG], ds[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -223,7 +227,7 @@ __global__ __launch_bounds__(256) void scan_backward_span_kernel(gdr2_scan_bwd_a
     const gdr2_scan_args& a = p.f;
     __shared__ __align__(16) float s_c[kScanChunk][NP];
     const uint32_t slot = blockIdx.x / ncb;
-    const Piece q = piece_of(seg, slot);
+    const Piece q = uniform(piece_of(seg, slot));
     if (q.seq < 0 || q.index == 0)
         return;
     const ScanLane l = scan_lane(a, blockIdx.x - slot * ncb, cb_per);
@@ -239,7 +243,10 @@ __global__ __launch_bounds__(256) void scan_backward_span_kernel(gdr2_scan_bwd_a
     const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
     for (int64_t t = t0 + ((t1 - t0 - 1) >> kScanLg << kScanLg); t >= t0; t -= kScanChunk) {
         __syncthreads();
-        stage_rows<T, NP>(a.Ct, a.c_stride, q.row0, t, t1, l.j, N, s_c);
+        const int left = (int)min(t1 - t, (int64_t)kScanChunk);
+        Staged<T, NP> rc(a.c_stride, l.j, (int)N);
+        rc.load(a.Ct, q.row0 + t, a.c_stride, left);
+        rc.store(s_c);
         __syncthreads();
 #pragma unroll 1
         for (int tt = kScanChunk - 4; tt >= 0; tt -= 4) {

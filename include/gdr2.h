@@ -328,8 +328,9 @@ gdr2_status gdr2_forward_chunked_noalloc(const gdr2_fwd_args *args, void *stream
  *   Gradients : of rows, in the rows' dtype, accumulated in fp32 and rounded
  *               once at the store.  Every sum runs in a fixed order (no
  *               atomics): a repeated call gives the same bits.
- *   Sizes     : all int64; a call that would need 2^24 or more workgroups in
- *               one launch returns GDR2_ERR_UNSUPPORTED.
+ *   Sizes     : all int64; rows further apart than 2^24 elements, and a call
+ *               that would need 2^24 or more workgroups in one launch, return
+ *               GDR2_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------ */
 
 /* Activation fused behind the convolution. */

@@ -112,7 +112,7 @@ MAKE = {"gdr2_conv_forward": conv, "gdr2_conv_step": conv_step, "gdr2_conv_backw
 CASES = {
     "gdr2_conv_forward": [("B", -1, INV), ("T", -1, INV), ("C", 0, INV), ("x_stride", 63, INV), ("width", 1, UNS),
                           ("width", 5, UNS), ("dtype", 2, INV), ("act", 2, INV), ("reserved", 1, INV), ("T", 1 << 50, UNS),
-                          ("B", 1 << 45, UNS), ("x_stride", 1 << 61, INV)],
+                          ("B", 1 << 45, UNS), ("x_stride", 1 << 61, UNS)],
     "gdr2_conv_step": [("N", -1, INV), ("C", -3, INV), ("x_stride", 10, INV), ("width", 0, UNS), ("dtype", -1, INV),
                        ("act", -1, INV), ("reserved", 7, INV), ("N", 1 << 40, UNS)],
     "gdr2_conv_backward": [("B", -1, INV), ("width", 5, UNS), ("dtype", 9, INV), ("act", 3, INV), ("x_stride", 1, INV),
