@@ -155,12 +155,18 @@ template <typename T> __device__ __forceinline__ auto chunk_buffer(const void* b
     return __builtin_amdgcn_make_buffer_rsrc((void*)((T*)base + row * ld), (short)0, (int)(left * (int)ld * (int)sizeof(T)),
                                              0x00020000);
 }
-template <typename T, typename R> __device__ __forceinline__ T buffer_get(R rsrc, uint32_t off)
+// A loaded element stays in a register of its own until it is used: as bf16
+// the compiler would pack pairs, and wait for the loads to do so.
+template <typename T, typename R> __device__ __forceinline__ uint32_t buffer_get(R rsrc, uint32_t off)
 {
     if constexpr (sizeof(T) == 2)
-        return __builtin_bit_cast(T, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, off, 0, 0));
+        return __builtin_amdgcn_raw_buffer_load_b16(rsrc, off, 0, 0);
     else
-        return __builtin_bit_cast(T, (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0));
+        return __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0);
+}
+template <typename T> __device__ __forceinline__ float raw_f32(uint32_t raw)
+{
+    return __builtin_bit_cast(float, sizeof(T) == 2 ? raw << 16 : raw);
 }
 template <typename T, typename R> __device__ __forceinline__ void buffer_put(R rsrc, uint32_t off, T v)
 {
@@ -179,7 +185,7 @@ template <typename T> struct TokenRows {
         for (int g = 0; g < kGroups; ++g)
             off[g] = on ? (uint32_t)((4 * g + s) * (int)ld + (int)c) * (uint32_t)sizeof(T) : kNowhere;
     }
-    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t ld, int left, T (&raw)[kGroups]) const
+    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t ld, int left, uint32_t (&raw)[kGroups]) const
     {
         const auto r = chunk_buffer<T>(base, row, ld, left);
 #pragma unroll
@@ -192,8 +198,7 @@ template <typename T> struct TokenRows {
 // [32][NP]: zero past the sequence and past N.
 template <typename T, int NP> struct Staged {
     static constexpr int PER = kScanChunk * NP / 256;
-    uint32_t off[PER];
-    T raw[PER];
+    uint32_t off[PER], raw[PER];
 
     __device__ __forceinline__ Staged(int64_t ld, int64_t j, int N)
     {
@@ -215,8 +220,50 @@ template <typename T, int NP> struct Staged {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = threadIdx.x + 256 * i;
-            dst[e / NP][e % NP] = to_f32(raw[i]);
+            dst[e / NP][e % NP] = raw_f32<T>(raw[i]);
         }
+    }
+};
+
+// The steps of a chunk's tokens, all groups side by side (the eight chains of
+// transcendentals fill each other's latencies); 0 past the sequence.
+template <typename T>
+__device__ __forceinline__ void chunk_steps(const uint32_t (&raw)[kGroups], float bias, int flags, int s, int left,
+                                            float (&pre)[kGroups], float (&d)[kGroups])
+{
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g)
+        d[g] = pre[g] = raw_f32<T>(raw[g]) + bias;
+    if (flags & GDR2_SCAN_SOFTPLUS) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            d[g] = softplus_f(pre[g]);
+    }
+    if (left < kScanChunk) {
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            d[g] = 4 * g + s < left ? d[g] : 0.f;
+    }
+}
+
+// The states s NS .. of B and / or C for four tokens, in registers.  Read one
+// group of tokens ahead of its use: a wave alone on its SIMD would otherwise
+// stand still for the LDS at every token.
+template <int NS> struct Quad {
+    float v[4][NS];
+    template <int NP> __device__ __forceinline__ void read(const float (*src)[NP], int tt, int s)
+    {
+        typedef float Vec __attribute__((ext_vector_type(NS < 4 ? NS : 4)));
+        constexpr int W = NS < 4 ? NS : 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < NS; i += W) {
+                const Vec x = *reinterpret_cast<const Vec*>(&src[tt + k][s * NS + i]);
+#pragma unroll
+                for (int e = 0; e < W; ++e)
+                    v[k][i + e] = x[e];
+            }
     }
 };
 

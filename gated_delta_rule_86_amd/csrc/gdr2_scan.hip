@@ -29,7 +29,7 @@ __device__ __forceinline__ float step_of(float dt, float bias, int flags)
 // requested before the current one is computed (there is about one wave per
 // SIMD, so nothing else hides their latency), and B and C alternate between
 // two LDS buffers, so a chunk costs one barrier.
-template <typename T, int NS>
+template <typename T, int NS, bool GATE>
 __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                            const float* starts)
 {
@@ -59,7 +59,7 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pie
     const int64_t t0 = q.index << seg.lg;
     const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
     const TokenRows<T> xs(a.x_stride, c, s, l.on), ts(a.dt_stride, c, s, l.on), zs(a.z_stride, c, s, l.on), ys(a.C, c, s, l.on);
-    T rx[kGroups], rt[kGroups], rz[kGroups] = {};
+    uint32_t rx[kGroups], rt[kGroups], rz[kGroups] = {};
     Staged<T, NP> rb(a.b_stride, j, N), rc(a.c_stride, j, N);
     auto fetch = [&](int64_t t) {
         const int left = (int)min(t1 - t, (int64_t)kScanChunk);
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pie
         rc.load(a.Ct, q.row0 + t, a.c_stride, left);
         ts.load(a.dt, q.row0 + t, a.dt_stride, left, rt);
         xs.load(a.x, q.row0 + t, a.x_stride, left, rx);
-        if (a.z)
+        if constexpr (GATE)
             zs.load(a.z, q.row0 + t, a.z_stride, left, rz);
     };
     if (t0 < t1)
@@ -75,14 +75,14 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pie
     int buf = 0;
     for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
         const int left = (int)min(t1 - t, (int64_t)kScanChunk);
-        float x[kGroups], d[kGroups], z[kGroups];
+        float x[kGroups], pre[kGroups], d[kGroups], z[kGroups];
         rb.store(s_b[buf]);
         rc.store(s_c[buf]);
+        chunk_steps<T>(rt, bias, a.flags, s, left, pre, d);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            x[g] = to_f32(rx[g]);
-            d[g] = 4 * g + s < left ? step_of(to_f32(rt[g]), bias, a.flags) : 0.f;
-            z[g] = to_f32(rz[g]);
+            x[g] = raw_f32<T>(rx[g]);
+            z[g] = raw_f32<T>(rz[g]);
         }
         if (t + kScanChunk < t1)
             fetch(t + kScanChunk);
@@ -90,22 +90,29 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pie
             store_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * a.C + c) * N, s, N, l.on, h);
         __syncthreads();
         const auto yb = chunk_buffer<T>(a.y, q.row0 + t, a.C, left);
+        Quad<NS> bq[2], cq[2];
+        bq[0].template read<NP>(s_b[buf], 0, s);
+        cq[0].template read<NP>(s_c[buf], 0, s);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
+            if (g + 1 < kGroups) {
+                bq[(g + 1) & 1].template read<NP>(s_b[buf], 4 * g + 4, s);
+                cq[(g + 1) & 1].template read<NP>(s_c[buf], 4 * g + 4, s);
+            }
+            __builtin_amdgcn_sched_barrier(0);
             const float u = d[g] * x[g];
             float p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float dk = quad_bcast_k(d[g], k), uk = quad_bcast_k(u, k);
-                p[k] = 0.f;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * s_b[buf][4 * g + k][s * NS + i]);
-                    p[k] = fmaf(s_c[buf][4 * g + k][s * NS + i], h[i], p[k]);
+                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * bq[g & 1].v[k][i]);
+                    p[k] = i == 0 ? cq[g & 1].v[k][0] * h[0] : fmaf(cq[g & 1].v[k][i], h[i], p[k]);
                 }
             }
             float y = fmaf(skip, x[g], quad_sum_transposed(p, s));
-            if (a.z)
+            if constexpr (GATE)
                 y *= silu_f(z[g]);
             buffer_put<T>(yb, ys.off[g], from_f32<T>(y));
         }
@@ -136,7 +143,7 @@ __global__ __launch_bounds__(256) void scan_span_kernel(gdr2_scan_args a, Pieces
         A2[i] *= kLog2e;
     const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
     const TokenRows<T> xs(a.x_stride, c, s, l.on), ts(a.dt_stride, c, s, l.on);
-    T rx[kGroups], rt[kGroups];
+    uint32_t rx[kGroups], rt[kGroups];
     Staged<T, NP> rb(a.b_stride, j, N);
     auto fetch = [&](int64_t t) {
         rb.load(a.Bt, q.row0 + t, a.b_stride, kScanChunk);
@@ -146,25 +153,29 @@ __global__ __launch_bounds__(256) void scan_span_kernel(gdr2_scan_args a, Pieces
     fetch(t0);
     int buf = 0;
     for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
-        float u[kGroups], d[kGroups];
+        float u[kGroups], pre[kGroups], d[kGroups];
         rb.store(s_b[buf]);
+        chunk_steps<T>(rt, bias, a.flags, s, kScanChunk, pre, d);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            d[g] = step_of(to_f32(rt[g]), bias, a.flags);
-            u[g] = d[g] * to_f32(rx[g]);
-        }
+        for (int g = 0; g < kGroups; ++g)
+            u[g] = d[g] * raw_f32<T>(rx[g]);
         if (t + kScanChunk < t1)
             fetch(t + kScanChunk);
         __syncthreads();
+        Quad<NS> bq[2];
+        bq[0].template read<NP>(s_b[buf], 0, s);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
+            if (g + 1 < kGroups)
+                bq[(g + 1) & 1].template read<NP>(s_b[buf], 4 * g + 4, s);
+            __builtin_amdgcn_sched_barrier(0);
             sum += d[g];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float dk = quad_bcast_k(d[g], k), uk = quad_bcast_k(u[g], k);
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
-                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * s_b[buf][4 * g + k][s * NS + i]);
+                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * bq[g & 1].v[k][i]);
             }
         }
     }
@@ -274,8 +285,12 @@ hipError_t forward_t(const gdr2_scan_args& a, hipStream_t stream)
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL((scan_forward_kernel<T, NS>), grid, dim3(256), 0, stream, a, p.seg, (uint32_t)p.ncb, (uint32_t)p.cb_per,
-                       states);
+    if (a.z)
+        hipLaunchKernelGGL((scan_forward_kernel<T, NS, true>), grid, dim3(256), 0, stream, a, p.seg, (uint32_t)p.ncb,
+                           (uint32_t)p.cb_per, states);
+    else
+        hipLaunchKernelGGL((scan_forward_kernel<T, NS, false>), grid, dim3(256), 0, stream, a, p.seg, (uint32_t)p.ncb,
+                           (uint32_t)p.cb_per, states);
     return hipGetLastError();
 }
 
@@ -298,15 +313,15 @@ hipError_t step_n(const gdr2_scan_step_args& a, hipStream_t stream)
 
 }  // namespace
 
-// One segment per sequence unless that leaves fewer than two workgroups per
-// compute unit; then the shortest power of two of chunks that gives about
+// One segment per sequence unless that leaves compute units without a
+// workgroup; then the shortest power of two of chunks that gives about
 // that many, at least four chunks.
 ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
 {
     ScanPlan p;
     p.cb_per = ceil_div(a.C / a.G, kScanCols);
     p.ncb = p.cb_per * a.G;
-    const int64_t want = (int64_t)device_cu_count() * 2;
+    const int64_t want = (int64_t)device_cu_count();
     int whole = kScanLg;                      // a segment that holds any sequence
     while (((int64_t)1 << whole) < a.T)
         ++whole;
