@@ -279,8 +279,8 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a
 // ---------------------------------------------------------------------------
 // Column sums.  A workgroup owns 64 columns; its 4 waves take every fourth
 // partial row and are added in wave order.
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int64_t P, int64_t M, ColumnOut a, ColumnOut b,
-                                                         ColumnOut c)
+__global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int64_t P, int64_t ld, int64_t M, ColumnOut a,
+                                                         ColumnOut b, ColumnOut c)
 {
     __shared__ float s_sum[4][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -289,7 +289,7 @@ __global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int6
     if (m < M) {
 #pragma unroll 8
         for (int64_t p = wave; p < P; p += 4)
-            s += part[p * M + m];
+            s += part[p * ld + m];
     }
     s_sum[wave][lane] = s;
     __syncthreads();
@@ -404,15 +404,16 @@ hipError_t backward_k(const gdr2_conv_bwd_args& a, const BackwardPlan& p, hipStr
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    return launch_column_sum(part, p.npb, {a.dweight, a.C * a.width}, {a.dbias, a.C}, {nullptr, 0}, stream);
+    return launch_column_sum(part, p.npb, a.C * (a.width + 1), {a.dweight, a.C * a.width}, {a.dbias, a.C}, {nullptr, 0}, stream);
 }
 
 }  // namespace
 
-hipError_t launch_column_sum(const float* part, int64_t P, ColumnOut a, ColumnOut b, ColumnOut c, hipStream_t stream)
+hipError_t launch_column_sum(const float* part, int64_t P, int64_t ld, ColumnOut a, ColumnOut b, ColumnOut c,
+                             hipStream_t stream)
 {
     const int64_t M = a.n + b.n + c.n;
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)ceil_div(M, 64)), dim3(256), 0, stream, part, P, M, a, b, c);
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)ceil_div(M, 64)), dim3(256), 0, stream, part, P, ld, M, a, b, c);
     return hipGetLastError();
 }
 

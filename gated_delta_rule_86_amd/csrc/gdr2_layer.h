@@ -27,13 +27,14 @@ hipError_t launch_norm_backward(const gdr2_norm_bwd_args& a, hipStream_t stream)
 size_t norm_backward_workspace_bytes(const gdr2_norm_bwd_args& a);
 int64_t norm_launch_groups(const gdr2_norm_args& a);
 
-// Column sums of part [P][M], in an order fixed by P alone.  The columns are
+// Column sums of part [P][M] (rows ld apart), in an order fixed by P alone.  The columns are
 // cut into up to three outputs (M = their n together); NULL ones are skipped.
 struct ColumnOut {
     float* p;
     int64_t n;
 };
-hipError_t launch_column_sum(const float* part, int64_t P, ColumnOut a, ColumnOut b, ColumnOut c, hipStream_t stream);
+hipError_t launch_column_sum(const float* part, int64_t P, int64_t ld, ColumnOut a, ColumnOut b, ColumnOut c,
+                             hipStream_t stream);
 
 constexpr int64_t kMaxGroups = (int64_t)1 << 24;   // 256-thread workgroups of one launch, exclusive
 

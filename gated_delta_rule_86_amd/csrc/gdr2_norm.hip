@@ -475,7 +475,7 @@ hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
         if (e != hipSuccess)
             return e;
     }
-    return sums ? launch_column_sum(part, P, {p.dweight, a.C}, {p.dbias, a.C}, {nullptr, 0}, stream) : hipSuccess;
+    return sums ? launch_column_sum(part, P, 2 * a.C, {p.dweight, a.C}, {p.dbias, a.C}, {nullptr, 0}, stream) : hipSuccess;
 }
 
 }  // namespace

@@ -1,15 +1,20 @@
 // gdr2_scan.h -- shared by the scan's forward and backward kernels: the lane
 // layout, the per-token pieces and the segment plan.
 //
-// Lane layout.  A workgroup of 4 waves holds 64 channels of one group, 16 per
-// wave; the four lanes of a quad hold one channel, lane s its states
-// s*NS .. s*NS + NS-1 (NP = 4 NS >= N, the padding has B = C = 0).  Tokens are
-// taken four at a time: lane s loads the rows' elements of token t + s, forms
-// that token's step once, and hands it to its quad by a DPP broadcast; the
-// four tokens' sums over the states come back the same way, one per lane.  So
-// no load and no transcendental of a token is repeated over the quad, and the
-// decay exponentials, the bulk of the work, are one per (token, channel, state).
-// B and C of 32 tokens are staged in LDS in fp32 for the 64 channels.
+// Two layouts share the work of a chunk of 32 tokens x 64 channels of a group:
+//
+//   rows     thread (token, V adjacent channels): 2048 elements over the
+//            workgroup, 64 LPC threads.  Row arrays move in whole 128-byte
+//            lines, each requested once per workgroup, and everything that is
+//            per (token, channel) is done here: the steps, the gate, stores.
+//   states   LPC adjacent lanes hold one channel, lane s its states s NS ..
+//            s NS + NS - 1 (NP = LPC NS >= N; the padding has B = C = 0), and
+//            walk the tokens one after the other.  Everything that is per
+//            (token, channel, state) is done here: the decay exponentials, the
+//            recurrence, the product with C.
+//
+// LDS carries (d, d x) from rows to states and the sums over n back; B and C
+// are staged there in fp32 for the 64 channels.
 #pragma once
 
 #include "gdr2_layer.h"
@@ -24,38 +29,53 @@ constexpr int kScanCols = 64;                 // channels of a workgroup
 // softplus(x) = max(x, 0) + log(1 + e^-|x|), relatively accurate over the whole
 // range (a step of 1e-5 scales the state's input as much as one of 0.1).
 // u = e^-|x| is exp2 of the rounded product t = -|x| log2(e), corrected by what
-// the rounding (of the product, by an fma, and of the constant) left out;
-// log(1 + u) is log(w) u / (w - 1) with w = fl(1 + u), where the rounding of w
-// cancels between log(w) and w - 1.
+// the rounding (of the product, by an fma, and of the constant) left out.
+// log(1 + u) is log(w) + (u - (w - 1)) with w = fl(1 + u): what w rounded away,
+// at most 2^-24, is added back (over w by the derivative; leaving that factor
+// out costs 2^-24 u).
 __device__ __forceinline__ float softplus_f(float x)
 {
-    constexpr float kLog2eLow = 1.92596299e-8f;   // log2(e) - fl(log2(e))
+    constexpr float kLn2 = 0.693147181f, kLog2eLow = 1.92596299e-8f;   // log2(e) - fl(log2(e))
     const float ax = fabsf(x), t = -kLog2e * ax;
-    const float rest = fmaf(-kLog2e, ax, -t) - kLog2eLow * ax;
-    const float e = fast_exp2(t), u = fmaf(e, rest * 0.693147181f, e);
+    const float rest = fmaf(-kLog2eLow, ax, fmaf(-kLog2e, ax, -t));
+    const float e = fast_exp2(t), u = fmaf(e, rest * kLn2, e);
     const float w = 1.f + u;
-    const float l = w == 1.f ? u : __logf(w) * (u * __builtin_amdgcn_rcpf(w - 1.f));
-    return fmaxf(x, 0.f) + l;
+    return fmaxf(x, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
-// Lane k of every quad broadcast to its quad.
-template <int K> __device__ __forceinline__ float quad_bcast(float v)
+template <int CTRL> __device__ __forceinline__ float dpp_move(float v)
 {
-    constexpr int ctrl = K * 0x55;   // quad_perm [K, K, K, K]
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, 0xF, 0xF, true));
-}
-__device__ __forceinline__ float quad_bcast_k(float v, int k)   // k a compile-time constant after unrolling
-{
-    return k == 0 ? quad_bcast<0>(v) : k == 1 ? quad_bcast<1>(v) : k == 2 ? quad_bcast<2>(v) : quad_bcast<3>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
-// p[k] of the four lanes of a quad: lane s returns the sum of p[s].
-__device__ __forceinline__ float quad_sum_transposed(const float (&p)[4], int s)
+// p[k] of the LPC lanes of a channel: lane s returns the sum of p[s].  Each
+// round adds half of the values to the partner that keeps the other half.
+__device__ __forceinline__ float sum_transposed(const float (&p)[4], int s)
 {
     const bool b0 = s & 1, b1 = s & 2;
     const float q0 = (b0 ? p[1] : p[0]) + dpp_quad_xor<1>(b0 ? p[0] : p[1]);
     const float q1 = (b0 ? p[3] : p[2]) + dpp_quad_xor<1>(b0 ? p[2] : p[3]);
     return (b1 ? q1 : q0) + dpp_quad_xor<2>(b1 ? q0 : q1);
+}
+__device__ __forceinline__ float sum_transposed(const float (&p)[8], int s)
+{
+    // the partner of the first round is lane 7 - s of the eight
+    const bool b2 = s & 4;
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        q[k] = (b2 ? p[4 + k] : p[k]) + dpp_move<0x141>(b2 ? p[k] : p[4 + k]);
+    return sum_transposed(q, s);
+}
+
+// Sum over the LPC lanes of a channel, in every lane.
+template <int LPC> __device__ __forceinline__ float channel_lanes_sum(float v)
+{
+    v += dpp_quad_xor<1>(v);
+    v += dpp_quad_xor<2>(v);
+    if constexpr (LPC == 8)
+        v += dpp_move<0x141>(v);
+    return v;
 }
 
 // Segments of a scan: L = 2^lg tokens each.
@@ -65,26 +85,33 @@ struct ScanPlan {
     int64_t cb_per;   // per group
     bool split;       // sequences may have more than one segment
 };
-ScanPlan scan_plan(const gdr2_scan_args& a, bool backward);
+ScanPlan scan_plan(const gdr2_scan_args& a);
 
-// This lane's place.
+// This lane's place in the states layout.
 struct ScanLane {
-    int64_t c;     // channel, or C when the lane has none
-    int64_t j;     // group
-    int s;         // lane of the quad
+    int64_t c;     // channel (the block's first when the lane has none)
+    int s;         // lane of the channel
     bool on;
 };
-__device__ __forceinline__ ScanLane scan_lane(const gdr2_scan_args& a, uint32_t cb, uint32_t cb_per)
+// The workgroup's channels: c0 .. c0 + n - 1 of group j.
+struct ScanBlock {
+    int64_t j, c0;
+    int n;
+};
+__device__ __forceinline__ ScanBlock scan_block(const gdr2_scan_args& a, uint32_t cb, uint32_t cb_per)
 {
-    ScanLane l;
+    ScanBlock b;
     const uint32_t j = cb / cb_per;
-    const int64_t cg = a.C / a.G;
-    const int64_t in = (int64_t)(cb - j * cb_per) * kScanCols + (threadIdx.x >> 2);
-    l.j = j;
-    l.s = threadIdx.x & 3;
-    l.on = in < cg;
-    l.c = j * cg + (l.on ? in : 0);
-    return l;
+    const int64_t cg = a.C / a.G, in = (int64_t)(cb - j * cb_per) * kScanCols;
+    b.j = j;
+    b.c0 = j * cg + in;
+    b.n = (int)min(cg - in, (int64_t)kScanCols);
+    return b;
+}
+template <int LPC> __device__ __forceinline__ ScanLane scan_lane(const ScanBlock& b)
+{
+    const int i = threadIdx.x / LPC;
+    return {b.c0 + (i < b.n ? i : 0), (int)(threadIdx.x % LPC), i < b.n};
 }
 
 // NS fp32 per lane from / to a row of N states (zero past N).  One access per
@@ -129,6 +156,11 @@ __device__ __forceinline__ void store_states(float* row, int s, int N, bool on, 
     }
 }
 
+// Waits for this wave's LDS accesses, then for the workgroup.  (__syncthreads()
+// would also wait for loads and stores in flight, which are left to run across
+// chunks.)
+__device__ __forceinline__ void lds_barrier() { __asm__ __volatile__("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // ---- loads ahead ----------------------------------------------------------
 // A workgroup-uniform value the compiler cannot see to be one (it came through
 // a vector load), kept in scalar registers.
@@ -147,16 +179,30 @@ __device__ __forceinline__ Piece uniform(const Piece& q)
 // chunk that exists, and an access past the length reads 0 or writes nothing.
 // So the tokens past a sequence cost no compare and no branch, and the lane
 // offsets stay the same from chunk to chunk.
-constexpr int kGroups = kScanChunk / 4;
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset past every length (32 rows, 2^24 elements apart, 4 bytes)
 
-template <typename T> __device__ __forceinline__ auto chunk_buffer(const void* base, int64_t row, int64_t ld, int left)
+// A row array walked chunk by chunk, in scalar registers: the address of a
+// chunk's first row and the bytes of one row.
+struct RowWalk {
+    const char* base;
+    uint32_t row_bytes;
+
+    template <typename T> static __device__ __forceinline__ RowWalk at(const void* p, int64_t row, int64_t ld)
+    {
+        return {(const char*)((const T*)p + row * ld), (uint32_t)ld * (uint32_t)sizeof(T)};
+    }
+    __device__ __forceinline__ void advance(int rows) { base += (int64_t)rows * (int32_t)row_bytes; }
+    // `left` rows from the base on
+    __device__ __forceinline__ auto buffer(int left) const
+    {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((int64_t)base), (short)0,
+                                                 __builtin_amdgcn_readfirstlane((int)(left * row_bytes)), 0x00020000);
+    }
+};
+template <typename T> __device__ __forceinline__ float raw_f32(uint32_t raw)
 {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((T*)base + row * ld), (short)0, (int)(left * (int)ld * (int)sizeof(T)),
-                                             0x00020000);
+    return __builtin_bit_cast(float, sizeof(T) == 2 ? raw << 16 : raw);
 }
-// A loaded element stays in a register of its own until it is used: as bf16
-// the compiler would pack pairs, and wait for the loads to do so.
 template <typename T, typename R> __device__ __forceinline__ uint32_t buffer_get(R rsrc, uint32_t off)
 {
     if constexpr (sizeof(T) == 2)
@@ -164,53 +210,105 @@ template <typename T, typename R> __device__ __forceinline__ uint32_t buffer_get
     else
         return __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0);
 }
-template <typename T> __device__ __forceinline__ float raw_f32(uint32_t raw)
-{
-    return __builtin_bit_cast(float, sizeof(T) == 2 ? raw << 16 : raw);
-}
-template <typename T, typename R> __device__ __forceinline__ void buffer_put(R rsrc, uint32_t off, T v)
-{
-    if constexpr (sizeof(T) == 2)
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), rsrc, off, 0, 0);
-    else
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), rsrc, off, 0, 0);
-}
 
-// One row array of a chunk: this lane's elements are tokens 4 g + s.
-template <typename T> struct TokenRows {
-    uint32_t off[kGroups];
-    __device__ __forceinline__ TokenRows(int64_t ld, int64_t c, int s, bool on)
+// The rows layout of one array: V channels of one token of every chunk.
+// WIDE: rows and blocks are aligned to V elements, which then move together;
+// otherwise one by one.  Loaded elements stay as they are until they are used.
+template <typename T, int V, bool WIDE> struct RowVec {
+    static constexpr int W = V * (int)sizeof(T) / 4;          // registers of a packed vector
+    static constexpr int REGS = WIDE ? W : V;
+    uint32_t off;
+    int n;             // channels of the vector that exist
+    uint32_t raw[REGS];
+
+    __device__ __forceinline__ RowVec(int64_t ld, const ScanBlock& b)
     {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            off[g] = on ? (uint32_t)((4 * g + s) * (int)ld + (int)c) * (uint32_t)sizeof(T) : kNowhere;
+        const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
+        n = min(V, max(0, b.n - ch));
+        off = n > 0 ? (uint32_t)(token * (int)ld + (int)b.c0 + ch) * (uint32_t)sizeof(T) : kNowhere;
     }
-    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t ld, int left, uint32_t (&raw)[kGroups]) const
+    __device__ __forceinline__ uint32_t at(int v) const { return v < n ? off + v * (uint32_t)sizeof(T) : kNowhere; }
+
+    __device__ __forceinline__ void load(const RowWalk& walk, int left)
     {
-        const auto r = chunk_buffer<T>(base, row, ld, left);
+        const auto r = walk.buffer(left);
+        if constexpr (WIDE) {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            raw[g] = buffer_get<T>(r, off[g]);
+            for (int w = 0; w < W; w += 4) {
+                typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+                typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+                if constexpr (W == 2) {
+                    const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+                    raw[0] = x[0];
+                    raw[1] = x[1];
+                } else {
+                    const U4 x = __builtin_bit_cast(U4, __builtin_amdgcn_raw_buffer_load_b128(r, off + 4 * w, 0, 0));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        raw[w + i] = x[i];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                raw[v] = buffer_get<T>(r, at(v));
+        }
+    }
+    __device__ __forceinline__ float get(int v) const
+    {
+        if constexpr (WIDE && sizeof(T) == 2)
+            return __builtin_bit_cast(float, v & 1 ? raw[v / 2] & 0xffff0000u : raw[v / 2] << 16);
+        else
+            return raw_f32<T>(raw[v]);
+    }
+    __device__ __forceinline__ void store(const RowWalk& walk, int left, const float (&y)[V]) const
+    {
+        const auto r = walk.buffer(left);
+        if constexpr (WIDE) {
+            typedef T VecT __attribute__((ext_vector_type(V)));
+            VecT o;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                o[v] = (T)y[v];
+            typedef uint32_t UW __attribute__((ext_vector_type(W)));
+            typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+            const UW x = __builtin_bit_cast(UW, o);
+            if constexpr (W == 2) {
+                __builtin_amdgcn_raw_buffer_store_b64(x, r, off, 0, 0);
+            } else {
+#pragma unroll
+                for (int w = 0; w < W; w += 4)
+                    __builtin_amdgcn_raw_buffer_store_b128(U4{x[w], x[w + 1], x[w + 2], x[w + 3]}, r, off + 4 * w, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if constexpr (sizeof(T) == 2)
+                    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)y[v]), r, at(v), 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y[v]), r, at(v), 0, 0);
+            }
+        }
     }
 };
 
 // B or C of a chunk's tokens for group j, on their way to LDS as fp32
 // [32][NP]: zero past the sequence and past N.
-template <typename T, int NP> struct Staged {
-    static constexpr int PER = kScanChunk * NP / 256;
+template <typename T, int NP, int NT> struct Staged {
+    static constexpr int PER = kScanChunk * NP / NT;
     uint32_t off[PER], raw[PER];
 
     __device__ __forceinline__ Staged(int64_t ld, int64_t j, int N)
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = threadIdx.x + 256 * i, r = e / NP, n = e % NP;
+            const int e = threadIdx.x + NT * i, r = e / NP, n = e % NP;
             off[i] = n < N ? (uint32_t)(r * (int)ld + (int)j * N + n) * (uint32_t)sizeof(T) : kNowhere;
         }
     }
-    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t ld, int left)
+    __device__ __forceinline__ void load(const RowWalk& walk, int left)
     {
-        const auto r = chunk_buffer<T>(base, row, ld, left);
+        const auto r = walk.buffer(left);
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             raw[i] = buffer_get<T>(r, off[i]);
@@ -219,52 +317,42 @@ template <typename T, int NP> struct Staged {
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = threadIdx.x + 256 * i;
+            const int e = threadIdx.x + NT * i;
             dst[e / NP][e % NP] = raw_f32<T>(raw[i]);
         }
     }
 };
 
-// The steps of a chunk's tokens, all groups side by side (the eight chains of
-// transcendentals fill each other's latencies); 0 past the sequence.
-template <typename T>
-__device__ __forceinline__ void chunk_steps(const uint32_t (&raw)[kGroups], float bias, int flags, int s, int left,
-                                            float (&pre)[kGroups], float (&d)[kGroups])
+// Whether every row array and block of a call moves V elements at a time.
+inline bool scan_wide(const gdr2_scan_args& a, int V)
 {
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g)
-        d[g] = pre[g] = raw_f32<T>(raw[g]) + bias;
-    if (flags & GDR2_SCAN_SOFTPLUS) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            d[g] = softplus_f(pre[g]);
-    }
-    if (left < kScanChunk) {
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            d[g] = 4 * g + s < left ? d[g] : 0.f;
-    }
+    const int64_t e = a.dtype == GDR2_BF16 ? 2 : 4, cg = a.C / a.G;
+    auto ok = [&](const void* p, int64_t ld) { return !p || (reinterpret_cast<uintptr_t>(p) % (V * e) == 0 && ld % V == 0); };
+    return cg % V == 0 && ok(a.x, a.x_stride) && ok(a.dt, a.dt_stride) && ok(a.z, a.z_stride);
 }
 
-// The states s NS .. of B and / or C for four tokens, in registers.  Read one
-// group of tokens ahead of its use: a wave alone on its SIMD would otherwise
-// stand still for the LDS at every token.
-template <int NS> struct Quad {
-    float v[4][NS];
-    template <int NP> __device__ __forceinline__ void read(const float (*src)[NP], int tt, int s)
-    {
-        typedef float Vec __attribute__((ext_vector_type(NS < 4 ? NS : 4)));
-        constexpr int W = NS < 4 ? NS : 4;
+// What one token needs in the states layout, read from LDS LPC tokens ahead of
+// its use: with few waves on a SIMD nothing else hides the LDS.  (d, d x) of
+// two tokens lie together there, [token / 2][channel][d, dx, d', dx'], so that
+// one read serves two.
+constexpr int kStepLd = 4 * kScanCols;
+
+template <int NS> __device__ __forceinline__ void read_states(const float* p, float (&v)[NS])
+{
+    typedef float Vec __attribute__((ext_vector_type(NS)));
+    const Vec x = *reinterpret_cast<const Vec*>(p);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+    for (int i = 0; i < NS; ++i)
+        v[i] = x[i];
+}
+
+// This thread's channels (rows layout) of a per-channel parameter; 0 without.
+template <int V> __device__ __forceinline__ void channel_params(const float* p, const ScanBlock& b, float (&out)[V])
+{
+    const int ch = threadIdx.x % (kScanCols / V) * V;
 #pragma unroll
-            for (int i = 0; i < NS; i += W) {
-                const Vec x = *reinterpret_cast<const Vec*>(&src[tt + k][s * NS + i]);
-#pragma unroll
-                for (int e = 0; e < W; ++e)
-                    v[k][i + e] = x[e];
-            }
-    }
-};
+    for (int v = 0; v < V; ++v)
+        out[v] = p && ch + v < b.n ? p[b.c0 + ch + v] : 0.f;
+}
 
 }  // namespace gdr2

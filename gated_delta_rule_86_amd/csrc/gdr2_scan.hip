@@ -25,23 +25,43 @@ __device__ __forceinline__ float step_of(float dt, float bias, int flags)
     return flags & GDR2_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
 }
 
-// Both passes walk a segment chunk by chunk.  The rows of the next chunk are
-// requested before the current one is computed (there is about one wave per
-// SIMD, so nothing else hides their latency), and B and C alternate between
-// two LDS buffers, so a chunk costs one barrier.
-template <typename T, int NS, bool GATE>
-__global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
-                                                           const float* starts)
+// (d, d x) of one channel of a thread's row vector into LDS; 0 past the
+// sequence, where the token then leaves the state as it is.
+__device__ __forceinline__ void step_to_lds(float dt, float x, float bias, bool softplus, bool in, float* at)
 {
-    constexpr int NP = 4 * NS;
+    typedef float Two __attribute__((ext_vector_type(2)));
+    const float raw = dt + bias;
+    float soft = softplus_f(raw);
+    asm volatile("" : "+v"(soft));   // formed either way: a branch would split the block it is scheduled in
+    float d = softplus ? soft : raw;
+    d = in ? d : 0.f;
+    *reinterpret_cast<Two*>(at) = Two{d, d * x};
+}
+
+// A workgroup walks its segment chunk by chunk, one barrier per chunk (the LDS
+// arrays alternate between two buffers).  Between two barriers, interleaved
+// token group by token group so that the latencies of one fill with the
+// arithmetic of the others:
+//   states: the recurrence over chunk i, its sums into LDS
+//   rows:   (d, d x) of chunk i + 1 into LDS; skip and gate of chunk i - 1's sums
+//   loads:  the rows of chunk i + 2 are on their way
+template <typename T, int LPC, int NS, bool GATE, bool WIDE>
+__global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
+                                                                const float* starts)
+{
+    constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT, YLD = kScanCols + 16;
+    static_assert(V == kScanChunk / LPC, "one row element per token group");
     __shared__ __align__(16) float s_b[2][kScanChunk][NP], s_c[2][kScanChunk][NP];
+    __shared__ __align__(16) float s_du[2][kScanChunk / 2][kStepLd];
+    __shared__ __align__(16) float s_y[2][kScanChunk][YLD];
     const uint32_t slot = blockIdx.x / ncb;
     const Piece q = uniform(piece_of(seg, slot));
     if (q.seq < 0)
         return;
-    const ScanLane l = scan_lane(a, blockIdx.x - slot * ncb, cb_per);
-    const int s = l.s, N = (int)a.N;
-    const int64_t c = l.c, j = uniform(l.j);
+    const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
+    const ScanLane l = scan_lane<LPC>(blk);
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC;
+    const int64_t c = l.c;
     float A2[NS], h[NS];
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
@@ -51,136 +71,215 @@ __global__ __launch_bounds__(256) void scan_forward_kernel(gdr2_scan_args a, Pie
         load_states<NS>(starts + ((int64_t)slot * a.C + c) * N, s, N, l.on, h);
     else
         load_states<NS>(a.h0 + (q.seq * a.C + c) * N, s, N, l.on && a.h0, h);
-    const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
-    const float skip = a.skip && l.on ? a.skip[c] : 0.f;
-    const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
-    const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
-
     const int64_t t0 = q.index << seg.lg;
     const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
-    const TokenRows<T> xs(a.x_stride, c, s, l.on), ts(a.dt_stride, c, s, l.on), zs(a.z_stride, c, s, l.on), ys(a.C, c, s, l.on);
-    uint32_t rx[kGroups], rt[kGroups], rz[kGroups] = {};
-    Staged<T, NP> rb(a.b_stride, j, N), rc(a.c_stride, j, N);
-    auto fetch = [&](int64_t t) {
-        const int left = (int)min(t1 - t, (int64_t)kScanChunk);
-        rb.load(a.Bt, q.row0 + t, a.b_stride, left);
-        rc.load(a.Ct, q.row0 + t, a.c_stride, left);
-        ts.load(a.dt, q.row0 + t, a.dt_stride, left, rt);
-        xs.load(a.x, q.row0 + t, a.x_stride, left, rx);
-        if constexpr (GATE)
-            zs.load(a.z, q.row0 + t, a.z_stride, left, rz);
-    };
-    if (t0 < t1)
-        fetch(t0);
-    int buf = 0;
-    for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
-        const int left = (int)min(t1 - t, (int64_t)kScanChunk);
-        float x[kGroups], pre[kGroups], d[kGroups], z[kGroups];
-        rb.store(s_b[buf]);
-        rc.store(s_c[buf]);
-        chunk_steps<T>(rt, bias, a.flags, s, left, pre, d);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            x[g] = raw_f32<T>(rx[g]);
-            z[g] = raw_f32<T>(rz[g]);
-        }
-        if (t + kScanChunk < t1)
-            fetch(t + kScanChunk);
-        if (a.h_chunks)
-            store_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * a.C + c) * N, s, N, l.on, h);
-        __syncthreads();
-        const auto yb = chunk_buffer<T>(a.y, q.row0 + t, a.C, left);
-        Quad<NS> bq[2], cq[2];
-        bq[0].template read<NP>(s_b[buf], 0, s);
-        cq[0].template read<NP>(s_c[buf], 0, s);
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            if (g + 1 < kGroups) {
-                bq[(g + 1) & 1].template read<NP>(s_b[buf], 4 * g + 4, s);
-                cq[(g + 1) & 1].template read<NP>(s_c[buf], 4 * g + 4, s);
+    if (t0 < t1) {
+        float bias[V], skip[V];
+        channel_params<V>(a.dt_bias, blk, bias);
+        channel_params<V>(a.skip, blk, skip);
+        const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
+        const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
+        const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
+        const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
+        const int du_at = 4 * ch + 2 * (token & 1);
+        auto left_at = [&](int64_t t) { return (int)max((int64_t)0, min(t1 - t, (int64_t)kScanChunk)); };
+
+        // rows of a chunk: dt, x (and z), B, C
+        RowVec<T, V, WIDE> rt(a.dt_stride, blk), rx(a.x_stride, blk), rz(a.z_stride, blk);
+        const RowVec<T, V, WIDE> ry(a.C, blk);
+        Staged<T, NP, NT> rb(a.b_stride, blk.j, N), rc(a.c_stride, blk.j, N);
+        const int64_t row = q.row0 + t0;
+        RowWalk wt = RowWalk::at<T>(a.dt, row, a.dt_stride), wx = RowWalk::at<T>(a.x, row, a.x_stride);
+        RowWalk wb = RowWalk::at<T>(a.Bt, row, a.b_stride), wc = RowWalk::at<T>(a.Ct, row, a.c_stride);
+        RowWalk wz = RowWalk::at<T>(a.z, row, a.z_stride), wy = RowWalk::at<T>(a.y, row, a.C);
+        auto fetch = [&](int left) {       // of no rows: reads nothing, whatever the base
+            rt.load(wt, left);
+            rx.load(wx, left);
+            rb.load(wb, left);
+            rc.load(wc, left);
+            wt.advance(kScanChunk);
+            wx.advance(kScanChunk);
+            wb.advance(kScanChunk);
+            wc.advance(kScanChunk);
+            if constexpr (GATE) {
+                rz.load(wz, left);
+                wz.advance(kScanChunk);
             }
-            __builtin_amdgcn_sched_barrier(0);
-            const float u = d[g] * x[g];
-            float p[4];
+        };
+        fetch(left_at(t0));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float dk = quad_bcast_k(d[g], k), uk = quad_bcast_k(u, k);
+        for (int v = 0; v < V; ++v) {
+            step_to_lds(rt.get(v), rx.get(v), bias[v], soft, token < left_at(t0), &s_du[0][token / 2][du_at + 4 * v]);
+        }
+        // x, z of the previous chunk (nothing yet) and of the current one
+        RowVec<T, V, WIDE> px = rx, pz = rz, cx = rx, cz = rz;
+        rb.store(s_b[0]);
+        rc.store(s_c[0]);
+        fetch(left_at(t0 + kScanChunk));
+        int buf = 0;
+        int64_t t = t0;
+        for (; t < t1; t += kScanChunk, buf ^= 1) {
+            if (a.h_chunks)
+                store_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * a.C + c) * N, s, N, l.on, h);
+            // the next chunk's rows have arrived; those after it are requested
+            RowVec<T, V, WIDE> nt = rt, nx = rx, nz = rz;
+            const bool in = token < left_at(t + kScanChunk);
+            lds_barrier();
+            rb.store(s_b[buf ^ 1]);
+            rc.store(s_c[buf ^ 1]);
+            fetch(left_at(t + 2 * kScanChunk));
+            float B[LPC][NS], C[LPC][NS], d[LPC], u[LPC], y[V];
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
-                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * bq[g & 1].v[k][i]);
-                    p[k] = i == 0 ? cq[g & 1].v[k][0] * h[0] : fmaf(cq[g & 1].v[k][i], h[i], p[k]);
+            for (int k = 0; k < LPC; ++k) {
+                read_states<NS>(&s_b[buf][k][s * NS], B[k]);
+                read_states<NS>(&s_c[buf][k][s * NS], C[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < LPC; k += 2) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lc]);
+                d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
+            }
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const f32x4 p = *reinterpret_cast<const f32x4*>(&s_y[buf ^ 1][token][ch + v]);
+                y[v] = p[0], y[v + 1] = p[1], y[v + 2] = p[2], y[v + 3] = p[3];
+            }
+#pragma unroll
+            for (int g = 0; g < V; ++g) {
+                float p[LPC];
+#pragma unroll
+                for (int k = 0; k < LPC; ++k) {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        h[i] = fmaf(fast_exp2(d[k] * A2[i]), h[i], u[k] * B[k][i]);
+                        p[k] = i == 0 ? C[k][0] * h[0] : fmaf(C[k][i], h[i], p[k]);
+                    }
+                    const int next = (g + 1) * LPC + k;
+                    if (next < kScanChunk) {
+                        read_states<NS>(&s_b[buf][next][s * NS], B[k]);
+                        read_states<NS>(&s_c[buf][next][s * NS], C[k]);
+                        if (k % 2) {
+                            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lc]);
+                            d[k - 1] = x[0], u[k - 1] = x[1], d[k] = x[2], u[k] = x[3];
+                        }
+                    }
+                    if (k == 1)
+                        step_to_lds(nt.get(g), nx.get(g), bias[g], soft, in, &s_du[buf ^ 1][token / 2][du_at + 4 * g]);
+                    if (k == LPC - 2) {
+                        y[g] = fmaf(skip[g], px.get(g), y[g]);
+                        if constexpr (GATE)
+                            y[g] *= silu_f(pz.get(g));
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+                s_y[buf][g * LPC + s][lc] = sum_transposed(p, s);
             }
-            float y = fmaf(skip, x[g], quad_sum_transposed(p, s));
-            if constexpr (GATE)
-                y *= silu_f(z[g]);
-            buffer_put<T>(yb, ys.off[g], from_f32<T>(y));
+            // (unconditional, into nothing for the first chunk: behind a branch the
+            // wait for the next chunk's loads would also wait for the store)
+            ry.store(wy, t > t0 ? kScanChunk : 0, y);
+            wy.advance(t > t0 ? kScanChunk : 0);
+            px = cx;
+            pz = cz;
+            cx = nx;
+            cz = nz;
         }
+        lds_barrier();
+        float y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            y[v] = fmaf(skip[v], px.get(v), s_y[buf ^ 1][token][ch + v]);
+            if constexpr (GATE)
+                y[v] *= silu_f(pz.get(v));
+        }
+        ry.store(wy, left_at(t - kScanChunk), y);
     }
     if (a.h_out && t1 == q.len)
         store_states<NS>(a.h_out + (q.seq * a.C + c) * N, s, N, l.on, h);
 }
 
 // (sum d, E) of every segment but the last of its sequence: whole segments.
-template <typename T, int NS>
-__global__ __launch_bounds__(256) void scan_span_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
-                                                        float* states, float* sums)
+template <typename T, int LPC, int NS, bool WIDE>
+__global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
+                                                             float* states, float* sums)
 {
-    constexpr int NP = 4 * NS;
+    constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT;
     __shared__ __align__(16) float s_b[2][kScanChunk][NP];
+    __shared__ __align__(16) float s_du[2][kScanChunk / 2][kStepLd];
     const uint32_t slot = blockIdx.x / ncb;
     const Piece q = uniform(piece_of(seg, slot));
     const int64_t t0 = q.index << seg.lg, t1 = t0 + ((int64_t)1 << seg.lg);
     if (q.seq < 0 || t1 >= q.len)
         return;
-    const ScanLane l = scan_lane(a, blockIdx.x - slot * ncb, cb_per);
-    const int s = l.s, N = (int)a.N;
-    const int64_t c = l.c, j = uniform(l.j);
+    const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
+    const ScanLane l = scan_lane<LPC>(blk);
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC;
+    const int64_t c = l.c;
     float A2[NS], h[NS] = {}, sum = 0.f;
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
         A2[i] *= kLog2e;
-    const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
-    const TokenRows<T> xs(a.x_stride, c, s, l.on), ts(a.dt_stride, c, s, l.on);
-    uint32_t rx[kGroups], rt[kGroups];
-    Staged<T, NP> rb(a.b_stride, j, N);
-    auto fetch = [&](int64_t t) {
-        rb.load(a.Bt, q.row0 + t, a.b_stride, kScanChunk);
-        ts.load(a.dt, q.row0 + t, a.dt_stride, kScanChunk, rt);
-        xs.load(a.x, q.row0 + t, a.x_stride, kScanChunk, rx);
+    float bias[V];
+    channel_params<V>(a.dt_bias, blk, bias);
+    const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
+    const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
+    const int du_at = 4 * ch + 2 * (token & 1);
+    RowVec<T, V, WIDE> rt(a.dt_stride, blk), rx(a.x_stride, blk);
+    Staged<T, NP, NT> rb(a.b_stride, blk.j, N);
+    const int64_t row = q.row0 + t0;
+    RowWalk wt = RowWalk::at<T>(a.dt, row, a.dt_stride), wx = RowWalk::at<T>(a.x, row, a.x_stride);
+    RowWalk wb = RowWalk::at<T>(a.Bt, row, a.b_stride);
+    auto fetch = [&](int left) {
+        rt.load(wt, left);
+        rx.load(wx, left);
+        rb.load(wb, left);
+        wt.advance(kScanChunk);
+        wx.advance(kScanChunk);
+        wb.advance(kScanChunk);
     };
-    fetch(t0);
+    fetch(kScanChunk);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        step_to_lds(rt.get(v), rx.get(v), bias[v], soft, true, &s_du[0][token / 2][du_at + 4 * v]);
+    rb.store(s_b[0]);
+    fetch(t0 + kScanChunk < t1 ? kScanChunk : 0);
     int buf = 0;
     for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
-        float u[kGroups], pre[kGroups], d[kGroups];
-        rb.store(s_b[buf]);
-        chunk_steps<T>(rt, bias, a.flags, s, kScanChunk, pre, d);
+        RowVec<T, V, WIDE> nt = rt, nx = rx;
+        lds_barrier();
+        rb.store(s_b[buf ^ 1]);
+        fetch(t + 2 * kScanChunk < t1 ? kScanChunk : 0);
+        float B[LPC][NS], d[LPC], u[LPC];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g)
-            u[g] = d[g] * raw_f32<T>(rx[g]);
-        if (t + kScanChunk < t1)
-            fetch(t + kScanChunk);
-        __syncthreads();
-        Quad<NS> bq[2];
-        bq[0].template read<NP>(s_b[buf], 0, s);
+        for (int k = 0; k < LPC; ++k)
+            read_states<NS>(&s_b[buf][k][s * NS], B[k]);
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            if (g + 1 < kGroups)
-                bq[(g + 1) & 1].template read<NP>(s_b[buf], 4 * g + 4, s);
-            __builtin_amdgcn_sched_barrier(0);
-            sum += d[g];
+        for (int k = 0; k < LPC; k += 2) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lc]);
+            d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float dk = quad_bcast_k(d[g], k), uk = quad_bcast_k(u[g], k);
+        for (int g = 0; g < V; ++g) {
+#pragma unroll
+            for (int k = 0; k < LPC; ++k) {
+                sum += d[k];
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
-                    h[i] = fmaf(fast_exp2(dk * A2[i]), h[i], uk * bq[g & 1].v[k][i]);
+                    h[i] = fmaf(fast_exp2(d[k] * A2[i]), h[i], u[k] * B[k][i]);
+                const int next = (g + 1) * LPC + k;
+                if (next < kScanChunk) {
+                    read_states<NS>(&s_b[buf][next][s * NS], B[k]);
+                    if (k % 2) {
+                        const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lc]);
+                        d[k - 1] = x[0], u[k - 1] = x[1], d[k] = x[2], u[k] = x[3];
+                    }
+                }
+                if (k == 1)
+                    step_to_lds(nt.get(g), nx.get(g), bias[g], soft, true, &s_du[buf ^ 1][token / 2][du_at + 4 * g]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
-    sum += dpp_quad_xor<1>(sum);
-    sum += dpp_quad_xor<2>(sum);
     store_states<NS>(states + ((int64_t)slot * a.C + c) * N, s, N, l.on, h);
     if (l.on && s == 0)
         sums[(int64_t)slot * a.C + c] = sum;
@@ -264,18 +363,18 @@ ForwardWork forward_work(const gdr2_scan_args& a, const ScanPlan& p)
     return {0, al, al + (size_t)p.seg.slots() * a.C * 4};
 }
 
-template <typename T, int NS>
+template <typename T, int LPC, int NS, bool WIDE>
 hipError_t forward_t(const gdr2_scan_args& a, hipStream_t stream)
 {
-    const ScanPlan p = scan_plan(a, false);
+    const ScanPlan p = scan_plan(a);
     const ForwardWork w = forward_work(a, p);
-    const dim3 grid((unsigned)(p.seg.slots() * p.ncb));
+    const dim3 grid((unsigned)(p.seg.slots() * p.ncb)), block(64 * LPC);
+    const uint32_t ncb = (uint32_t)p.ncb, cb_per = (uint32_t)p.cb_per;
     float* states = nullptr;
     if (p.split) {
         states = (float*)((char*)a.workspace + w.states);
         float* sums = (float*)((char*)a.workspace + w.sums);
-        hipLaunchKernelGGL((scan_span_kernel<T, NS>), grid, dim3(256), 0, stream, a, p.seg, (uint32_t)p.ncb, (uint32_t)p.cb_per,
-                           states, sums);
+        hipLaunchKernelGGL((scan_span_kernel<T, LPC, NS, WIDE>), grid, block, 0, stream, a, p.seg, ncb, cb_per, states, sums);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -286,12 +385,16 @@ hipError_t forward_t(const gdr2_scan_args& a, hipStream_t stream)
             return e;
     }
     if (a.z)
-        hipLaunchKernelGGL((scan_forward_kernel<T, NS, true>), grid, dim3(256), 0, stream, a, p.seg, (uint32_t)p.ncb,
-                           (uint32_t)p.cb_per, states);
+        hipLaunchKernelGGL((scan_forward_kernel<T, LPC, NS, true, WIDE>), grid, block, 0, stream, a, p.seg, ncb, cb_per, states);
     else
-        hipLaunchKernelGGL((scan_forward_kernel<T, NS, false>), grid, dim3(256), 0, stream, a, p.seg, (uint32_t)p.ncb,
-                           (uint32_t)p.cb_per, states);
+        hipLaunchKernelGGL((scan_forward_kernel<T, LPC, NS, false, WIDE>), grid, block, 0, stream, a, p.seg, ncb, cb_per, states);
     return hipGetLastError();
+}
+
+template <typename T, int LPC, int NS>
+hipError_t forward_w(const gdr2_scan_args& a, hipStream_t stream)
+{
+    return scan_wide(a, kScanChunk / LPC) ? forward_t<T, LPC, NS, true>(a, stream) : forward_t<T, LPC, NS, false>(a, stream);
 }
 
 template <typename T, int LPC>
@@ -313,24 +416,38 @@ hipError_t step_n(const gdr2_scan_step_args& a, hipStream_t stream)
 
 }  // namespace
 
-// One segment per sequence unless that leaves compute units without a
-// workgroup; then the shortest power of two of chunks that gives about
-// that many, at least four chunks.
-ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
+// How a call is cut into segments.
+// One segment per sequence when that gives every compute unit a workgroup:
+// at 8 x 4096 tokens and 2048 channels (256 workgroups) 353 us, against 407 us
+// with twice as many segments, for the span pass repeats most of the work.
+// Otherwise the longest segments that give every unit four workgroups, at
+// least 128 tokens: 1 x 32768 tokens (32 channel blocks) 467 us with 1024
+// workgroups, 485 us with 512, 610 us with 256, 1200 us with 128.
+// A packed batch is cut at twice its mean length in any case: the host does
+// not know the lengths, one sequence may hold nearly all rows, and sequences
+// that fit one segment skip the span pass.
+ScanPlan scan_plan(const gdr2_scan_args& a)
 {
     ScanPlan p;
     p.cb_per = ceil_div(a.C / a.G, kScanCols);
     p.ncb = p.cb_per * a.G;
-    const int64_t want = (int64_t)device_cu_count();
     int whole = kScanLg;                      // a segment that holds any sequence
     while (((int64_t)1 << whole) < a.T)
         ++whole;
+    const int shortest = min(whole, kScanLg + 2);
     int lg = whole;
-    if (a.algo == GDR2_ALGO_SEGMENTED)
+    auto groups = [&](int g) { return Pieces{a.offsets, a.B, a.T, g}.slots() * p.ncb; };
+    if (a.algo == GDR2_ALGO_SEGMENTED) {
         lg = min(whole, kScanLg + 1);
-    else if (a.algo == GDR2_ALGO_AUTO)
-        while (lg > kScanLg + 2 && Pieces{a.offsets, a.B, a.T, lg}.slots() * p.ncb < want)
-            --lg;
+    } else if (a.algo == GDR2_ALGO_AUTO) {
+        if (a.offsets)
+            while (lg > shortest && ((int64_t)1 << (lg - 1)) >= 2 * ceil_div(a.T, max(a.B, (int64_t)1)))
+                --lg;
+        const int64_t cus = device_cu_count();
+        if (groups(lg) < cus)
+            while (lg > shortest && groups(lg) < 4 * cus)
+                --lg;
+    }
     p.seg = Pieces{a.offsets, a.B, a.T, lg};
     p.split = lg < whole;
     return p;
@@ -338,23 +455,26 @@ ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
 
 int64_t scan_launch_groups(const gdr2_scan_args& a)
 {
-    const ScanPlan p = scan_plan(a, true);
+    const ScanPlan p = scan_plan(a);
     int64_t n;
     if (__builtin_mul_overflow(p.seg.slots(), p.ncb, &n))
         return kMaxGroups;
     return max(n, ceil_div(a.B * a.C * max((int64_t)8, a.N), 256));
 }
 
-size_t scan_workspace_bytes(const gdr2_scan_args& a) { return forward_work(a, scan_plan(a, false)).total; }
+size_t scan_workspace_bytes(const gdr2_scan_args& a) { return forward_work(a, scan_plan(a)).total; }
 
+// Lanes per channel and states per lane.  16 states run on 4 lanes of 4: 8 lanes
+// of 2 (twice the waves) took 351 us against 353 at 8 x 4096 x 2048, 561 against
+// 485 in segments; 32 states need the 8 lanes for their registers.
 hipError_t launch_scan_forward(const gdr2_scan_args& a, hipStream_t stream)
 {
     const bool bf = a.dtype == GDR2_BF16;
     if (a.N <= 8)
-        return bf ? forward_t<bf16, 2>(a, stream) : forward_t<float, 2>(a, stream);
+        return bf ? forward_w<bf16, 4, 2>(a, stream) : forward_w<float, 4, 2>(a, stream);
     if (a.N <= 16)
-        return bf ? forward_t<bf16, 4>(a, stream) : forward_t<float, 4>(a, stream);
-    return bf ? forward_t<bf16, 8>(a, stream) : forward_t<float, 8>(a, stream);
+        return bf ? forward_w<bf16, 4, 4>(a, stream) : forward_w<float, 4, 4>(a, stream);
+    return bf ? forward_w<bf16, 8, 4>(a, stream) : forward_w<float, 8, 4>(a, stream);
 }
 
 hipError_t launch_scan_step(const gdr2_scan_step_args& a, hipStream_t stream)

@@ -6,271 +6,396 @@
 //   q = lam a h_{t-1},  dd = x du + sum_n q A,  ddt = dd sigmoid(raw),  dA = sum d q
 //   dz = dy v silu'(z),  dskip = sum dv x,  dh0 = a_0 lam_0
 // The states come from the forward's record of every 32nd one: a chunk's
-// states are formed again from its start, SUB tokens at a time, and stay in
-// registers with their decays while the chunk is walked backwards.
+// states are formed again from its start, kSub tokens at a time, and stay in
+// registers with their decays while those tokens are walked backwards.
 //
-// The sums over channels (dB, dC) are the expensive ones: per token group a
-// transposing reduction over the 16 channels of a wave, then LDS over the
-// waves, then one partial row per channel block, added by a last kernel in
-// block order.  The sums over tokens (dA, dskip, ddt_bias) stay in registers
-// for a whole segment and leave as one partial row per segment.
+// About 95 VALU operations per token and wave of 16 channels bound it.  The
+// sums over channels (dB, dC) are the expensive ones: a transposing reduction
+// over the channels of a wave, LDS over the waves, one partial row per channel
+// block, added by a last kernel in block order.  The sums over tokens (dA,
+// dskip, ddt_bias) stay in registers for a whole segment and leave as one
+// partial row per segment.
 #include "gdr2_scan.h"
 
 namespace gdr2 {
 
 namespace {
 
-template <int NS> constexpr int kSub = NS <= 4 ? 16 : 8;   // tokens whose states are held
+constexpr int kSub = 8;                       // tokens whose states are held
+constexpr int kSubs = kScanChunk / kSub;
 
-// Sum over lanes that differ in bits 2..5 (the 16 channels of a wave) of
-// v[k][i], k the token of a group of four: lane (b5, b4) returns token
-// k = 2 b5 + b4 in r[i].
-template <int NS>
-__device__ __forceinline__ void channel_sum(const float (&v)[4][NS], int lane, float (&r)[NS])
+// Lanes of the lower half (even rows) return the sum of a over the lane pair,
+// the others that of b: one v_permlane*_swap and one add for two values.
+__device__ __forceinline__ float pair_sum32(float a, float b)
 {
-    const bool b5 = lane & 32, b4 = lane & 16;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const float w0 = (b5 ? v[2][i] : v[0][i]) + __shfl_xor(b5 ? v[0][i] : v[2][i], 32);
-        const float w1 = (b5 ? v[3][i] : v[1][i]) + __shfl_xor(b5 ? v[1][i] : v[3][i], 32);
-        float x = (b4 ? w1 : w0) + __shfl_xor(b4 ? w0 : w1, 16);
-        x += __shfl_xor(x, 8);
-        x += __shfl_xor(x, 4);
-        r[i] = x;
-    }
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
+__device__ __forceinline__ float pair_sum16(float a, float b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Sum of v[k][i] over the channels of a wave.  LPC = 4: k < 4, lanes of row
+// r = lane / 16 return token k = r.  LPC = 8: k < 8, they return tokens r and
+// r + 4.  (Rounds over lane bits 5 and 4 halve the values held; bit 3, and bit
+// 2 with four lanes a channel, are rotations within the row.)
+template <int LPC, int NS>
+__device__ __forceinline__ void channel_sum(const float (&v)[LPC][NS], float (&r)[LPC / 4][NS])
+{
+#pragma unroll
+    for (int g = 0; g < LPC / 4; ++g)
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const float lo = pair_sum32(v[4 * g][i], v[4 * g + 2][i]), hi = pair_sum32(v[4 * g + 1][i], v[4 * g + 3][i]);
+            float x = pair_sum16(lo, hi);
+            x += dpp_move<0x128>(x);          // row_ror:8
+            if constexpr (LPC == 4)
+                x += dpp_move<0x124>(x);      // row_ror:4
+            r[g][i] = x;
+        }
+}
+
+// Floats of one segment's row of token sums (rows start on 16 bytes).
+__host__ __device__ inline int64_t sums_ld(int64_t C, int64_t N) { return (C * (N + 2) + 3) / 4 * 4; }
 
 struct BackwardPtrs {
     float* parts;       // [ncb][rows][2][N]: dB, dC of one channel block
-    float* sums;        // [slots][C (N + 2)]
+    float* sums;        // [slots][sums_ld]: dA [C][N], dskip [C], ddt_bias [C]
     const float* lam;   // [slots][C][N] gradients entering each segment from behind, or NULL
 };
 
-template <typename T, int NS>
-__global__ __launch_bounds__(256) void scan_backward_kernel(gdr2_scan_bwd_args p, Pieces seg, uint32_t ncb, uint32_t cb_per,
-                                                            BackwardPtrs w)
+// One chunk at a time, last to first:
+//   rows:   d, d x, dv of the chunk into LDS       | barrier
+//   states: forwards for the states, backwards for the gradients, the sums over
+//           n into the places of d x, dv, and the sums over channels | barrier
+//   rows:   dx, ddt, dz from the sums; dB, dC over the waves
+template <typename T, int LPC, int NS, bool GATE, bool WIDE>
+__global__ __launch_bounds__(64 * LPC) void scan_backward_kernel(gdr2_scan_bwd_args p, Pieces seg, uint32_t ncb, uint32_t cb_per,
+                                                                 BackwardPtrs w)
 {
-    constexpr int NP = 4 * NS, SUB = kSub<NS>, NSUB = kScanChunk / SUB, NG = kScanChunk / 4;
+    constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT, NW = NT / 64;
     const gdr2_scan_args& a = p.f;
     __shared__ __align__(16) float s_b[kScanChunk][NP], s_c[kScanChunk][NP];
-    __shared__ __align__(16) float s_red[2][4][SUB][NP];
+    __shared__ __align__(16) f32x4 s_tok[kScanChunk][kScanCols];          // d, d x, dv, - and then d, du, qA, v
+    __shared__ __align__(16) float s_red[2][NW][kScanChunk][NP];
+    __shared__ __align__(16) float s_h[kSubs][NT][NS];
     const uint32_t slot = blockIdx.x / ncb, cb = blockIdx.x - slot * ncb;
     const Piece q = uniform(piece_of(seg, slot));
-    const ScanLane l = scan_lane(a, cb, cb_per);
-    const int s = l.s, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t N = a.N, C = a.C, c = l.c;
-    float* sums = w.sums + (int64_t)slot * C * (N + 2);
-    float dA[NS] = {}, dskip = 0.f, dbias = 0.f;
+    const ScanBlock blk = scan_block(a, cb, cb_per);
+    const ScanLane l = scan_lane<LPC>(blk);
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t C = a.C, c = l.c;
+    const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
+    float* sums = w.sums + (int64_t)slot * sums_ld(C, N);
+    float dA[NS] = {}, dskip[V] = {}, dbias[V] = {};
+    const int64_t t0 = q.seq < 0 ? 0 : q.index << seg.lg;
+    const int64_t t1 = q.seq < 0 ? 0 : min(q.len, t0 + ((int64_t)1 << seg.lg));
+    float lam[NS] = {};
     if (q.seq >= 0) {
-        float A[NS], A2[NS], lam[NS];
-        load_states<NS>(a.A + c * N, s, N, l.on, A);
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-            A2[i] = A[i] * kLog2e;
         if (w.lam)
             load_states<NS>(w.lam + ((int64_t)slot * C + c) * N, s, N, l.on, lam);
         else
             load_states<NS>(p.dh_out + (q.seq * C + c) * N, s, N, l.on && p.dh_out, lam);
-        const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
-        const float skip = a.skip && l.on ? a.skip[c] : 0.f;
+    }
+    if (t0 < t1) {
+        float A[NS], A2[NS];
+        load_states<NS>(a.A + c * N, s, N, l.on, A);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            A2[i] = A[i] * kLog2e;
+        float bias[V], skip[V];
+        channel_params<V>(a.dt_bias, blk, bias);
+        channel_params<V>(a.skip, blk, skip);
+        const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
         const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
-        const int64_t ck0 = sequence_of(ckp, q.seq).first;
+        const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
         const int64_t rows = a.offsets ? a.T : a.B * a.T;
         float* part = w.parts + (int64_t)cb * rows * 2 * N;
-        const int64_t t0 = q.index << seg.lg;
-        const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
-        for (int64_t t = t0 + ((t1 - t0 - 1) >> kScanLg << kScanLg); t1 > t0 && t >= t0; t -= kScanChunk) {
-            __syncthreads();
-            const int left = (int)min(t1 - t, (int64_t)kScanChunk);
-            Staged<T, NP> rb(a.b_stride, l.j, (int)N), rc(a.c_stride, l.j, (int)N);
-            rb.load(a.Bt, q.row0 + t, a.b_stride, left);
-            rc.load(a.Ct, q.row0 + t, a.c_stride, left);
+
+        int64_t t = t0 + ((t1 - t0 - 1) >> kScanLg << kScanLg);
+        const int64_t row = q.row0 + t;
+        RowVec<T, V, WIDE> rt(a.dt_stride, blk), rx(a.x_stride, blk), rd(C, blk), rz(a.z_stride, blk);
+        const RowVec<T, V, WIDE> ro(C, blk);
+        Staged<T, NP, NT> rb(a.b_stride, blk.j, N), rc(a.c_stride, blk.j, N);
+        RowWalk wt = RowWalk::at<T>(a.dt, row, a.dt_stride), wx = RowWalk::at<T>(a.x, row, a.x_stride);
+        RowWalk wb = RowWalk::at<T>(a.Bt, row, a.b_stride), wc = RowWalk::at<T>(a.Ct, row, a.c_stride);
+        RowWalk wz = RowWalk::at<T>(a.z, row, a.z_stride), wd = RowWalk::at<T>(p.dy, row, C);
+        RowWalk wdx = RowWalk::at<T>(p.dx, row, C), wdt = RowWalk::at<T>(p.ddt, row, C), wdz = RowWalk::at<T>(p.dz, row, C);
+        auto fetch = [&](int left) {
+            rt.load(wt, left);
+            rx.load(wx, left);
+            rd.load(wd, left);
+            rb.load(wb, left);
+            rc.load(wc, left);
+            wt.advance(-kScanChunk);
+            wx.advance(-kScanChunk);
+            wd.advance(-kScanChunk);
+            wb.advance(-kScanChunk);
+            wc.advance(-kScanChunk);
+            if constexpr (GATE) {
+                rz.load(wz, left);
+                wz.advance(-kScanChunk);
+            }
+        };
+        int left = (int)(t1 - t);
+        fetch(left);
+        float h0[NS];
+        load_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * C + c) * N, s, N, l.on, h0);
+        for (;; t -= kScanChunk) {
+            // rows of this chunk
             rb.store(s_b);
             rc.store(s_c);
-            float xs[NG], raws[NG], ds[NG];
+            const RowVec<T, V, WIDE> xt = rt, xx = rx, xd = rd, xz = rz;
+            const bool in = token < left;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const int64_t mt = t + 4 * g + s, row = q.row0 + mt;
-                xs[g] = raws[g] = ds[g] = 0.f;
-                if (l.on && mt < t1) {
-                    xs[g] = to_f32(((const T*)a.x)[row * a.x_stride + c]);
-                    raws[g] = to_f32(((const T*)a.dt)[row * a.dt_stride + c]) + bias;
-                    ds[g] = a.flags & GDR2_SCAN_SOFTPLUS ? softplus_f(raws[g]) : raws[g];
-                }
+            for (int v = 0; v < V; ++v) {
+                const float raw = xt.get(v) + bias[v], x = xx.get(v);
+                float d = soft ? softplus_f(raw) : raw, dv = xd.get(v);
+                if constexpr (GATE)
+                    dv *= silu_f(xz.get(v));
+                d = in ? d : 0.f;
+                dv = in ? dv : 0.f;
+                s_tok[token][ch + v] = f32x4{d, d * x, dv, 0.f};
             }
-            __syncthreads();
-            // the states before every SUB tokens
-            float hs[NSUB][NS];
-            load_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * C + c) * N, s, N, l.on, hs[0]);
 #pragma unroll
-            for (int b = 1; b < NSUB; ++b) {
+            for (int i = 0; i < NS; ++i)
+                s_h[0][threadIdx.x][i] = h0[i];
+            lds_barrier();
+            const bool more = t > t0;
+            fetch(more ? kScanChunk : 0);
+            // the states before every kSub tokens
+            {
+                float h[NS];
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
-                    hs[b][i] = hs[b - 1][i];
+                    h[i] = h0[i];
+#pragma unroll 1
+                for (int b = 0; b < kSubs - 1; ++b) {
 #pragma unroll
-                for (int k = 0; k < SUB; ++k) {
-                    const int tt = (b - 1) * SUB + k;
-                    const float dk = quad_bcast_k(ds[tt / 4], tt % 4);
-                    const float uk = quad_bcast_k(ds[tt / 4] * xs[tt / 4], tt % 4);
+                    for (int k = 0; k < kSub; ++k) {
+                        const f32x4 tk = s_tok[b * kSub + k][lc];
+                        float B[NS];
+                        read_states<NS>(&s_b[b * kSub + k][s * NS], B);
+#pragma unroll
+                        for (int i = 0; i < NS; ++i)
+                            h[i] = fmaf(fast_exp2(tk[0] * A2[i]), h[i], tk[1] * B[i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < NS; ++i)
-                        hs[b][i] = fmaf(fast_exp2(dk * A2[i]), hs[b][i], uk * s_b[tt][s * NS + i]);
+                        s_h[b + 1][threadIdx.x][i] = h[i];
                 }
             }
+#pragma unroll 1
+            for (int b = kSubs - 1; b >= 0; --b) {
+                float av[kSub][NS], hv[kSub + 1][NS];
+                read_states<NS>(&s_h[b][threadIdx.x][0], hv[0]);
 #pragma unroll
-            for (int b = NSUB - 1; b >= 0; --b) {
-                float av[SUB][NS], hv[SUB + 1][NS];
-#pragma unroll
-                for (int i = 0; i < NS; ++i)
-                    hv[0][i] = hs[b][i];
-#pragma unroll
-                for (int k = 0; k < SUB; ++k) {
-                    const int tt = b * SUB + k;
-                    const float dk = quad_bcast_k(ds[tt / 4], tt % 4);
-                    const float uk = quad_bcast_k(ds[tt / 4] * xs[tt / 4], tt % 4);
+                for (int k = 0; k < kSub; ++k) {
+                    const f32x4 tk = s_tok[b * kSub + k][lc];
+                    float B[NS];
+                    read_states<NS>(&s_b[b * kSub + k][s * NS], B);
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
-                        av[k][i] = fast_exp2(dk * A2[i]);
-                        hv[k + 1][i] = fmaf(av[k][i], hv[k][i], uk * s_b[tt][s * NS + i]);
+                        av[k][i] = fast_exp2(tk[0] * A2[i]);
+                        hv[k + 1][i] = fmaf(av[k][i], hv[k][i], tk[1] * B[i]);
                     }
                 }
 #pragma unroll
-                for (int g = SUB / 4 - 1; g >= 0; --g) {
-                    const int gg = b * (SUB / 4) + g;           // group within the chunk
-                    const int64_t mt = t + 4 * gg + s, row = q.row0 + mt;
-                    const bool in = l.on && mt < t1;
-                    const float x = xs[gg], d = ds[gg], u = x * d;
-                    float dy = in ? to_f32(((const T*)p.dy)[row * C + c]) : 0.f, z = 0.f, dv = dy;
-                    if (a.z && in) {
-                        z = to_f32(((const T*)a.z)[row * a.z_stride + c]);
-                        dv = dy * silu_f(z);
-                    }
-                    float pu[4], pa[4], pv[4], vb[4][NS], vc[4][NS];
+                for (int g = kSub / LPC - 1; g >= 0; --g) {
+                    float pu[LPC], pa[LPC], pv[LPC], vb[LPC][NS], vc[LPC][NS];
 #pragma unroll
-                    for (int k = 3; k >= 0; --k) {
-                        const int tt = 4 * gg + k, kk = 4 * g + k;
-                        const float dk = quad_bcast_k(d, k), uk = quad_bcast_k(u, k), dvk = quad_bcast_k(dv, k);
-                        pu[k] = pa[k] = pv[k] = 0.f;
+                    for (int k = LPC - 1; k >= 0; --k) {
+                        const int kk = g * LPC + k;
+                        const f32x4 tk = s_tok[b * kSub + kk][lc];
+                        float B[NS], Cn[NS];
+                        read_states<NS>(&s_b[b * kSub + kk][s * NS], B);
+                        read_states<NS>(&s_c[b * kSub + kk][s * NS], Cn);
 #pragma unroll
                         for (int i = 0; i < NS; ++i) {
-                            const float bn = s_b[tt][s * NS + i], cn = s_c[tt][s * NS + i];
-                            const float gr = fmaf(cn, dvk, lam[i]);
-                            vc[k][i] = dvk * hv[kk + 1][i];
-                            vb[k][i] = gr * uk;
-                            pu[k] = fmaf(gr, bn, pu[k]);
-                            pv[k] = fmaf(cn, hv[kk + 1][i], pv[k]);
+                            const float gr = fmaf(Cn[i], tk[2], lam[i]);
+                            vc[k][i] = tk[2] * hv[kk + 1][i];
+                            vb[k][i] = gr * tk[1];
                             lam[i] = gr * av[kk][i];
                             const float qq = lam[i] * hv[kk][i];
-                            pa[k] = fmaf(qq, A[i], pa[k]);
-                            dA[i] = fmaf(qq, dk, dA[i]);
+                            dA[i] = fmaf(qq, tk[0], dA[i]);
+                            pu[k] = i == 0 ? gr * B[0] : fmaf(gr, B[i], pu[k]);
+                            pa[k] = i == 0 ? qq * A[0] : fmaf(qq, A[i], pa[k]);
+                            if constexpr (GATE)
+                                pv[k] = i == 0 ? Cn[0] * hv[kk + 1][0] : fmaf(Cn[i], hv[kk + 1][i], pv[k]);
                         }
                     }
-                    const float du = quad_sum_transposed(pu, s), qa = quad_sum_transposed(pa, s);
-                    float dd = fmaf(x, du, qa);
-                    if (a.flags & GDR2_SCAN_SOFTPLUS)
-                        dd *= sigmoid_f(raws[gg]);
-                    if (a.z) {
-                        const float v = fmaf(skip, x, quad_sum_transposed(pv, s));
-                        if (in)
-                            ((T*)p.dz)[row * C + c] = from_f32<T>(dy * v * silu_slope_f(z));
-                    }
-                    if (in) {
-                        ((T*)p.dx)[row * C + c] = from_f32<T>(fmaf(d, du, skip * dv));
-                        ((T*)p.ddt)[row * C + c] = from_f32<T>(dd);
-                        dskip = fmaf(dv, x, dskip);
-                        dbias += dd;
-                    }
-                    float rb[NS], rc[NS];
-                    channel_sum<NS>(vb, lane, rb);
-                    channel_sum<NS>(vc, lane, rc);
-                    if ((lane & 12) == 0) {
-                        const int kr = 4 * g + (lane >> 4);
+                    // lane s: token s of the group
+                    float* at = (float*)&s_tok[b * kSub + g * LPC + s][lc];
+                    at[1] = sum_transposed(pu, s);
+                    at[2] = sum_transposed(pa, s);
+                    if constexpr (GATE)
+                        at[3] = sum_transposed(pv, s);
+                    float rbs[LPC / 4][NS], rcs[LPC / 4][NS];
+                    channel_sum<LPC, NS>(vb, rbs);
+                    channel_sum<LPC, NS>(vc, rcs);
+                    if ((lane & 15) < LPC) {
 #pragma unroll
-                        for (int i = 0; i < NS; ++i) {
-                            s_red[0][wave][kr][s * NS + i] = rb[i];
-                            s_red[1][wave][kr][s * NS + i] = rc[i];
+                        for (int e = 0; e < LPC / 4; ++e) {
+                            const int r = b * kSub + g * LPC + 4 * e + (lane >> 4);
+#pragma unroll
+                            for (int i = 0; i < NS; ++i) {
+                                s_red[0][wave][r][s * NS + i] = rbs[e][i];
+                                s_red[1][wave][r][s * NS + i] = rcs[e][i];
+                            }
                         }
                     }
                 }
-                __syncthreads();
-                for (int e = threadIdx.x; e < 2 * SUB * NP; e += 256) {
-                    const int which = e / (SUB * NP), r = e / NP % SUB, n = e % NP;
-                    const int64_t mt = t + b * SUB + r;
-                    if (mt < t1 && n < N)
-                        part[((q.row0 + mt) * 2 + which) * N + n] = (s_red[which][0][r][n] + s_red[which][1][r][n]) +
-                                                                     (s_red[which][2][r][n] + s_red[which][3][r][n]);
-                }
-                __syncthreads();
             }
+            if (more)
+                load_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg) - 1) * C + c) * N, s, N, l.on, h0);
+            lds_barrier();
+            float dx[V], ddt[V], dz[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const f32x4 tk = s_tok[token][ch + v];
+                const float x = xx.get(v), dy = xd.get(v), raw = xt.get(v) + bias[v];
+                float dv = dy;
+                if constexpr (GATE) {
+                    const float z = xz.get(v), sg = sigmoid_f(z);
+                    dv = dy * z * sg;
+                    dz[v] = dy * fmaf(skip[v], x, tk[3]) * (sg * fmaf(z, 1.f - sg, 1.f));
+                }
+                float dd = fmaf(x, tk[1], tk[2]);
+                dd = soft ? dd * sigmoid_f(raw) : dd;
+                dx[v] = fmaf(tk[0], tk[1], skip[v] * dv);
+                ddt[v] = dd;
+                // (rows past the sequence read as zero, and so add nothing: dv = x = 0,
+                // and dd is qA = 0 for d = 0 times a state that nothing changed)
+                dskip[v] = fmaf(dv, x, dskip[v]);
+                dbias[v] += in ? dd : 0.f;
+            }
+            ro.store(wdx, left, dx);
+            ro.store(wdt, left, ddt);
+            if constexpr (GATE)
+                ro.store(wdz, left, dz);
+            wdx.advance(-kScanChunk);
+            wdt.advance(-kScanChunk);
+            wdz.advance(-kScanChunk);
+            for (int e = threadIdx.x; e < 2 * kScanChunk * NP; e += NT) {
+                const int r = e / (2 * NP), which = e / NP % 2, n = e % NP;
+                float x = 0.f;
+#pragma unroll
+                for (int k = 0; k < NW; ++k)
+                    x += s_red[which][k][r][n];
+                if (r < left && n < N)
+                    part[((q.row0 + t + r) * 2 + which) * N + n] = x;
+            }
+            if (!more)
+                break;
+            left = kScanChunk;
+            lds_barrier();
         }
-        if (p.dh0 && q.index == 0)
-            store_states<NS>(p.dh0 + (q.seq * C + c) * N, s, N, l.on, lam);
     }
+    if (q.seq >= 0 && p.dh0 && q.index == 0)
+        store_states<NS>(p.dh0 + (q.seq * C + c) * N, s, N, l.on, lam);
     store_states<NS>(sums + c * N, s, N, l.on, dA);
-    dskip += dpp_quad_xor<1>(dskip);
-    dskip += dpp_quad_xor<2>(dskip);
-    dbias += dpp_quad_xor<1>(dbias);
-    dbias += dpp_quad_xor<2>(dbias);
-    if (l.on && s == 0) {
-        sums[C * N + c] = dskip;
-        sums[C * (N + 1) + c] = dbias;
+    // dskip and ddt_bias over the threads that share their channels, in token order
+    lds_barrier();
+    f32x4* both = &s_tok[0][0];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        both[token * kScanCols + ch + v] = f32x4{dskip[v], dbias[v], 0.f, 0.f};
+    lds_barrier();
+    if ((int)threadIdx.x < blk.n) {
+        float x = 0.f, y = 0.f;
+        for (int k = 0; k < kScanChunk; ++k) {
+            const f32x4 e = both[k * kScanCols + threadIdx.x];
+            x += e[0];
+            y += e[1];
+        }
+        sums[C * N + blk.c0 + threadIdx.x] = x;
+        sums[C * (N + 1) + blk.c0 + threadIdx.x] = y;
     }
 }
 
 // Per segment but the first of its sequence: the gradient of its start state
 // when none enters from behind, and sum d.
-template <typename T, int NS>
-__global__ __launch_bounds__(256) void scan_backward_span_kernel(gdr2_scan_bwd_args p, Pieces seg, uint32_t ncb,
-                                                                 uint32_t cb_per, float* states, float* sums)
+template <typename T, int LPC, int NS, bool GATE, bool WIDE>
+__global__ __launch_bounds__(64 * LPC) void scan_backward_span_kernel(gdr2_scan_bwd_args p, Pieces seg, uint32_t ncb,
+                                                                      uint32_t cb_per, float* states, float* sums)
 {
-    constexpr int NP = 4 * NS;
+    constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT;
     const gdr2_scan_args& a = p.f;
-    __shared__ __align__(16) float s_c[kScanChunk][NP];
+    __shared__ __align__(16) float s_c[2][kScanChunk][NP];
+    __shared__ __align__(16) float s_du[2][kScanChunk / 2][kStepLd];      // d, dv as the forward's d, d x
     const uint32_t slot = blockIdx.x / ncb;
     const Piece q = uniform(piece_of(seg, slot));
     if (q.seq < 0 || q.index == 0)
         return;
-    const ScanLane l = scan_lane(a, blockIdx.x - slot * ncb, cb_per);
-    const int s = l.s;
-    const int64_t N = a.N, C = a.C, c = l.c;
+    const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
+    const ScanLane l = scan_lane<LPC>(blk);
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC;
+    const int64_t C = a.C, c = l.c;
     float A2[NS], lam[NS] = {}, sum = 0.f;
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
         A2[i] *= kLog2e;
-    const float bias = a.dt_bias && l.on ? a.dt_bias[c] : 0.f;
+    float bias[V];
+    channel_params<V>(a.dt_bias, blk, bias);
+    const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
+    const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
     const int64_t t0 = q.index << seg.lg;
     const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
-    for (int64_t t = t0 + ((t1 - t0 - 1) >> kScanLg << kScanLg); t >= t0; t -= kScanChunk) {
-        __syncthreads();
-        const int left = (int)min(t1 - t, (int64_t)kScanChunk);
-        Staged<T, NP> rc(a.c_stride, l.j, (int)N);
-        rc.load(a.Ct, q.row0 + t, a.c_stride, left);
-        rc.store(s_c);
-        __syncthreads();
-#pragma unroll 1
-        for (int tt = kScanChunk - 4; tt >= 0; tt -= 4) {
-            const int64_t mt = t + tt + s, row = q.row0 + mt;
-            float d = 0.f, dv = 0.f;
-            if (l.on && mt < t1) {
-                const float raw = to_f32(((const T*)a.dt)[row * a.dt_stride + c]) + bias;
-                d = a.flags & GDR2_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
-                dv = to_f32(((const T*)p.dy)[row * C + c]);
-                if (a.z)
-                    dv *= silu_f(to_f32(((const T*)a.z)[row * a.z_stride + c]));
-            }
-            sum += d;
+    int64_t t = t0 + ((t1 - t0 - 1) >> kScanLg << kScanLg);
+    const int64_t row = q.row0 + t;
+    RowVec<T, V, WIDE> rt(a.dt_stride, blk), rd(C, blk), rz(a.z_stride, blk);
+    Staged<T, NP, NT> rc(a.c_stride, blk.j, N);
+    RowWalk wt = RowWalk::at<T>(a.dt, row, a.dt_stride), wd = RowWalk::at<T>(p.dy, row, C);
+    RowWalk wz = RowWalk::at<T>(a.z, row, a.z_stride), wc = RowWalk::at<T>(a.Ct, row, a.c_stride);
+    auto fetch = [&](int left) {
+        rt.load(wt, left);
+        rd.load(wd, left);
+        rc.load(wc, left);
+        wt.advance(-kScanChunk);
+        wd.advance(-kScanChunk);
+        wc.advance(-kScanChunk);
+        if constexpr (GATE) {
+            rz.load(wz, left);
+            wz.advance(-kScanChunk);
+        }
+    };
+    int left = (int)(t1 - t), buf = 0;
+    fetch(left);
+    for (; t >= t0; t -= kScanChunk, buf ^= 1) {
+        rc.store(s_c[buf]);
 #pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                const float dk = quad_bcast_k(d, k), dvk = quad_bcast_k(dv, k);
+        for (int v = 0; v < V; ++v) {
+            typedef float Two __attribute__((ext_vector_type(2)));
+            const float raw = rt.get(v) + bias[v];
+            float d = soft ? softplus_f(raw) : raw, dv = rd.get(v);
+            if constexpr (GATE)
+                dv *= silu_f(rz.get(v));
+            d = token < left ? d : 0.f;
+            dv = token < left ? dv : 0.f;
+            *reinterpret_cast<Two*>(&s_du[buf][token / 2][4 * (ch + v) + 2 * (token & 1)]) = Two{d, dv};
+        }
+        left = kScanChunk;
+        fetch(t > t0 ? kScanChunk : 0);
+        lds_barrier();
 #pragma unroll
-                for (int i = 0; i < NS; ++i)
-                    lam[i] = fmaf(s_c[tt + k][s * NS + i], dvk, lam[i]) * fast_exp2(dk * A2[i]);
+        for (int tt = kScanChunk - 2; tt >= 0; tt -= 2) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][tt / 2][4 * lc]);
+            sum += x[0] + x[2];
+            float C0[NS], C1[NS];
+            read_states<NS>(&s_c[buf][tt][s * NS], C0);
+            read_states<NS>(&s_c[buf][tt + 1][s * NS], C1);
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                lam[i] = fmaf(C1[i], x[3], lam[i]) * fast_exp2(x[2] * A2[i]);
+                lam[i] = fmaf(C0[i], x[1], lam[i]) * fast_exp2(x[0] * A2[i]);
             }
         }
     }
-    sum += dpp_quad_xor<1>(sum);
-    sum += dpp_quad_xor<2>(sum);
     store_states<NS>(states + ((int64_t)slot * C + c) * N, s, N, l.on, lam);
     if (l.on && s == 0)
         sums[(int64_t)slot * C + c] = sum;
@@ -303,27 +428,27 @@ __global__ __launch_bounds__(256) void scan_backward_fold_kernel(gdr2_scan_bwd_a
 
 // dB and dC: the channel blocks' partial sums of each row, in block order.
 template <typename T>
-__global__ __launch_bounds__(256) void scan_rows_sum_kernel(gdr2_scan_bwd_args p, const float* parts, int64_t rows, int64_t cb_per)
+__global__ __launch_bounds__(256) void scan_rows_sum_kernel(gdr2_scan_bwd_args p, const float* parts, int64_t rows,
+                                                            uint32_t cb_per)
 {
     const gdr2_scan_args& a = p.f;
-    const int64_t N = a.N, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= rows * a.G * N)
+    const uint32_t N = (uint32_t)a.N, G = (uint32_t)a.G, id = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t g = id / (2 * N), e = id - g * 2 * N, row = g / G, j = g - row * G;   // e: dB, then dC
+    if (row >= rows)
         return;
-    const int64_t row = id / (a.G * N), jn = id - row * a.G * N, j = jn / N, n = jn - j * N;
     if (a.offsets) {
         // rows of no sequence: before the first or behind the last
         const Pieces pc{a.offsets, a.B, a.T, 0};
         if (row < clamp_offset(pc, 0) || row >= clamp_offset(pc, a.B))
             return;
     }
-    const float* at = parts + ((j * cb_per * rows + row) * 2) * N + n;
-    float db = 0.f, dc = 0.f;
-    for (int64_t i = 0; i < cb_per; ++i) {
-        db += at[i * rows * 2 * N];
-        dc += at[i * rows * 2 * N + N];
-    }
-    ((T*)p.dBt)[id] = from_f32<T>(db);
-    ((T*)p.dCt)[id] = from_f32<T>(dc);
+    const float* at = parts + ((int64_t)j * cb_per * rows + row) * 2 * N + e;
+    float x = 0.f;
+#pragma unroll 8
+    for (uint32_t i = 0; i < cb_per; ++i)
+        x += at[(int64_t)i * rows * 2 * N];
+    T* to = (T*)(e < N ? p.dBt : p.dCt);
+    to[(int64_t)g * N + (e < N ? e : e - N)] = from_f32<T>(x);
 }
 
 struct BackwardWork {
@@ -338,30 +463,29 @@ BackwardWork backward_work(const gdr2_scan_bwd_args& p, const ScanPlan& pl)
     BackwardWork w;
     w.parts = 0;
     w.sums = al((size_t)pl.ncb * rows * 2 * a.N * 4);
-    w.lam = w.sums + al((size_t)slots * a.C * (a.N + 2) * 4);
+    w.lam = w.sums + al((size_t)slots * sums_ld(a.C, a.N) * 4);
     w.span = w.lam + (pl.split ? al((size_t)slots * a.C * a.N * 4) : 0);
     w.total = w.span + (pl.split ? (size_t)slots * a.C * 4 : 0);
     return w;
 }
 
-template <typename T, int NS>
+template <typename T, int LPC, int NS, bool GATE, bool WIDE>
 hipError_t backward_t(const gdr2_scan_bwd_args& p, hipStream_t stream)
 {
     const gdr2_scan_args& a = p.f;
-    const ScanPlan pl = scan_plan(a, true);
+    const ScanPlan pl = scan_plan(a);
     const BackwardWork w = backward_work(p, pl);
     char* ws = (char*)p.workspace;
-    const dim3 grid((unsigned)(pl.seg.slots() * pl.ncb));
+    const dim3 grid((unsigned)(pl.seg.slots() * pl.ncb)), block(64 * LPC);
+    const uint32_t ncb = (uint32_t)pl.ncb, cb_per = (uint32_t)pl.cb_per;
     const int64_t rows = a.offsets ? a.T : a.B * a.T;
     BackwardPtrs ptr{(float*)(ws + w.parts), (float*)(ws + w.sums), nullptr};
     hipError_t e;
-    if (a.B == 0)      // no rows: zeros are all there is to write
-        return launch_column_sum(ptr.sums, 0, {p.dA, a.C * a.N}, {p.dskip, a.C}, {p.ddt_bias, a.C}, stream);
     if (pl.split) {
         float* lam = (float*)(ws + w.lam);
         float* span = (float*)(ws + w.span);
-        hipLaunchKernelGGL((scan_backward_span_kernel<T, NS>), grid, dim3(256), 0, stream, p, pl.seg, (uint32_t)pl.ncb,
-                           (uint32_t)pl.cb_per, lam, span);
+        hipLaunchKernelGGL((scan_backward_span_kernel<T, LPC, NS, GATE, WIDE>), grid, block, 0, stream, p, pl.seg, ncb, cb_per,
+                           lam, span);
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
         hipLaunchKernelGGL(scan_backward_fold_kernel, dim3((unsigned)ceil_div(a.B * a.C * a.N, 256)), dim3(256), 0, stream, p,
@@ -370,32 +494,45 @@ hipError_t backward_t(const gdr2_scan_bwd_args& p, hipStream_t stream)
             return e;
         ptr.lam = lam;
     }
-    hipLaunchKernelGGL((scan_backward_kernel<T, NS>), grid, dim3(256), 0, stream, p, pl.seg, (uint32_t)pl.ncb,
-                       (uint32_t)pl.cb_per, ptr);
+    hipLaunchKernelGGL((scan_backward_kernel<T, LPC, NS, GATE, WIDE>), grid, block, 0, stream, p, pl.seg, ncb, cb_per, ptr);
     if ((e = hipGetLastError()) != hipSuccess)
         return e;
     if (rows > 0) {
-        hipLaunchKernelGGL((scan_rows_sum_kernel<T>), dim3((unsigned)ceil_div(rows * a.G * a.N, 256)), dim3(256), 0, stream, p,
-                           ptr.parts, rows, pl.cb_per);
+        hipLaunchKernelGGL((scan_rows_sum_kernel<T>), dim3((unsigned)ceil_div(rows * a.G * 2 * a.N, 256)), dim3(256), 0, stream,
+                           p, ptr.parts, rows, cb_per);
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
     }
-    return launch_column_sum(ptr.sums, pl.seg.slots(), {p.dA, a.C * a.N}, {p.dskip, a.C}, {p.ddt_bias, a.C}, stream);
+    return launch_column_sum(ptr.sums, pl.seg.slots(), sums_ld(a.C, a.N), {p.dA, a.C * a.N}, {p.dskip, a.C}, {p.ddt_bias, a.C}, stream);
+}
+
+template <typename T, int LPC, int NS>
+hipError_t backward_w(const gdr2_scan_bwd_args& p, hipStream_t stream)
+{
+    constexpr int V = kScanChunk / LPC;
+    const int64_t e = sizeof(T);
+    auto ok = [&](const void* q) { return !q || reinterpret_cast<uintptr_t>(q) % (V * e) == 0; };
+    const bool wide = scan_wide(p.f, V) && ok(p.dy) && ok(p.dx) && ok(p.ddt) && ok(p.dz);
+    if (p.f.z)
+        return wide ? backward_t<T, LPC, NS, true, true>(p, stream) : backward_t<T, LPC, NS, true, false>(p, stream);
+    return wide ? backward_t<T, LPC, NS, false, true>(p, stream) : backward_t<T, LPC, NS, false, false>(p, stream);
 }
 
 }  // namespace
 
-size_t scan_backward_workspace_bytes(const gdr2_scan_bwd_args& p) { return backward_work(p, scan_plan(p.f, true)).total; }
+size_t scan_backward_workspace_bytes(const gdr2_scan_bwd_args& p) { return backward_work(p, scan_plan(p.f)).total; }
 
 hipError_t launch_scan_backward(const gdr2_scan_bwd_args& p, hipStream_t stream)
 {
     const gdr2_scan_args& a = p.f;
+    if (a.B == 0)      // no rows: zeros are all there is to write
+        return launch_column_sum(nullptr, 0, 0, {p.dA, a.C * a.N}, {p.dskip, a.C}, {p.ddt_bias, a.C}, stream);
     const bool bf = a.dtype == GDR2_BF16;
     if (a.N <= 8)
-        return bf ? backward_t<bf16, 2>(p, stream) : backward_t<float, 2>(p, stream);
+        return bf ? backward_w<bf16, 4, 2>(p, stream) : backward_w<float, 4, 2>(p, stream);
     if (a.N <= 16)
-        return bf ? backward_t<bf16, 4>(p, stream) : backward_t<float, 4>(p, stream);
-    return bf ? backward_t<bf16, 8>(p, stream) : backward_t<float, 8>(p, stream);
+        return bf ? backward_w<bf16, 4, 4>(p, stream) : backward_w<float, 4, 4>(p, stream);
+    return bf ? backward_w<bf16, 8, 4>(p, stream) : backward_w<float, 8, 4>(p, stream);
 }
 
 }  // namespace gdr2
