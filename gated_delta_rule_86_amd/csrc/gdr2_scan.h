@@ -337,6 +337,11 @@ inline bool scan_wide(const gdr2_scan_args& a, int V)
 // one read serves two.
 constexpr int kStepLd = 4 * kScanCols;
 
+// Where a channel's 16 bytes of a token lie in LDS.  A thread of the rows
+// layout writes 8 (or 4) channels in turn; in channel order the lanes of a
+// wave would be 128 bytes apart, all on the same banks.
+__device__ __forceinline__ int step_place(int channel) { return channel ^ ((channel >> 3) & 7); }
+
 template <int NS> __device__ __forceinline__ void read_states(const float* p, float (&v)[NS])
 {
     typedef float Vec __attribute__((ext_vector_type(NS)));
@@ -353,6 +358,15 @@ template <int V> __device__ __forceinline__ void channel_params(const float* p, 
 #pragma unroll
     for (int v = 0; v < V; ++v)
         out[v] = p && ch + v < b.n ? p[b.c0 + ch + v] : 0.f;
+}
+
+// The step from its raw value.  softplus is formed either way: behind a branch
+// per element it would split the block it is scheduled in.
+__device__ __forceinline__ float step_of(float raw, bool softplus)
+{
+    float soft = softplus_f(raw);
+    asm volatile("" : "+v"(soft));
+    return softplus ? soft : raw;
 }
 
 }  // namespace gdr2

@@ -18,22 +18,12 @@ namespace gdr2 {
 
 namespace {
 
-// The step of a token.
-__device__ __forceinline__ float step_of(float dt, float bias, int flags)
-{
-    const float raw = dt + bias;
-    return flags & GDR2_SCAN_SOFTPLUS ? softplus_f(raw) : raw;
-}
-
 // (d, d x) of one channel of a thread's row vector into LDS; 0 past the
 // sequence, where the token then leaves the state as it is.
 __device__ __forceinline__ void step_to_lds(float dt, float x, float bias, bool softplus, bool in, float* at)
 {
     typedef float Two __attribute__((ext_vector_type(2)));
-    const float raw = dt + bias;
-    float soft = softplus_f(raw);
-    asm volatile("" : "+v"(soft));   // formed either way: a branch would split the block it is scheduled in
-    float d = softplus ? soft : raw;
+    float d = step_of(dt + bias, softplus);
     d = in ? d : 0.f;
     *reinterpret_cast<Two*>(at) = Two{d, d * x};
 }
@@ -60,7 +50,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
         return;
     const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
     const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC;
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, lp = step_place(lc);
     const int64_t c = l.c;
     float A2[NS], h[NS];
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
@@ -81,7 +71,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
         const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
         const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
         const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
-        const int du_at = 4 * ch + 2 * (token & 1);
+        const int du_at = 2 * (token & 1);
         auto left_at = [&](int64_t t) { return (int)max((int64_t)0, min(t1 - t, (int64_t)kScanChunk)); };
 
         // rows of a chunk: dt, x (and z), B, C
@@ -109,7 +99,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
         fetch(left_at(t0));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            step_to_lds(rt.get(v), rx.get(v), bias[v], soft, token < left_at(t0), &s_du[0][token / 2][du_at + 4 * v]);
+            step_to_lds(rt.get(v), rx.get(v), bias[v], soft, token < left_at(t0), &s_du[0][token / 2][du_at + 4 * step_place(ch + v)]);
         }
         // x, z of the previous chunk (nothing yet) and of the current one
         RowVec<T, V, WIDE> px = rx, pz = rz, cx = rx, cz = rz;
@@ -136,7 +126,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
             }
 #pragma unroll
             for (int k = 0; k < LPC; k += 2) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lc]);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lp]);
                 d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
             }
 #pragma unroll
@@ -159,12 +149,12 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
                         read_states<NS>(&s_b[buf][next][s * NS], B[k]);
                         read_states<NS>(&s_c[buf][next][s * NS], C[k]);
                         if (k % 2) {
-                            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lc]);
+                            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lp]);
                             d[k - 1] = x[0], u[k - 1] = x[1], d[k] = x[2], u[k] = x[3];
                         }
                     }
                     if (k == 1)
-                        step_to_lds(nt.get(g), nx.get(g), bias[g], soft, in, &s_du[buf ^ 1][token / 2][du_at + 4 * g]);
+                        step_to_lds(nt.get(g), nx.get(g), bias[g], soft, in, &s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + g)]);
                     if (k == LPC - 2) {
                         y[g] = fmaf(skip[g], px.get(g), y[g]);
                         if constexpr (GATE)
@@ -212,7 +202,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
         return;
     const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
     const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC;
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, lp = step_place(lc);
     const int64_t c = l.c;
     float A2[NS], h[NS] = {}, sum = 0.f;
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
@@ -223,7 +213,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
     channel_params<V>(a.dt_bias, blk, bias);
     const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
     const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
-    const int du_at = 4 * ch + 2 * (token & 1);
+    const int du_at = 2 * (token & 1);
     RowVec<T, V, WIDE> rt(a.dt_stride, blk), rx(a.x_stride, blk);
     Staged<T, NP, NT> rb(a.b_stride, blk.j, N);
     const int64_t row = q.row0 + t0;
@@ -240,7 +230,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
     fetch(kScanChunk);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        step_to_lds(rt.get(v), rx.get(v), bias[v], soft, true, &s_du[0][token / 2][du_at + 4 * v]);
+        step_to_lds(rt.get(v), rx.get(v), bias[v], soft, true, &s_du[0][token / 2][du_at + 4 * step_place(ch + v)]);
     rb.store(s_b[0]);
     fetch(t0 + kScanChunk < t1 ? kScanChunk : 0);
     int buf = 0;
@@ -255,7 +245,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
             read_states<NS>(&s_b[buf][k][s * NS], B[k]);
 #pragma unroll
         for (int k = 0; k < LPC; k += 2) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lc]);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lp]);
             d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
         }
 #pragma unroll
@@ -270,12 +260,12 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
                 if (next < kScanChunk) {
                     read_states<NS>(&s_b[buf][next][s * NS], B[k]);
                     if (k % 2) {
-                        const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lc]);
+                        const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lp]);
                         d[k - 1] = x[0], u[k - 1] = x[1], d[k] = x[2], u[k] = x[3];
                     }
                 }
                 if (k == 1)
-                    step_to_lds(nt.get(g), nx.get(g), bias[g], soft, true, &s_du[buf ^ 1][token / 2][du_at + 4 * g]);
+                    step_to_lds(nt.get(g), nx.get(g), bias[g], soft, true, &s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + g)]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -332,7 +322,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p)
         Cv[i] = in ? to_f32(Ct[s * 4 + i]) : 0.f;
     }
     const float x = on ? to_f32(((const T*)a.x)[b * a.x_stride + c]) : 0.f;
-    const float d = on ? step_of(to_f32(((const T*)a.dt)[b * a.dt_stride + c]), a.dt_bias ? a.dt_bias[c] : 0.f, a.flags) : 0.f;
+    const float d = on ? step_of(to_f32(((const T*)a.dt)[b * a.dt_stride + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f), a.flags & GDR2_SCAN_SOFTPLUS) : 0.f;
     float y = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -39,25 +39,38 @@ __device__ __forceinline__ float pair_sum16(float a, float b)
     return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
 }
 
-// Sum of v[k][i] over the channels of a wave.  LPC = 4: k < 4, lanes of row
-// r = lane / 16 return token k = r.  LPC = 8: k < 8, they return tokens r and
-// r + 4.  (Rounds over lane bits 5 and 4 halve the values held; bit 3, and bit
-// 2 with four lanes a channel, are rotations within the row.)
+// Sum of v[k][i], four tokens k, over the channels of a wave: lanes of row
+// r = lane / 16 return token k = r.  (Rounds over lane bits 5 and 4 halve the
+// values held; bit 3, and bit 2 with four lanes a channel, are rotations
+// within the row.)
 template <int LPC, int NS>
-__device__ __forceinline__ void channel_sum(const float (&v)[LPC][NS], float (&r)[LPC / 4][NS])
+__device__ __forceinline__ void channel_sum(const float (&v)[4][NS], float (&r)[NS])
 {
 #pragma unroll
-    for (int g = 0; g < LPC / 4; ++g)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const float lo = pair_sum32(v[4 * g][i], v[4 * g + 2][i]), hi = pair_sum32(v[4 * g + 1][i], v[4 * g + 3][i]);
-            float x = pair_sum16(lo, hi);
-            x += dpp_move<0x128>(x);          // row_ror:8
-            if constexpr (LPC == 4)
-                x += dpp_move<0x124>(x);      // row_ror:4
-            r[g][i] = x;
-        }
+    for (int i = 0; i < NS; ++i) {
+        float x = pair_sum16(pair_sum32(v[0][i], v[2][i]), pair_sum32(v[1][i], v[3][i]));
+        x += dpp_move<0x128>(x);          // row_ror:8
+        if constexpr (LPC == 4)
+            x += dpp_move<0x124>(x);      // row_ror:4
+        r[i] = x;
+    }
 }
+
+// sum_transposed with its values arriving from k = LPC - 1 down to 0: of eight
+// values the upper four are combined with the lower ones as these come.
+template <int LPC> struct TransposedSum {
+    float q[4], up[4];
+    __device__ __forceinline__ void put(int k, float p, int s)   // k is known after unrolling
+    {
+        if (LPC == 4)
+            q[k] = p;
+        else if (k >= 4)
+            up[k - 4] = p;
+        else
+            q[k] = (s & 4 ? up[k] : p) + dpp_move<0x141>(s & 4 ? p : up[k]);
+    }
+    __device__ __forceinline__ float get(int s) const { return sum_transposed(q, s); }
+};
 
 // Floats of one segment's row of token sums (rows start on 16 bytes).
 __host__ __device__ inline int64_t sums_ld(int64_t C, int64_t N) { return (C * (N + 2) + 3) / 4 * 4; }
@@ -74,7 +87,7 @@ struct BackwardPtrs {
 //           n into the places of d x, dv, and the sums over channels | barrier
 //   rows:   dx, ddt, dz from the sums; dB, dC over the waves
 template <typename T, int LPC, int NS, bool GATE, bool WIDE>
-__global__ __launch_bounds__(64 * LPC) void scan_backward_kernel(gdr2_scan_bwd_args p, Pieces seg, uint32_t ncb, uint32_t cb_per,
+__global__ __launch_bounds__(64 * LPC, 2) void scan_backward_kernel(gdr2_scan_bwd_args p, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                                  BackwardPtrs w)
 {
     constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT, NW = NT / 64;
@@ -82,12 +95,12 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_kernel(gdr2_scan_bwd_a
     __shared__ __align__(16) float s_b[kScanChunk][NP], s_c[kScanChunk][NP];
     __shared__ __align__(16) f32x4 s_tok[kScanChunk][kScanCols];          // d, d x, dv, - and then d, du, qA, v
     __shared__ __align__(16) float s_red[2][NW][kScanChunk][NP];
-    __shared__ __align__(16) float s_h[kSubs][NT][NS];
+    __shared__ __align__(16) float s_h[kSubs - 1][NT][NS];               // before sub-chunks 1, 2, ..
     const uint32_t slot = blockIdx.x / ncb, cb = blockIdx.x - slot * ncb;
     const Piece q = uniform(piece_of(seg, slot));
     const ScanBlock blk = scan_block(a, cb, cb_per);
     const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int s = l.s, N = (int)a.N, lp = step_place(threadIdx.x / LPC), wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int64_t C = a.C, c = l.c;
     const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
     float* sums = w.sums + (int64_t)slot * sums_ld(C, N);
@@ -107,9 +120,9 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_kernel(gdr2_scan_bwd_a
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             A2[i] = A[i] * kLog2e;
-        float bias[V], skip[V];
+        float bias[V], skips[V];
         channel_params<V>(a.dt_bias, blk, bias);
-        channel_params<V>(a.skip, blk, skip);
+        channel_params<V>(a.skip, blk, skips);
         const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
         const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
         const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
@@ -154,100 +167,123 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_kernel(gdr2_scan_bwd_a
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float raw = xt.get(v) + bias[v], x = xx.get(v);
-                float d = soft ? softplus_f(raw) : raw, dv = xd.get(v);
+                float d = step_of(raw, soft), dv = xd.get(v);
                 if constexpr (GATE)
                     dv *= silu_f(xz.get(v));
                 d = in ? d : 0.f;
                 dv = in ? dv : 0.f;
-                s_tok[token][ch + v] = f32x4{d, d * x, dv, 0.f};
+                s_tok[token][step_place(ch + v)] = f32x4{d, d * x, dv, 0.f};
             }
-#pragma unroll
-            for (int i = 0; i < NS; ++i)
-                s_h[0][threadIdx.x][i] = h0[i];
             lds_barrier();
             const bool more = t > t0;
             fetch(more ? kScanChunk : 0);
+            // Tokens are read from LDS two ahead, in rings by parity; the scheduling
+            // barriers keep the compiler from gathering the reads in front of their uses.
+            f32x4 tk[2];
+            float Bq[2][NS], Cq[2][NS];
+            auto read = [&](int tt, int r) {
+                tk[r] = s_tok[tt][lp];
+                read_states<NS>(&s_b[tt][s * NS], Bq[r]);
+            };
             // the states before every kSub tokens
             {
                 float h[NS];
 #pragma unroll
                 for (int i = 0; i < NS; ++i)
                     h[i] = h0[i];
+                read(0, 0);
+                read(1, 1);
 #pragma unroll 1
                 for (int b = 0; b < kSubs - 1; ++b) {
 #pragma unroll
                     for (int k = 0; k < kSub; ++k) {
-                        const f32x4 tk = s_tok[b * kSub + k][lc];
-                        float B[NS];
-                        read_states<NS>(&s_b[b * kSub + k][s * NS], B);
 #pragma unroll
                         for (int i = 0; i < NS; ++i)
-                            h[i] = fmaf(fast_exp2(tk[0] * A2[i]), h[i], tk[1] * B[i]);
+                            h[i] = fmaf(fast_exp2(tk[k & 1][0] * A2[i]), h[i], tk[k & 1][1] * Bq[k & 1][i]);
+                        read(b * kSub + k + 2, k & 1);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
 #pragma unroll
                     for (int i = 0; i < NS; ++i)
-                        s_h[b + 1][threadIdx.x][i] = h[i];
+                        s_h[b][threadIdx.x][i] = h[i];
                 }
             }
+            // (the rings now hold the last sub-chunk's first two tokens)
 #pragma unroll 1
             for (int b = kSubs - 1; b >= 0; --b) {
+                const int first = b * kSub, before = b > 0 ? first - kSub : 0;
                 float av[kSub][NS], hv[kSub + 1][NS];
-                read_states<NS>(&s_h[b][threadIdx.x][0], hv[0]);
+                if (b > 0) {
+                    read_states<NS>(&s_h[b - 1][threadIdx.x][0], hv[0]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i)
+                        hv[0][i] = h0[i];
+                }
 #pragma unroll
                 for (int k = 0; k < kSub; ++k) {
-                    const f32x4 tk = s_tok[b * kSub + k][lc];
-                    float B[NS];
-                    read_states<NS>(&s_b[b * kSub + k][s * NS], B);
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
-                        av[k][i] = fast_exp2(tk[0] * A2[i]);
-                        hv[k + 1][i] = fmaf(av[k][i], hv[k][i], tk[1] * B[i]);
+                        av[k][i] = fast_exp2(tk[k & 1][0] * A2[i]);
+                        hv[k + 1][i] = fmaf(av[k][i], hv[k][i], tk[k & 1][1] * Bq[k & 1][i]);
                     }
+                    if (k + 2 < kSub)
+                        read(first + k + 2, k & 1);
+                    else
+                        read_states<NS>(&s_c[first + k][s * NS], Cq[k & 1]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
                 for (int g = kSub / LPC - 1; g >= 0; --g) {
-                    float pu[LPC], pa[LPC], pv[LPC], vb[LPC][NS], vc[LPC][NS];
+                    TransposedSum<LPC> su, sa, sv;
+                    float vb[4][NS], vc[4][NS];
 #pragma unroll
                     for (int k = LPC - 1; k >= 0; --k) {
-                        const int kk = g * LPC + k;
-                        const f32x4 tk = s_tok[b * kSub + kk][lc];
-                        float B[NS], Cn[NS];
-                        read_states<NS>(&s_b[b * kSub + kk][s * NS], B);
-                        read_states<NS>(&s_c[b * kSub + kk][s * NS], Cn);
+                        const int kk = g * LPC + k, r = kk & 1;
+                        float pu = 0.f, pa = 0.f, pv = 0.f;
 #pragma unroll
                         for (int i = 0; i < NS; ++i) {
-                            const float gr = fmaf(Cn[i], tk[2], lam[i]);
-                            vc[k][i] = tk[2] * hv[kk + 1][i];
-                            vb[k][i] = gr * tk[1];
+                            const float gr = fmaf(Cq[r][i], tk[r][2], lam[i]);
+                            vc[k % 4][i] = tk[r][2] * hv[kk + 1][i];
+                            vb[k % 4][i] = gr * tk[r][1];
                             lam[i] = gr * av[kk][i];
                             const float qq = lam[i] * hv[kk][i];
-                            dA[i] = fmaf(qq, tk[0], dA[i]);
-                            pu[k] = i == 0 ? gr * B[0] : fmaf(gr, B[i], pu[k]);
-                            pa[k] = i == 0 ? qq * A[0] : fmaf(qq, A[i], pa[k]);
+                            dA[i] = fmaf(qq, tk[r][0], dA[i]);
+                            pu = i == 0 ? gr * Bq[r][0] : fmaf(gr, Bq[r][i], pu);
+                            pa = i == 0 ? qq * A[0] : fmaf(qq, A[i], pa);
                             if constexpr (GATE)
-                                pv[k] = i == 0 ? Cn[0] * hv[kk + 1][0] : fmaf(Cn[i], hv[kk + 1][i], pv[k]);
+                                pv = i == 0 ? Cq[r][0] * hv[kk + 1][0] : fmaf(Cq[r][i], hv[kk + 1][i], pv);
                         }
-                    }
-                    // lane s: token s of the group
-                    float* at = (float*)&s_tok[b * kSub + g * LPC + s][lc];
-                    at[1] = sum_transposed(pu, s);
-                    at[2] = sum_transposed(pa, s);
-                    if constexpr (GATE)
-                        at[3] = sum_transposed(pv, s);
-                    float rbs[LPC / 4][NS], rcs[LPC / 4][NS];
-                    channel_sum<LPC, NS>(vb, rbs);
-                    channel_sum<LPC, NS>(vc, rcs);
-                    if ((lane & 15) < LPC) {
-#pragma unroll
-                        for (int e = 0; e < LPC / 4; ++e) {
-                            const int r = b * kSub + g * LPC + 4 * e + (lane >> 4);
+                        if (kk >= 2) {
+                            read(first + kk - 2, r);
+                            read_states<NS>(&s_c[first + kk - 2][s * NS], Cq[r]);
+                        } else {
+                            read(before + kk, r);
+                        }
+                        su.put(k, pu, s);
+                        sa.put(k, pa, s);
+                        if constexpr (GATE)
+                            sv.put(k, pv, s);
+                        if (k % 4 == 0) {
+                            float xb[NS], xc[NS];
+                            channel_sum<LPC, NS>(vb, xb);
+                            channel_sum<LPC, NS>(vc, xc);
+                            // (the lanes of a row that share s hold and write the same value)
+                            const int at = first + kk + (lane >> 4);
 #pragma unroll
                             for (int i = 0; i < NS; ++i) {
-                                s_red[0][wave][r][s * NS + i] = rbs[e][i];
-                                s_red[1][wave][r][s * NS + i] = rcs[e][i];
+                                s_red[0][wave][at][s * NS + i] = xb[i];
+                                s_red[1][wave][at][s * NS + i] = xc[i];
                             }
                         }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
+                    // lane s: token s of the group, whose values every lane has read
+                    float* at = (float*)&s_tok[first + g * LPC + s][lp];
+                    at[1] = su.get(s);
+                    at[2] = sa.get(s);
+                    if constexpr (GATE)
+                        at[3] = sv.get(s);
                 }
             }
             if (more)
@@ -256,17 +292,17 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_kernel(gdr2_scan_bwd_a
             float dx[V], ddt[V], dz[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const f32x4 tk = s_tok[token][ch + v];
-                const float x = xx.get(v), dy = xd.get(v), raw = xt.get(v) + bias[v];
+                const f32x4 tk = s_tok[token][step_place(ch + v)];
+                const float x = xx.get(v), dy = xd.get(v), raw = xt.get(v) + bias[v], skip = skips[v];
                 float dv = dy;
                 if constexpr (GATE) {
                     const float z = xz.get(v), sg = sigmoid_f(z);
                     dv = dy * z * sg;
-                    dz[v] = dy * fmaf(skip[v], x, tk[3]) * (sg * fmaf(z, 1.f - sg, 1.f));
+                    dz[v] = dy * fmaf(skip, x, tk[3]) * (sg * fmaf(z, 1.f - sg, 1.f));
                 }
                 float dd = fmaf(x, tk[1], tk[2]);
                 dd = soft ? dd * sigmoid_f(raw) : dd;
-                dx[v] = fmaf(tk[0], tk[1], skip[v] * dv);
+                dx[v] = fmaf(tk[0], tk[1], skip * dv);
                 ddt[v] = dd;
                 // (rows past the sequence read as zero, and so add nothing: dv = x = 0,
                 // and dd is qA = 0 for d = 0 times a state that nothing changed)
@@ -333,7 +369,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_span_kernel(gdr2_scan_
         return;
     const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
     const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC;
+    const int s = l.s, N = (int)a.N, lp = step_place(threadIdx.x / LPC);
     const int64_t C = a.C, c = l.c;
     float A2[NS], lam[NS] = {}, sum = 0.f;
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
@@ -372,19 +408,19 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_span_kernel(gdr2_scan_
         for (int v = 0; v < V; ++v) {
             typedef float Two __attribute__((ext_vector_type(2)));
             const float raw = rt.get(v) + bias[v];
-            float d = soft ? softplus_f(raw) : raw, dv = rd.get(v);
+            float d = step_of(raw, soft), dv = rd.get(v);
             if constexpr (GATE)
                 dv *= silu_f(rz.get(v));
             d = token < left ? d : 0.f;
             dv = token < left ? dv : 0.f;
-            *reinterpret_cast<Two*>(&s_du[buf][token / 2][4 * (ch + v) + 2 * (token & 1)]) = Two{d, dv};
+            *reinterpret_cast<Two*>(&s_du[buf][token / 2][4 * step_place(ch + v) + 2 * (token & 1)]) = Two{d, dv};
         }
         left = kScanChunk;
         fetch(t > t0 ? kScanChunk : 0);
         lds_barrier();
 #pragma unroll
         for (int tt = kScanChunk - 2; tt >= 0; tt -= 2) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][tt / 2][4 * lc]);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][tt / 2][4 * lp]);
             sum += x[0] + x[2];
             float C0[NS], C1[NS];
             read_states<NS>(&s_c[buf][tt][s * NS], C0);
