@@ -214,4 +214,42 @@ __device__ __forceinline__ float silu_slope_f(float x)
     return s * (1.f + x * (1.f - s));
 }
 
+// ---- sums over lanes -------------------------------------------------------
+template <int CTRL> __device__ __forceinline__ float dpp_move(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
+// Lanes of the lower half (even rows) return the sum of a over the lane pair,
+// the others that of b: one v_permlane*_swap and one add for two values.
+__device__ __forceinline__ float pair_sum32(float a, float b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float pair_sum16(float a, float b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Sum over aligned groups of W lanes (8 .. 64), in every lane: within a row of
+// 16 by DPP (quads, then the mirrored half row and row: both partners hold
+// their half's sum), across rows by a lane swap of the value with itself.
+template <int W> __device__ __forceinline__ float lanes_sum(float v)
+{
+    v += dpp_quad_xor<1>(v);
+    v += dpp_quad_xor<2>(v);
+    v += dpp_move<0x141>(v);       // row_half_mirror
+    if constexpr (W >= 16)
+        v += dpp_move<0x140>(v);   // row_mirror
+    if constexpr (W >= 32)
+        v = pair_sum16(v, v);
+    if constexpr (W >= 64)
+        v = pair_sum32(v, v);
+    return v;
+}
+
 }  // namespace gdr2

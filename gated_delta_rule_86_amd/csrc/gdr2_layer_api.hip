@@ -247,7 +247,7 @@ gdr2_status check_scan(const gdr2_scan_args& a)
     GDR2_TRY(check_stride("c_stride", a.c_stride, a.G * a.N));
     const int64_t rows = a.offsets ? a.T : mul(a.B, a.T);
     if (a.B > ((int64_t)1 << 31) || a.T > ((int64_t)1 << 40) || rows > ((int64_t)1 << 40) ||
-        mul(mul(a.B, a.C), 32) >= gdr2::kMaxGroups * 256 || mul(rows, 2 * a.G * a.N) >= gdr2::kMaxGroups * 256 || gdr2::scan_launch_groups(a) >= gdr2::kMaxGroups)
+        mul(a.B, a.C * 32 + 256) >= gdr2::kMaxGroups * 256 || mul(rows, 2 * a.G * a.N) >= gdr2::kMaxGroups * 256 || gdr2::scan_launch_groups(a) >= gdr2::kMaxGroups)
         return too_many();
     return GDR2_OK;
 }

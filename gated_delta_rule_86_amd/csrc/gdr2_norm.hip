@@ -10,27 +10,32 @@
 // Memory bounds both.  A row is held in registers by a group of LPR lanes
 // (8 .. 64 of a wave, or a whole workgroup of 256), NV vectors of V elements
 // each, so it is read once; mean and variance are two passes over those
-// registers (no E[x^2] - m^2 cancellation), sums in fp32.
+// registers (no E[x^2] - m^2 cancellation), sums in fp32.  A group keeps its
+// share of the weights in registers and walks rows g, g + groups, ..., with the
+// next row's loads in flight while it works on one.
 #include "gdr2_layer.h"
 
 namespace gdr2 {
 
 namespace {
 
+// Workgroup of a kernel whose groups have LPR lanes.
+template <int LPR> constexpr int kThreads = LPR > 256 ? LPR : 256;
+
 // Sum over the LPR lanes that hold one row; every lane gets it.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v, float* s_part)
 {
-    constexpr int W = LPR < 64 ? LPR : 64;
-#pragma unroll
-    for (int off = W / 2; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off);
+    v = lanes_sum<(LPR < 64 ? LPR : 64)>(v);
     if constexpr (LPR > 64) {
         __syncthreads();                       // the previous sum has been read
         if ((threadIdx.x & 63) == 0)
             s_part[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
+        v = s_part[0];
+#pragma unroll
+        for (int k = 1; k < LPR / 64; ++k)
+            v += s_part[k];
     }
     return v;
 }
@@ -39,23 +44,39 @@ __device__ __forceinline__ float row_sum(float v, float* s_part)
 template <int LPR>
 __device__ __forceinline__ void row_sum2(float& a, float& b, float* s_part)
 {
-    constexpr int W = LPR < 64 ? LPR : 64;
-#pragma unroll
-    for (int off = W / 2; off >= 1; off >>= 1) {
-        a += __shfl_xor(a, off);
-        b += __shfl_xor(b, off);
-    }
+    a = lanes_sum<(LPR < 64 ? LPR : 64)>(a);
+    b = lanes_sum<(LPR < 64 ? LPR : 64)>(b);
     if constexpr (LPR > 64) {
+        constexpr int W = LPR / 64;
         __syncthreads();
         if ((threadIdx.x & 63) == 0) {
             s_part[threadIdx.x >> 6] = a;
-            s_part[4 + (threadIdx.x >> 6)] = b;
+            s_part[W + (threadIdx.x >> 6)] = b;
         }
         __syncthreads();
-        a = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
-        b = (s_part[4] + s_part[5]) + (s_part[6] + s_part[7]);
+        a = s_part[0];
+        b = s_part[W];
+#pragma unroll
+        for (int k = 1; k < W; ++k) {
+            a += s_part[k];
+            b += s_part[W + k];
+        }
     }
 }
+
+// A group's share of one row array, unconverted; nothing is read past C or R.
+template <typename T, int V, int LPR, int NV> struct RowRegs {
+    typename Raw<T, V>::Type raw[NV];
+    __device__ __forceinline__ void load(const void* base, int64_t row, int64_t stride, int64_t C, int lane, bool on)
+    {
+        const T* p = (const T*)base + row * stride;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int64_t c = ((int64_t)j * LPR + lane) * V;
+            raw[j] = on && c < C ? Raw<T, V>::load(p + c) : Raw<T, V>::zero();
+        }
+    }
+};
 
 // Mean (0 for rms) and 1/rms of the row in x (elements past C are zero and
 // `in` is false for their vectors).
@@ -85,47 +106,62 @@ __device__ __forceinline__ void row_stats(const float (&x)[NV][V], const bool (&
     rstd = 1.f / sqrtf(row_sum<LPR>(ss, s_part) * inv + eps);
 }
 
-template <typename T, int V, int LPR, int NV>
+template <int V, int LPR, int NV>
+__device__ __forceinline__ void group_params(const float* p, float without, int64_t C, int lane, float (&out)[NV][V])
+{
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int64_t c = ((int64_t)j * LPR + lane) * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            out[j][v] = p && c < C ? p[c + v] : without;
+    }
+}
+
+template <typename T, int V, int LPR, int NV, bool GATE>
 __global__ __launch_bounds__(256) void norm_forward_kernel(gdr2_norm_args a)
 {
     __shared__ float s_part[8];
     constexpr int RPB = 256 / LPR;
     const int lane = threadIdx.x % LPR;
-    const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-    if (row >= a.R)                            // whole groups of lanes; LPR = 256 has one row
-        return;
-    const T* x = (const T*)a.x + row * a.x_stride;
-    float xv[NV][V];
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    float w[NV][V], b[NV][V];
     bool in[NV];
+    group_params<V, LPR, NV>(a.weight, 1.f, a.C, lane, w);
+    group_params<V, LPR, NV>(a.bias, 0.f, a.C, lane, b);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int64_t c = ((int64_t)j * LPR + lane) * V;
-        in[j] = c < a.C;
-        if (in[j])
-            load_row<V>(x + c, xv[j]);
-        else
+    for (int j = 0; j < NV; ++j)
+        in[j] = ((int64_t)j * LPR + lane) * V < a.C;
+    int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+    RowRegs<T, V, LPR, NV> nx, nz;
+    nx.load(a.x, row, a.x_stride, a.C, lane, row < a.R);
+    if constexpr (GATE)
+        nz.load(a.z, row, a.z_stride, a.C, lane, row < a.R);
+    for (; row < a.R; row += step) {          // LPR = 256: the same rows in every lane
+        const RowRegs<T, V, LPR, NV> cx = nx, cz = nz;
+        nx.load(a.x, row + step, a.x_stride, a.C, lane, row + step < a.R);
+        if constexpr (GATE)
+            nz.load(a.z, row + step, a.z_stride, a.C, lane, row + step < a.R);
+        float x[NV][V], mean, rstd;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                xv[j][v] = 0.f;
-    }
-    float mean, rstd;
-    row_stats<LPR, V, NV>(xv, in, a.C, a.kind, a.eps, s_part, mean, rstd);
+        for (int j = 0; j < NV; ++j)
+            Raw<T, V>::get(cx.raw[j], x[j]);
+        row_stats<LPR, V, NV>(x, in, a.C, a.kind, a.eps, s_part, mean, rstd);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        if (!in[j])
-            continue;
-        const int64_t c = ((int64_t)j * LPR + lane) * V;
-        float o[V], z[V];
-        if (a.z)
-            load_row<V>((const T*)a.z + row * a.z_stride + c, z);
+        for (int j = 0; j < NV; ++j) {
+            if (!in[j])
+                continue;
+            float o[V], z[V];
+            if constexpr (GATE)
+                Raw<T, V>::get(cz.raw[j], z);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float w = a.weight ? a.weight[c + v] : 1.f, b = a.bias ? a.bias[c + v] : 0.f;
-            o[v] = fmaf((xv[j][v] - mean) * rstd, w, b);
-            if (a.z)
-                o[v] *= silu_f(z[v]);
+            for (int v = 0; v < V; ++v) {
+                o[v] = fmaf((x[j][v] - mean) * rstd, w[j][v], b[j][v]);
+                if constexpr (GATE)
+                    o[v] *= silu_f(z[v]);
+            }
+            store_row<V>((T*)a.y + row * a.C + ((int64_t)j * LPR + lane) * V, o);
         }
-        store_row<V>((T*)a.y + row * a.C + c, o);
     }
 }
 
@@ -169,41 +205,48 @@ __global__ __launch_bounds__(256) void norm_forward_long_kernel(gdr2_norm_args a
     }
 }
 
-// Every group of LPR lanes walks rows g, g + groups, ...; its sums of dweight
-// and dbias stay in registers, are added over the workgroup's groups in LDS
-// (in group order), and leave as one row [2][C] of partial sums.
-template <typename T, int V, int LPR, int NV>
-__global__ __launch_bounds__(256) void norm_backward_kernel(gdr2_norm_bwd_args p, float* part)
+// A group's sums of dweight and dbias stay in registers, are added over the
+// workgroup's groups in LDS (in group order), and leave as one row [2][C] of
+// partial sums.
+template <typename T, int V, int LPR, int NV, bool GATE>
+__global__ __launch_bounds__(kThreads<LPR>, 2) void norm_backward_kernel(gdr2_norm_bwd_args p, float* part)
 {
     const gdr2_norm_args& a = p.f;
-    __shared__ float s_part[8];
-    constexpr int RPB = 256 / LPR;
+    __shared__ float s_part[16];
+    constexpr int RPB = kThreads<LPR> / LPR;
     __shared__ float s_red[RPB > 1 ? 256 * NV * V : 1];
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR;
+    const int64_t step = (int64_t)gridDim.x * RPB;
     const float inv = 1.f / (float)a.C;
-    float dw[NV][V] = {}, db[NV][V] = {};
+    // the weights stay in registers where they fit beside the sums and the loads
+    constexpr bool HOLD = NV * V <= 16 || !GATE;
+    float dw[NV][V] = {}, db[NV][V] = {}, wr[HOLD ? NV : 1][V];
     bool in[NV];
+    if constexpr (HOLD)
+        group_params<V, LPR, NV>(a.weight, 1.f, a.C, lane, wr);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         in[j] = ((int64_t)j * LPR + lane) * V < a.C;
-    for (int64_t row = (int64_t)blockIdx.x * RPB + grp; row < a.R; row += (int64_t)gridDim.x * RPB) {
-        const T* x = (const T*)a.x + row * a.x_stride;
-        const T* dy = (const T*)p.dy + row * a.C;
-        float xv[NV][V], dv[NV][V];
+    int64_t row = (int64_t)blockIdx.x * RPB + grp;
+    RowRegs<T, V, LPR, NV> nx, nd, nz;
+    auto fetch = [&](int64_t r) {
+        nx.load(a.x, r, a.x_stride, a.C, lane, r < a.R);
+        nd.load(p.dy, r, a.C, a.C, lane, r < a.R);
+        if constexpr (GATE)
+            nz.load(a.z, r, a.z_stride, a.C, lane, r < a.R);
+    };
+    fetch(row);
+    for (; row < a.R; row += step) {
+        float x[NV][V], g[NV][V];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t c = ((int64_t)j * LPR + lane) * V;
-            if (in[j]) {
-                load_row<V>(x + c, xv[j]);
-                load_row<V>(dy + c, dv[j]);
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    xv[j][v] = dv[j][v] = 0.f;
-            }
+            Raw<T, V>::get(nx.raw[j], x[j]);
+            Raw<T, V>::get(nd.raw[j], g[j]);
         }
+        const RowRegs<T, V, LPR, NV> cz = nz;
+        fetch(row + step);
         float mean, rstd;
-        row_stats<LPR, V, NV>(xv, in, a.C, a.kind, a.eps, s_part, mean, rstd);
+        row_stats<LPR, V, NV>(x, in, a.C, a.kind, a.eps, s_part, mean, rstd);
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -211,27 +254,27 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(gdr2_norm_bwd_args p
                 continue;
             const int64_t c = ((int64_t)j * LPR + lane) * V;
             float z[V], dz[V];
-            if (a.z)
-                load_row<V>((const T*)a.z + row * a.z_stride + c, z);
+            if constexpr (GATE)
+                Raw<T, V>::get(cz.raw[j], z);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float w = a.weight ? a.weight[c + v] : 1.f;
-                const float xh = (xv[j][v] - mean) * rstd;
-                float dn = dv[j][v];
-                if (a.z) {
-                    const float b = a.bias ? a.bias[c + v] : 0.f;
-                    dz[v] = dn * fmaf(xh, w, b) * silu_slope_f(z[v]);
-                    dn *= silu_f(z[v]);
+                const float xh = (x[j][v] - mean) * rstd;
+                const float w = HOLD ? wr[HOLD ? j : 0][v] : a.weight ? a.weight[c + v] : 1.f;
+                float dn = g[j][v];
+                if constexpr (GATE) {
+                    const float b = a.bias ? a.bias[c + v] : 0.f, sg = sigmoid_f(z[v]);
+                    dz[v] = dn * fmaf(xh, w, b) * (sg * fmaf(z[v], 1.f - sg, 1.f));
+                    dn *= z[v] * sg;
                 }
                 dw[j][v] = fmaf(dn, xh, dw[j][v]);
                 db[j][v] += dn;
-                const float g = dn * w;
-                s1 += g;
-                s2 = fmaf(g, xh, s2);
-                xv[j][v] = xh;
-                dv[j][v] = g;
+                const float e = dn * w;
+                s1 += e;
+                s2 = fmaf(e, xh, s2);
+                x[j][v] = xh;
+                g[j][v] = e;
             }
-            if (a.z)
+            if constexpr (GATE)
                 store_row<V>((T*)p.dz + row * a.C + c, dz);
         }
         row_sum2<LPR>(s1, s2, s_part);
@@ -243,7 +286,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(gdr2_norm_bwd_args p
             float o[V];
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                o[v] = rstd * (dv[j][v] - m1 - xv[j][v] * m2);
+                o[v] = rstd * (g[j][v] - m1 - x[j][v] * m2);
             store_row<V>((T*)p.dx + row * a.C + ((int64_t)j * LPR + lane) * V, o);
         }
     }
@@ -348,31 +391,35 @@ __global__ __launch_bounds__(256) void norm_backward_columns_kernel(gdr2_norm_bw
 }
 
 // ---- variants --------------------------------------------------------------
-// The narrowest group of lanes whose registers hold the row: a wave (or part
-// of one) up to 32 elements a lane, then a workgroup up to 64 forwards and 32
-// backwards (which also holds dy, dweight and dbias), then passes.
+// The narrowest group of lanes whose registers hold the row: a wave, or part
+// of one, while a lane has at most 32 elements; backwards, where a lane also
+// holds dy, dweight, dbias and the next row's loads, 32 in bf16 without a gate
+// and 16 otherwise.  Then a workgroup of 256 with up to 64 elements a lane
+// forwards and 16 backwards, backwards one of 512, then passes over the row.
+// (More elements backwards spill: 8192 columns on 256 lanes kept 130 to 1200
+// bytes a lane in scratch.)
 struct Shape {
     int lpr, nv;   // lpr == 0: passes
 };
 
-Shape shape_of(int64_t C, int V, bool backward)
+Shape shape_of(int64_t C, int V, bool backward, bool gate)
 {
     const int64_t nvec = (C + V - 1) / V;
     for (int lpr = 8; lpr <= 64; lpr *= 2)
         if (nvec <= lpr)
             return {lpr, 1};
-    const int most = backward ? 32 / V : 64 / V;
-    for (int nv = 2; nv * V <= 32; nv *= 2) {
-        // V = 1 keeps a wave to 8 loads before it takes a workgroup
-        if ((V > 1 || nv <= 8) && nvec <= 64 * nv)
+    const int wave = V == 1 ? 8 : backward && (V == 4 || gate) ? 16 / V : 32 / V;
+    for (int nv = 2; nv <= wave; nv *= 2)
+        if (nvec <= 64 * nv)
             return {64, nv};
-    }
-    for (int nv = 1; nv <= most && nv <= 32; nv *= 2)
+    const int most = backward ? 16 / V : V == 1 ? 32 : 64 / V;
+    for (int nv = 1; nv <= most; nv *= 2)
         if (nvec <= 256 * nv)
             return {256, nv};
+    if (backward && nvec <= 512 * most)
+        return {512, most};
     return {0, 0};
 }
-
 
 #define GDR2_NORM_CASE(L, N)                                                                     \
     if (s.lpr == L && s.nv == N) {                                                               \
@@ -385,34 +432,59 @@ template <typename T, int V> struct ForwardLaunch {
     hipStream_t stream;
     template <int L, int N> void operator()() const
     {
-        hipLaunchKernelGGL((norm_forward_kernel<T, V, L, N>), dim3((unsigned)ceil_div(a.R, 256 / L)), dim3(256), 0, stream, a);
+        // eight workgroups per compute unit, then the rows are walked
+        const dim3 grid((unsigned)min(ceil_div(a.R, 256 / L), (int64_t)device_cu_count() * 8));
+        if (a.z)
+            hipLaunchKernelGGL((norm_forward_kernel<T, V, L, N, true>), grid, dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((norm_forward_kernel<T, V, L, N, false>), grid, dim3(256), 0, stream, a);
     }
 };
 
-template <typename T, int V> struct BackwardLaunch {
+template <typename T, int V, bool GATE> struct BackwardLaunch {
     const gdr2_norm_bwd_args& p;
     float* part;
     int64_t groups;
     hipStream_t stream;
     template <int L, int N> void operator()() const
     {
-        if constexpr (N * V <= 32)
-            hipLaunchKernelGGL((norm_backward_kernel<T, V, L, N>), dim3((unsigned)groups), dim3(256), 0, stream, p, part);
+        hipLaunchKernelGGL((norm_backward_kernel<T, V, L, N, GATE>), dim3((unsigned)groups), dim3(kThreads<L>), 0, stream, p,
+                           part);
     }
 };
 
-// Exactly the shapes shape_of can return for V.
-template <int V, typename F> hipError_t dispatch(const Shape& s, const F& f)
+// Exactly the shapes shape_of can return for V forwards ..
+template <int V, typename F> hipError_t dispatch_forward(const Shape& s, const F& f)
 {
     GDR2_NORM_CASE(8, 1) GDR2_NORM_CASE(16, 1) GDR2_NORM_CASE(32, 1) GDR2_NORM_CASE(64, 1)
-    GDR2_NORM_CASE(64, 2) GDR2_NORM_CASE(64, 4)
+    GDR2_NORM_CASE(64, 2) GDR2_NORM_CASE(64, 4) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(256, 8)
     if constexpr (V == 8) {
-        GDR2_NORM_CASE(256, 2) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(256, 8)
+        GDR2_NORM_CASE(256, 2)
     } else {
-        GDR2_NORM_CASE(64, 8) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(256, 8) GDR2_NORM_CASE(256, 16)
+        GDR2_NORM_CASE(64, 8) GDR2_NORM_CASE(256, 16)
     }
     if constexpr (V == 1) {
         GDR2_NORM_CASE(256, 32)
+    }
+    return hipErrorInvalidValue;
+}
+
+// .. and backwards.
+template <int V, bool GATE, typename F> hipError_t dispatch_backward(const Shape& s, const F& f)
+{
+    GDR2_NORM_CASE(8, 1) GDR2_NORM_CASE(16, 1) GDR2_NORM_CASE(32, 1) GDR2_NORM_CASE(64, 1) GDR2_NORM_CASE(64, 2)
+    if constexpr (V == 8) {
+        if constexpr (GATE) {
+            GDR2_NORM_CASE(256, 1)
+        } else {
+            GDR2_NORM_CASE(64, 4)
+        }
+        GDR2_NORM_CASE(256, 2) GDR2_NORM_CASE(512, 2)
+    } else if constexpr (V == 4) {
+        GDR2_NORM_CASE(64, 4) GDR2_NORM_CASE(256, 2) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(512, 4)
+    } else {
+        GDR2_NORM_CASE(64, 4) GDR2_NORM_CASE(64, 8) GDR2_NORM_CASE(256, 4) GDR2_NORM_CASE(256, 8) GDR2_NORM_CASE(256, 16)
+        GDR2_NORM_CASE(512, 16)
     }
     return hipErrorInvalidValue;
 }
@@ -426,19 +498,19 @@ bool norm_vec(const gdr2_norm_args& a)
 template <typename T, int V>
 hipError_t forward_v(const gdr2_norm_args& a, hipStream_t stream)
 {
-    const Shape s = shape_of(a.C, V, false);
+    const Shape s = shape_of(a.C, V, false, a.z);
     if (s.lpr == 0) {
         hipLaunchKernelGGL((norm_forward_long_kernel<T>), dim3((unsigned)a.R), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
-    return dispatch<V>(s, ForwardLaunch<T, V>{a, stream});
+    return dispatch_forward<V>(s, ForwardLaunch<T, V>{a, stream});
 }
 
 // Workgroups of the backward: two per compute unit, fewer when there are
 // fewer rows.
 int64_t backward_groups(int64_t R, const Shape& s)
 {
-    return min(ceil_div(R, 256 / s.lpr), (int64_t)device_cu_count() * 2);
+    return min(ceil_div(R, max(1, 256 / s.lpr)), (int64_t)device_cu_count() * 2);
 }
 
 int64_t long_row_blocks(int64_t R, int64_t C)
@@ -450,7 +522,7 @@ template <typename T, int V>
 hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
 {
     const gdr2_norm_args& a = p.f;
-    const Shape s = shape_of(a.C, V, true);
+    const Shape s = shape_of(a.C, V, true, a.z);
     const bool sums = p.dweight || p.dbias;
     float* part = (float*)p.workspace;
     int64_t P = 0;
@@ -458,7 +530,9 @@ hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
         // nothing but the sums' zeros to write
     } else if (s.lpr != 0) {
         P = backward_groups(a.R, s);
-        const hipError_t e = dispatch<V>(s, BackwardLaunch<T, V>{p, sums ? part : nullptr, P, stream});
+        float* to = sums ? part : nullptr;
+        const hipError_t e = a.z ? dispatch_backward<V, true>(s, BackwardLaunch<T, V, true>{p, to, P, stream})
+                                 : dispatch_backward<V, false>(s, BackwardLaunch<T, V, false>{p, to, P, stream});
         if (e != hipSuccess || !sums)
             return e;
     } else {
@@ -483,8 +557,8 @@ hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
 // Workgroups of the forward's launch (the backward's rows take at most as many).
 int64_t norm_launch_groups(const gdr2_norm_args& a)
 {
-    const Shape s = shape_of(a.C, norm_vec(a) ? (a.dtype == GDR2_BF16 ? 8 : 4) : 1, true);
-    return s.lpr ? ceil_div(a.R, 256 / s.lpr) : a.R;
+    const Shape s = shape_of(a.C, norm_vec(a) ? (a.dtype == GDR2_BF16 ? 8 : 4) : 1, true, a.z);
+    return s.lpr ? ceil_div(a.R, max(1, 256 / s.lpr)) : a.R;
 }
 
 hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream)
@@ -501,7 +575,7 @@ size_t norm_backward_workspace_bytes(const gdr2_norm_bwd_args& p)
     const gdr2_norm_args& a = p.f;
     int64_t floats = 0;
     for (int V : {1, a.dtype == GDR2_BF16 ? 8 : 4}) {
-        const Shape s = shape_of(a.C, V, true);
+        const Shape s = shape_of(a.C, V, true, a.z);
         floats = max(floats, s.lpr ? backward_groups(a.R, s) * 2 * a.C : 2 * a.R + long_row_blocks(a.R, a.C) * 2 * a.C);
     }
     return (size_t)floats * sizeof(float);

@@ -43,11 +43,6 @@ __device__ __forceinline__ float softplus_f(float x)
     return fmaxf(x, 0.f) + fmaf(kLn2, __builtin_amdgcn_logf(w), u - (w - 1.f));
 }
 
-template <int CTRL> __device__ __forceinline__ float dpp_move(float v)
-{
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
-}
-
 // p[k] of the LPC lanes of a channel: lane s returns the sum of p[s].  Each
 // round adds half of the values to the partner that keeps the other half.
 __device__ __forceinline__ float sum_transposed(const float (&p)[4], int s)

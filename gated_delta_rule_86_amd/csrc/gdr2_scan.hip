@@ -298,46 +298,77 @@ __global__ __launch_bounds__(256) void scan_fold_kernel(gdr2_scan_args a, Pieces
     }
 }
 
-// One token.  LPC lanes per channel, four states each.
-template <typename T, int LPC>
-__global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p)
+// One token.  LPC lanes per channel, four states each; a thread keeps its
+// channel's A and parameters over R sequences, whose states are all requested
+// before the first is used.  The states' traffic bounds it.
+template <typename T, int LPC, int R, bool VEC>
+__global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p, uint32_t lanes)
 {
     const gdr2_scan_args& a = p.s;
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t bc = item / LPC;
-    const int s = threadIdx.x % LPC;
-    const bool on = bc < a.B * a.C;
-    const int64_t b = on ? bc / a.C : 0, c = on ? bc - b * a.C : 0;
-    const int64_t N = a.N, j = c / (a.C / a.G);
-    float* st = p.state + (b * a.C + c) * N;
-    float h[4], A[4], Bv[4], Cv[4];
-    load_states<4>(st, s, N, on, h);
-    load_states<4>(a.A + c * N, s, N, on, A);
-    const T* Bt = (const T*)a.Bt + b * a.b_stride + j * N;
-    const T* Ct = (const T*)a.Ct + b * a.c_stride + j * N;
+    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+    const uint32_t rb = item / lanes, cs = item - rb * lanes;         // lanes = C * LPC rounded up to 256
+    const int64_t c = cs / LPC, C = a.C, b0 = (int64_t)rb * R;
+    if (b0 >= a.B)
+        return;                                                       // a whole workgroup
+    const int s = threadIdx.x % LPC, N = (int)a.N;
+    const bool on = c < C;
+    const uint32_t j = on ? (uint32_t)c / (uint32_t)(C / a.G) : 0;
+    const int64_t cc = on ? c : 0;
+    const T* Bt = (const T*)a.Bt + b0 * a.b_stride + j * N;
+    const T* Ct = (const T*)a.Ct + b0 * a.c_stride + j * N;
+    float h[R][4], A[4], Bv[R][4], Cv[R][4], x[R], dt[R], z[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool in = on && s * 4 + i < N;
-        Bv[i] = in ? to_f32(Bt[s * 4 + i]) : 0.f;
-        Cv[i] = in ? to_f32(Ct[s * 4 + i]) : 0.f;
+    for (int r = 0; r < R; ++r) {
+        const bool in = on && b0 + r < a.B;
+        load_states<4>(p.state + ((b0 + r) * C + cc) * N, s, N, in, h[r]);
+        x[r] = in ? to_f32(((const T*)a.x)[(b0 + r) * a.x_stride + c]) : 0.f;
+        dt[r] = in ? to_f32(((const T*)a.dt)[(b0 + r) * a.dt_stride + c]) : 0.f;
+        z[r] = in && a.z ? to_f32(((const T*)a.z)[(b0 + r) * a.z_stride + c]) : 0.f;
+        if constexpr (VEC) {
+            const bool q = in && s * 4 < N;
+            const f32x4 bv = q ? load4(Bt + r * a.b_stride + s * 4) : f32x4{}, cv = q ? load4(Ct + r * a.c_stride + s * 4) : f32x4{};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                Bv[r][i] = bv[i];
+                Cv[r][i] = cv[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool q = in && s * 4 + i < N;
+                Bv[r][i] = q ? to_f32(Bt[r * a.b_stride + s * 4 + i]) : 0.f;
+                Cv[r][i] = q ? to_f32(Ct[r * a.c_stride + s * 4 + i]) : 0.f;
+            }
+        }
     }
-    const float x = on ? to_f32(((const T*)a.x)[b * a.x_stride + c]) : 0.f;
-    const float d = on ? step_of(to_f32(((const T*)a.dt)[b * a.dt_stride + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f), a.flags & GDR2_SCAN_SOFTPLUS) : 0.f;
-    float y = 0.f;
+    load_states<4>(a.A + cc * N, s, N, on, A);
+    const float bias = a.dt_bias ? a.dt_bias[cc] : 0.f, skip = a.skip ? a.skip[cc] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(fast_exp2(d * (A[i] * kLog2e)), h[i], d * x * Bv[i]);
-        y = fmaf(Cv[i], h[i], y);
-    }
-    store_states<4>(st, s, N, on, h);
+    for (int i = 0; i < 4; ++i)
+        A[i] *= kLog2e;
 #pragma unroll
-    for (int off = LPC / 2; off >= 1; off >>= 1)
-        y += __shfl_xor(y, off);
-    if (on && s == 0) {
-        y = fmaf(a.skip ? a.skip[c] : 0.f, x, y);
-        if (a.z)
-            y *= silu_f(to_f32(((const T*)a.z)[b * a.z_stride + c]));
-        ((T*)a.y)[b * a.C + c] = from_f32<T>(y);
+    for (int r = 0; r < R; ++r) {
+        const bool in = on && b0 + r < a.B;
+        const float d = step_of(dt[r] + bias, a.flags & GDR2_SCAN_SOFTPLUS), u = d * x[r];
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[r][i] = fmaf(fast_exp2(d * A[i]), h[r][i], u * Bv[r][i]);
+            y = fmaf(Cv[r][i], h[r][i], y);
+        }
+        store_states<4>(p.state + ((b0 + r) * C + cc) * N, s, N, in, h[r]);
+        if constexpr (LPC >= 2)
+            y += dpp_quad_xor<1>(y);
+        if constexpr (LPC >= 4)
+            y += dpp_quad_xor<2>(y);
+        if constexpr (LPC == 8)
+            y += dpp_move<0x141>(y);
+        if (in && s == 0) {
+            y = fmaf(skip, x[r], y);
+            if (a.z)
+                y *= silu_f(z[r]);
+            ((T*)a.y)[(b0 + r) * C + c] = from_f32<T>(y);
+        }
     }
 }
 
@@ -387,11 +418,26 @@ hipError_t forward_w(const gdr2_scan_args& a, hipStream_t stream)
     return scan_wide(a, kScanChunk / LPC) ? forward_t<T, LPC, NS, true>(a, stream) : forward_t<T, LPC, NS, false>(a, stream);
 }
 
+// Sequences per thread: two once that leaves four waves per SIMD (256 x 2048
+// channels, 16 states: 16.8 us; one 19.4, four 20.0, eight 26; streaming
+// accesses to the state 22), else one.
+template <typename T, int LPC, int R, bool VEC>
+hipError_t step_r(const gdr2_scan_step_args& a, hipStream_t stream)
+{
+    const int64_t lanes = ceil_div(a.s.C * LPC, 256) * 256;
+    hipLaunchKernelGGL((scan_step_kernel<T, LPC, R, VEC>), dim3((unsigned)(ceil_div(a.s.B, R) * (lanes / 256))), dim3(256), 0,
+                       stream, a, (uint32_t)lanes);
+    return hipGetLastError();
+}
 template <typename T, int LPC>
 hipError_t step_t(const gdr2_scan_step_args& a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((scan_step_kernel<T, LPC>), dim3((unsigned)ceil_div(a.s.B * a.s.C * LPC, 256)), dim3(256), 0, stream, a);
-    return hipGetLastError();
+    const int64_t e = sizeof(T);
+    auto ok = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (4 * e) == 0 && ld % 4 == 0; };
+    const bool vec = a.s.N % 4 == 0 && ok(a.s.Bt, a.s.b_stride) && ok(a.s.Ct, a.s.c_stride);
+    if (a.s.B / 2 * a.s.C * LPC >= (int64_t)device_cu_count() * 4 * 4 * 64)
+        return vec ? step_r<T, LPC, 2, true>(a, stream) : step_r<T, LPC, 2, false>(a, stream);
+    return vec ? step_r<T, LPC, 1, true>(a, stream) : step_r<T, LPC, 1, false>(a, stream);
 }
 
 template <typename T>

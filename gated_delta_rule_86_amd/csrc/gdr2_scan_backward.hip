@@ -24,21 +24,6 @@ namespace {
 constexpr int kSub = 8;                       // tokens whose states are held
 constexpr int kSubs = kScanChunk / kSub;
 
-// Lanes of the lower half (even rows) return the sum of a over the lane pair,
-// the others that of b: one v_permlane*_swap and one add for two values.
-__device__ __forceinline__ float pair_sum32(float a, float b)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
-    const uint32_t x = r[0], y = r[1];
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-__device__ __forceinline__ float pair_sum16(float a, float b)
-{
-    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), false, false);
-    const uint32_t x = r[0], y = r[1];
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-
 // Sum of v[k][i], four tokens k, over the channels of a wave: lanes of row
 // r = lane / 16 return token k = r.  (Rounds over lane bits 5 and 4 halve the
 // values held; bit 3, and bit 2 with four lanes a channel, are rotations

@@ -18,6 +18,7 @@ Argument marshalling only, as in ``gdr2``.  Common to all functions:
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -94,11 +95,26 @@ SIZES = {"gdr2_conv_backward_workspace_size": ConvBwdArgs, "gdr2_scan_workspace_
          "gdr2_scan_backward_workspace_size": ScanBwdArgs, "gdr2_norm_backward_workspace_size": NormBwdArgs}
 
 
+# The single-token steps are all host time at small batches: their argument
+# structs are packed in one go, and handed over as bytes.
+_packed = {}
+_CONV_STEP = struct.Struct("@3q4i5P")
+_SCAN_STEP = struct.Struct("@10q4i14PNP")
+assert _CONV_STEP.size == ctypes.sizeof(ConvStepArgs) and _SCAN_STEP.size == ctypes.sizeof(ScanStepArgs)
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream of a device as a hipStream_t."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def declare(lib):
     """Signatures of the layer operators in a loaded library."""
     for name, args in ENTRIES.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(args), _vp]
+        f = _packed[name] = lib[name]          # a second object of the same function
+        f.restype, f.argtypes = ctypes.c_int, [ctypes.c_char_p, _vp]
     for name, args in SIZES.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = _size, [ctypes.POINTER(args)]
@@ -112,6 +128,8 @@ def declare(lib):
 def _row_stride(t: torch.Tensor, name: str, lead: int, width: int) -> int:
     """Elements between consecutive rows: the first ``lead`` dimensions number
     the rows, the others hold ``width`` dense elements."""
+    if t.is_contiguous():
+        return width
     if t.numel() == 0:
         return width
     shape, stride = t.shape, t.stride()
@@ -149,16 +167,28 @@ def _mode(table, value, name: str) -> int:
     return table[value]
 
 
-def _on(dev, dense=(), rows=()):
-    for n, t in rows:
-        if t is not None:
-            if not t.is_cuda:
-                raise ValueError(f"{n} must be a device tensor")
-            if t.device != dev:
-                raise ValueError(f"{n} is on {t.device}, expected {dev}")
-    for n, t in dense:
-        if t is not None:
+def _on(dev, dense, rows, names: str):
+    """Every tensor on ``dev``, the ``dense`` ones contiguous; ``names``
+    (dense first) only serve the message."""
+    if dev.type == "cuda":
+        for t in dense:
+            if t is not None and (t.device != dev or not t.is_contiguous()):
+                break
+        else:
+            for t in rows:
+                if t is not None and t.device != dev:
+                    break
+            else:
+                return
+    for i, (n, t) in enumerate(zip(names.split(), (*dense, *rows))):
+        if t is None:
+            continue
+        if i < len(dense):
             _req_dev(t, n, dev)
+        elif not t.is_cuda:
+            raise ValueError(f"{n} must be a device tensor")
+        elif t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, expected {dev}")
 
 
 def _offsets(offsets) -> int:
@@ -170,21 +200,30 @@ def _offsets(offsets) -> int:
 
 
 def _call(entry: str, args, dev):
+    """Calls an entry point with its argument struct (a ctypes Structure, or
+    the same bytes packed) on the current stream of ``dev``."""
     lib = load_library()
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    f = getattr(lib, entry)
-    if torch.cuda.current_device() == dev.index:
-        _check(lib, f(ctypes.byref(args), stream))
+    f = _packed[entry] if type(args) is bytes else getattr(lib, entry)
+    a = args if type(args) is bytes else ctypes.byref(args)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = f(a, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            _check(lib, f(ctypes.byref(args), stream))
+            status = f(a, _raw_stream(index))
+    if status:
+        _check(lib, status)
 
 
 def _with_workspace(size: str, args, workspace, dev):
     """Fills the workspace fields; the size depends on the device's compute
     units, so it is asked for with that device current."""
-    with torch.cuda.device(dev):
-        need = int(getattr(load_library(), size)(ctypes.byref(args)))
+    f = getattr(load_library(), size)
+    if torch.cuda.current_device() == dev.index:
+        need = int(f(ctypes.byref(args)))
+    else:
+        with torch.cuda.device(dev):
+            need = int(f(ctypes.byref(args)))
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
@@ -237,8 +276,7 @@ def conv_forward(x, weight, bias=None, state0=None, offsets=None, activation="si
     if state_out is not None:
         _req_shape(state_out, "state_out", x.dtype, (B, K - 1, C))
     ld = _row_stride(x, "x", x.dim() - 1, C)
-    _on(x.device, [("weight", weight), ("bias", bias), ("state0", state0), ("offsets", offsets), ("out", out),
-                   ("state_out", state_out)], [("x", x)])
+    _on(x.device, (weight, bias, state0, offsets, out, state_out), (x,), "weight bias state0 offsets out state_out x")
     out = _empty(out, x.shape, x)
     if state_out is None and final_state:
         state_out = torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=x.device)
@@ -251,26 +289,27 @@ def conv_forward(x, weight, bias=None, state0=None, offsets=None, activation="si
 def conv_step(state, x, weight, bias=None, activation="silu", out=None):
     """The convolution for one token of each of N sequences, in place on
     ``state`` [N,K-1,C]; x [N,C].  Returns y [N,C]."""
-    _rows_dtype(x)
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError(f"x and weight must have shapes (N, C) and (C, width), got {tuple(x.shape)} and "
                          f"{tuple(weight.shape)}")
     act = _mode(ACTIVATIONS, activation, "activation")
-    C, K = weight.shape
-    N = x.shape[0]
-    _req_shape(x, "x", None, (N, C))
-    _req_shape(weight, "weight", torch.float32)
-    _req_shape(state, "state", x.dtype, (N, K - 1, C))
-    if bias is not None:
+    (C, K), N, e = weight.shape, x.shape[0], x.dtype
+    if not (x.shape == (N, C) and state.shape == (N, K - 1, C) and (e is torch.bfloat16 or e is torch.float32)
+            and state.dtype is e and weight.dtype is torch.float32
+            and (bias is None or bias.dtype is torch.float32 and bias.shape == (C,))):
+        _rows_dtype(x)
+        _req_shape(x, "x", None, (N, C))
+        _req_shape(weight, "weight", torch.float32)
+        _req_shape(state, "state", e, (N, K - 1, C))
         _req_shape(bias, "bias", torch.float32, (C,))
     if out is not None:
         _req_shape(out, "out", x.dtype, (N, C))
     ld = _row_stride(x, "x", 1, C)
-    _on(x.device, [("state", state), ("weight", weight), ("bias", bias), ("out", out)], [("x", x)])
+    dev = x.device
+    _on(dev, (state, weight, bias, out), (x,), "state weight bias out x")
     out = _empty(out, (N, C), x)
-    a = ConvStepArgs(N, C, ld, K, _dtype_code(x), act, 0, state.data_ptr(), x.data_ptr(),
-                     weight.data_ptr(), _ptr(bias), out.data_ptr())
-    _call("gdr2_conv_step", a, x.device)
+    _call("gdr2_conv_step", _CONV_STEP.pack(N, C, ld, K, _dtype_code(x), act, 0, state.data_ptr(), x.data_ptr(),
+                                            weight.data_ptr(), 0 if bias is None else bias.data_ptr(), out.data_ptr()), dev)
     return out
 
 
@@ -286,8 +325,8 @@ def conv_backward(x, weight, dy, bias=None, state0=None, offsets=None, activatio
         _req_shape(dstate, "dstate", x.dtype, (B, K - 1, C))
     ld = _row_stride(x, "x", x.dim() - 1, C)
     dev = x.device
-    _on(dev, [("weight", weight), ("bias", bias), ("state0", state0), ("offsets", offsets), ("dy", dy), ("dstate", dstate),
-              ("workspace", workspace)], [("x", x)])
+    _on(dev, (weight, bias, state0, offsets, dy, dstate, workspace), (x,),
+        "weight bias state0 offsets dy dstate workspace x")
     want = state0 is not None if want_dstate0 is None else want_dstate0
     g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
          "dweight": torch.empty_like(weight),
@@ -306,6 +345,14 @@ def conv_backward(x, weight, dy, bias=None, state0=None, offsets=None, activatio
 def check_scan_shapes(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, offsets=None, lead=None):
     """Dtypes and shapes of the scan's inputs; returns (B, T, C, N, G).
     ``lead``: the number of leading dimensions (a step has one)."""
+    if lead == 1 and A.dim() == 2 and Bt.dim() == 3:      # a step: all in one expression, the reasons below
+        (B, _), (C, N), G, e = x.shape[:2] if x.dim() == 2 else (0, 0), A.shape, Bt.shape[1], x.dtype
+        if (x.shape == (B, C) == dt.shape and Bt.shape == (B, G, N) == Ct.shape and A.dtype is torch.float32
+                and (e is torch.bfloat16 or e is torch.float32) and dt.dtype is e and Bt.dtype is e and Ct.dtype is e
+                and (z is None or z.dtype is e and z.shape == (B, C))
+                and (skip is None or skip.dtype is torch.float32 and skip.shape == (C,))
+                and (dt_bias is None or dt_bias.dtype is torch.float32 and dt_bias.shape == (C,))):
+            return B, 1, C, N, G
     _rows_dtype(x)
     if A.dim() != 2:
         raise ValueError(f"A must have shape (C, N), got {tuple(A.shape)}")
@@ -364,9 +411,8 @@ def scan_forward(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, h0=None, off
     if ck is not None:
         _req_shape(ck, "chunk_states", torch.float32, (scan_chunk_count(B, T, offsets is not None), C, N))
     dev = x.device
-    _on(dev, [("A", A), ("skip", skip), ("dt_bias", dt_bias), ("h0", h0), ("offsets", offsets), ("out", out),
-              ("h_out", h_out), ("chunk_states", ck), ("workspace", workspace)],
-        [("x", x), ("dt", dt), ("Bt", Bt), ("Ct", Ct), ("z", z)])
+    _on(dev, (A, skip, dt_bias, h0, offsets, out, h_out, ck, workspace), (x, dt, Bt, Ct, z),
+        "A skip dt_bias h0 offsets out h_out chunk_states workspace x dt Bt Ct z")
     a = scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets, algo)
     out = _empty(out, x.shape, x)
     if h_out is None and final_state:
@@ -387,12 +433,14 @@ def scan_step(state, x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, softplus
     if out is not None:
         _req_shape(out, "out", x.dtype, (B, C))
     dev = x.device
-    _on(dev, [("state", state), ("A", A), ("skip", skip), ("dt_bias", dt_bias), ("out", out)],
-        [("x", x), ("dt", dt), ("Bt", Bt), ("Ct", Ct), ("z", z)])
+    _on(dev, (state, A, skip, dt_bias, out), (x, dt, Bt, Ct, z), "state A skip dt_bias out x dt Bt Ct z")
     out = _empty(out, (B, C), x)
-    a = ScanStepArgs(scan_args(B, 1, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus), state.data_ptr())
-    a.s.y = out.data_ptr()
-    _call("gdr2_scan_step", a, dev)
+    _call("gdr2_scan_step", _SCAN_STEP.pack(
+        B, 1, C, N, G, _row_stride(x, "x", 1, C), _row_stride(dt, "dt", 1, C), _row_stride(Bt, "Bt", 1, G * N),
+        _row_stride(Ct, "Ct", 1, G * N), 0 if z is None else _row_stride(z, "z", 1, C), _dtype_code(x),
+        SCAN_SOFTPLUS if softplus else 0, 0, 0, x.data_ptr(), dt.data_ptr(), Bt.data_ptr(), Ct.data_ptr(),
+        0 if z is None else z.data_ptr(), A.data_ptr(), 0 if skip is None else skip.data_ptr(),
+        0 if dt_bias is None else dt_bias.data_ptr(), 0, 0, out.data_ptr(), 0, 0, 0, 0, state.data_ptr()), dev)
     return out
 
 
@@ -408,9 +456,8 @@ def scan_backward(x, dt, A, Bt, Ct, dy, h_chunks, skip=None, z=None, dt_bias=Non
     if dh_out is not None:
         _req_shape(dh_out, "dh_out", torch.float32, (B, C, N))
     dev = x.device
-    _on(dev, [("A", A), ("skip", skip), ("dt_bias", dt_bias), ("offsets", offsets), ("dy", dy), ("h_chunks", h_chunks),
-              ("dh_out", dh_out), ("workspace", workspace)],
-        [("x", x), ("dt", dt), ("Bt", Bt), ("Ct", Ct), ("z", z)])
+    _on(dev, (A, skip, dt_bias, offsets, dy, h_chunks, dh_out, workspace), (x, dt, Bt, Ct, z),
+        "A skip dt_bias offsets dy h_chunks dh_out workspace x dt Bt Ct z")
     f = scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets, algo)
     f.h_chunks = h_chunks.data_ptr()
 
@@ -456,7 +503,7 @@ def norm_forward(x, weight=None, bias=None, z=None, eps: float = 1e-5, kind: str
     R, C = check_norm_shapes(x, weight, bias, z)
     if out is not None:
         _req_shape(out, "out", x.dtype, tuple(x.shape))
-    _on(x.device, [("weight", weight), ("bias", bias), ("out", out)], [("x", x), ("z", z)])
+    _on(x.device, (weight, bias, out), (x, z), "weight bias out x z")
     a = norm_args(R, C, x, weight, bias, z, eps, kind)
     out = _empty(out, x.shape, x)
     a.y = out.data_ptr()
@@ -470,7 +517,7 @@ def norm_backward(x, dy, weight=None, bias=None, z=None, eps: float = 1e-5, kind
     R, C = check_norm_shapes(x, weight, bias, z)
     _req_shape(dy, "dy", x.dtype, tuple(x.shape))
     dev = x.device
-    _on(dev, [("weight", weight), ("bias", bias), ("dy", dy), ("workspace", workspace)], [("x", x), ("z", z)])
+    _on(dev, (weight, bias, dy, workspace), (x, z), "weight bias dy workspace x z")
     f = norm_args(R, C, x, weight, bias, z, eps, kind)
     g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
          "dz": None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev),

@@ -551,9 +551,10 @@ gdr2_status gdr2_conv_step(const gdr2_conv_step_args *args, void *stream);
 size_t gdr2_conv_backward_workspace_size(const gdr2_conv_bwd_args *args);
 gdr2_status gdr2_conv_backward(const gdr2_conv_bwd_args *args, void *stream);
 
-/* The scan, its single-token step, its gradients.  The workspace queries read
- * no pointer but whether offsets, and the optional outputs, are NULL; 0 when
- * none is needed or the arguments are invalid or unsupported. */
+/* The scan, its single-token step, its gradients.  The workspace queries
+ * (here and above) look at sizes, at whether an optional pointer is NULL, and
+ * at the current device's compute units; 0 when none is needed or the
+ * arguments are invalid or unsupported. */
 int64_t gdr2_scan_chunk_count(int64_t B, int64_t T, int packed);
 size_t gdr2_scan_workspace_size(const gdr2_scan_args *args);
 gdr2_status gdr2_scan_forward(const gdr2_scan_args *args, void *stream);
