@@ -6,7 +6,7 @@
 //   dw[k] = sum_t dp[t] x[t - (K-1) + k];  dbias = sum_t dp[t]
 //
 // K <= 4 products per element against 2 to 6 bytes of traffic: memory bounds
-// it.  A thread walks a piece of rows of V adjacent channels (16 bytes) with
+// it.  A thread walks a piece of rows of V adjacent channels with
 // the last K - 1 rows in registers, so each row is loaded once per piece and
 // only K - 1 rows per piece are read twice.
 #include "gdr2_layer.h"
@@ -163,21 +163,33 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a
         const T* dst = a.dstate ? (const T*)a.dstate + q.seq * (K - 1) * C + c0 : nullptr;
         const T* dy = (const T*)a.dy + q.row0 * C + c0;
         T* dx = (T*)a.dx + q.row0 * C + c0;
+        T* ds = a.dstate0 ? (T*)a.dstate0 + q.seq * (K - 1) * C + c0 : nullptr;
         const int64_t t0 = q.index << pc.lg;
         const int64_t t1 = min(q.len, t0 + ((int64_t)1 << pc.lg));
-        float win[K - 1][V], dpw[K - 1][V] = {}, dp0[K - 1][V] = {};
+        float win[K - 1][V], dpw[K - 1][V] = {};
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
             Raw<T, V>::get(conv_row<T, V, K>(x, a.x_stride, state, C, t0 - (K - 1) + j, q.len), win[j]);
         // rows t0 .. t1 + K-2: the K - 1 beyond the piece only feed its dx
-        for (int64_t t = t0; t < t1 + K - 1; t += kRows) {
+        const int64_t end = t1 + K - 1, exist = min(q.len, end);
+        typename Raw<T, V>::Type nx[kRows], nd[kRows];
+        auto fetch = [&](int64_t t) {
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const bool in = t + u < exist;
+                nx[u] = in ? Raw<T, V>::load(x + (t + u) * a.x_stride) : Raw<T, V>::zero();
+                nd[u] = in ? Raw<T, V>::load(dy + (t + u) * C) : Raw<T, V>::zero();
+            }
+        };
+        fetch(t0);
+        for (int64_t t = t0; t < end; t += kRows) {
             typename Raw<T, V>::Type rx[kRows], rd[kRows];
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
-                const bool in = t + u < q.len && t + u < t1 + K - 1;
-                rx[u] = in ? Raw<T, V>::load(x + (t + u) * a.x_stride) : Raw<T, V>::zero();
-                rd[u] = in ? Raw<T, V>::load(dy + (t + u) * C) : Raw<T, V>::zero();
+                rx[u] = nx[u];
+                rd[u] = nd[u];
             }
+            fetch(t + kRows);
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 float xv[V], dv[V], o[V];
@@ -217,12 +229,12 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a
                     }
                     win[K - 2][v] = xv[v];
                     dpw[K - 2][v] = dp;
-                    if (u < K - 1 && t == 0)
-                        dp0[u < K - 1 ? u : 0][v] = dp;
                 }
+                // the rows before a sequence are its state's
                 const int64_t r = t + u - (K - 1);
-                if (r >= t0 && r < t1) {
-                    const int64_t back = r - (q.len - (K - 1));      // its row of the final state, if >= 0
+                T* to = r >= t0 && r < t1 ? dx + r * C : r < 0 && ds && t + u < end ? ds + (r + K - 1) * C : nullptr;
+                if (to) {
+                    const int64_t back = r - (q.len - (K - 1));      // the row of the final state it is, if >= 0
                     if (dst && back >= 0) {
                         float e[V];
                         Raw<T, V>::get(Raw<T, V>::load(dst + back * C), e);
@@ -230,29 +242,8 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a
                         for (int v = 0; v < V; ++v)
                             o[v] += e[v];
                     }
-                    store_row<V>(dx + r * C, o);
+                    store_row<V>(to, o);
                 }
-            }
-        }
-        if (q.index == 0 && a.dstate0) {
-            // state row j meets tap k of the token j - k
-            T* ds = (T*)a.dstate0 + q.seq * (K - 1) * C + c0;
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j) {
-                float o[V] = {};
-#pragma unroll
-                for (int k = 0; k <= j; ++k)
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        o[v] = fmaf(w[k][v], dp0[j - k][v], o[v]);
-                if (dst && j >= q.len) {
-                    float e[V];
-                    Raw<T, V>::get(Raw<T, V>::load(dst + (j - q.len) * C), e);
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        o[v] += e[v];
-                }
-                store_row<V>(ds + j * C, o);
             }
         }
     }
@@ -327,8 +318,8 @@ int forward_lg(int64_t B, int64_t T, int64_t ncv, bool packed)
 
 int backward_lg(int64_t B, int64_t T, int64_t ncv, bool packed)
 {
-    const int64_t want = (int64_t)device_cu_count() * 4 * 64;
-    int lg = 6;
+    const int64_t want = (int64_t)device_cu_count() * 4 * 2 * 64;
+    int lg = 7;
     while (lg > 3 && items_of(B, T, ncv, packed, lg) < want)
         --lg;
     return lg;
@@ -340,9 +331,15 @@ struct BackwardPlan {
     int lw, lg;
 };
 
+// Channels of a thread when rows are aligned to them.  Eight of bf16 (16 bytes)
+// were slower: 60 us against 51 forwards at 8 x 4096 x 2048, 138 against 111
+// backwards, where the taps, windows and sums of eight channels leave one wave
+// per SIMD.
+constexpr int kVec = 4;
+
 bool conv_vec(const void* x, int64_t x_stride, int64_t C, int32_t dtype)
 {
-    return rows_aligned(x, x_stride, C, dtype == GDR2_BF16 ? 2 : 4);
+    return rows_aligned(x, x_stride, C, dtype == GDR2_BF16 ? 2 : 4, kVec);
 }
 
 // The workspace query sees no pointers, so its size takes the larger of the
@@ -351,7 +348,7 @@ BackwardPlan backward_plan(const gdr2_conv_bwd_args& a, bool vec)
 {
     BackwardPlan p;
     p.vec = vec;
-    p.ncv = vec ? a.C / (a.dtype == GDR2_BF16 ? 8 : 4) : a.C;
+    p.ncv = vec ? a.C / kVec : a.C;
     p.lw = 3;
     while (p.lw < 6 && ((int64_t)1 << p.lw) < p.ncv)
         ++p.lw;
@@ -429,22 +426,22 @@ hipError_t launch_conv_forward(const gdr2_conv_args& a, hipStream_t stream)
 {
     const bool vec = conv_vec(a.x, a.x_stride, a.C, a.dtype);
     if (a.dtype == GDR2_BF16)
-        return vec ? forward_k<bf16, 8>(a, stream) : forward_k<bf16, 1>(a, stream);
-    return vec ? forward_k<float, 4>(a, stream) : forward_k<float, 1>(a, stream);
+        return vec ? forward_k<bf16, kVec>(a, stream) : forward_k<bf16, 1>(a, stream);
+    return vec ? forward_k<float, kVec>(a, stream) : forward_k<float, 1>(a, stream);
 }
 
 hipError_t launch_conv_step(const gdr2_conv_step_args& a, hipStream_t stream)
 {
     const bool vec = conv_vec(a.x, a.x_stride, a.C, a.dtype);
     if (a.dtype == GDR2_BF16)
-        return vec ? step_k<bf16, 8>(a, stream) : step_k<bf16, 1>(a, stream);
-    return vec ? step_k<float, 4>(a, stream) : step_k<float, 1>(a, stream);
+        return vec ? step_k<bf16, kVec>(a, stream) : step_k<bf16, 1>(a, stream);
+    return vec ? step_k<float, kVec>(a, stream) : step_k<float, 1>(a, stream);
 }
 
 size_t conv_backward_workspace_bytes(const gdr2_conv_bwd_args& a)
 {
     int64_t rows = backward_plan(a, false).npb;
-    if (a.C % (a.dtype == GDR2_BF16 ? 8 : 4) == 0)
+    if (a.C % kVec == 0)
         rows = max(rows, backward_plan(a, true).npb);
     return (size_t)rows * a.C * (a.width + 1) * sizeof(float);
 }
@@ -453,8 +450,8 @@ hipError_t launch_conv_backward(const gdr2_conv_bwd_args& a, hipStream_t stream)
 {
     const BackwardPlan p = backward_plan(a, conv_vec(a.x, a.x_stride, a.C, a.dtype));
     if (a.dtype == GDR2_BF16)
-        return p.vec ? backward_k<bf16, 8>(a, p, stream) : backward_k<bf16, 1>(a, p, stream);
-    return p.vec ? backward_k<float, 4>(a, p, stream) : backward_k<float, 1>(a, p, stream);
+        return p.vec ? backward_k<bf16, kVec>(a, p, stream) : backward_k<bf16, 1>(a, p, stream);
+    return p.vec ? backward_k<float, kVec>(a, p, stream) : backward_k<float, 1>(a, p, stream);
 }
 
 }  // namespace gdr2

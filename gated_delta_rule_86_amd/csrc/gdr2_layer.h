@@ -123,54 +123,21 @@ __device__ __forceinline__ Piece piece_of(const Pieces& p, int64_t slot)
 }
 
 // ---- rows ------------------------------------------------------------------
-// V consecutive elements as fp32, one load (V = 1, or 16 bytes when the
-// caller has checked the alignment).
-template <int V> __device__ __forceinline__ void load_row(const float* p, float* v)
+// V consecutive elements, one access (V > 1 when the caller has checked the
+// alignment).
+template <int V, typename T> __device__ __forceinline__ void store_row(T* p, const float* v)
 {
     if constexpr (V == 1) {
-        v[0] = *p;
+        *p = from_f32<T>(v[0]);
     } else {
-        static_assert(V == 4, "16 bytes");
-        const f32x4 x = *reinterpret_cast<const f32x4*>(p);
+        typedef T Vec __attribute__((ext_vector_type(V)));
+        Vec x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = x[i];
+        for (int i = 0; i < V; ++i)
+            x[i] = (T)v[i];
+        *reinterpret_cast<Vec*>(p) = x;
     }
 }
-template <int V> __device__ __forceinline__ void load_row(const bf16* p, float* v)
-{
-    if constexpr (V == 1) {
-        v[0] = (float)*p;
-    } else {
-        static_assert(V == 8, "16 bytes");
-        const bf16x8 x = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = (float)x[i];
-    }
-}
-template <int V> __device__ __forceinline__ void store_row(float* p, const float* v)
-{
-    if constexpr (V == 1) {
-        *p = v[0];
-    } else {
-        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    }
-}
-template <int V> __device__ __forceinline__ void store_row(bf16* p, const float* v)
-{
-    if constexpr (V == 1) {
-        *p = (bf16)v[0];
-    } else {
-        bf16x8 x;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = (bf16)v[i];
-        *reinterpret_cast<bf16x8*>(p) = x;
-    }
-}
-
-template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
 // The same elements unconverted: a load in flight holds half the registers.
 template <typename T, int V> struct Raw {
@@ -191,10 +158,10 @@ template <typename T> struct Raw<T, 1> {
     static __device__ __forceinline__ void get(Type r, float* v) { v[0] = (float)r; }
 };
 
-// Every row of this matrix starts on 16 bytes and holds whole vectors.
-inline bool rows_aligned(const void* p, int64_t stride, int64_t width, int64_t elt)
+// Every row of this matrix is whole, aligned vectors of V elements.
+inline bool rows_aligned(const void* p, int64_t stride, int64_t width, int64_t elt, int V)
 {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * elt) % 16 == 0 && (width * elt) % 16 == 0;
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)(V * elt) == 0 && stride % V == 0 && width % V == 0;
 }
 
 // ---- gate functions --------------------------------------------------------

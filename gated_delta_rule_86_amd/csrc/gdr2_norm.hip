@@ -492,7 +492,8 @@ template <int V, bool GATE, typename F> hipError_t dispatch_backward(const Shape
 bool norm_vec(const gdr2_norm_args& a)
 {
     const int64_t e = a.dtype == GDR2_BF16 ? 2 : 4;
-    return rows_aligned(a.x, a.x_stride, a.C, e) && (!a.z || rows_aligned(a.z, a.z_stride, a.C, e));
+    const int V = (int)(16 / e);
+    return rows_aligned(a.x, a.x_stride, a.C, e, V) && (!a.z || rows_aligned(a.z, a.z_stride, a.C, e, V));
 }
 
 template <typename T, int V>
