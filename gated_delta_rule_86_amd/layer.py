@@ -232,7 +232,7 @@ def _with_workspace(size: str, args, workspace, dev):
 
 
 def _empty(t, shape, like):
-    return torch.empty(shape, dtype=like.dtype, device=like.device) if t is None else t
+    return like.new_empty(shape) if t is None else t
 
 
 # ---- convolution -----------------------------------------------------------
@@ -279,7 +279,7 @@ def conv_forward(x, weight, bias=None, state0=None, offsets=None, activation="si
     _on(x.device, (weight, bias, state0, offsets, out, state_out), (x,), "weight bias state0 offsets out state_out x")
     out = _empty(out, x.shape, x)
     if state_out is None and final_state:
-        state_out = torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=x.device)
+        state_out = x.new_empty((B, max(K - 1, 0), C))
     a = ConvArgs(B, T, C, ld, K, _dtype_code(x), act, 0, x.data_ptr(), weight.data_ptr(), _ptr(bias),
                  _ptr(state0), _ptr(offsets), out.data_ptr(), _ptr(state_out))
     _call("gdr2_conv_forward", a, x.device)
@@ -328,10 +328,10 @@ def conv_backward(x, weight, dy, bias=None, state0=None, offsets=None, activatio
     _on(dev, (weight, bias, state0, offsets, dy, dstate, workspace), (x,),
         "weight bias state0 offsets dy dstate workspace x")
     want = state0 is not None if want_dstate0 is None else want_dstate0
-    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
+    g = {"dx": x.new_empty(x.shape),
          "dweight": torch.empty_like(weight),
          "dbias": None if bias is None else torch.empty_like(bias),
-         "dstate0": torch.empty((B, max(K - 1, 0), C), dtype=x.dtype, device=dev) if want else None}
+         "dstate0": x.new_empty((B, max(K - 1, 0), C)) if want else None}
     a = ConvBwdArgs(B, T, C, ld, K, _dtype_code(x), act, 0, x.data_ptr(), weight.data_ptr(), _ptr(bias),
                     _ptr(state0), _ptr(offsets), dy.data_ptr(), _ptr(dstate), g["dx"].data_ptr(), g["dweight"].data_ptr(),
                     _ptr(g["dbias"]), _ptr(g["dstate0"]))
@@ -416,9 +416,9 @@ def scan_forward(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, h0=None, off
     a = scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets, algo)
     out = _empty(out, x.shape, x)
     if h_out is None and final_state:
-        h_out = torch.empty((B, C, N), dtype=torch.float32, device=dev)
+        h_out = A.new_empty((B, C, N))
     if chunk_states is True:
-        ck = torch.empty((scan_chunk_count(B, T, offsets is not None), C, N), dtype=torch.float32, device=dev)
+        ck = A.new_empty((scan_chunk_count(B, T, offsets is not None), C, N))
     a.h0, a.y, a.h_out, a.h_chunks = _ptr(h0), out.data_ptr(), _ptr(h_out), _ptr(ck)
     workspace = _with_workspace("gdr2_scan_workspace_size", a, workspace, dev)
     _call("gdr2_scan_forward", a, dev)
@@ -462,11 +462,11 @@ def scan_backward(x, dt, A, Bt, Ct, dy, h_chunks, skip=None, z=None, dt_bias=Non
     f.h_chunks = h_chunks.data_ptr()
 
     def rows(t):
-        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
+        return None if t is None else t.new_empty(t.shape)
 
     g = {"dx": rows(x), "ddt": rows(dt), "dBt": rows(Bt), "dCt": rows(Ct), "dz": rows(z),
          "dA": torch.empty_like(A), "dskip": rows(skip), "ddt_bias": rows(dt_bias),
-         "dh0": torch.empty((B, C, N), dtype=torch.float32, device=dev) if want_dh0 else None}
+         "dh0": A.new_empty((B, C, N)) if want_dh0 else None}
     a = ScanBwdArgs(f, dy.data_ptr(), _ptr(dh_out), *(_ptr(g[n]) for n in ("dx", "ddt", "dBt", "dCt", "dz", "dA", "dskip",
                                                                           "ddt_bias", "dh0")))
     workspace = _with_workspace("gdr2_scan_backward_workspace_size", a, workspace, dev)
@@ -519,8 +519,8 @@ def norm_backward(x, dy, weight=None, bias=None, z=None, eps: float = 1e-5, kind
     dev = x.device
     _on(dev, (weight, bias, dy, workspace), (x, z), "weight bias dy workspace x z")
     f = norm_args(R, C, x, weight, bias, z, eps, kind)
-    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev),
-         "dz": None if z is None else torch.empty(x.shape, dtype=x.dtype, device=dev),
+    g = {"dx": x.new_empty(x.shape),
+         "dz": None if z is None else x.new_empty(x.shape),
          "dweight": None if weight is None else torch.empty_like(weight),
          "dbias": None if bias is None else torch.empty_like(bias)}
     a = NormBwdArgs(f, dy.data_ptr(), g["dx"].data_ptr(), _ptr(g["dz"]), _ptr(g["dweight"]), _ptr(g["dbias"]))

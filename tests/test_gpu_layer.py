@@ -359,6 +359,138 @@ def test_norm_of_no_rows():
     assert bool((g["dweight"] == 0).all()) and bool((g["dbias"] == 0).all())
 
 
+# ---- variants that only larger or aligned calls reach ----------------------
+
+WIDE = [
+    # B, T, C, N, G: rows aligned to whole vectors, contiguous or as aligned slices
+    (2, 77, 64, 16, 1), (1, 130, 128, 16, 2), (2, 45, 72, 8, 1), (1, 70, 24, 32, 1), (3, 33, 200, 13, 1),
+]
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("B,T,C,N,G", WIDE)
+def test_scan_aligned_rows(B, T, C, N, G, dtype, gate):
+    g = gen(71)
+    dt_ = DT[dtype]
+    a = dict(x=sliced(rn(g, B, T, C, dtype=dt_), C, 0), dt=rn(g, B, T, C, dtype=dt_, std=0.7),
+             A=-torch.rand(C, N, generator=g).cuda() * 1.5, Bt=rn(g, B, T, G, N, dtype=dt_), Ct=rn(g, B, T, G, N, dtype=dt_))
+    kw = dict(skip=rn(g, C), z=sliced(rn(g, B, T, C, dtype=dt_), C, C) if gate else None, dt_bias=rn(g, C, std=0.5))
+    h0, dy, dh = rn(g, B, C, N), rn(g, B, T, C, dtype=dt_), rn(g, B, C, N)
+    y, h, ck = layer.scan_forward(**a, **kw, h0=h0, chunk_states=True)
+    got = layer.scan_backward(**a, **kw, dy=dy, h_chunks=ck, dh_out=dh)
+    steps = 64 + 32 * T
+    want, wh, _ = ref.scan(**a, **kw, h0=h0)
+    by, bh, _ = ref.scan(**a, **kw, h0=h0, absolute=True)
+    close(y, want, by, steps, "y")
+    close(h, wh, bh, steps, "h")
+    wg = ref.scan_grad(**a, **kw, dy=dy, h0=h0, dh_out=dh)
+    bg = ref.scan_grad(**a, **kw, dy=dy, h0=h0, dh_out=dh, absolute=True)
+    for n in got:
+        if got[n] is not None:
+            close(got[n], wg[n], bg[n], 2 * steps + B * T, n)
+
+
+def test_scan_step_of_many_sequences():
+    """Enough sequences that a thread takes two, an odd number of them."""
+    B, C, N = 33, 8200, 16
+    g = gen(72)
+    tok = dict(x=rn(g, B, C), dt=rn(g, B, C), A=-torch.rand(C, N, generator=g).cuda(), Bt=rn(g, B, 1, N), Ct=rn(g, B, 1, N))
+    s = rn(g, B, C, N)
+    s0 = s.clone()
+    y = layer.scan_step(s, **tok)
+    one = s0.clone()
+    for b in range(B):       # one at a time: the same operations on the same values
+        r = {n: (t if n == "A" else t[b:b + 1]) for n, t in tok.items()}
+        assert torch.equal(layer.scan_step(one[b:b + 1], **r)[0], y[b])
+    assert torch.equal(one, s)
+    b = B - 1
+    want, wh, _ = ref.scan(**{n: (t if n == "A" else t[b:, None]) for n, t in tok.items()}, h0=s0[b:])
+    by, bh, _ = ref.scan(**{n: (t if n == "A" else t[b:, None]) for n, t in tok.items()}, h0=s0[b:], absolute=True)
+    close(y[b:], want[:, 0], by[:, 0], 128, "y")
+    close(s[b:], wh, bh, 128, "state")
+
+
+@pytest.mark.parametrize("R,C,dtype,gate", [(70001, 16, "f32", False), (2501, 2048, "bf16", False), (2100, 1500, "f32", True),
+                                            (1100, 2048, "bf16", True)])
+def test_norm_walks_its_rows(R, C, dtype, gate):
+    """More rows than groups of lanes: each walks several."""
+    g = gen(73)
+    x, dy = rn(g, R, C, dtype=DT[dtype]), rn(g, R, C, dtype=DT[dtype])
+    z = rn(g, R, C, dtype=DT[dtype]) if gate else None
+    w, b = 1 + 0.2 * rn(g, C), rn(g, C)
+    want, bound = ref.norm(x, w, b, z)
+    close(layer.norm_forward(x, w, b, z), want, bound, 64 + C / 8, "y")
+    got = layer.norm_backward(x, dy, w, b, z)
+    wg, bg = ref.norm_grad(x, dy, w, b, z)
+    for n in got:
+        if got[n] is not None:
+            close(got[n], wg[n], bg[n], 128 + C / 4 + R, n)
+
+
+def test_conv_of_a_training_batch_equals_its_channel_slices():
+    """The longest pieces against the shorter ones that a slice of the channels
+    takes: rows bit for bit, the taps' sums to their rounding."""
+    B, T, C = 4, 4100, 2048
+    g = gen(74)
+    x, dy = rn(g, B, T, C, dtype=torch.bfloat16), rn(g, B, T, C, dtype=torch.bfloat16)
+    w, b = rn(g, C, 4) * 0.5, rn(g, C)
+    y, st = layer.conv_forward(x, w, b)
+    full = layer.conv_backward(x, w, dy, b)
+    for c in (slice(0, 64), slice(1000, 1072), slice(2040, 2048)):
+        ys, ss = layer.conv_forward(x[..., c], w[c].contiguous(), b[c].contiguous())
+        assert torch.equal(ys, y[..., c]) and torch.equal(ss, st[..., c])
+        part = layer.conv_backward(x[..., c], w[c].contiguous(), dy[..., c].contiguous(), b[c].contiguous())
+        assert torch.equal(part["dx"], full["dx"][..., c])
+        bound = ref.conv_grad(x[..., c], w[c], dy[..., c], b[c], None, None, "silu", absolute=True)
+        for n in ("dweight", "dbias"):
+            close(full[n][c], ref.d64(part[n]), bound[n], 2 * (64 + B * T), n)
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements: the last rows come out as they do from a call
+    of their own that starts from the state before them."""
+    T, C, N, tail = 1_060_000, 2048, 4, 97
+    g = torch.Generator(device="cuda").manual_seed(75)
+    x = torch.randn(1, T, C, generator=g, device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 1 << 31
+    w = torch.rand(C, 4, generator=g, device="cuda") - 0.5
+    end = x[:, T - tail:].contiguous()
+    y, _ = layer.conv_forward(x, w)
+    again, _ = layer.conv_forward(end, w, state0=x[:, T - tail - 3:T - tail].contiguous())
+    assert torch.equal(y[:, T - tail:], again)
+    n = layer.norm_forward(x, kind="rms", out=y)
+    assert torch.equal(n[:, T - tail:], layer.norm_forward(end, kind="rms"))
+    A = -torch.rand(C, N, generator=g, device="cuda") - 0.5
+    Bt = torch.randn(1, T, 1, N, generator=g, device="cuda", dtype=torch.bfloat16)
+    y, h = layer.scan_forward(x, x, A, Bt, Bt, out=y)
+    # the state before the tail has forgotten everything older than 3000 tokens (exp(-0.5 * 0.31 * 3000) at most)
+    near = slice(T - tail - 3000, T - tail)
+    _, h0 = layer.scan_forward(x[:, near], x[:, near], A, Bt[:, near], Bt[:, near])
+    again, h1 = layer.scan_forward(end, end, A, Bt[:, T - tail:], Bt[:, T - tail:], h0=h0)
+    assert float((h - h1).abs().max()) <= 1e-4 * float(h.abs().max())
+    assert float((y[:, T - tail:].float() - again.float()).abs().max()) <= 2.0 ** -7 * float(again.float().abs().max())
+
+
+def test_empty_packed_batches():
+    """Only empty sequences, with and without rows around them; no sequence."""
+    for T, offs in ((0, [0, 0, 0]), (9, [4, 4, 4]), (9, [3]), (0, [0])):
+        offsets = torch.tensor(offs, dtype=torch.int64).cuda()
+        B = len(offs) - 1
+        g = gen(76)
+        x, w = rn(g, T, 8), rn(g, 8, 4)
+        st, h0 = rn(g, B, 3, 8), rn(g, B, 8, 4)
+        y, s = layer.conv_forward(x, w, state0=st, offsets=offsets, out=torch.full_like(x, SENT))
+        assert torch.equal(s, st) and bool((y == SENT).all())
+        gc = layer.conv_backward(x, w, x, w[:, 0].contiguous(), state0=st, offsets=offsets, dstate=st)
+        assert bool((gc["dweight"] == 0).all()) and bool((gc["dbias"] == 0).all()) and torch.equal(gc["dstate0"], st)
+        A, bc = -torch.ones(8, 4).cuda(), rn(g, T, 1, 4)
+        y, h, ck = layer.scan_forward(x, x, A, bc, bc, h0=h0, offsets=offsets, chunk_states=True, out=torch.full_like(x, SENT))
+        assert torch.equal(h, h0) and bool((y == SENT).all())
+        gs = layer.scan_backward(x, x, A, bc, bc, x, ck, offsets=offsets, dh_out=h0)
+        assert bool((gs["dA"] == 0).all()) and torch.equal(gs["dh0"], h0)
+
+
 # ---- what no sequence owns, and bad values ---------------------------------
 
 def test_values_outside_the_sequences_do_not_matter():
