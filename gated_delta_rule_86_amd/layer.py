@@ -139,21 +139,19 @@ def _row_stride(t: torch.Tensor, name: str, lead: int, width: int) -> int:
             if stride[d] != step:
                 raise ValueError(f"{name}: the elements of a row must be contiguous")
             step *= shape[d]
-    ld = 0
+    ld = None
     for d in range(lead - 1, -1, -1):
         if shape[d] == 1:
             continue
-        if ld == 0:
+        if ld is None:
             ld, span = stride[d], stride[d] * shape[d]
+            if ld < width:              # an expanded dimension has stride 0
+                raise ValueError(f"{name}: rows must not overlap")
         elif stride[d] != span:
             raise ValueError(f"{name}: rows must be equally spaced")
         else:
             span *= shape[d]
-    if ld == 0:
-        return width
-    if ld < width:
-        raise ValueError(f"{name}: rows must not overlap")
-    return ld
+    return width if ld is None else ld
 
 
 def _rows_dtype(t: torch.Tensor):

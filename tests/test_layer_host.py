@@ -332,3 +332,15 @@ def test_row_strides():
             layer._row_stride(bad, "x", 2, bad.shape[-1])
     with pytest.raises(ValueError):
         layer._row_stride(x[0].unfold(1, 8, 4), "x", 2, 8)      # overlapping rows
+
+
+def test_row_strides_of_expanded_rows():
+    """A row repeated by expand has stride 0: taken for dense rows it would be
+    read far past its end."""
+    one = torch.zeros(1, 1, 8)
+    for bad in (one.expand(1, 5, 8), one.expand(5, 1, 8), one.expand(4, 5, 8), torch.zeros(4, 1, 8).expand(4, 5, 8),
+                torch.zeros(1, 5, 8).expand(4, 5, 8), torch.zeros(8).expand(3, 8), torch.zeros(1, 1, 1).expand(2, 3, 1)):
+        with pytest.raises(ValueError):
+            layer._row_stride(bad, "x", bad.dim() - 1, bad.shape[-1])
+    with pytest.raises(ValueError):
+        layer._row_stride(torch.zeros(4, 5, 1).expand(4, 5, 8), "x", 2, 8)      # one element for a whole row
