@@ -355,6 +355,16 @@ template <int V> __device__ __forceinline__ void channel_params(const float* p, 
         out[v] = p && ch + v < b.n ? p[b.c0 + ch + v] : 0.f;
 }
 
+// A and log2(e) A, kept finite: the tokens past a sequence have d = 0, and d
+// times an infinite A would be NaN in the state they are to leave as it is.
+// (A NaN stays one.)
+__device__ __forceinline__ float finite(float v)
+{
+    v = v < -__FLT_MAX__ ? -__FLT_MAX__ : v;
+    return v > __FLT_MAX__ ? __FLT_MAX__ : v;
+}
+__device__ __forceinline__ float exponent_scale(float A) { return finite(A * kLog2e); }
+
 // The step from its raw value.  softplus is formed either way: behind a branch
 // per element it would split the block it is scheduled in.
 __device__ __forceinline__ float step_of(float raw, bool softplus)

@@ -55,7 +55,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        A2[i] *= kLog2e;
+        A2[i] = exponent_scale(A2[i]);
     if (starts)
         load_states<NS>(starts + ((int64_t)slot * a.C + c) * N, s, N, l.on, h);
     else
@@ -208,7 +208,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        A2[i] *= kLog2e;
+        A2[i] = exponent_scale(A2[i]);
     float bias[V];
     channel_params<V>(a.dt_bias, blk, bias);
     const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(256) void scan_fold_kernel(gdr2_scan_args a, Pieces
         return;
     const int64_t seq = id / per, cn = id - seq * per, c = cn / a.N;
     const Piece q = sequence_of(seg, seq);
-    const float A2 = a.A[cn] * kLog2e;
+    const float A2 = exponent_scale(a.A[cn]);
     float h = a.h0 ? a.h0[id] : 0.f;
     const int64_t nseg = max((int64_t)1, (q.len + ((int64_t)1 << seg.lg) - 1) >> seg.lg);
     for (int64_t i = 0; i < nseg; ++i) {
@@ -345,7 +345,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p, u
     const float bias = a.dt_bias ? a.dt_bias[cc] : 0.f, skip = a.skip ? a.skip[cc] : 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        A[i] *= kLog2e;
+        A[i] = exponent_scale(A[i]);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool in = on && b0 + r < a.B;
@@ -495,6 +495,7 @@ int64_t scan_launch_groups(const gdr2_scan_args& a)
     int64_t n;
     if (__builtin_mul_overflow(p.seg.slots(), p.ncb, &n))
         return kMaxGroups;
+    n *= a.N > 16 ? 2 : 1;            // workgroups of 512 threads: counted as two of 256
     return max(n, ceil_div(a.B * a.C * max((int64_t)8, a.N), 256));
 }
 

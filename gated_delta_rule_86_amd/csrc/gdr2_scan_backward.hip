@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * LPC, 2) void scan_backward_kernel(gdr2_scan_bw
         load_states<NS>(a.A + c * N, s, N, l.on, A);
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-            A2[i] = A[i] * kLog2e;
+            A2[i] = exponent_scale(A[i]), A[i] = finite(A[i]);
         float bias[V], skips[V];
         channel_params<V>(a.dt_bias, blk, bias);
         channel_params<V>(a.skip, blk, skips);
@@ -289,8 +289,7 @@ __global__ __launch_bounds__(64 * LPC, 2) void scan_backward_kernel(gdr2_scan_bw
                 dd = soft ? dd * sigmoid_f(raw) : dd;
                 dx[v] = fmaf(tk[0], tk[1], skip * dv);
                 ddt[v] = dd;
-                // (rows past the sequence read as zero, and so add nothing: dv = x = 0,
-                // and dd is qA = 0 for d = 0 times a state that nothing changed)
+                // (rows past the sequence read as zero: dv = x = 0)
                 dskip[v] = fmaf(dv, x, dskip[v]);
                 dbias[v] += in ? dd : 0.f;
             }
@@ -360,7 +359,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_span_kernel(gdr2_scan_
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
 #pragma unroll
     for (int i = 0; i < NS; ++i)
-        A2[i] *= kLog2e;
+        A2[i] = exponent_scale(A2[i]);
     float bias[V];
     channel_params<V>(a.dt_bias, blk, bias);
     const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
@@ -434,7 +433,7 @@ __global__ __launch_bounds__(256) void scan_backward_fold_kernel(gdr2_scan_bwd_a
         return;
     const int64_t seq = id / per, cn = id - seq * per, c = cn / a.N;
     const Piece q = sequence_of(seg, seq);
-    const float A2 = a.A[cn] * kLog2e;
+    const float A2 = exponent_scale(a.A[cn]);
     float lam = p.dh_out ? p.dh_out[id] : 0.f;
     const int64_t nseg = max((int64_t)1, (q.len + ((int64_t)1 << seg.lg) - 1) >> seg.lg);
     for (int64_t i = nseg - 1; i >= 0; --i) {

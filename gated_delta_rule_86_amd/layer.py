@@ -10,7 +10,9 @@ Argument marshalling only, as in ``gdr2``.  Common to all functions:
   contiguous.
 - a batch is dense, ``[B, T, ...]``, or packed: ``[T, ...]`` with ``offsets``,
   an int64 device tensor of ``B + 1`` ascending row numbers (sequences may be
-  empty; rows of no sequence are not touched: pass ``out`` to keep them).
+  empty).  Rows of no sequence are not touched, in gradients neither: in a
+  result the call allocates they hold what the memory held before.  Pass
+  ``out`` where that matters (zeros, for a padded batch that is trained on).
 - gradients of rows have the rows' dtype, gradients of parameters and states
   are float32.
 - the call is enqueued on the current stream of the tensors' device.
@@ -233,6 +235,24 @@ def _empty(t, shape, like):
     return like.new_empty(shape) if t is None else t
 
 
+def _grad_buffers(out, dev, **want):
+    """The tensors gradients are written to, by name: the caller's ``out[name]``
+    or fresh memory; ``want`` gives (dtype, shape), or None for no gradient."""
+    out = out or {}
+    for n in out:
+        if want.get(n) is None:
+            raise ValueError(f"out: no gradient {n!r} is formed ({', '.join(k for k, v in want.items() if v)})")
+    g = {}
+    for n, spec in want.items():
+        if spec is not None and n in out:
+            _req_shape(out[n], n, *spec)
+            _req_dev(out[n], n, dev)
+            g[n] = out[n]
+        else:
+            g[n] = None if spec is None else torch.empty(spec[1], dtype=spec[0], device=dev)
+    return g
+
+
 # ---- convolution -----------------------------------------------------------
 
 def check_conv_shapes(x, weight, bias=None, state0=None, offsets=None):
@@ -312,10 +332,11 @@ def conv_step(state, x, weight, bias=None, activation="silu", out=None):
 
 
 def conv_backward(x, weight, dy, bias=None, state0=None, offsets=None, activation="silu", dstate=None,
-                  want_dstate0=None, workspace=None):
+                  want_dstate0=None, out=None, workspace=None):
     """Gradients of ``conv_forward`` for dL/dy (shaped like y) and optionally
     dL/dstate ``dstate`` [B,K-1,C].  Returns a dict: dx, dweight, dbias (None
-    without bias), dstate0 (by default when state0 is given)."""
+    without bias), dstate0 (by default when state0 is given); ``out``: a dict
+    of tensors to write some of them into."""
     B, T, C, K = check_conv_shapes(x, weight, bias, state0, offsets)
     act = _mode(ACTIVATIONS, activation, "activation")
     _req_shape(dy, "dy", x.dtype, tuple(x.shape))
@@ -326,10 +347,9 @@ def conv_backward(x, weight, dy, bias=None, state0=None, offsets=None, activatio
     _on(dev, (weight, bias, state0, offsets, dy, dstate, workspace), (x,),
         "weight bias state0 offsets dy dstate workspace x")
     want = state0 is not None if want_dstate0 is None else want_dstate0
-    g = {"dx": x.new_empty(x.shape),
-         "dweight": torch.empty_like(weight),
-         "dbias": None if bias is None else torch.empty_like(bias),
-         "dstate0": x.new_empty((B, max(K - 1, 0), C)) if want else None}
+    e, f32 = x.dtype, torch.float32
+    g = _grad_buffers(out, dev, dx=(e, tuple(x.shape)), dweight=(f32, (C, K)), dbias=None if bias is None else (f32, (C,)),
+                      dstate0=(e, (B, max(K - 1, 0), C)) if want else None)
     a = ConvBwdArgs(B, T, C, ld, K, _dtype_code(x), act, 0, x.data_ptr(), weight.data_ptr(), _ptr(bias),
                     _ptr(state0), _ptr(offsets), dy.data_ptr(), _ptr(dstate), g["dx"].data_ptr(), g["dweight"].data_ptr(),
                     _ptr(g["dbias"]), _ptr(g["dstate0"]))
@@ -415,7 +435,7 @@ def scan_forward(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, h0=None, off
     out = _empty(out, x.shape, x)
     if h_out is None and final_state:
         h_out = A.new_empty((B, C, N))
-    if chunk_states is True:
+    if ck is None and chunk_states:
         ck = A.new_empty((scan_chunk_count(B, T, offsets is not None), C, N))
     a.h0, a.y, a.h_out, a.h_chunks = _ptr(h0), out.data_ptr(), _ptr(h_out), _ptr(ck)
     workspace = _with_workspace("gdr2_scan_workspace_size", a, workspace, dev)
@@ -443,11 +463,12 @@ def scan_step(state, x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, softplus
 
 
 def scan_backward(x, dt, A, Bt, Ct, dy, h_chunks, skip=None, z=None, dt_bias=None, offsets=None, softplus: bool = True,
-                  dh_out=None, want_dh0: bool = True, algo: str = "auto", workspace=None):
+                  dh_out=None, want_dh0: bool = True, algo: str = "auto", out=None, workspace=None):
     """Gradients of ``scan_forward`` for dL/dy and optionally dL/dh ``dh_out``
     float32 [B,C,N]; h_chunks as the forward of the same inputs returned them.
     Returns a dict: dx, ddt, dBt, dCt, dz (None without z) in the rows' dtype;
-    dA, dskip, ddt_bias (None without their parameter), dh0 float32."""
+    dA, dskip, ddt_bias (None without their parameter), dh0 float32; ``out``:
+    a dict of tensors to write some of them into (dh0 may be dh_out)."""
     B, T, C, N, G = check_scan_shapes(x, dt, A, Bt, Ct, skip, z, dt_bias, offsets)
     _req_shape(dy, "dy", x.dtype, tuple(x.shape))
     _req_shape(h_chunks, "h_chunks", torch.float32, (scan_chunk_count(B, T, offsets is not None), C, N))
@@ -459,12 +480,11 @@ def scan_backward(x, dt, A, Bt, Ct, dy, h_chunks, skip=None, z=None, dt_bias=Non
     f = scan_args(B, T, C, N, G, x, dt, A, Bt, Ct, skip, z, dt_bias, softplus, offsets, algo)
     f.h_chunks = h_chunks.data_ptr()
 
-    def rows(t):
-        return None if t is None else t.new_empty(t.shape)
+    def like(t):
+        return None if t is None else (t.dtype, tuple(t.shape))
 
-    g = {"dx": rows(x), "ddt": rows(dt), "dBt": rows(Bt), "dCt": rows(Ct), "dz": rows(z),
-         "dA": torch.empty_like(A), "dskip": rows(skip), "ddt_bias": rows(dt_bias),
-         "dh0": A.new_empty((B, C, N)) if want_dh0 else None}
+    g = _grad_buffers(out, dev, dx=like(x), ddt=like(dt), dBt=like(Bt), dCt=like(Ct), dz=like(z), dA=like(A), dskip=like(skip),
+                      ddt_bias=like(dt_bias), dh0=(torch.float32, (B, C, N)) if want_dh0 else None)
     a = ScanBwdArgs(f, dy.data_ptr(), _ptr(dh_out), *(_ptr(g[n]) for n in ("dx", "ddt", "dBt", "dCt", "dz", "dA", "dskip",
                                                                           "ddt_bias", "dh0")))
     workspace = _with_workspace("gdr2_scan_backward_workspace_size", a, workspace, dev)
@@ -509,18 +529,18 @@ def norm_forward(x, weight=None, bias=None, z=None, eps: float = 1e-5, kind: str
     return out
 
 
-def norm_backward(x, dy, weight=None, bias=None, z=None, eps: float = 1e-5, kind: str = "layer", workspace=None):
+def norm_backward(x, dy, weight=None, bias=None, z=None, eps: float = 1e-5, kind: str = "layer", out=None, workspace=None):
     """Gradients of ``norm_forward`` for dL/dy.  Returns a dict: dx, dz (None
-    without z), dweight and dbias (float32, None without their parameter)."""
+    without z), dweight and dbias (float32, None without their parameter);
+    ``out``: a dict of tensors to write some of them into."""
     R, C = check_norm_shapes(x, weight, bias, z)
     _req_shape(dy, "dy", x.dtype, tuple(x.shape))
     dev = x.device
     _on(dev, (weight, bias, dy, workspace), (x, z), "weight bias dy workspace x z")
     f = norm_args(R, C, x, weight, bias, z, eps, kind)
-    g = {"dx": x.new_empty(x.shape),
-         "dz": None if z is None else x.new_empty(x.shape),
-         "dweight": None if weight is None else torch.empty_like(weight),
-         "dbias": None if bias is None else torch.empty_like(bias)}
+    rows, param = (x.dtype, tuple(x.shape)), (torch.float32, (C,))
+    g = _grad_buffers(out, dev, dx=rows, dz=None if z is None else rows, dweight=None if weight is None else param,
+                      dbias=None if bias is None else param)
     a = NormBwdArgs(f, dy.data_ptr(), g["dx"].data_ptr(), _ptr(g["dz"]), _ptr(g["dweight"]), _ptr(g["dbias"]))
     workspace = _with_workspace("gdr2_norm_backward_workspace_size", a, workspace, dev)
     _call("gdr2_norm_backward", a, dev)

@@ -535,6 +535,51 @@ def test_values_outside_the_sequences_do_not_matter():
     assert bool(dirty["y"][o[s]].isnan().any())
 
 
+@pytest.mark.parametrize("algo", ["staged", "segmented"])
+def test_infinite_decay(algo):
+    """A = -inf (and values whose multiple by log2(e) overflows) forgets the
+    state at every step, as any large finite decay does: also at the tokens
+    that fill up the last chunk, and in the gradients."""
+    B, T, C, N = 2, 70, 5, 6
+    g = gen(44)
+    x, dt, bc = rn(g, B, T, C), rn(g, B, T, C).abs() + 0.25, rn(g, B, T, 1, N)
+    h0, dy = rn(g, B, C, N), rn(g, B, T, C)
+    A = -torch.rand(C, N, generator=g).cuda()
+    A[:, 1], A[:, 4] = -float("inf"), -3e38
+    big = A.clone()
+    big[:, 1] = big[:, 4] = -1e6                     # exp(-0.25e6) is 0 in every format
+    res = []
+    for a in (A, big):
+        y, h, ck = layer.scan_forward(x, dt, a, bc, bc, h0=h0, softplus=False, chunk_states=True, algo=algo)
+        res.append({"y": y, "h": h, **layer.scan_backward(x, dt, a, bc, bc, dy, ck, softplus=False, algo=algo)})
+    for n, want in res[1].items():
+        if want is not None:
+            assert bool(want.isfinite().all()) and torch.equal(res[0][n], want), n
+
+
+def test_gradients_into_given_buffers():
+    """Rows of no sequence keep what the given buffers hold there; the rest is
+    what a call without buffers returns."""
+    offsets, T = packed()
+    lo, hi = int(offsets[0]), int(offsets[-1])
+    a, kw, h0, B, _ = scan_case(SCAN[10], "bf16", 45)
+    dy = rn(gen(46), *a["x"].shape, dtype=a["x"].dtype)
+    _, _, ck = layer.scan_forward(**a, **kw, h0=h0, chunk_states=1)
+    w = torch.linspace(-1, 1, 20 * 4).view(20, 4).cuda()
+    calls = {("dx", "ddt", "dBt", "dCt", "dz"): lambda o: layer.scan_backward(**a, **kw, dy=dy, h_chunks=ck, out=o),
+             ("dx",): lambda o: layer.conv_backward(a["x"], w, dy, offsets=offsets, out=o)}
+    for names, call in calls.items():
+        want = call(None)
+        given = {n: torch.full_like(want[n], SENT) for n in names}
+        got = call(given)
+        for n in names:
+            assert got[n] is given[n] and untouched(got[n], offsets, T) and torch.equal(got[n][lo:hi], want[n][lo:hi]), n
+    wn = torch.ones(20).cuda()
+    want, given = layer.norm_backward(dy, dy, wn), {"dx": torch.empty_like(dy), "dweight": torch.empty_like(wn)}
+    got = layer.norm_backward(dy, dy, wn, out=given)
+    assert all(got[n] is given[n] and torch.equal(got[n], want[n]) for n in given)
+
+
 def test_bad_offsets_stay_inside():
     """Offsets out of range or descending are clamped on the device: the call
     returns and writes only its outputs' rows."""

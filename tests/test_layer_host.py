@@ -344,3 +344,26 @@ def test_row_strides_of_expanded_rows():
             layer._row_stride(bad, "x", bad.dim() - 1, bad.shape[-1])
     with pytest.raises(ValueError):
         layer._row_stride(torch.zeros(4, 5, 1).expand(4, 5, 8), "x", 2, 8)      # one element for a whole row
+
+
+def test_refuses_more_threads_than_one_launch_takes(lib):  # noqa: F811
+    """State sizes above 16 run in workgroups of 512 threads: a grid of 2^32
+    threads is refused here, not by the launch."""
+    for N, C, B, ok in ((32, 1, 9_000_000, False), (16, 1, 9_000_000, True), (32, 1, 8_000_000, True)):
+        a = layer.ScanArgs(B=B, T=1, C=C, N=N, G=1, x_stride=1, dt_stride=1, b_stride=N, c_stride=N, dtype=gdr2.F32)
+        status = lib.gdr2_scan_forward(ctypes.byref(a), None)       # every pointer is NULL: nothing launches
+        assert status == (INV if ok else UNS), (N, B)
+
+
+def test_gradient_buffers_by_name():
+    dev = torch.device("cuda", 0)
+    f32 = torch.float32
+    for out in ({"dy": _t(2, 3)}, {"dz": _t(2, 3)}):
+        with pytest.raises(ValueError, match="no gradient"):
+            layer._grad_buffers(out, dev, dx=(f32, (2, 3)), dz=None)
+    with pytest.raises(ValueError, match="shape"):
+        layer._grad_buffers({"dx": _t(3, 2)}, dev, dx=(f32, (2, 3)))
+    with pytest.raises(TypeError):
+        layer._grad_buffers({"dx": _t(2, 3).bfloat16()}, dev, dx=(f32, (2, 3)))
+    with pytest.raises(ValueError, match="device tensor"):
+        layer._grad_buffers({"dx": _t(2, 3)}, dev, dx=(f32, (2, 3)))
