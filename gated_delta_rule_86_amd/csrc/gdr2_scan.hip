@@ -32,24 +32,25 @@ __device__ __forceinline__ void step_to_lds(float dt, float x, float bias, bool 
 // arrays alternate between two buffers).  Between two barriers, interleaved
 // token group by token group so that the latencies of one fill with the
 // arithmetic of the others:
-//   states: the recurrence over chunk i, its sums over n into the places of d
+//   states: the recurrence over chunk i, its sums into LDS
 //   rows:   (d, d x) of chunk i + 1 into LDS; skip and gate of chunk i - 1's sums
 //   loads:  the rows of chunk i + 2 are on their way
 template <typename T, int LPC, int NS, bool GATE, bool WIDE>
 __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                                 const float* starts)
 {
-    constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT;
+    constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT, YLD = kScanCols + 16;
     static_assert(V == kScanChunk / LPC, "one row element per token group");
     __shared__ __align__(16) float s_b[2][kScanChunk][NP], s_c[2][kScanChunk][NP];
     __shared__ __align__(16) float s_du[2][kScanChunk / 2][kStepLd];
+    __shared__ __align__(16) float s_y[2][kScanChunk][YLD];
     const uint32_t slot = blockIdx.x / ncb;
     const Piece q = uniform(piece_of(seg, slot));
     if (q.seq < 0)
         return;
     const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
     const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lp = step_place(threadIdx.x / LPC);
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, lp = step_place(lc);
     const int64_t c = l.c;
     float A2[NS], h[NS];
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
@@ -128,11 +129,11 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
                 const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lp]);
                 d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
             }
-            // (the previous chunk's sums lie where its d were: this thread's own
-            // places, which it fills with the next chunk's below)
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                y[v] = s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + v)];
+            for (int v = 0; v < V; v += 4) {
+                const f32x4 p = *reinterpret_cast<const f32x4*>(&s_y[buf ^ 1][token][ch + v]);
+                y[v] = p[0], y[v + 1] = p[1], y[v + 2] = p[2], y[v + 3] = p[3];
+            }
 #pragma unroll
             for (int g = 0; g < V; ++g) {
                 float p[LPC];
@@ -161,8 +162,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
-                // lane s: token s of the group, whose d the channel's lanes have read
-                s_du[buf][(g * LPC + s) / 2][4 * lp + 2 * (s & 1)] = sum_transposed(p, s);
+                s_y[buf][g * LPC + s][lc] = sum_transposed(p, s);
             }
             // (unconditional, into nothing for the first chunk: behind a branch the
             // wait for the next chunk's loads would also wait for the store)
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
         float y[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            y[v] = fmaf(skip[v], px.get(v), s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + v)]);
+            y[v] = fmaf(skip[v], px.get(v), s_y[buf ^ 1][token][ch + v]);
             if constexpr (GATE)
                 y[v] *= silu_f(pz.get(v));
         }
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
         return;
     const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
     const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lp = step_place(threadIdx.x / LPC);
+    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, lp = step_place(lc);
     const int64_t c = l.c;
     float A2[NS], h[NS] = {}, sum = 0.f;
     load_states<NS>(a.A + c * N, s, N, l.on, A2);
