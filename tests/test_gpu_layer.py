@@ -535,6 +535,17 @@ def test_values_outside_the_sequences_do_not_matter():
     assert bool(dirty["y"][o[s]].isnan().any())
 
 
+def test_scan_small_and_large_steps_of_bf16_rows():
+    """bf16 rows form softplus with its exponent x log2(e) as rounded: one
+    rounding of the product and one of the constant, each 2^-24 |x| of the
+    result at most, beside the 16 of the rest."""
+    raw = torch.linspace(-60, 60, 481).bfloat16().cuda()
+    x, one = torch.ones(1, 1, 481).bfloat16().cuda(), torch.ones(1, 1, 1, 1).bfloat16().cuda()
+    _, h = layer.scan_forward(x, raw.view(1, 1, -1), torch.zeros(481, 1).cuda(), one, one)
+    want = torch.nn.functional.softplus(raw.cpu().double(), threshold=100)
+    close(h.view(-1), want, want.abs(), 16 + 2 * 60, "softplus")
+
+
 @pytest.mark.parametrize("algo", ["staged", "segmented"])
 def test_infinite_decay(algo):
     """A = -inf (and values whose multiple by log2(e) overflows) forgets the
