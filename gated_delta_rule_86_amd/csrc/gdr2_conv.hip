@@ -268,25 +268,31 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a
 }
 
 // ---------------------------------------------------------------------------
-// Column sums.  A workgroup owns 64 columns; its 4 waves take every fourth
-// partial row and are added in wave order.
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int64_t P, int64_t ld, int64_t M, ColumnOut a,
-                                                         ColumnOut b, ColumnOut c)
+// Column sums.  A workgroup owns 64 columns; its 4 or 16 waves take every 4th
+// or 16th partial row and are added in wave order.  The latency of a wave's rows
+// in turn is the time, so many rows get 16 waves: 512 rows of 4096 columns 4.9 us
+// (with 4 waves 6.6); the launch of larger workgroups costs more than that saves
+// on 64 rows (0.6 us).
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void column_sum_kernel(const float* part, int64_t P, int64_t ld, int64_t M, ColumnOut a,
+                                                                ColumnOut b, ColumnOut c)
 {
-    __shared__ float s_sum[4][64];
+    __shared__ float s_sum[WAVES][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t m = (int64_t)blockIdx.x * 64 + lane;
     float s = 0.f;
     if (m < M) {
 #pragma unroll 8
-        for (int64_t p = wave; p < P; p += 4)
+        for (int64_t p = wave; p < P; p += WAVES)
             s += part[p * ld + m];
     }
     s_sum[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || m >= M)
         return;
-    s = (s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]);
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k)
+        s += s_sum[k][lane];
     if (m < a.n) {
         if (a.p)
             a.p[m] = s;
@@ -410,7 +416,11 @@ hipError_t launch_column_sum(const float* part, int64_t P, int64_t ld, ColumnOut
                              hipStream_t stream)
 {
     const int64_t M = a.n + b.n + c.n;
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)ceil_div(M, 64)), dim3(256), 0, stream, part, P, ld, M, a, b, c);
+    const dim3 grid((unsigned)ceil_div(M, 64));
+    if (P >= 256)
+        hipLaunchKernelGGL(column_sum_kernel<16>, grid, dim3(1024), 0, stream, part, P, ld, M, a, b, c);
+    else
+        hipLaunchKernelGGL(column_sum_kernel<4>, grid, dim3(256), 0, stream, part, P, ld, M, a, b, c);
     return hipGetLastError();
 }
 

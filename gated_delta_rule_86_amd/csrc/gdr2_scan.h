@@ -85,6 +85,7 @@ struct ScanPlan {
     bool split;       // sequences may have more than one segment
 };
 ScanPlan scan_plan(const gdr2_scan_args& a);
+constexpr int kFoldAhead = 8;     // segments whose values the folds load together
 
 // This lane's place in the states layout.
 struct ScanLane {

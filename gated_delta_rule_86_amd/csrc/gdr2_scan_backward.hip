@@ -436,14 +436,25 @@ __global__ __launch_bounds__(256) void scan_backward_fold_kernel(gdr2_scan_bwd_a
     const float A2 = exponent_scale(a.A[cn]);
     float lam = p.dh_out ? p.dh_out[id] : 0.f;
     const int64_t nseg = max((int64_t)1, (q.len + ((int64_t)1 << seg.lg) - 1) >> seg.lg);
-    for (int64_t i = nseg - 1; i >= 0; --i) {
-        float* at = states + (q.first + i) * per + cn;
-        float next = 0.f;
-        if (i > 0)
-            next = fmaf(fast_exp2(A2 * sums[(q.first + i) * a.C + c]), lam, *at);
-        *at = lam;
-        lam = next;
+    float* at = states + q.first * per + cn;
+    const float* sum = sums + q.first * a.C + c;
+    // the first segment has nothing before it to pass its gradient to
+    for (int64_t i = nseg - 1; i > 0; i -= kFoldAhead) {
+        float e[kFoldAhead], d[kFoldAhead];
+#pragma unroll
+        for (int k = 0; k < kFoldAhead; ++k) {
+            const bool in = i - k > 0;
+            e[k] = in ? at[(i - k) * per] : 0.f;
+            d[k] = in ? sum[(i - k) * a.C] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kFoldAhead; ++k)
+            if (i - k > 0) {
+                at[(i - k) * per] = lam;
+                lam = fmaf(fast_exp2(A2 * d[k]), lam, e[k]);
+            }
     }
+    at[0] = lam;
 }
 
 // dB and dC: the channel blocks' partial sums of each row, in block order.
