@@ -6,16 +6,25 @@
 //   dw[k] = sum_t dp[t] x[t - (K-1) + k];  dbias = sum_t dp[t]
 //
 // K <= 4 products per element against 2 to 6 bytes of traffic: memory bounds
-// it.  A thread walks a piece of rows of V adjacent channels with
-// the last K - 1 rows in registers, so each row is loaded once per piece and
-// only K - 1 rows per piece are read twice.
+// it.  A thread walks a piece of rows of V adjacent channels with the last K - 1
+// rows in registers, so each row is loaded once per piece and only K - 1 rows per
+// piece are read twice.  At 8 x 4096 x 2048 bf16, four taps: 268 MB in 56 us, 4.8
+// TB/s (a large copy: 5.1); gradients 403 MB in 92.8 us, 4.3 TB/s, where forming
+// p, its slope, dx and the five sums (32 operations an element) keeps the vector
+// units busy three quarters of the time.
 #include "gdr2_layer.h"
 
 namespace gdr2 {
 
 namespace {
 
-constexpr int kRows = 4;   // rows loaded together; >= K
+// Rows of V channels loaded together (>= K), so that enough bytes are in flight.
+// Forwards 8 (8 x 4096 x 2048 bf16: 57 us, with 4 rows 60); backwards, where two
+// row arrays are loaded and the next rows too, 8 of single channels (41.4 us for
+// 10007 x 1003 fp32 rows, with 4 44.1) and 4 of wider ones (8 there take all the
+// registers: 95 us against 92.8 at 8 x 4096 x 2048).
+constexpr int kForwardRows = 8;
+template <int V> constexpr int kBackwardRows = V == 1 ? 8 : 4;
 
 template <typename T, int V, int K>
 __device__ __forceinline__ void load_taps(const float* weight, const float* bias, int64_t c0, float (&w)[K][V], float (&b)[V])
@@ -74,13 +83,13 @@ __global__ __launch_bounds__(256) void conv_forward_kernel(gdr2_conv_args a, Pie
         for (int j = 0; j < K - 1; ++j)
             *reinterpret_cast<typename Raw<T, V>::Type*>(so + j * C) = last[j];
     }
-    for (int64_t t = t0; t < t1; t += kRows) {
-        typename Raw<T, V>::Type raw[kRows];
+    for (int64_t t = t0; t < t1; t += kForwardRows) {
+        typename Raw<T, V>::Type raw[kForwardRows];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u)
+        for (int u = 0; u < kForwardRows; ++u)
             raw[u] = t + u < t1 ? Raw<T, V>::load(x + (t + u) * a.x_stride) : Raw<T, V>::zero();
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
+        for (int u = 0; u < kForwardRows; ++u) {
             float xv[V], o[V];
             Raw<T, V>::get(raw[u], xv);
 #pragma unroll
@@ -144,6 +153,7 @@ template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a, Pieces pc, uint32_t ncv, int lw,
                                                             uint32_t ncb, float* part)
 {
+    constexpr int ROWS = kBackwardRows<V>;
     __shared__ float s_red[256 * V];
     const uint32_t rows_per = 256u >> lw;
     const uint32_t pb = blockIdx.x / ncb;                      // piece block
@@ -172,26 +182,26 @@ __global__ __launch_bounds__(256) void conv_backward_kernel(gdr2_conv_bwd_args a
             Raw<T, V>::get(conv_row<T, V, K>(x, a.x_stride, state, C, t0 - (K - 1) + j, q.len), win[j]);
         // rows t0 .. t1 + K-2: the K - 1 beyond the piece only feed its dx
         const int64_t end = t1 + K - 1, exist = min(q.len, end);
-        typename Raw<T, V>::Type nx[kRows], nd[kRows];
+        typename Raw<T, V>::Type nx[ROWS], nd[ROWS];
         auto fetch = [&](int64_t t) {
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 const bool in = t + u < exist;
                 nx[u] = in ? Raw<T, V>::load(x + (t + u) * a.x_stride) : Raw<T, V>::zero();
                 nd[u] = in ? Raw<T, V>::load(dy + (t + u) * C) : Raw<T, V>::zero();
             }
         };
         fetch(t0);
-        for (int64_t t = t0; t < end; t += kRows) {
-            typename Raw<T, V>::Type rx[kRows], rd[kRows];
+        for (int64_t t = t0; t < end; t += ROWS) {
+            typename Raw<T, V>::Type rx[ROWS], rd[ROWS];
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 rx[u] = nx[u];
                 rd[u] = nd[u];
             }
-            fetch(t + kRows);
+            fetch(t + ROWS);
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
+            for (int u = 0; u < ROWS; ++u) {
                 float xv[V], dv[V], o[V];
                 Raw<T, V>::get(rx[u], xv);
                 Raw<T, V>::get(rd[u], dv);
@@ -311,25 +321,18 @@ int64_t items_of(int64_t B, int64_t T, int64_t ncv, bool packed, int lg)
     return p.slots() * ncv;
 }
 
-// Rows of one piece: 32, fewer (down to 8) while that leaves threads below
-// two waves per SIMD.
-int forward_lg(int64_t B, int64_t T, int64_t ncv, bool packed)
+// Rows of one piece, fewer (down to 8) while that leaves threads below two waves
+// per SIMD.  Forwards 64 at most (8 x 4096 x 2048 bf16: 56.1 us; 32 rows 56.9, 16
+// rows 60), backwards 128 (with four waves per SIMD asked for instead of two, and so
+// 64 rows: 108 us against 92.8).
+int piece_lg(int lg, int64_t B, int64_t T, int64_t ncv, bool packed)
 {
     const int64_t want = (int64_t)device_cu_count() * 4 * 2 * 64;
-    int lg = 5;
     while (lg > 3 && items_of(B, T, ncv, packed, lg) < want)
         --lg;
     return lg;
 }
-
-int backward_lg(int64_t B, int64_t T, int64_t ncv, bool packed)
-{
-    const int64_t want = (int64_t)device_cu_count() * 4 * 2 * 64;
-    int lg = 7;
-    while (lg > 3 && items_of(B, T, ncv, packed, lg) < want)
-        --lg;
-    return lg;
-}
+constexpr int kForwardLg = 6, kBackwardLg = 7;
 
 struct BackwardPlan {
     bool vec;
@@ -359,7 +362,7 @@ BackwardPlan backward_plan(const gdr2_conv_bwd_args& a, bool vec)
     while (p.lw < 6 && ((int64_t)1 << p.lw) < p.ncv)
         ++p.lw;
     p.ncb = ceil_div(p.ncv, (int64_t)1 << p.lw);
-    p.lg = backward_lg(a.B, a.T, p.ncv, a.offsets != nullptr);
+    p.lg = piece_lg(kBackwardLg, a.B, a.T, p.ncv, a.offsets != nullptr);
     Pieces pc{a.offsets, a.B, a.T, p.lg};
     p.npb = ceil_div(pc.slots(), 256 >> p.lw);
     return p;
@@ -369,7 +372,7 @@ template <typename T, int V>
 hipError_t forward_k(const gdr2_conv_args& a, hipStream_t stream)
 {
     const int64_t ncv = a.C / V;
-    const int lg = forward_lg(a.B, a.T, ncv, a.offsets != nullptr);
+    const int lg = piece_lg(kForwardLg, a.B, a.T, ncv, a.offsets != nullptr);
     const Pieces pc{a.offsets, a.B, a.T, lg};
     const dim3 grid((unsigned)ceil_div(pc.slots() * ncv, 256));
     switch (a.width) {
