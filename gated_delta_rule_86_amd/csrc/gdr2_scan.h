@@ -110,7 +110,7 @@ __device__ __forceinline__ ScanBlock scan_block(const gdr2_scan_args& a, uint32_
 }
 template <int LPC> __device__ __forceinline__ ScanLane scan_lane(const ScanBlock& b)
 {
-    const int i = threadIdx.x / LPC;
+    const int i = threadIdx.x % (64 * LPC) / LPC;
     return {b.c0 + (i < b.n ? i : 0), (int)(threadIdx.x % LPC), i < b.n};
 }
 
@@ -223,7 +223,7 @@ template <typename T, int V, bool WIDE> struct RowVec {
 
     __device__ __forceinline__ RowVec(int64_t ld, const ScanBlock& b)
     {
-        const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
+        const int token = threadIdx.x / (kScanCols / V) % kScanChunk, ch = threadIdx.x % (kScanCols / V) * V;
         n = min(V, max(0, b.n - ch));
         off = n > 0 ? (uint32_t)(token * (int)ld + (int)b.c0 + ch) * (uint32_t)sizeof(T) : kNowhere;
     }
@@ -302,7 +302,7 @@ template <typename T, int NP, int NT> struct Staged {
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = threadIdx.x + NT * i, r = e / NP, n = e % NP;
+            const int e = threadIdx.x % NT + NT * i, r = e / NP, n = e % NP;
             off[i] = n < N ? (uint32_t)(r * (int)ld + (int)j * N + n) * (uint32_t)sizeof(T) : kNowhere;
         }
     }
@@ -317,7 +317,7 @@ template <typename T, int NP, int NT> struct Staged {
     {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int e = threadIdx.x + NT * i;
+            const int e = threadIdx.x % NT + NT * i;
             dst[e / NP][e % NP] = raw_f32<T>(raw[i]);
         }
     }

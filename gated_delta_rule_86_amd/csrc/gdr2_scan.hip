@@ -29,18 +29,17 @@ template <typename T> __device__ __forceinline__ void step_to_lds(float dt, floa
 }
 
 // A workgroup walks its segment chunk by chunk, one barrier per chunk (the LDS
-// arrays alternate between two buffers).  Between two barriers, interleaved
-// token group by token group so that the latencies of one fill with the
-// arithmetic of the others:
-//   states: the recurrence over chunk i, its sums into LDS
-//   rows:   (d, d x) of chunk i + 1 into LDS; skip and gate of chunk i - 1's sums
-//   loads:  the rows of chunk i + 2 are on their way
+// arrays alternate between two buffers).  Between two barriers the waves of its
+// two halves run
+//   states: the recurrence over chunk i, its sums over n into LDS
+//   rows:   (d, d x), B and C of chunk i + 1 into LDS; skip and gate of chunk
+//           i - 1's sums and the store of its rows; the loads of chunk i + 2
+// Each SIMD holds a wave of either kind, which fill each other's latencies.
 template <typename T, int LPC, int NS, bool GATE, bool WIDE>
-__global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
-                                                                const float* starts)
+__global__ __launch_bounds__(128 * LPC) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
+                                                                 const float* starts)
 {
     constexpr int NP = LPC * NS, NT = 64 * LPC, V = kScanChunk * kScanCols / NT, YLD = kScanCols + 16;
-    static_assert(V == kScanChunk / LPC, "one row element per token group");
     __shared__ __align__(16) float s_b[2][kScanChunk][NP], s_c[2][kScanChunk][NP];
     __shared__ __align__(16) float s_du[2][kScanChunk / 2][kStepLd];
     __shared__ __align__(16) float s_y[2][kScanChunk][YLD];
@@ -49,28 +48,77 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
     if (q.seq < 0)
         return;
     const ScanBlock blk = scan_block(a, blockIdx.x - slot * ncb, cb_per);
-    const ScanLane l = scan_lane<LPC>(blk);
-    const int s = l.s, N = (int)a.N, lc = threadIdx.x / LPC, lp = step_place(lc);
-    const int64_t c = l.c;
-    float A2[NS], h[NS];
-    load_states<NS>(a.A + c * N, s, N, l.on, A2);
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-        A2[i] = exponent_scale(A2[i]);
-    if (starts)
-        load_states<NS>(starts + ((int64_t)slot * a.C + c) * N, s, N, l.on, h);
-    else
-        load_states<NS>(a.h0 + (q.seq * a.C + c) * N, s, N, l.on && a.h0, h);
+    const int N = (int)a.N;
     const int64_t t0 = q.index << seg.lg;
     const int64_t t1 = min(q.len, t0 + ((int64_t)1 << seg.lg));
-    if (t0 < t1) {
+    int buf = 0;
+    if (__builtin_amdgcn_readfirstlane(threadIdx.x) < NT) {
+        // ---- states
+        const ScanLane l = scan_lane<LPC>(blk);
+        const int s = l.s, lc = threadIdx.x / LPC, lp = step_place(lc);
+        const int64_t c = l.c;
+        float A2[NS], h[NS];
+        load_states<NS>(a.A + c * N, s, N, l.on, A2);
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            A2[i] = exponent_scale(A2[i]);
+        if (starts)
+            load_states<NS>(starts + ((int64_t)slot * a.C + c) * N, s, N, l.on, h);
+        else
+            load_states<NS>(a.h0 + (q.seq * a.C + c) * N, s, N, l.on && a.h0, h);
+        const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
+        const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
+        for (int64_t t = t0; t < t1; t += kScanChunk, buf ^= 1) {
+            if (a.h_chunks)
+                store_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * a.C + c) * N, s, N, l.on, h);
+            lds_barrier();
+            // what a token needs is read one token group ahead of its use
+            float B[LPC][NS], C[LPC][NS], d[LPC], u[LPC];
+#pragma unroll
+            for (int k = 0; k < LPC; ++k) {
+                read_states<NS>(&s_b[buf][k][s * NS], B[k]);
+                read_states<NS>(&s_c[buf][k][s * NS], C[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < LPC; k += 2) {
+                const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lp]);
+                d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
+            }
+#pragma unroll
+            for (int g = 0; g < kScanChunk / LPC; ++g) {
+                float p[LPC];
+#pragma unroll
+                for (int k = 0; k < LPC; ++k) {
+#pragma unroll
+                    for (int i = 0; i < NS; ++i) {
+                        h[i] = fmaf(fast_exp2(d[k] * A2[i]), h[i], u[k] * B[k][i]);
+                        p[k] = i == 0 ? C[k][0] * h[0] : fmaf(C[k][i], h[i], p[k]);
+                    }
+                    const int next = (g + 1) * LPC + k;
+                    if (next < kScanChunk) {
+                        read_states<NS>(&s_b[buf][next][s * NS], B[k]);
+                        read_states<NS>(&s_c[buf][next][s * NS], C[k]);
+                        if (k % 2) {
+                            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lp]);
+                            d[k - 1] = x[0], u[k - 1] = x[1], d[k] = x[2], u[k] = x[3];
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                s_y[buf][g * LPC + s][lc] = sum_transposed(p, s);
+            }
+        }
+        if (t0 < t1)
+            lds_barrier();
+        if (a.h_out && t1 == q.len)
+            store_states<NS>(a.h_out + (q.seq * a.C + c) * N, s, N, l.on, h);
+    } else if (t0 < t1) {
+        // ---- rows
         float bias[V], skip[V];
         channel_params<V>(a.dt_bias, blk, bias);
         channel_params<V>(a.skip, blk, skip);
         const bool soft = a.flags & GDR2_SCAN_SOFTPLUS;
-        const Pieces ckp{a.offsets, a.B, a.T, kScanLg};
-        const int64_t ck0 = uniform(sequence_of(ckp, q.seq).first);
-        const int token = threadIdx.x / (kScanCols / V), ch = threadIdx.x % (kScanCols / V) * V;
+        const int token = threadIdx.x / (kScanCols / V) % kScanChunk, ch = threadIdx.x % (kScanCols / V) * V;
         const int du_at = 2 * (token & 1);
         auto left_at = [&](int64_t t) { return (int)max((int64_t)0, min(t1 - t, (int64_t)kScanChunk)); };
 
@@ -96,76 +144,43 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
                 wz.advance(kScanChunk);
             }
         };
-        fetch(left_at(t0));
+        auto steps = [&](const RowVec<T, V, WIDE>& dt, const RowVec<T, V, WIDE>& x, bool in, int to) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            step_to_lds<T>(rt.get(v), rx.get(v), bias[v], soft, token < left_at(t0), &s_du[0][token / 2][du_at + 4 * step_place(ch + v)]);
-        }
+            for (int v = 0; v < V; ++v)
+                step_to_lds<T>(dt.get(v), x.get(v), bias[v], soft, in, &s_du[to][token / 2][du_at + 4 * step_place(ch + v)]);
+        };
+        auto outputs = [&](const RowVec<T, V, WIDE>& x, const RowVec<T, V, WIDE>& z, int from, float (&y)[V]) {
+#pragma unroll
+            for (int v = 0; v < V; v += 4) {
+                const f32x4 p = *reinterpret_cast<const f32x4*>(&s_y[from][token][ch + v]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[v + i] = fmaf(skip[v + i], x.get(v + i), p[i]);
+                    if constexpr (GATE)
+                        y[v + i] *= silu_f(z.get(v + i));
+                }
+            }
+        };
+        fetch(left_at(t0));
+        steps(rt, rx, token < left_at(t0), 0);
         // x, z of the previous chunk (nothing yet) and of the current one
         RowVec<T, V, WIDE> px = rx, pz = rz, cx = rx, cz = rz;
         rb.store(s_b[0]);
         rc.store(s_c[0]);
         fetch(left_at(t0 + kScanChunk));
-        int buf = 0;
         int64_t t = t0;
+        float y[V];
         for (; t < t1; t += kScanChunk, buf ^= 1) {
-            if (a.h_chunks)
-                store_states<NS>(a.h_chunks + ((ck0 + (t >> kScanLg)) * a.C + c) * N, s, N, l.on, h);
             // the next chunk's rows have arrived; those after it are requested
             RowVec<T, V, WIDE> nt = rt, nx = rx, nz = rz;
-            const bool in = token < left_at(t + kScanChunk);
             lds_barrier();
             rb.store(s_b[buf ^ 1]);
             rc.store(s_c[buf ^ 1]);
             fetch(left_at(t + 2 * kScanChunk));
-            float B[LPC][NS], C[LPC][NS], d[LPC], u[LPC], y[V];
-#pragma unroll
-            for (int k = 0; k < LPC; ++k) {
-                read_states<NS>(&s_b[buf][k][s * NS], B[k]);
-                read_states<NS>(&s_c[buf][k][s * NS], C[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < LPC; k += 2) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][k / 2][4 * lp]);
-                d[k] = x[0], u[k] = x[1], d[k + 1] = x[2], u[k + 1] = x[3];
-            }
-#pragma unroll
-            for (int v = 0; v < V; v += 4) {
-                const f32x4 p = *reinterpret_cast<const f32x4*>(&s_y[buf ^ 1][token][ch + v]);
-                y[v] = p[0], y[v + 1] = p[1], y[v + 2] = p[2], y[v + 3] = p[3];
-            }
-#pragma unroll
-            for (int g = 0; g < V; ++g) {
-                float p[LPC];
-#pragma unroll
-                for (int k = 0; k < LPC; ++k) {
-#pragma unroll
-                    for (int i = 0; i < NS; ++i) {
-                        h[i] = fmaf(fast_exp2(d[k] * A2[i]), h[i], u[k] * B[k][i]);
-                        p[k] = i == 0 ? C[k][0] * h[0] : fmaf(C[k][i], h[i], p[k]);
-                    }
-                    const int next = (g + 1) * LPC + k;
-                    if (next < kScanChunk) {
-                        read_states<NS>(&s_b[buf][next][s * NS], B[k]);
-                        read_states<NS>(&s_c[buf][next][s * NS], C[k]);
-                        if (k % 2) {
-                            const f32x4 x = *reinterpret_cast<const f32x4*>(&s_du[buf][next / 2][4 * lp]);
-                            d[k - 1] = x[0], u[k - 1] = x[1], d[k] = x[2], u[k] = x[3];
-                        }
-                    }
-                    if (k == 1)
-                        step_to_lds<T>(nt.get(g), nx.get(g), bias[g], soft, in, &s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + g)]);
-                    if (k == LPC - 2) {
-                        y[g] = fmaf(skip[g], px.get(g), y[g]);
-                        if constexpr (GATE)
-                            y[g] *= silu_f(pz.get(g));
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                s_y[buf][g * LPC + s][lc] = sum_transposed(p, s);
-            }
+            steps(nt, nx, token < left_at(t + kScanChunk), buf ^ 1);
             // (unconditional, into nothing for the first chunk: behind a branch the
             // wait for the next chunk's loads would also wait for the store)
+            outputs(px, pz, buf ^ 1, y);
             ry.store(wy, t > t0 ? kScanChunk : 0, y);
             wy.advance(t > t0 ? kScanChunk : 0);
             px = cx;
@@ -174,17 +189,9 @@ __global__ __launch_bounds__(64 * LPC) void scan_forward_kernel(gdr2_scan_args a
             cz = nz;
         }
         lds_barrier();
-        float y[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            y[v] = fmaf(skip[v], px.get(v), s_y[buf ^ 1][token][ch + v]);
-            if constexpr (GATE)
-                y[v] *= silu_f(pz.get(v));
-        }
+        outputs(px, pz, buf ^ 1, y);
         ry.store(wy, left_at(t - kScanChunk), y);
     }
-    if (a.h_out && t1 == q.len)
-        store_states<NS>(a.h_out + (q.seq * a.C + c) * N, s, N, l.on, h);
 }
 
 // (sum d, E) of every segment but the last of its sequence: whole segments.
@@ -419,9 +426,9 @@ hipError_t forward_t(const gdr2_scan_args& a, hipStream_t stream)
             return e;
     }
     if (a.z)
-        hipLaunchKernelGGL((scan_forward_kernel<T, LPC, NS, true, WIDE>), grid, block, 0, stream, a, p.seg, ncb, cb_per, states);
+        hipLaunchKernelGGL((scan_forward_kernel<T, LPC, NS, true, WIDE>), grid, dim3(128 * LPC), 0, stream, a, p.seg, ncb, cb_per, states);
     else
-        hipLaunchKernelGGL((scan_forward_kernel<T, LPC, NS, false, WIDE>), grid, block, 0, stream, a, p.seg, ncb, cb_per, states);
+        hipLaunchKernelGGL((scan_forward_kernel<T, LPC, NS, false, WIDE>), grid, dim3(128 * LPC), 0, stream, a, p.seg, ncb, cb_per, states);
     return hipGetLastError();
 }
 
@@ -508,7 +515,7 @@ int64_t scan_launch_groups(const gdr2_scan_args& a)
     int64_t n;
     if (__builtin_mul_overflow(p.seg.slots(), p.ncb, &n))
         return kMaxGroups;
-    n *= a.N > 16 ? 2 : 1;            // workgroups of 512 threads: counted as two of 256
+    n *= a.N > 16 ? 4 : 2;            // workgroups of 1024 and 512 threads, counted as of 256
     return max(n, ceil_div(a.B * a.C * max((int64_t)8, a.N), 256));
 }
 

@@ -347,9 +347,9 @@ def test_row_strides_of_expanded_rows():
 
 
 def test_refuses_more_threads_than_one_launch_takes(lib):  # noqa: F811
-    """State sizes above 16 run in workgroups of 512 threads: a grid of 2^32
-    threads is refused here, not by the launch."""
-    for N, C, B, ok in ((32, 1, 9_000_000, False), (16, 1, 9_000_000, True), (32, 1, 8_000_000, True)):
+    """The scan runs in workgroups of 512 threads, of 1024 for state sizes above
+    16: a grid of 2^32 threads is refused here, not by the launch."""
+    for N, C, B, ok in ((32, 1, 4_200_000, False), (32, 1, 4_100_000, True), (16, 1, 8_400_000, False), (16, 1, 8_300_000, True)):
         a = layer.ScanArgs(B=B, T=1, C=C, N=N, G=1, x_stride=1, dt_stride=1, b_stride=N, c_stride=N, dtype=gdr2.F32)
         status = lib.gdr2_scan_forward(ctypes.byref(a), None)       # every pointer is NULL: nothing launches
         assert status == (INV if ok else UNS), (N, B)
