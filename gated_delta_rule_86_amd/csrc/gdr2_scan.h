@@ -84,7 +84,7 @@ struct ScanPlan {
     int64_t cb_per;   // per group
     bool split;       // sequences may have more than one segment
 };
-ScanPlan scan_plan(const gdr2_scan_args& a);
+ScanPlan scan_plan(const gdr2_scan_args& a, bool backward);
 constexpr int kFoldAhead = 8;     // segments whose values the folds load together
 
 // This lane's place in the states layout.

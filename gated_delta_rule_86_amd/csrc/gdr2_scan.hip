@@ -5,8 +5,11 @@
 //   y_t = v_t silu(z_t)
 //
 // Per (token, channel, state): one multiply for the exponent, one exp2, and
-// three multiply-adds.  At 16 states that arithmetic, not the 8 bytes a
-// channel moves per token, bounds a prompt.
+// three multiply-adds.  At 16 states that arithmetic, not the 8 bytes a channel
+// moves per token, bounds a prompt: 8 x 4096 x 2048 channels, gated, in bf16 take
+// 254 us, of which the exponentials, multiplies and adds are 178 us at the issue
+// rate measured for them (4.3 cycles a wave, 8.9 for exp2) and the 540 MB 106 us
+// at the rate of a large copy.
 //
 // Segments: h is linear in its start, so over a segment h_end = P h_start + E
 // with P = exp(A sum d) and E the end state from zero.  A span pass forms
@@ -34,7 +37,9 @@ template <typename T> __device__ __forceinline__ void step_to_lds(float dt, floa
 //   states: the recurrence over chunk i, its sums over n into LDS
 //   rows:   (d, d x), B and C of chunk i + 1 into LDS; skip and gate of chunk
 //           i - 1's sums and the store of its rows; the loads of chunk i + 2
-// Each SIMD holds a wave of either kind, which fill each other's latencies.
+// Each SIMD holds a wave of either kind, which fill each other's latencies: 254 us
+// at 8 x 4096 x 2048 (256 workgroups), where waves that did both in turn, token
+// group by token group, took 346 us and kept the vector units busy 71 % of the time.
 template <typename T, int LPC, int NS, bool GATE, bool WIDE>
 __global__ __launch_bounds__(128 * LPC) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                                  const float* starts)
@@ -407,7 +412,7 @@ ForwardWork forward_work(const gdr2_scan_args& a, const ScanPlan& p)
 template <typename T, int LPC, int NS, bool WIDE>
 hipError_t forward_t(const gdr2_scan_args& a, hipStream_t stream)
 {
-    const ScanPlan p = scan_plan(a);
+    const ScanPlan p = scan_plan(a, false);
     const ForwardWork w = forward_work(a, p);
     const dim3 grid((unsigned)(p.seg.slots() * p.ncb)), block(64 * LPC);
     const uint32_t ncb = (uint32_t)p.ncb, cb_per = (uint32_t)p.cb_per;
@@ -473,16 +478,20 @@ hipError_t step_n(const gdr2_scan_step_args& a, hipStream_t stream)
 }  // namespace
 
 // How a call is cut into segments.
-// One segment per sequence when that gives every compute unit a workgroup:
-// at 8 x 4096 tokens and 2048 channels (256 workgroups) 353 us, against 407 us
-// with twice as many segments, for the span pass repeats most of the work.
-// Otherwise the longest segments that give every unit four workgroups, at
-// least 128 tokens: 1 x 32768 tokens (32 channel blocks) 467 us with 1024
-// workgroups, 485 us with 512, 610 us with 256, 1200 us with 128.
+// One segment per sequence where that keeps the compute units busy, for the span
+// pass repeats most of the work: forwards from 9/16 of a workgroup per unit on (2048
+// channels, 16 states, 4096 tokens: 128 workgroups 250 us whole, 228 in segments;
+// 160: 251 and 286; 256: 254 and 403), backwards, where two workgroups share a
+// unit, from 7/4 (2048 tokens: 256 workgroups 835 us whole, 678 in segments; 448:
+// 1107 and 1134; 512: 1126 and 1314).  Otherwise the longest segments that give
+// every unit four workgroups, at least 128 tokens: 1 x 32768 tokens (32 channel
+// blocks) 410 us with 1024 workgroups, 424 us with 512.
 // A packed batch is cut at twice its mean length in any case: the host does
 // not know the lengths, one sequence may hold nearly all rows, and sequences
-// that fit one segment skip the span pass.
-ScanPlan scan_plan(const gdr2_scan_args& a)
+// that fit one segment skip the span pass.  Some of its slots are idle and some
+// segments short, so whole segments have to give a workgroup per unit there (9
+// sequences, 5003 rows of 1002 channels: 75 us, with the dense rule 116).
+ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
 {
     ScanPlan p;
     p.cb_per = ceil_div(a.C / a.G, kScanCols);
@@ -500,7 +509,7 @@ ScanPlan scan_plan(const gdr2_scan_args& a)
             while (lg > shortest && ((int64_t)1 << (lg - 1)) >= 2 * ceil_div(a.T, max(a.B, (int64_t)1)))
                 --lg;
         const int64_t cus = device_cu_count();
-        if (groups(lg) < cus)
+        if (16 * groups(lg) < (backward ? 28 : a.offsets ? 16 : 9) * cus)
             while (lg > shortest && groups(lg) < 4 * cus)
                 --lg;
     }
@@ -511,7 +520,7 @@ ScanPlan scan_plan(const gdr2_scan_args& a)
 
 int64_t scan_launch_groups(const gdr2_scan_args& a)
 {
-    const ScanPlan p = scan_plan(a);
+    const ScanPlan p = scan_plan(a, true);      // never fewer segments than forwards
     int64_t n;
     if (__builtin_mul_overflow(p.seg.slots(), p.ncb, &n))
         return kMaxGroups;
@@ -519,11 +528,10 @@ int64_t scan_launch_groups(const gdr2_scan_args& a)
     return max(n, ceil_div(a.B * a.C * max((int64_t)8, a.N), 256));
 }
 
-size_t scan_workspace_bytes(const gdr2_scan_args& a) { return forward_work(a, scan_plan(a)).total; }
+size_t scan_workspace_bytes(const gdr2_scan_args& a) { return forward_work(a, scan_plan(a, false)).total; }
 
-// Lanes per channel and states per lane.  16 states run on 4 lanes of 4: 8 lanes
-// of 2 (twice the waves) took 351 us against 353 at 8 x 4096 x 2048, 561 against
-// 485 in segments; 32 states need the 8 lanes for their registers.
+// Lanes per channel and states per lane.  16 states run on 4 lanes of 4, which need
+// half the LDS reads of 8 lanes of 2; 32 states need the 8 lanes for their registers.
 hipError_t launch_scan_forward(const gdr2_scan_args& a, hipStream_t stream)
 {
     const bool bf = a.dtype == GDR2_BF16;
