@@ -111,6 +111,8 @@ __global__ __launch_bounds__(256) void conv_forward_kernel(gdr2_conv_args a, Pie
     }
 }
 
+// One token: a thread per sequence and vector of channels.  256 sequences of 2048
+// bf16 channels, 8.4 MB, take 4.2 us, about a launch.
 template <typename T, int V, int K>
 __global__ __launch_bounds__(256) void conv_step_kernel(gdr2_conv_step_args a, uint32_t ncv)
 {

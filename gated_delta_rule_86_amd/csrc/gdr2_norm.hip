@@ -12,7 +12,9 @@
 // each, so it is read once; mean and variance are two passes over those
 // registers (no E[x^2] - m^2 cancellation), sums in fp32.  A group keeps its
 // share of the weights in registers and walks rows g, g + groups, ..., with the
-// next row's loads in flight while it works on one.
+// next row's loads in flight while it works on one.  In bf16: 524288 gated rows of
+// 128, 403 MB, in 75 us, 5.4 TB/s (a large copy: 5.1); layer norm's gradients of
+// 32768 rows of 2048, 403 MB, in 81.5 us, 4.9 TB/s, 4.9 us of it the column sums.
 #include "gdr2_layer.h"
 
 namespace gdr2 {

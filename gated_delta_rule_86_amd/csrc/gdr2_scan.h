@@ -3,8 +3,8 @@
 //
 // Two layouts share the work of a chunk of 32 tokens x 64 channels of a group:
 //
-//   rows     thread (token, V adjacent channels): 2048 elements over the
-//            workgroup, 64 LPC threads.  Row arrays move in whole 128-byte
+//   rows     thread (token, V adjacent channels): 2048 elements over 64 LPC
+//            threads.  Row arrays move in whole 128-byte
 //            lines, each requested once per workgroup, and everything that is
 //            per (token, channel) is done here: the steps, the gate, stores.
 //   states   LPC adjacent lanes hold one channel, lane s its states s NS ..
@@ -13,7 +13,8 @@
 //            (token, channel, state) is done here: the decay exponentials, the
 //            recurrence, the product with C.
 //
-// LDS carries (d, d x) from rows to states and the sums over n back; B and C
+// The forward kernel has waves of its own for each; in the others the same waves
+// do both in turn.  LDS carries (d, d x) from rows to states and the sums over n back; B and C
 // are staged there in fp32 for the 64 channels.
 #pragma once
 

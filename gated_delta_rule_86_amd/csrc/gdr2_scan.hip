@@ -325,7 +325,9 @@ __global__ __launch_bounds__(256) void scan_fold_kernel(gdr2_scan_args a, Pieces
 
 // One token.  LPC lanes per channel, four states each; a thread keeps its
 // channel's A and parameters over R sequences, whose states are all requested
-// before the first is used.  The states' traffic bounds it.
+// before the first is used.  The states' traffic bounds it: 256 sequences of 2048
+// channels, 16 states, gated, in bf16 are 71 MB in 16.8 us, 4.3 TB/s; one sequence
+// takes 4 us, a launch.
 template <typename T, int LPC, int R, bool VEC>
 __global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p, uint32_t lanes)
 {
