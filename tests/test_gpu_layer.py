@@ -731,6 +731,31 @@ def test_other_stream():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("algo", ["staged", "segmented"])
+def test_two_calls_at_once(algo):
+    """Calls on two streams, each with memory of its own, do not meet; state
+    sizes of both workgroup sizes."""
+    cases = [scan_case((3, 300, 130, N, 1, False, True, True, True, True, algo), "bf16", 64 + N) for N in (16, 32)]
+    dys = [rn(gen(66), *a["x"].shape, dtype=a["x"].dtype) for a, *_ in cases]
+
+    def work(i):
+        a, kw, h0, _, _ = cases[i]
+        y, h, ck = layer.scan_forward(**a, **kw, h0=h0, chunk_states=True, algo=algo)
+        return [y, h, *(v for v in layer.scan_backward(**a, **kw, dy=dys[i], h_chunks=ck, algo=algo).values())]
+
+    want = [work(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(work(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for res in got[i]:
+            assert all(torch.equal(g, w) for g, w in zip(res, want[i]))
+
+
 def test_captured_and_replayed():
     """Forward and backward of all three in one graph, replayed on new inputs
     with eager work between the replays."""
