@@ -1,0 +1,91 @@
+"""GPU tests of the layer operators at the ends of their inputs' ranges, against
+the plain 64-bit implementation.  Tolerances as in tests/test_gpu_layer.py: half
+a step of the stored type, plus the number of fp32 roundings a term can pass
+through times 2^-24 times the magnitude sum of the terms."""
+import pytest
+import torch
+
+from gated_delta_rule_86_amd import layer
+from tests import layer_reference as ref
+from tests.layer_reference import close
+from tests.test_gpu_layer import DT, gen, rn, scan_case
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def lowest(dtype):
+    return torch.finfo(DT[dtype]).min
+
+
+# ---- steps that a mask or an overflow has made extreme ----------------------
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_step_at_the_ends_of_the_range(dtype):
+    """A state of one token from a zero state is d x B alone: softplus is 0 for
+    -inf and the type's lowest values (whose multiple by log2(e) overflows), x
+    for its largest, and NaN for NaN."""
+    big = -lowest(dtype)
+    raw = torch.tensor([-INF, -big, -2.4e38, -2.3e38, -1e30, -1e4, -200.0, 200.0, 1e4, 1e30, 2.3e38, 2.4e38, big, INF,
+                        float("nan")]).to(DT[dtype])
+    want = torch.where(raw < 0, torch.zeros_like(raw), raw).float()
+    C = raw.numel()
+    x, one = torch.ones(1, 1, C, dtype=DT[dtype]).cuda(), torch.ones(1, 1, 1, 1, dtype=DT[dtype]).cuda()
+    A = -torch.ones(C, 1).cuda()
+    _, h = layer.scan_forward(x, raw.cuda().view(1, 1, C), A, one, one)
+    s = torch.zeros(1, C, 1).cuda()
+    layer.scan_step(s, x[:, 0], raw.cuda().view(1, C), A, one[:, 0], one[:, 0])
+    for got in (h, s):
+        assert torch.equal(got.view(-1).cpu().nan_to_num(nan=-7.0, posinf=INF), want.nan_to_num(nan=-7.0, posinf=INF)), got
+
+
+MASKED = [
+    # B, T, C, N, G, packed, init, gate, extras, softplus, algo
+    (2, 130, 24, 16, 3, False, True, True, True, True, "staged"),
+    (2, 130, 24, 16, 3, False, True, True, True, True, "segmented"),
+    (1, 200, 40, 12, 1, False, True, False, True, True, "segmented"),
+    (1, 97, 64, 32, 1, False, True, True, True, True, "segmented"),
+    (0, 0, 20, 16, 2, True, True, True, True, True, "segmented"),
+]
+
+
+@pytest.mark.parametrize("value", ["-inf", "lowest"])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("c", MASKED, ids=[f"N{c[3]}{'p' if c[5] else ''}-{c[10]}" for c in MASKED])
+def test_masked_steps(c, dtype, value):
+    """Tokens whose dt is -inf or the type's lowest value leave the state as it
+    is, and no gradient reaches their dt."""
+    a, kw, h0, B, T = scan_case(c, dtype, 81)
+    g = gen(82)
+    off = torch.rand(a["dt"].shape[:-1], generator=g) < 0.3
+    off[..., :2] = True
+    off[..., 40:75] = True
+    off = off.cuda()
+    a["dt"][off] = -INF if value == "-inf" else lowest(dtype)
+    dy, dh = rn(g, *a["x"].shape, dtype=a["x"].dtype), rn(g, *h0.shape)
+    y, h, ck = layer.scan_forward(**a, **kw, h0=h0, chunk_states=True, algo=c[10])
+    got = layer.scan_backward(**a, **kw, dy=dy, h_chunks=ck, dh_out=dh, algo=c[10])
+    rkw = dict(kw, offsets=None if kw["offsets"] is None else kw["offsets"].cpu())
+    rows = slice(None) if not c[5] else slice(int(kw["offsets"][0]), int(kw["offsets"][-1]))
+    steps = 64 + 32 * (100 if c[5] else T)
+    (wy, wh, _), (by, bh, _) = (ref.scan(**a, **rkw, h0=h0, absolute=ab) for ab in (False, True))
+    close(y[rows], wy[rows], by[rows], steps, "y")
+    close(h, wh, bh, steps, "h")
+    wg, bg = (ref.scan_grad(**a, **rkw, dy=dy, h0=h0, dh_out=dh, absolute=ab) for ab in (False, True))
+    for n in got:
+        if got[n] is not None:
+            cut = rows if n in ("dx", "ddt", "dBt", "dCt", "dz") else slice(None)
+            close(got[n][cut], wg[n][cut], bg[n][cut], 2 * steps + a["x"].shape[0] * (1 if c[5] else T), n)
+    assert bool((got["ddt"][rows][off[rows]] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_masked_single_tokens(dtype):
+    """A step whose dt is -inf leaves its sequence's state bit for bit."""
+    c = (6, 1, 40, 16, 2, False, True, True, True, True, "auto")
+    a, kw, h0, _, _ = scan_case(c, dtype, 83)
+    a["dt"][1], a["dt"][4] = -INF, lowest(dtype)
+    s = h0.clone()
+    layer.scan_step(s, **{n: (t if n == "A" else t[:, 0]) for n, t in a.items()}, skip=kw["skip"], z=kw["z"][:, 0],
+                    dt_bias=kw["dt_bias"])
+    assert torch.equal(s[[1, 4]], h0[[1, 4]]) and bool(s.isfinite().all()) and not torch.equal(s[0], h0[0])
