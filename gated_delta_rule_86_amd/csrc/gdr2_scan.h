@@ -374,6 +374,18 @@ __device__ __forceinline__ float finite(float v)
 }
 __device__ __forceinline__ float exponent_scale(float A) { return finite(A * kLog2e); }
 
+// 2^t h + e, t a whole segment's exponent.  Where 2^t nears the ends of the
+// format it would be inf or 0 while the state, before and after, is neither
+// (and inf times a zero state NaN): there the power of two is applied to the
+// product, exactly.  (A NaN t takes the first form.)
+__device__ __forceinline__ float segment_decay(float t, float h, float e)
+{
+    if (!(fabsf(t) > 120.f))
+        return fmaf(fast_exp2(t), h, e);
+    const float c = fminf(fmaxf(t, -1000.f), 1000.f), n = rintf(c);
+    return ldexpf(fast_exp2(c - n) * h, (int)n) + e;
+}
+
 // The step from its raw value.  softplus is formed either way: behind a branch
 // per element it would split the block it is scheduled in.
 template <typename T> __device__ __forceinline__ float step_of(float raw, bool softplus)

@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256) void scan_fold_kernel(gdr2_scan_args a, Pieces
         for (int k = 0; k < kFoldAhead; ++k)
             if (i + k + 1 < nseg) {
                 at[(i + k) * per] = h;
-                h = fmaf(fast_exp2(A2 * d[k]), h, e[k]);
+                h = segment_decay(A2 * d[k], h, e[k]);
             }
     }
     at[(nseg - 1) * per] = h;

@@ -453,7 +453,7 @@ __global__ __launch_bounds__(256) void scan_backward_fold_kernel(gdr2_scan_bwd_a
         for (int k = 0; k < kFoldAhead; ++k)
             if (i - k > 0) {
                 at[(i - k) * per] = lam;
-                lam = fmaf(fast_exp2(A2 * d[k]), lam, e[k]);
+                lam = segment_decay(A2 * d[k], lam, e[k]);
             }
     }
     at[0] = lam;

@@ -89,3 +89,66 @@ def test_masked_single_tokens(dtype):
     layer.scan_step(s, **{n: (t if n == "A" else t[:, 0]) for n, t in a.items()}, skip=kw["skip"], z=kw["z"][:, 0],
                     dt_bias=kw["dt_bias"])
     assert torch.equal(s[[1, 4]], h0[[1, 4]]) and bool(s.isfinite().all()) and not torch.equal(s[0], h0[0])
+
+
+# ---- decays of a whole segment outside the format's range -------------------
+
+# the steps of three segments of 64 tokens, then 64 tokens of little decay
+LEAD, TAIL = 192, 64
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("algo", ["staged", "segmented"])
+def test_growth_of_a_zero_state(algo, sign):
+    """A segment's decay exp(A sum d) overflows (A > 0, or negative steps) over
+    tokens that leave a zero state zero: nothing comes of it, in one pass and in
+    segments; backwards likewise where no gradient comes in from behind."""
+    B, C, N = 2, 20, 6
+    g = gen(84)
+    A = sign * (3.5 + torch.rand(C, N, generator=g)).cuda()
+    T = LEAD + TAIL
+    d = torch.full((B, T, C), float(sign))
+    d[:, LEAD:] *= 0.01
+    x, bt, ct = rn(g, B, T, C), rn(g, B, T, 1, N), rn(g, B, T, 1, N)
+    x[:, :LEAD] = 0
+    kw = dict(softplus=False)
+    y, h = layer.scan_forward(x, d.cuda(), A, bt, ct, algo=algo, **kw)
+    steps = 64 + 32 * T
+    (wy, wh, _), (by, bh, _) = (ref.scan(x, d, A, bt, ct, absolute=ab, **kw) for ab in (False, True))
+    close(y, wy, by, steps, "y")
+    close(h, wh, bh, steps, "h")
+    # backwards: the little decay first, x = 0 so that the states are
+    d, x, dy = d.flip(1), torch.zeros_like(x), rn(g, B, T, C)
+    dy[:, TAIL:] = 0
+    _, _, ck = layer.scan_forward(x, d.cuda(), A, bt, ct, algo=algo, chunk_states=True, **kw)
+    got = layer.scan_backward(x, d.cuda(), A, bt, ct, dy, ck, algo=algo, **kw)
+    want, bound = (ref.scan_grad(x, d, A, bt, ct, dy, absolute=ab, **kw) for ab in (False, True))
+    for n in got:
+        if got[n] is not None:
+            close(got[n], want[n], bound[n], 2 * steps + B * T, n)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("algo", ["staged", "segmented"])
+def test_decay_of_a_segment_past_the_range(algo, sign):
+    """A segment's decay lies outside fp32 (2^+-130 and more), the state that it
+    scales does not, before or after."""
+    B, C, N, T = 2, 20, 6, 128
+    g = gen(85)
+    A = sign * (0.97 + 0.03 * torch.rand(C, N, generator=g)).cuda()
+    d = torch.full((B, T, C), 95.0 / 64)
+    d[:, 64:] = 0.01
+    scale = 1e-30 if sign > 0 else 1e30
+    h0 = rn(g, B, C, N) * scale
+    x, bt, ct = torch.zeros(B, T, C).cuda(), rn(g, B, T, 1, N), rn(g, B, T, 1, N)
+    y, h, ck = layer.scan_forward(x, d.cuda(), A, bt, ct, h0=h0, softplus=False, chunk_states=True, algo=algo)
+    steps = 64 + 32 * T
+    (wy, wh, _), (by, bh, _) = (ref.scan(x, d, A, bt, ct, h0=h0, softplus=False, absolute=ab) for ab in (False, True))
+    assert float(wh.abs().max()) > 1e6 or sign < 0
+    close(h, wh, bh, steps, "h")
+    close(y[:, 64:], wy[:, 64:], by[:, 64:], steps, "y")
+    # the gradient of the state passes the same segments from behind
+    d, dh = d.flip(1), rn(g, B, C, N) * scale
+    got = layer.scan_backward(x, d.cuda(), A, bt, ct, x, torch.zeros_like(ck), softplus=False, dh_out=dh, algo=algo)
+    want, bound = (ref.scan_grad(x, d, A, bt, ct, x, softplus=False, dh_out=dh, absolute=ab)["dh0"] for ab in (False, True))
+    close(got["dh0"], want, bound, 2 * steps, "dh0")
