@@ -376,14 +376,14 @@ __device__ __forceinline__ float exponent_scale(float A) { return finite(A * kLo
 
 // 2^t h + e, t a whole segment's exponent.  Where 2^t nears the ends of the
 // format it would be inf or 0 while the state, before and after, is neither
-// (and inf times a zero state NaN): there the power of two is applied to the
-// product, exactly.  (A NaN t takes the first form.)
+// (and inf times a zero state NaN): there it is applied in two halves.  At
+// +-254 these are finite, and any normal state goes out of range or to 0 with
+// them.  (A NaN t stays one.)
 __device__ __forceinline__ float segment_decay(float t, float h, float e)
 {
-    if (!(fabsf(t) > 120.f))
-        return fmaf(fast_exp2(t), h, e);
-    const float c = fminf(fmaxf(t, -1000.f), 1000.f), n = rintf(c);
-    return ldexpf(fast_exp2(c - n) * h, (int)n) + e;
+    const float c = __builtin_elementwise_maximum(__builtin_elementwise_minimum(t, 254.f), -254.f);
+    const float half = fabsf(c) > 120.f ? 0.5f * c : 0.f;
+    return fmaf(fast_exp2(c - half), fast_exp2(half) * h, e);
 }
 
 // The step from its raw value.  softplus is formed either way: behind a branch
