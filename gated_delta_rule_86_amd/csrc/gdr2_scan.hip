@@ -23,10 +23,10 @@ namespace {
 
 // (d, d x) of one channel of a thread's row vector into LDS; 0 past the
 // sequence, where the token then leaves the state as it is.
-template <typename T> __device__ __forceinline__ void step_to_lds(float dt, float x, float bias, bool softplus, bool in, float* at)
+__device__ __forceinline__ void step_to_lds(float dt, float x, float bias, bool softplus, bool in, float* at)
 {
     typedef float Two __attribute__((ext_vector_type(2)));
-    float d = step_of<T>(dt + bias, softplus);
+    float d = step_of(dt + bias, softplus);
     d = in ? d : 0.f;
     *reinterpret_cast<Two*>(at) = Two{d, d * x};
 }
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(128 * LPC) void scan_forward_kernel(gdr2_scan_args 
         auto steps = [&](const RowVec<T, V, WIDE>& dt, const RowVec<T, V, WIDE>& x, bool in, int to) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                step_to_lds<T>(dt.get(v), x.get(v), bias[v], soft, in, &s_du[to][token / 2][du_at + 4 * step_place(ch + v)]);
+                step_to_lds(dt.get(v), x.get(v), bias[v], soft, in, &s_du[to][token / 2][du_at + 4 * step_place(ch + v)]);
         };
         auto outputs = [&](const RowVec<T, V, WIDE>& x, const RowVec<T, V, WIDE>& z, int from, float (&y)[V]) {
 #pragma unroll
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
     fetch(kScanChunk);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-        step_to_lds<T>(rt.get(v), rx.get(v), bias[v], soft, true, &s_du[0][token / 2][du_at + 4 * step_place(ch + v)]);
+        step_to_lds(rt.get(v), rx.get(v), bias[v], soft, true, &s_du[0][token / 2][du_at + 4 * step_place(ch + v)]);
     rb.store(s_b[0]);
     fetch(t0 + kScanChunk < t1 ? kScanChunk : 0);
     int buf = 0;
@@ -277,7 +277,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
                     }
                 }
                 if (k == 1)
-                    step_to_lds<T>(nt.get(g), nx.get(g), bias[g], soft, true, &s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + g)]);
+                    step_to_lds(nt.get(g), nx.get(g), bias[g], soft, true, &s_du[buf ^ 1][token / 2][du_at + 4 * step_place(ch + g)]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -376,7 +376,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p, u
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const bool in = on && b0 + r < a.B;
-        const float d = step_of<T>(dt[r] + bias, a.flags & GDR2_SCAN_SOFTPLUS), u = d * x[r];
+        const float d = step_of(dt[r] + bias, a.flags & GDR2_SCAN_SOFTPLUS), u = d * x[r];
         float y = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * LPC, 2) void scan_backward_kernel(gdr2_scan_bw
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float raw = xt.get(v) + bias[v], x = xx.get(v);
-                float d = step_of<T>(raw, soft), dv = xd.get(v);
+                float d = step_of(raw, soft), dv = xd.get(v);
                 if constexpr (GATE)
                     dv *= silu_f(xz.get(v));
                 d = in ? d : 0.f;
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_backward_span_kernel(gdr2_scan_
         for (int v = 0; v < V; ++v) {
             typedef float Two __attribute__((ext_vector_type(2)));
             const float raw = rt.get(v) + bias[v];
-            float d = step_of<T>(raw, soft), dv = rd.get(v);
+            float d = step_of(raw, soft), dv = rd.get(v);
             if constexpr (GATE)
                 dv *= silu_f(rz.get(v));
             d = token < left ? d : 0.f;

@@ -39,6 +39,29 @@ def test_step_at_the_ends_of_the_range(dtype):
         assert torch.equal(got.view(-1).cpu().nan_to_num(nan=-7.0, posinf=INF), want.nan_to_num(nan=-7.0, posinf=INF)), got
 
 
+@pytest.mark.parametrize("dtype", list(DT))
+def test_step_keeps_fp32_accuracy(dtype):
+    """softplus is as exact for bf16 rows as for fp32 ones: the states it goes
+    into are fp32.  Every bf16 number in (-80, 60), and a bias that is none.
+    Half steps of fp32 on the way: exp2 2, its correction 1, log2 2, ln 2 and its
+    product 2, the two sums 2, what the missing 1/w leaves 1, d x B 2; the sum
+    with the bias is the oracle's own, in fp32."""
+    every = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    raw = every[(every.float() > -80) & (every.float() < 60)].to(DT[dtype])
+    C = raw.numel()
+    x, one = torch.ones(1, 1, C, dtype=DT[dtype]).cuda(), torch.ones(1, 1, 1, 1, dtype=DT[dtype]).cuda()
+    A = torch.zeros(C, 1).cuda()
+    for bias in (None, torch.full((C,), 0.337)):
+        b = None if bias is None else bias.cuda()
+        _, h = layer.scan_forward(x, raw.cuda().view(1, 1, C), A, one, one, dt_bias=b)
+        s = torch.zeros(1, C, 1).cuda()
+        layer.scan_step(s, x[:, 0], raw.cuda().view(1, C), A, one[:, 0], one[:, 0], dt_bias=b)
+        v = raw.float() if bias is None else raw.float() + bias
+        want = torch.nn.functional.softplus(v.double(), threshold=100)
+        for got in (h, s):
+            close(got.view(-1), want, want.abs(), 16, "softplus")
+
+
 MASKED = [
     # B, T, C, N, G, packed, init, gate, extras, softplus, algo
     (2, 130, 24, 16, 3, False, True, True, True, True, "staged"),
