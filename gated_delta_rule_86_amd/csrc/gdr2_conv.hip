@@ -453,6 +453,20 @@ hipError_t launch_conv_step(const gdr2_conv_step_args& a, hipStream_t stream)
     return vec ? step_k<float, kVec>(a, stream) : step_k<float, 1>(a, stream);
 }
 
+// Workgroups of the backward, the larger of the two plans (sizes within
+// conv_launch_groups' bound).
+int64_t conv_backward_groups(const gdr2_conv_bwd_args& a)
+{
+    int64_t n = 0;
+    for (const bool vec : {false, true}) {
+        if (vec && a.C % kVec)
+            continue;
+        const BackwardPlan p = backward_plan(a, vec);
+        n = max(n, p.ncb * p.npb);
+    }
+    return n;
+}
+
 size_t conv_backward_workspace_bytes(const gdr2_conv_bwd_args& a)
 {
     int64_t rows = backward_plan(a, false).npb;

@@ -194,7 +194,9 @@ gdr2_status check_sizes(const gdr2_conv_bwd_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    return check_conv(a->B, a->T, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved, a->offsets != nullptr);
+    GDR2_TRY(check_conv(a->B, a->T, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved, a->offsets != nullptr));
+    // its blocks of channels are wider than the channels may be
+    return gdr2::conv_backward_groups(*a) >= gdr2::kMaxGroups ? too_many() : GDR2_OK;
 }
 
 gdr2_status validate(const gdr2_conv_bwd_args* a)
