@@ -429,12 +429,45 @@ hipError_t launch_column_sum(const float* part, int64_t P, int64_t ld, ColumnOut
     return hipGetLastError();
 }
 
-// Workgroups of the widest launch (scalar rows, the shortest pieces).
-int64_t conv_launch_groups(int64_t B, int64_t T, int64_t C, bool packed)
+namespace {
+
+// Workgroups of 256 items for pieces of at most 2^lg rows; kMaxGroups stands for
+// that many and for more.  (Sizes up to 2^40 each: their product is taken in
+// floating point first, and below the bound every later one fits int64.)
+int64_t piece_groups(int lg, int64_t B, int64_t T, int64_t ncv, bool packed)
 {
-    const double slots = packed ? (double)T / 8 + (double)B : (double)B * (double)(T / 8 + 1);
-    const double g = slots * (double)C / 256.0 + 1.0;
-    return g >= (double)kMaxGroups ? kMaxGroups : (int64_t)g;
+    const double L = (double)((int64_t)1 << lg), b = (double)B, pieces = (double)T / L;
+    const double slots = packed ? pieces + b : b * (pieces < 1.0 ? 1.0 : pieces);
+    if (slots * (double)ncv >= (double)kMaxGroups * 256.0)
+        return kMaxGroups;
+    return min(kMaxGroups, ceil_div(items_of(B, T, ncv, packed, piece_lg(lg, B, T, ncv, packed)), 256));
+}
+
+}  // namespace
+
+int64_t conv_forward_groups(const gdr2_conv_args& a)
+{
+    return piece_groups(kForwardLg, a.B, a.T, conv_vec(a.x, a.x_stride, a.C, a.dtype) ? a.C / kVec : a.C, a.offsets != nullptr);
+}
+
+int64_t conv_step_groups(const gdr2_conv_step_args& a)
+{
+    return piece_groups(kForwardLg, a.N, 1, conv_vec(a.x, a.x_stride, a.C, a.dtype) ? a.C / kVec : a.C, false);
+}
+
+// The larger of the two plans (the workspace query sees no pointers).
+int64_t conv_backward_groups(const gdr2_conv_bwd_args& a)
+{
+    int64_t n = 0;
+    for (const bool vec : {false, true}) {
+        if (vec && a.C % kVec)
+            continue;
+        if (piece_groups(kBackwardLg, a.B, a.T, vec ? a.C / kVec : a.C, a.offsets != nullptr) >= kMaxGroups)
+            return kMaxGroups;
+        const BackwardPlan p = backward_plan(a, vec);
+        n = max(n, p.ncb * p.npb);
+    }
+    return n;
 }
 
 hipError_t launch_conv_forward(const gdr2_conv_args& a, hipStream_t stream)
@@ -451,20 +484,6 @@ hipError_t launch_conv_step(const gdr2_conv_step_args& a, hipStream_t stream)
     if (a.dtype == GDR2_BF16)
         return vec ? step_k<bf16, kVec>(a, stream) : step_k<bf16, 1>(a, stream);
     return vec ? step_k<float, kVec>(a, stream) : step_k<float, 1>(a, stream);
-}
-
-// Workgroups of the backward, the larger of the two plans (sizes within
-// conv_launch_groups' bound).
-int64_t conv_backward_groups(const gdr2_conv_bwd_args& a)
-{
-    int64_t n = 0;
-    for (const bool vec : {false, true}) {
-        if (vec && a.C % kVec)
-            continue;
-        const BackwardPlan p = backward_plan(a, vec);
-        n = max(n, p.ncb * p.npb);
-    }
-    return n;
 }
 
 size_t conv_backward_workspace_bytes(const gdr2_conv_bwd_args& a)

@@ -13,7 +13,8 @@ hipError_t launch_conv_forward(const gdr2_conv_args& a, hipStream_t stream);
 hipError_t launch_conv_step(const gdr2_conv_step_args& a, hipStream_t stream);
 hipError_t launch_conv_backward(const gdr2_conv_bwd_args& a, hipStream_t stream);
 size_t conv_backward_workspace_bytes(const gdr2_conv_bwd_args& a);
-int64_t conv_launch_groups(int64_t B, int64_t T, int64_t C, bool packed);
+int64_t conv_forward_groups(const gdr2_conv_args& a);
+int64_t conv_step_groups(const gdr2_conv_step_args& a);
 int64_t conv_backward_groups(const gdr2_conv_bwd_args& a);
 
 hipError_t launch_scan_forward(const gdr2_scan_args& a, hipStream_t stream);

@@ -134,10 +134,9 @@ gdr2_status check_workspace(const void* p, size_t given, size_t need)
 
 // ---- convolution -----------------------------------------------------------
 
-// Sizes and modes common to the convolution's entry points; every product of
-// sizes the launchers form stays far inside int64.
+// Sizes and modes common to the convolution's entry points.
 gdr2_status check_conv(int64_t B, int64_t T, int64_t C, int64_t x_stride, int32_t width, int32_t dtype, int32_t act,
-                       int32_t reserved, bool packed)
+                       int32_t reserved)
 {
     if (B < 0 || T < 0)
         return set_error(GDR2_ERR_INVALID_ARG, "sizes must be >= 0");
@@ -149,17 +148,16 @@ gdr2_status check_conv(int64_t B, int64_t T, int64_t C, int64_t x_stride, int32_
     if (width < 2 || width > 4)
         return set_error(GDR2_ERR_UNSUPPORTED, "supported widths: 2, 3, 4 (got %d)", width);
     GDR2_TRY(check_stride("x_stride", x_stride, C));
-    if (B > ((int64_t)1 << 40) || T > ((int64_t)1 << 40) ||
-        gdr2::conv_launch_groups(B, T, C, packed) >= gdr2::kMaxGroups)
-        return too_many();
-    return GDR2_OK;
+    return B > ((int64_t)1 << 40) || T > ((int64_t)1 << 40) ? too_many() : GDR2_OK;
 }
 
 gdr2_status validate(const gdr2_conv_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    GDR2_TRY(check_conv(a->B, a->T, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved, a->offsets != nullptr));
+    GDR2_TRY(check_conv(a->B, a->T, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved));
+    if (gdr2::conv_forward_groups(*a) >= gdr2::kMaxGroups)
+        return too_many();
     const int64_t e = elt(a->dtype), rows = a->B == 0 ? 0 : a->offsets ? a->T : mul(a->B, a->T);
     const int64_t st = mul(mul(a->B, a->width - 1), a->C);
     const Buf b[] = {
@@ -178,7 +176,9 @@ gdr2_status validate(const gdr2_conv_step_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    GDR2_TRY(check_conv(a->N, 1, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved, false));
+    GDR2_TRY(check_conv(a->N, 1, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved));
+    if (gdr2::conv_step_groups(*a) >= gdr2::kMaxGroups)
+        return too_many();
     const int64_t e = elt(a->dtype);
     const Buf b[] = {
         rows_in("x", a->x, a->N, a->C, a->x_stride, e),
@@ -194,8 +194,7 @@ gdr2_status check_sizes(const gdr2_conv_bwd_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    GDR2_TRY(check_conv(a->B, a->T, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved, a->offsets != nullptr));
-    // its blocks of channels are wider than the channels may be
+    GDR2_TRY(check_conv(a->B, a->T, a->C, a->x_stride, a->width, a->dtype, a->act, a->reserved));
     return gdr2::conv_backward_groups(*a) >= gdr2::kMaxGroups ? too_many() : GDR2_OK;
 }
 

@@ -39,3 +39,44 @@ def test_conv_backward(lib, C, B, ok, packed):  # noqa: F811
         a.offsets = 1 << 40           # read on the device only
     assert taken(lib, "gdr2_conv_backward", a) == ok
     assert (lib.gdr2_conv_backward_workspace_size(ctypes.byref(a)) > 0) == ok
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("C,B,T,vec,ok", [
+    # pieces of 64 rows: 2^32 - 256 of them with one channel each
+    (1, 1, (1 << 38) - (1 << 15), False, True), (1, 1, 1 << 38, False, False),
+    # four channels a thread where rows are aligned to them
+    (2048, 64, (1 << 23) - 64, True, True), (2048, 64, (1 << 23) - 64, False, False), (2048, 1, 1 << 29, True, False),
+    (2048, 1, (1 << 29) - (1 << 18), True, True),
+    # one row each: a thread per sequence and channel
+    (1, (1 << 32) - 1024, 1, False, True), (1, 1 << 32, 1, False, False),
+    (64, (1 << 28) - 16, 1, True, True), (64, 1 << 28, 1, True, False),
+])
+def test_conv_forward(lib, C, B, T, vec, ok, packed):  # noqa: F811
+    """Its own pieces and channel vectors count, not those of the gradients."""
+    a = layer.ConvArgs(B=B, T=T, C=C, x_stride=C if vec else C + 1, width=4, dtype=gdr2.BF16)
+    if packed:
+        if T > 1:
+            a.T = B * T - 64 * B            # at most one piece more per sequence
+        else:
+            a.T = 0
+        a.offsets = 1 << 40
+    assert taken(lib, "gdr2_conv_forward", a) == ok
+
+
+@pytest.mark.parametrize("C,N,vec,ok", [(2048, (1 << 23) - 1, True, True), (2048, 1 << 23, True, False),
+                                        (2048, (1 << 21) - 1, False, True), (2048, 1 << 21, False, False)])
+def test_conv_step(lib, C, N, vec, ok):  # noqa: F811
+    a = layer.ConvStepArgs(N=N, C=C, x_stride=C if vec else C + 1, width=4, dtype=gdr2.BF16)
+    assert taken(lib, "gdr2_conv_step", a) == ok
+
+
+def test_conv_sizes_past_int64(lib):  # noqa: F811
+    """Products of sizes beyond every integer are refused like the others."""
+    big = 1 << 40
+    for B, T, C in ((big, big, 1), (big, big, 1 << 24), (1, big, 1 << 24), (big, 1, 1 << 24)):
+        for packed in (False, True):
+            for entry, a in (("gdr2_conv_forward", layer.ConvArgs()), ("gdr2_conv_backward", layer.ConvBwdArgs())):
+                a.B, a.T, a.C, a.x_stride, a.width = B, T, C, C, 4
+                a.offsets = big if packed else None
+                assert not taken(lib, entry, a), (entry, B, T, C)
