@@ -22,7 +22,9 @@ hipError_t launch_scan_step(const gdr2_scan_step_args& a, hipStream_t stream);
 hipError_t launch_scan_backward(const gdr2_scan_bwd_args& a, hipStream_t stream);
 size_t scan_workspace_bytes(const gdr2_scan_args& a);
 size_t scan_backward_workspace_bytes(const gdr2_scan_bwd_args& a);
-int64_t scan_launch_groups(const gdr2_scan_args& a);
+// Workgroups, counted as of 256 threads, of a call's largest launch.
+enum class ScanCall { Forward, Step, Backward };
+int64_t scan_launch_groups(const gdr2_scan_args& a, ScanCall call);
 
 hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream);
 hipError_t launch_norm_backward(const gdr2_norm_bwd_args& a, hipStream_t stream);

@@ -224,7 +224,7 @@ gdr2_status validate(const gdr2_conv_bwd_args* a)
 
 // ---- scan ------------------------------------------------------------------
 
-gdr2_status check_scan(const gdr2_scan_args& a)
+gdr2_status check_scan(const gdr2_scan_args& a, gdr2::ScanCall call)
 {
     if (a.B < 0 || a.T < 0)
         return set_error(GDR2_ERR_INVALID_ARG, "B, T must be >= 0");
@@ -248,7 +248,7 @@ gdr2_status check_scan(const gdr2_scan_args& a)
     GDR2_TRY(check_stride("c_stride", a.c_stride, a.G * a.N));
     const int64_t rows = a.offsets ? a.T : mul(a.B, a.T);
     if (a.B > ((int64_t)1 << 31) || a.T > ((int64_t)1 << 40) || rows > ((int64_t)1 << 40) ||
-        mul(a.B, a.C * 32 + 256) >= gdr2::kMaxGroups * 256 || mul(rows, 2 * a.G * a.N) >= gdr2::kMaxGroups * 256 || gdr2::scan_launch_groups(a) >= gdr2::kMaxGroups)
+        gdr2::scan_launch_groups(a, call) >= gdr2::kMaxGroups)
         return too_many();
     return GDR2_OK;
 }
@@ -279,7 +279,7 @@ gdr2_status validate(const gdr2_scan_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    GDR2_TRY(check_scan(*a));
+    GDR2_TRY(check_scan(*a, gdr2::ScanCall::Forward));
     const size_t need = gdr2::scan_workspace_bytes(*a);
     GDR2_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
     const int64_t st = mul(mul(a->B, a->C), a->N);
@@ -300,7 +300,7 @@ gdr2_status validate(const gdr2_scan_step_args* p)
     const gdr2_scan_args& a = p->s;
     if (a.T != 1 || a.offsets || a.h0 || a.h_out || a.h_chunks)
         return set_error(GDR2_ERR_INVALID_ARG, "a step has T = 1 and no offsets, h0, h_out or h_chunks");
-    GDR2_TRY(check_scan(a));
+    GDR2_TRY(check_scan(a, gdr2::ScanCall::Step));
     Buf b[11];
     scan_inputs(a, b);
     b[9] = dense("state", p->state, mul(mul(a.B, a.C), a.N), 4, true);
@@ -312,7 +312,7 @@ gdr2_status check_sizes(const gdr2_scan_bwd_args* p)
 {
     if (!p)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    return check_scan(p->f);
+    return check_scan(p->f, gdr2::ScanCall::Backward);
 }
 
 gdr2_status validate(const gdr2_scan_bwd_args* p)
@@ -450,7 +450,7 @@ int64_t gdr2_scan_chunk_count(int64_t B, int64_t T, int packed)
 
 size_t gdr2_scan_workspace_size(const gdr2_scan_args* a)
 {
-    return a && check_scan(*a) == GDR2_OK ? gdr2::scan_workspace_bytes(*a) : 0;
+    return a && check_scan(*a, gdr2::ScanCall::Forward) == GDR2_OK ? gdr2::scan_workspace_bytes(*a) : 0;
 }
 
 gdr2_status gdr2_scan_forward(const gdr2_scan_args* a, void* stream)

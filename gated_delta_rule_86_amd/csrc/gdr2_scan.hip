@@ -445,13 +445,22 @@ hipError_t forward_w(const gdr2_scan_args& a, hipStream_t stream)
     return scan_wide(a, kScanChunk / LPC) ? forward_t<T, LPC, NS, true>(a, stream) : forward_t<T, LPC, NS, false>(a, stream);
 }
 
+// Lanes per channel of the step; a sequence's lanes, in whole workgroups.
+int step_lpc(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
+int64_t step_lanes(int64_t C, int lpc) { return ceil_div(C * lpc, 256) * 256; }
+
 // Sequences per thread: two once that leaves four waves per SIMD (256 x 2048
 // channels, 16 states: 16.8 us; one 19.4, four 20.0, eight 26; streaming
 // accesses to the state 22), else one.
+int step_sequences(const gdr2_scan_args& a)
+{
+    return a.B / 2 * a.C * step_lpc(a.N) >= (int64_t)device_cu_count() * 4 * 4 * 64 ? 2 : 1;
+}
+
 template <typename T, int LPC, int R, bool VEC>
 hipError_t step_r(const gdr2_scan_step_args& a, hipStream_t stream)
 {
-    const int64_t lanes = ceil_div(a.s.C * LPC, 256) * 256;
+    const int64_t lanes = step_lanes(a.s.C, LPC);
     hipLaunchKernelGGL((scan_step_kernel<T, LPC, R, VEC>), dim3((unsigned)(ceil_div(a.s.B, R) * (lanes / 256))), dim3(256), 0,
                        stream, a, (uint32_t)lanes);
     return hipGetLastError();
@@ -462,7 +471,7 @@ hipError_t step_t(const gdr2_scan_step_args& a, hipStream_t stream)
     const int64_t e = sizeof(T);
     auto ok = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (4 * e) == 0 && ld % 4 == 0; };
     const bool vec = a.s.N % 4 == 0 && ok(a.s.Bt, a.s.b_stride) && ok(a.s.Ct, a.s.c_stride);
-    if (a.s.B / 2 * a.s.C * LPC >= (int64_t)device_cu_count() * 4 * 4 * 64)
+    if (step_sequences(a.s) == 2)
         return vec ? step_r<T, LPC, 2, true>(a, stream) : step_r<T, LPC, 2, false>(a, stream);
     return vec ? step_r<T, LPC, 1, true>(a, stream) : step_r<T, LPC, 1, false>(a, stream);
 }
@@ -470,11 +479,12 @@ hipError_t step_t(const gdr2_scan_step_args& a, hipStream_t stream)
 template <typename T>
 hipError_t step_n(const gdr2_scan_step_args& a, hipStream_t stream)
 {
-    if (a.s.N <= 4)
-        return step_t<T, 1>(a, stream);
-    if (a.s.N <= 8)
-        return step_t<T, 2>(a, stream);
-    return a.s.N <= 16 ? step_t<T, 4>(a, stream) : step_t<T, 8>(a, stream);
+    switch (step_lpc(a.s.N)) {
+    case 1: return step_t<T, 1>(a, stream);
+    case 2: return step_t<T, 2>(a, stream);
+    case 4: return step_t<T, 4>(a, stream);
+    default: return step_t<T, 8>(a, stream);
+    }
 }
 
 }  // namespace
@@ -520,14 +530,26 @@ ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
     return p;
 }
 
-int64_t scan_launch_groups(const gdr2_scan_args& a)
+int64_t scan_launch_groups(const gdr2_scan_args& a, ScanCall call)
 {
-    const ScanPlan p = scan_plan(a, true);      // never fewer segments than forwards
+    if (call == ScanCall::Step) {
+        const int64_t lanes = step_lanes(a.C, step_lpc(a.N));
+        return ceil_div(a.B, step_sequences(a)) * (lanes / 256);
+    }
+    const bool backward = call == ScanCall::Backward;
+    const ScanPlan p = scan_plan(a, backward);
     int64_t n;
-    if (__builtin_mul_overflow(p.seg.slots(), p.ncb, &n))
+    if (__builtin_mul_overflow(p.seg.slots(), p.ncb, &n) || n >= kMaxGroups)
         return kMaxGroups;
-    n *= a.N > 16 ? 4 : 2;            // workgroups of 1024 and 512 threads, counted as of 256
-    return max(n, ceil_div(a.B * a.C * max((int64_t)8, a.N), 256));
+    // 64 threads for every lane of a channel, twice that forwards
+    n *= (a.N > 16 ? 2 : 1) * (backward ? 1 : 2);
+    if (p.split)
+        n = max(n, ceil_div(a.B * a.C * a.N, 256));
+    if (backward) {
+        const double sums = (double)(a.offsets ? a.T : a.B * a.T) * (double)(a.G * 2 * a.N) / 256.0;
+        n = max(n, sums >= (double)kMaxGroups ? kMaxGroups : (int64_t)sums + 1);
+    }
+    return n;
 }
 
 size_t scan_workspace_bytes(const gdr2_scan_args& a) { return forward_work(a, scan_plan(a, false)).total; }

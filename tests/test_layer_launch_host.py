@@ -80,3 +80,63 @@ def test_conv_sizes_past_int64(lib):  # noqa: F811
                 a.B, a.T, a.C, a.x_stride, a.width = B, T, C, C, 4
                 a.offsets = big if packed else None
                 assert not taken(lib, entry, a), (entry, B, T, C)
+
+
+def scan_sizes(a, B, T, C, N, G, packed=False):
+    a.B, a.T, a.C, a.N, a.G, a.dtype = B, T, C, N, G, gdr2.F32
+    a.x_stride = a.dt_stride = C
+    a.b_stride = a.c_stride = G * N
+    a.offsets = 1 << 40 if packed else None
+    return a
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("B,T,C,N,G,ok", [
+    # one workgroup of 512 threads per sequence and 64 channels (1024 above 16 states); the
+    # row sums of the gradients would need 2 G N threads a token, the single tokens 32 lanes a channel
+    (256, 1 << 18, 64, 32, 1, True), (64, 1 << 19, 1024, 16, 4, True), (1, 1 << 30, 64, 16, 1, True),
+    (200_000, 1000, 64, 16, 8, True), (1_000_000, 1, 4096, 4, 1, False),
+    ((1 << 23) - 64, 1, 64, 16, 1, True), (1 << 23, 1, 64, 16, 1, False), (1 << 22, 1, 64, 17, 1, False),
+    (130_000, 1, 4096, 8, 1, True), (1 << 31, 0, 64, 16, 1, False),
+])
+def test_scan_forward(lib, B, T, C, N, G, ok, packed):  # noqa: F811
+    """Its own workgroups count, not those of the gradients or of single tokens."""
+    a = scan_sizes(layer.ScanArgs(), B, B * (T - 1) if packed and T > 1 else 0 if packed else T, C, N, G, packed)
+    assert taken(lib, "gdr2_scan_forward", a) == ok
+
+
+@pytest.mark.parametrize("B,C,N,ok", [
+    # four states a lane, lanes of a sequence rounded up to 256
+    (1_000_000, 256, 4, True), (1_000_000, 2048, 16, True), (1 << 22, 2048, 16, False), (1_000_000, 4096, 4, True),
+    ((1 << 25) - 2, 256, 4, True), (1 << 25, 256, 4, False), ((1 << 25) - 2, 1, 1, True), (1 << 25, 1, 1, False),
+])
+def test_scan_step(lib, B, C, N, ok):  # noqa: F811
+    a = layer.ScanStepArgs()
+    scan_sizes(a.s, B, 1, C, N, 1)
+    assert taken(lib, "gdr2_scan_step", a) == ok
+
+
+@pytest.mark.parametrize("B,T,C,N,G,ok", [
+    # a thread per token, group, and state of dB and dC
+    (1, (1 << 27) - 64, 64, 16, 1, True), (1, 1 << 27, 64, 16, 1, False), (256, 1 << 18, 64, 32, 1, False),
+    (100, 1 << 18, 64, 16, 4, True),
+    ((1 << 24) - 64, 1, 64, 16, 1, True), (1 << 24, 1, 64, 16, 1, False), ((1 << 23) - 64, 1, 64, 32, 1, True),
+    (1 << 23, 1, 64, 32, 1, False),
+])
+def test_scan_backward(lib, B, T, C, N, G, ok):  # noqa: F811
+    a = layer.ScanBwdArgs()
+    scan_sizes(a.f, B, T, C, N, G)
+    assert taken(lib, "gdr2_scan_backward", a) == ok
+    assert (lib.gdr2_scan_backward_workspace_size(ctypes.byref(a)) > 0) == ok
+
+
+def test_scan_sizes_past_int64(lib):  # noqa: F811
+    for B, T, C, N, G in ((1 << 31, 1 << 40, 1 << 24, 32, 1), (1, 1 << 40, 1 << 24, 1, 1 << 24), (1 << 31, 512, 1 << 24, 1, 1 << 24)):
+        for packed in (False, True):
+            for algo in ("auto", "staged", "segmented"):
+                a, s, b = layer.ScanArgs(), layer.ScanStepArgs(), layer.ScanBwdArgs()
+                scan_sizes(s.s, B, 1, C, N, G)
+                for f in (a, b.f):
+                    scan_sizes(f, B, T, C, N, G, packed).algo = gdr2.ALGOS[algo]
+                for entry, v in (("gdr2_scan_forward", a), ("gdr2_scan_step", s), ("gdr2_scan_backward", b)):
+                    assert taken(lib, entry, v) == (B == 1 and v is s), (entry, B, T, C, packed, algo)
