@@ -12,6 +12,8 @@
 // TB/s (a large copy: 5.1); gradients 403 MB in 92.8 us, 4.3 TB/s, where forming
 // p, its slope, dx and the five sums (32 operations an element) keeps the vector
 // units busy three quarters of the time.
+#include <algorithm>
+
 #include "gdr2_layer.h"
 
 namespace gdr2 {
@@ -440,7 +442,7 @@ int64_t piece_groups(int lg, int64_t B, int64_t T, int64_t ncv, bool packed)
     const double slots = packed ? pieces + b : b * (pieces < 1.0 ? 1.0 : pieces);
     if (slots * (double)ncv >= (double)kMaxGroups * 256.0)
         return kMaxGroups;
-    return min(kMaxGroups, ceil_div(items_of(B, T, ncv, packed, piece_lg(lg, B, T, ncv, packed)), 256));
+    return std::min(kMaxGroups, ceil_div(items_of(B, T, ncv, packed, piece_lg(lg, B, T, ncv, packed)), 256));
 }
 
 }  // namespace
@@ -465,7 +467,7 @@ int64_t conv_backward_groups(const gdr2_conv_bwd_args& a)
         if (piece_groups(kBackwardLg, a.B, a.T, vec ? a.C / kVec : a.C, a.offsets != nullptr) >= kMaxGroups)
             return kMaxGroups;
         const BackwardPlan p = backward_plan(a, vec);
-        n = max(n, p.ncb * p.npb);
+        n = std::max(n, p.ncb * p.npb);
     }
     return n;
 }
@@ -490,7 +492,7 @@ size_t conv_backward_workspace_bytes(const gdr2_conv_bwd_args& a)
 {
     int64_t rows = backward_plan(a, false).npb;
     if (a.C % kVec == 0)
-        rows = max(rows, backward_plan(a, true).npb);
+        rows = std::max(rows, backward_plan(a, true).npb);
     return (size_t)rows * a.C * (a.width + 1) * sizeof(float);
 }
 

@@ -15,6 +15,8 @@
 // next row's loads in flight while it works on one.  In bf16: 524288 gated rows of
 // 128, 403 MB, in 75 us, 5.4 TB/s (a large copy: 5.1); layer norm's gradients of
 // 32768 rows of 2048, 403 MB, in 81.5 us, 4.9 TB/s, 4.9 us of it the column sums.
+#include <algorithm>
+
 #include "gdr2_layer.h"
 
 namespace gdr2 {
@@ -435,7 +437,7 @@ template <typename T, int V> struct ForwardLaunch {
     template <int L, int N> void operator()() const
     {
         // eight workgroups per compute unit, then the rows are walked
-        const dim3 grid((unsigned)min(ceil_div(a.R, 256 / L), (int64_t)device_cu_count() * 8));
+        const dim3 grid((unsigned)std::min(ceil_div(a.R, 256 / L), (int64_t)device_cu_count() * 8));
         if (a.z)
             hipLaunchKernelGGL((norm_forward_kernel<T, V, L, N, true>), grid, dim3(256), 0, stream, a);
         else
@@ -513,12 +515,12 @@ hipError_t forward_v(const gdr2_norm_args& a, hipStream_t stream)
 // fewer rows.
 int64_t backward_groups(int64_t R, const Shape& s)
 {
-    return min(ceil_div(R, max(1, 256 / s.lpr)), (int64_t)device_cu_count() * 2);
+    return std::min(ceil_div(R, std::max(1, 256 / s.lpr)), (int64_t)device_cu_count() * 2);
 }
 
 int64_t long_row_blocks(int64_t R, int64_t C)
 {
-    return max((int64_t)1, min(ceil_div(R, 4), (int64_t)device_cu_count() * 4 / ceil_div(C, 64)));
+    return std::max((int64_t)1, std::min(ceil_div(R, 4), (int64_t)device_cu_count() * 4 / ceil_div(C, 64)));
 }
 
 template <typename T, int V>
@@ -561,7 +563,7 @@ hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
 int64_t norm_launch_groups(const gdr2_norm_args& a)
 {
     const Shape s = shape_of(a.C, norm_vec(a) ? (a.dtype == GDR2_BF16 ? 8 : 4) : 1, true, a.z);
-    return s.lpr ? ceil_div(a.R, max(1, 256 / s.lpr)) : a.R;
+    return s.lpr ? ceil_div(a.R, std::max(1, 256 / s.lpr)) : a.R;
 }
 
 hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream)
@@ -579,7 +581,7 @@ size_t norm_backward_workspace_bytes(const gdr2_norm_bwd_args& p)
     int64_t floats = 0;
     for (int V : {1, a.dtype == GDR2_BF16 ? 8 : 4}) {
         const Shape s = shape_of(a.C, V, true, a.z);
-        floats = max(floats, s.lpr ? backward_groups(a.R, s) * 2 * a.C : 2 * a.R + long_row_blocks(a.R, a.C) * 2 * a.C);
+        floats = std::max(floats, s.lpr ? backward_groups(a.R, s) * 2 * a.C : 2 * a.R + long_row_blocks(a.R, a.C) * 2 * a.C);
     }
     return (size_t)floats * sizeof(float);
 }

@@ -15,6 +15,8 @@
 // with P = exp(A sum d) and E the end state from zero.  A span pass forms
 // (sum d, E) of every segment but a sequence's last, a fold chains the
 // segments' start states, and the main pass runs them all at once.
+#include <algorithm>
+
 #include "gdr2_scan.h"
 
 namespace gdr2 {
@@ -511,14 +513,14 @@ ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
     int whole = kScanLg;                      // a segment that holds any sequence
     while (((int64_t)1 << whole) < a.T)
         ++whole;
-    const int shortest = min(whole, kScanLg + 2);
+    const int shortest = std::min(whole, kScanLg + 2);
     int lg = whole;
     auto groups = [&](int g) { return Pieces{a.offsets, a.B, a.T, g}.slots() * p.ncb; };
     if (a.algo == GDR2_ALGO_SEGMENTED) {
-        lg = min(whole, kScanLg + 1);
+        lg = std::min(whole, kScanLg + 1);
     } else if (a.algo == GDR2_ALGO_AUTO) {
         if (a.offsets)
-            while (lg > shortest && ((int64_t)1 << (lg - 1)) >= 2 * ceil_div(a.T, max(a.B, (int64_t)1)))
+            while (lg > shortest && ((int64_t)1 << (lg - 1)) >= 2 * ceil_div(a.T, std::max(a.B, (int64_t)1)))
                 --lg;
         const int64_t cus = device_cu_count();
         if (16 * groups(lg) < (backward ? 28 : a.offsets ? 16 : 9) * cus)
@@ -544,10 +546,10 @@ int64_t scan_launch_groups(const gdr2_scan_args& a, ScanCall call)
     // 64 threads for every lane of a channel, twice that forwards
     n *= (a.N > 16 ? 2 : 1) * (backward ? 1 : 2);
     if (p.split)
-        n = max(n, ceil_div(a.B * a.C * a.N, 256));
+        n = std::max(n, ceil_div(a.B * a.C * a.N, 256));
     if (backward) {
         const double sums = (double)(a.offsets ? a.T : a.B * a.T) * (double)(a.G * 2 * a.N) / 256.0;
-        n = max(n, sums >= (double)kMaxGroups ? kMaxGroups : (int64_t)sums + 1);
+        n = std::max(n, sums >= (double)kMaxGroups ? kMaxGroups : (int64_t)sums + 1);
     }
     return n;
 }
