@@ -29,7 +29,7 @@ int64_t scan_launch_groups(const gdr2_scan_args& a, ScanCall call);
 hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream);
 hipError_t launch_norm_backward(const gdr2_norm_bwd_args& a, hipStream_t stream);
 size_t norm_backward_workspace_bytes(const gdr2_norm_bwd_args& a);
-int64_t norm_launch_groups(const gdr2_norm_args& a);
+int64_t norm_launch_groups(const gdr2_norm_args& a, bool backward);
 
 // Column sums of part [P][M] (rows ld apart), in an order fixed by P alone.  The columns are
 // cut into up to three outputs (M = their n together); NULL ones are skipped.

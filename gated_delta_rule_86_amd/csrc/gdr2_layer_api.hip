@@ -344,7 +344,7 @@ gdr2_status validate(const gdr2_scan_bwd_args* p)
 
 // ---- norm ------------------------------------------------------------------
 
-gdr2_status check_norm(const gdr2_norm_args& a)
+gdr2_status check_norm(const gdr2_norm_args& a, bool backward)
 {
     if (a.R < 0)
         return set_error(GDR2_ERR_INVALID_ARG, "R must be >= 0");
@@ -358,7 +358,7 @@ gdr2_status check_norm(const gdr2_norm_args& a)
     GDR2_TRY(check_stride("x_stride", a.x_stride, a.C));
     if (a.z)
         GDR2_TRY(check_stride("z_stride", a.z_stride, a.C));
-    if (a.R > ((int64_t)1 << 40) || gdr2::norm_launch_groups(a) >= gdr2::kMaxGroups)
+    if (a.R >= ((int64_t)1 << 40) || gdr2::norm_launch_groups(a, backward) >= gdr2::kMaxGroups)
         return too_many();
     return GDR2_OK;
 }
@@ -367,7 +367,7 @@ gdr2_status validate(const gdr2_norm_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    GDR2_TRY(check_norm(*a));
+    GDR2_TRY(check_norm(*a, false));
     const int64_t e = elt(a->dtype);
     const Buf b[] = {
         rows_in("x", a->x, a->R, a->C, a->x_stride, e),
@@ -383,7 +383,7 @@ gdr2_status check_sizes(const gdr2_norm_bwd_args* p)
 {
     if (!p)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    return check_norm(p->f);
+    return check_norm(p->f, true);
 }
 
 gdr2_status validate(const gdr2_norm_bwd_args* p)

@@ -559,11 +559,16 @@ hipError_t backward_v(const gdr2_norm_bwd_args& p, hipStream_t stream)
 
 }  // namespace
 
-// Workgroups of the forward's launch (the backward's rows take at most as many).
-int64_t norm_launch_groups(const gdr2_norm_args& a)
+// Workgroups of a call's largest launch: rows held in registers are walked by a
+// few per compute unit, longer ones take one each.  (Backwards for either width
+// of access: the workspace query sees no pointers.)
+int64_t norm_launch_groups(const gdr2_norm_args& a, bool backward)
 {
-    const Shape s = shape_of(a.C, norm_vec(a) ? (a.dtype == GDR2_BF16 ? 8 : 4) : 1, true, a.z);
-    return s.lpr ? ceil_div(a.R, std::max(1, 256 / s.lpr)) : a.R;
+    const int wide = a.dtype == GDR2_BF16 ? 8 : 4;
+    bool whole = shape_of(a.C, backward || !norm_vec(a) ? 1 : wide, backward, a.z).lpr != 0;
+    if (backward)
+        whole = whole && shape_of(a.C, wide, backward, a.z).lpr != 0;
+    return whole ? std::min(a.R, (int64_t)device_cu_count() * 8) : a.R;
 }
 
 hipError_t launch_norm_forward(const gdr2_norm_args& a, hipStream_t stream)

@@ -140,3 +140,26 @@ def test_scan_sizes_past_int64(lib):  # noqa: F811
                     scan_sizes(f, B, T, C, N, G, packed).algo = gdr2.ALGOS[algo]
                 for entry, v in (("gdr2_scan_forward", a), ("gdr2_scan_step", s), ("gdr2_scan_backward", b)):
                     assert taken(lib, entry, v) == (B == 1 and v is s), (entry, B, T, C, packed, algo)
+
+
+@pytest.mark.parametrize("dtype", [gdr2.F32, gdr2.BF16])
+@pytest.mark.parametrize("C,R,forward,backward", [
+    # rows held in registers are walked by a fixed number of workgroups
+    (64, (1 << 40) - 1, True, True), (128, 1 << 32, True, True), (8192, 1 << 30, True, True), (2048, (1 << 40) + 1, False, False),
+    # longer ones take a workgroup each: above 8192 elements backwards, above 16384 of whole vectors forwards
+    (8200, (1 << 24) - 1, True, True), (8200, 1 << 24, True, False), (16384, 1 << 30, True, False),
+    (16392, (1 << 24) - 1, True, True), (16392, 1 << 24, False, False),
+])
+def test_norm(lib, C, R, forward, backward, dtype):  # noqa: F811
+    """Rows that a workgroup walks do not count as workgroups."""
+    a = layer.NormArgs(R=R, C=C, x_stride=C, dtype=dtype, eps=1e-5)
+    assert taken(lib, "gdr2_norm_forward", a) == forward
+    b = layer.NormBwdArgs(f=a)
+    assert taken(lib, "gdr2_norm_backward", b) == backward
+    assert (lib.gdr2_norm_backward_workspace_size(ctypes.byref(b)) > 0) == backward
+
+
+def test_norm_unaligned(lib):  # noqa: F811
+    """Rows of single elements: a workgroup each above 8192."""
+    for C, R, ok in ((8192, 1 << 30, True), (8193, (1 << 24) - 1, True), (8193, 1 << 24, False)):
+        assert taken(lib, "gdr2_norm_forward", layer.NormArgs(R=R, C=C, x_stride=C + 1, dtype=gdr2.BF16, eps=1e-5)) == ok
