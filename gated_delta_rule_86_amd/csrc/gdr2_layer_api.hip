@@ -28,7 +28,9 @@ gdr2_status hip_result(hipError_t e, hipStream_t stream, const char* what)
 }
 
 constexpr int64_t kHuge = (int64_t)1 << 62;
-constexpr int64_t kMaxStride = (int64_t)1 << 24;
+// Elements of a row, and between two rows.  The scan's prompt and gradient kernels form offsets
+// within 32 rows in 32 bits of bytes; the others in 64 bits.
+constexpr int64_t kMaxWidth = (int64_t)1 << 24, kMaxStride = (int64_t)1 << 40, kScanMaxStride = (int64_t)1 << 24;
 
 // One buffer of a call: its bytes from the first to the last element.
 struct Buf {
@@ -105,14 +107,15 @@ gdr2_status check_dtype(int32_t dtype, int32_t reserved)
     return GDR2_OK;
 }
 
-gdr2_status check_stride(const char* name, int64_t stride, int64_t width)
+gdr2_status check_stride(const char* name, int64_t stride, int64_t width, int64_t most = kMaxStride)
 {
     if (stride < width)
         return set_error(GDR2_ERR_INVALID_ARG, "%s must be at least the row's %lld elements (got %lld)", name,
                          (long long)width, (long long)stride);
-    // the kernels form offsets within 32 rows in 32 bits of bytes
-    if (stride > kMaxStride)
-        return set_error(GDR2_ERR_UNSUPPORTED, "%s: rows may be at most 2^24 elements apart", name);
+    if (width > kMaxWidth)
+        return set_error(GDR2_ERR_UNSUPPORTED, "rows may have at most 2^24 elements (got %lld)", (long long)width);
+    if (stride > most)
+        return set_error(GDR2_ERR_UNSUPPORTED, "%s: rows may be at most 2^%d elements apart", name, most == kMaxStride ? 40 : 24);
     return GDR2_OK;
 }
 
@@ -240,12 +243,13 @@ gdr2_status check_scan(const gdr2_scan_args& a, gdr2::ScanCall call)
         return set_error(GDR2_ERR_INVALID_ARG, "unknown algo %d", a.algo);
     if (a.N > 32)
         return set_error(GDR2_ERR_UNSUPPORTED, "supported state sizes: 1 to 32 (got %lld)", (long long)a.N);
-    GDR2_TRY(check_stride("x_stride", a.x_stride, a.C));
-    GDR2_TRY(check_stride("dt_stride", a.dt_stride, a.C));
+    const int64_t most = call == gdr2::ScanCall::Step ? kMaxStride : kScanMaxStride;
+    GDR2_TRY(check_stride("x_stride", a.x_stride, a.C, most));
+    GDR2_TRY(check_stride("dt_stride", a.dt_stride, a.C, most));
     if (a.z)
-        GDR2_TRY(check_stride("z_stride", a.z_stride, a.C));
-    GDR2_TRY(check_stride("b_stride", a.b_stride, a.G * a.N));
-    GDR2_TRY(check_stride("c_stride", a.c_stride, a.G * a.N));
+        GDR2_TRY(check_stride("z_stride", a.z_stride, a.C, most));
+    GDR2_TRY(check_stride("b_stride", a.b_stride, a.G * a.N, most));
+    GDR2_TRY(check_stride("c_stride", a.c_stride, a.G * a.N, most));
     const int64_t rows = a.offsets ? a.T : mul(a.B, a.T);
     if (a.B > ((int64_t)1 << 31) || a.T > ((int64_t)1 << 40) || rows > ((int64_t)1 << 40) ||
         gdr2::scan_launch_groups(a, call) >= gdr2::kMaxGroups)

@@ -328,9 +328,11 @@ gdr2_status gdr2_forward_chunked_noalloc(const gdr2_fwd_args *args, void *stream
  *   Gradients : of rows, in the rows' dtype, accumulated in fp32 and rounded
  *               once at the store.  Every sum runs in a fixed order (no
  *               atomics): a repeated call gives the same bits.
- *   Sizes     : all int64; rows further apart than 2^24 elements, and a call
- *               that would need 2^24 or more workgroups in one launch, return
- *               GDR2_ERR_UNSUPPORTED.
+ *   Sizes     : all int64; rows of more than 2^24 elements, rows further apart
+ *               than 2^40 (in gdr2_scan_forward and gdr2_scan_backward 2^24),
+ *               2^40 or more rows, and a call one of whose launches would need
+ *               2^24 or more workgroups (of 256 threads, larger ones counted as
+ *               several) return GDR2_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------ */
 
 /* Activation fused behind the convolution. */

@@ -175,3 +175,34 @@ def test_decay_of_a_segment_past_the_range(algo, sign):
     got = layer.scan_backward(x, d.cuda(), A, bt, ct, x, torch.zeros_like(ck), softplus=False, dh_out=dh, algo=algo)
     want, bound = (ref.scan_grad(x, d, A, bt, ct, x, softplus=False, dh_out=dh, absolute=ab)["dh0"] for ab in (False, True))
     close(got["dh0"], want, bound, 2 * steps, "dh0")
+
+
+# ---- rows far apart ---------------------------------------------------------
+
+def test_last_tokens_of_long_sequences():
+    """The last rows of two sequences more than 2^24 elements long, as they lie,
+    through the norm, the convolution's step and the scan's step."""
+    B, T, C, N = 2, 8200, 2048, 16
+    g = gen(86)
+    long = torch.zeros(B, T, C, dtype=torch.bfloat16, device="cuda")
+    assert T * C > 1 << 24
+    long[:, -1] = rn(g, B, C, dtype=torch.bfloat16)
+    last = long[:, -1]
+    row = last.contiguous()
+    assert not last.is_contiguous()
+    w, dy = 1 + 0.1 * rn(g, C), rn(g, B, C, dtype=torch.bfloat16)
+    assert torch.equal(layer.norm_forward(last, w, z=last), layer.norm_forward(row, w, z=row))
+    got, want = (layer.norm_backward(t, dy, w, z=t) for t in (last, row))
+    assert all(torch.equal(got[n], want[n]) for n in ("dx", "dz", "dweight"))
+    cw, st, h = rn(g, C, 4), rn(g, B, 3, C, dtype=torch.bfloat16), rn(g, B, C, N)
+    sts, hs = [st.clone(), st.clone()], [h.clone(), h.clone()]
+    ys = [layer.conv_step(s, t, cw) for s, t in zip(sts, (last, row))]
+    assert torch.equal(*ys) and torch.equal(*sts)
+    A = -torch.rand(C, N, generator=g).cuda()
+    bc = [t[:, :2 * N].unflatten(1, (2, N)) for t in (last, row)]
+    ys = [layer.scan_step(s, t, t, A, b[:, :1], b[:, 1:], z=t) for s, t, b in zip(hs, (last, row), bc)]
+    assert torch.equal(*ys) and torch.equal(*hs)
+    far = long[:, ::T - 1]                      # two rows of each sequence, T - 1 rows apart
+    assert torch.equal(layer.conv_forward(far[:1], cw)[0], layer.conv_forward(far[:1].contiguous(), cw)[0])
+    got, want = (layer.conv_backward(t, cw, dy.view(1, B, C)) for t in (far[:1], far[:1].contiguous()))
+    assert all(torch.equal(got[n], want[n]) for n in ("dx", "dweight"))

@@ -163,3 +163,44 @@ def test_norm_unaligned(lib):  # noqa: F811
     """Rows of single elements: a workgroup each above 8192."""
     for C, R, ok in ((8192, 1 << 30, True), (8193, (1 << 24) - 1, True), (8193, 1 << 24, False)):
         assert taken(lib, "gdr2_norm_forward", layer.NormArgs(R=R, C=C, x_stride=C + 1, dtype=gdr2.BF16, eps=1e-5)) == ok
+
+
+def test_row_strides_of_64_bits(lib):  # noqa: F811
+    """Only the scan's prompts and their gradients form row offsets in 32 bits;
+    the last tokens of long sequences, 2^24 elements apart and more, go through
+    everything else."""
+    far, C = (1 << 24) + 8, 64
+    ok = [("gdr2_conv_forward", layer.ConvArgs(B=1, T=3, C=C, x_stride=far, width=4)),
+          ("gdr2_conv_step", layer.ConvStepArgs(N=3, C=C, x_stride=far, width=4)),
+          ("gdr2_conv_backward", layer.ConvBwdArgs(B=1, T=3, C=C, x_stride=far, width=4)),
+          ("gdr2_norm_forward", layer.NormArgs(R=3, C=C, x_stride=far)),
+          ("gdr2_norm_backward", layer.NormBwdArgs(f=layer.NormArgs(R=3, C=C, x_stride=far)))]
+    s = layer.ScanStepArgs()
+    for n in ("x_stride", "dt_stride", "b_stride", "c_stride"):
+        scan_sizes(s.s, 3, 1, C, 16, 1)
+        setattr(s.s, n, far)
+        assert taken(lib, "gdr2_scan_step", s), n
+        for a, f, entry in ((layer.ScanArgs(), None, "gdr2_scan_forward"), (layer.ScanBwdArgs(), "f", "gdr2_scan_backward")):
+            at = getattr(a, f) if f else a
+            scan_sizes(at, 1, 3, C, 16, 1)
+            setattr(at, n, far)
+            assert not taken(lib, entry, a) and b"2^24" in lib.gdr2_last_error(), (entry, n)
+            setattr(at, n, 1 << 24)
+            assert taken(lib, entry, a), (entry, n)
+    for entry, a in ok:
+        assert taken(lib, entry, a), entry
+        (a.f if hasattr(a, "f") else a).x_stride = (1 << 40) + 1
+        assert not taken(lib, entry, a), entry
+
+
+def test_widths(lib):  # noqa: F811
+    for C, ok in ((1 << 24, True), ((1 << 24) + 8, False), (1 << 50, False)):
+        wide = dict(C=C, x_stride=max(C, 1 << 24))
+        s = layer.ScanStepArgs()
+        scan_sizes(s.s, 1, 1, C, 1, 1)
+        for entry, a in (("gdr2_conv_forward", layer.ConvArgs(B=1, T=1, width=4, **wide)),
+                         ("gdr2_conv_step", layer.ConvStepArgs(N=1, width=4, **wide)),
+                         ("gdr2_conv_backward", layer.ConvBwdArgs(B=1, T=1, width=4, **wide)), ("gdr2_scan_step", s),
+                         ("gdr2_norm_forward", layer.NormArgs(R=1, **wide)),
+                         ("gdr2_norm_backward", layer.NormBwdArgs(f=layer.NormArgs(R=1, **wide)))):
+            assert taken(lib, entry, a) == ok, (entry, C)
