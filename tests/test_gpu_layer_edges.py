@@ -8,7 +8,7 @@ import torch
 from gated_delta_rule_86_amd import layer
 from tests import layer_reference as ref
 from tests.layer_reference import close
-from tests.test_gpu_layer import DT, gen, rn, scan_case
+from tests.test_gpu_layer import DT, SCAN, SCAN_IDS, gen, rn, scan_case, scan_steps
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -206,3 +206,56 @@ def test_last_tokens_of_long_sequences():
     assert torch.equal(layer.conv_forward(far[:1], cw)[0], layer.conv_forward(far[:1].contiguous(), cw)[0])
     got, want = (layer.conv_backward(t, cw, dy.view(1, B, C)) for t in (far[:1], far[:1].contiguous()))
     assert all(torch.equal(got[n], want[n]) for n in ("dx", "dweight"))
+
+
+# ---- gradients of rows, however many there are ------------------------------
+
+# no rounding of a row's gradient depends on the number of rows: the bounds are
+# those of one row (two sums over its elements) or of one sequence
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("R,C,dtype,gate", [
+    (70001, 16, "f32", False), (70001, 16, "f32", True), (2501, 2048, "bf16", False), (2501, 2048, "f32", False),
+    (2100, 1500, "f32", True), (1100, 2048, "bf16", True), (4200, 128, "f32", True), (4200, 128, "bf16", True),
+    (1500, 1003, "f32", False), (1500, 1003, "f32", True), (600, 4096, "f32", False), (300, 8192, "f32", True),
+    (300, 8200, "f32", True), (300, 20001, "f32", False)])
+def test_norm_gradients_of_rows(R, C, dtype, gate, kind):
+    g = gen(87)
+    x, dy = rn(g, R, C, dtype=DT[dtype]) * 1.5 + 0.5, rn(g, R, C, dtype=DT[dtype])
+    z = rn(g, R, C, dtype=DT[dtype]) if gate else None
+    w, b = 1 + 0.2 * rn(g, C), rn(g, C) if kind == "layer" else None
+    got = layer.norm_backward(x, dy, w, b, z, kind=kind)
+    want, bound = ref.norm_grad(x, dy, w, b, z, kind=kind)
+    for n in ("dx", "dz") if gate else ("dx",):
+        close(got[n], want[n], bound[n], 2 * (64 + C / 8), n)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("c", SCAN, ids=SCAN_IDS)
+def test_scan_gradients_of_rows(c, dtype):
+    a, kw, h0, B, T = scan_case(c, dtype, 88)
+    g = gen(89)
+    dy = rn(g, *a["x"].shape, dtype=a["x"].dtype)
+    dh = rn(g, B, *a["A"].shape)
+    _, _, ck = layer.scan_forward(**a, **kw, h0=h0, chunk_states=True, algo=c[10])
+    got = layer.scan_backward(**a, **kw, dy=dy, h_chunks=ck, dh_out=dh, algo=c[10])
+    rkw = dict(kw, offsets=None if kw["offsets"] is None else kw["offsets"].cpu())
+    want, bound = (ref.scan_grad(**a, **rkw, dy=dy, h0=h0, dh_out=dh, absolute=ab) for ab in (False, True))
+    rows = slice(None) if not c[5] else slice(int(kw["offsets"][0]), int(kw["offsets"][-1]))
+    for n in ("dx", "ddt", "dBt", "dCt", "dz", "dh0"):
+        if got[n] is not None:
+            cut = slice(None) if n == "dh0" else rows
+            close(got[n][cut], want[n][cut], bound[n][cut], 2 * scan_steps(c, T), n)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_scan_gradients_of_many_sequences(dtype):
+    """1500 rows in sequences of five: the bound is that of five tokens."""
+    c = (300, 5, 72, 16, 1, False, True, True, True, True, "auto")
+    a, kw, h0, B, T = scan_case(c, dtype, 90)
+    dy = rn(gen(91), *a["x"].shape, dtype=a["x"].dtype)
+    _, _, ck = layer.scan_forward(**a, **kw, h0=h0, chunk_states=True)
+    got = layer.scan_backward(**a, **kw, dy=dy, h_chunks=ck)
+    want, bound = (ref.scan_grad(**a, **kw, dy=dy, h0=h0, absolute=ab) for ab in (False, True))
+    for n in ("dx", "ddt", "dBt", "dCt", "dz", "dh0"):
+        close(got[n], want[n], bound[n], 2 * scan_steps(c, T), n)
