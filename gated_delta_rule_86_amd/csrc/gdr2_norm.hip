@@ -366,8 +366,8 @@ __global__ __launch_bounds__(256) void norm_backward_long_kernel(gdr2_norm_bwd_a
     }
 }
 
-// dweight and dbias of long rows: a workgroup sums 64 columns over every
-// gridDim.y-th block of 64 rows.
+// dweight and dbias of long rows: a workgroup sums 64 columns, a wave every
+// fourth row of every gridDim.y-th block of four.
 template <typename T>
 __global__ __launch_bounds__(256) void norm_backward_columns_kernel(gdr2_norm_bwd_args p, const float* stats, float* part)
 {

@@ -67,16 +67,6 @@ __device__ __forceinline__ float sum_transposed(const float (&p)[8], int s)
     return sum_transposed(q, s);
 }
 
-// Sum over the LPC lanes of a channel, in every lane.
-template <int LPC> __device__ __forceinline__ float channel_lanes_sum(float v)
-{
-    v += dpp_quad_xor<1>(v);
-    v += dpp_quad_xor<2>(v);
-    if constexpr (LPC == 8)
-        v += dpp_move<0x141>(v);
-    return v;
-}
-
 // Segments of a scan: L = 2^lg tokens each.
 struct ScanPlan {
     Pieces seg;
