@@ -345,9 +345,9 @@ struct BackwardPlan {
 };
 
 // Channels of a thread when rows are aligned to them.  Eight of bf16 (16 bytes)
-// were slower: 60 us against 51 forwards at 8 x 4096 x 2048, 138 against 111
-// backwards, where the taps, windows and sums of eight channels leave one wave
-// per SIMD.
+// take 48.5 us against 49.8 forwards at 8 x 4096 x 2048 (one input over and over,
+// part of it in the memory-side cache), but 123 against 92.1 backwards, where the
+// taps, windows and sums of eight channels leave one wave per SIMD.
 constexpr int kVec = 4;
 
 bool conv_vec(const void* x, int64_t x_stride, int64_t C, int32_t dtype)

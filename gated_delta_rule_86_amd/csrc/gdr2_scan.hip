@@ -7,7 +7,7 @@
 // Per (token, channel, state): one multiply for the exponent, one exp2, and
 // three multiply-adds.  At 16 states that arithmetic, not the 8 bytes a channel
 // moves per token, bounds a prompt: 8 x 4096 x 2048 channels, gated, in bf16 take
-// 254 us, of which the exponentials, multiplies and adds are 178 us at the issue
+// 255 us, of which the exponentials, multiplies and adds are 178 us at the issue
 // rate measured for them (4.3 cycles a wave, 8.9 for exp2) and the 540 MB 106 us
 // at the rate of a large copy.
 //
@@ -39,9 +39,10 @@ __device__ __forceinline__ void step_to_lds(float dt, float x, float bias, bool 
 //   states: the recurrence over chunk i, its sums over n into LDS
 //   rows:   (d, d x), B and C of chunk i + 1 into LDS; skip and gate of chunk
 //           i - 1's sums and the store of its rows; the loads of chunk i + 2
-// Each SIMD holds a wave of either kind, which fill each other's latencies: 254 us
-// at 8 x 4096 x 2048 (256 workgroups), where waves that did both in turn, token
-// group by token group, took 346 us and kept the vector units busy 71 % of the time.
+// Each SIMD holds a wave of either kind, which fill each other's latencies: 255 us
+// at 8 x 4096 x 2048 (256 workgroups), the vector units issuing all the time, where
+// waves that did both in turn, token group by token group, took 346 us and kept them
+// busy 71 % of it.
 template <typename T, int LPC, int NS, bool GATE, bool WIDE>
 __global__ __launch_bounds__(128 * LPC) void scan_forward_kernel(gdr2_scan_args a, Pieces seg, uint32_t ncb, uint32_t cb_per,
                                                                  const float* starts)
@@ -291,7 +292,7 @@ __global__ __launch_bounds__(64 * LPC) void scan_span_kernel(gdr2_scan_args a, P
 
 // Start states of a sequence's segments, written over the E of each.  One
 // thread per (sequence, channel, state), whose loads run kFoldAhead segments
-// ahead of the chain (32 segments of 2048 channels of 16 states: 6.6 us,
+// ahead of the chain (32 segments of 2048 channels of 16 states: 6.9 us,
 // loaded one by one 13.1).
 __global__ __launch_bounds__(256) void scan_fold_kernel(gdr2_scan_args a, Pieces seg, float* states, const float* sums)
 {
@@ -328,7 +329,7 @@ __global__ __launch_bounds__(256) void scan_fold_kernel(gdr2_scan_args a, Pieces
 // One token.  LPC lanes per channel, four states each; a thread keeps its
 // channel's A and parameters over R sequences, whose states are all requested
 // before the first is used.  The states' traffic bounds it: 256 sequences of 2048
-// channels, 16 states, gated, in bf16 are 71 MB in 16.8 us, 4.3 TB/s; one sequence
+// channels, 16 states, gated, in bf16 are 71 MB in 17.0 us, 4.2 TB/s; one sequence
 // takes 4 us, a launch.
 template <typename T, int LPC, int R, bool VEC>
 __global__ __launch_bounds__(256) void scan_step_kernel(gdr2_scan_step_args p, uint32_t lanes)
@@ -452,8 +453,8 @@ int step_lpc(int64_t N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : 8; }
 int64_t step_lanes(int64_t C, int lpc) { return ceil_div(C * lpc, 256) * 256; }
 
 // Sequences per thread: two once that leaves four waves per SIMD (256 x 2048
-// channels, 16 states: 16.8 us; one 19.4, four 20.0, eight 26; streaming
-// accesses to the state 22), else one.
+// channels, 16 states: 16.8 us when all were timed; one 19.4, four 20.0, eight 26;
+// streaming accesses to the state 22), else one.
 int step_sequences(const gdr2_scan_args& a)
 {
     return a.B / 2 * a.C * step_lpc(a.N) >= (int64_t)device_cu_count() * 4 * 4 * 64 ? 2 : 1;
@@ -494,17 +495,18 @@ hipError_t step_n(const gdr2_scan_step_args& a, hipStream_t stream)
 // How a call is cut into segments.
 // One segment per sequence where that keeps the compute units busy, for the span
 // pass repeats most of the work: forwards from 9/16 of a workgroup per unit on (2048
-// channels, 16 states, 4096 tokens: 128 workgroups 250 us whole, 228 in segments;
-// 160: 251 and 286; 256: 254 and 403), backwards, where two workgroups share a
-// unit, from 7/4 (2048 tokens: 256 workgroups 835 us whole, 678 in segments; 448:
-// 1107 and 1134; 512: 1126 and 1314).  Otherwise the longest segments that give
-// every unit four workgroups, at least 128 tokens: 1 x 32768 tokens (32 channel
-// blocks) 410 us with 1024 workgroups, 424 us with 512.
+// channels, 16 states, 4096 tokens: 128 workgroups 251 us whole, 226 in segments;
+// 160: 251 and 274; 256: 258 and 417), backwards, where two workgroups share a
+// unit, from 7/4 (2048 tokens: 256 workgroups 848 us whole, 684 in segments; 448:
+// 1108 and 1149; 512: 1128 and 1327).  Otherwise the longest segments that give
+// every unit four workgroups, two rounds of what is resident, at least 128 tokens:
+// 1 x 32768 tokens (32 channel blocks) 426 us with 1024 workgroups, 438 us with 512.
 // A packed batch is cut at twice its mean length in any case: the host does
 // not know the lengths, one sequence may hold nearly all rows, and sequences
 // that fit one segment skip the span pass.  Some of its slots are idle and some
 // segments short, so whole segments have to give a workgroup per unit there (9
-// sequences, 5003 rows of 1002 channels: 75 us, with the dense rule 116).
+// sequences, 5003 rows of 1002 channels, four draws of the lengths: 76 to 80 us,
+// with the dense rule 77 to 318).
 ScanPlan scan_plan(const gdr2_scan_args& a, bool backward)
 {
     ScanPlan p;

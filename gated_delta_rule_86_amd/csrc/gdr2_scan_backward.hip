@@ -10,8 +10,8 @@
 // registers with their decays while those tokens are walked backwards.
 //
 // The arithmetic bounds it: about 104 vector operations per token and wave of 16
-// channels (26.6 thousand for 256 tokens).  4 x 2048 x 2048 channels of 16 states,
-// gated: 298 us for the main pass, 57 us for the segments' gradients.  The sums
+// channels (26.8 thousand for 256 tokens).  4 x 2048 x 2048 channels of 16 states,
+// gated: 278 us for the main pass, 53 us for the segments' gradients.  The sums
 // over channels (dB, dC) are the expensive ones: a transposing reduction
 // over the channels of a wave, LDS over the waves, one partial row per channel
 // block, added by a last kernel in block order.  The sums over tokens (dA,

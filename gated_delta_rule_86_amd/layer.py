@@ -418,7 +418,9 @@ def scan_forward(x, dt, A, Bt, Ct, skip=None, z=None, dt_bias=None, h0=None, off
     Returns (y, h) or, when chunk_states is True or a float32 tensor
     [scan_chunk_count,C,N], (y, h, h_chunks): the state before every 32nd
     token, which ``scan_backward`` takes.  h is the state after each sequence
-    (None when final_state is false and no h_out is given; h_out may be h0)."""
+    (None when final_state is false and no h_out is given; h_out may be h0).
+    Tokens masked with dt = -inf (or the dtype's lowest value) leave the state
+    as it is, with softplus."""
     B, T, C, N, G = check_scan_shapes(x, dt, A, Bt, Ct, skip, z, dt_bias, offsets)
     for n, t in (("h0", h0), ("h_out", h_out)):
         if t is not None:

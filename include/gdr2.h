@@ -433,7 +433,9 @@ typedef enum gdr2_scan_flags {
  *     v_t[c]    = sum_n Ct_t[j, n] h_t[c, n] + skip[c] x_t[c]
  *     y_t       = v_t, or v_t z_t / (1 + exp(-z_t)) with a gate z
  * (the erase-free relative of the update above, with a decay of its own for
- * every state element instead of one per key channel).
+ * every state element instead of one per key channel).  A token whose dt is
+ * -inf or the dtype's lowest value, as a mask sets it, has d = 0 under softplus:
+ * it leaves the state as it is, and its ddt is 0.
  *   x, dt, z  [.., C]   dtype, rows of x_stride, dt_stride, z_stride elements;
  *                       z may be NULL
  *   Bt, Ct    [.., G, N] dtype, rows (of G*N elements) b_stride, c_stride apart
