@@ -27,7 +27,7 @@ def taken(lib, entry, args):  # noqa: F811
 @pytest.mark.parametrize("C,B,ok", [
     # one channel takes one lane of eight: 32 sequences of a token a workgroup
     (1, (1 << 29) - 64, True), (1, 1 << 29, False),
-    # 65 channels, one by one: two blocks of 64 lanes, four sequences each; (B, T) beyond that is refused
+    # 65 channels, one by one: two blocks of 64 lanes, four sequences each
     (65, (1 << 25) - 64, True), (65, 1 << 25, False),
     # 64: one block, in fours 16 lanes of 16 sequences
     (64, (1 << 26) - 64, True), (64, 1 << 26, False),
