@@ -259,3 +259,61 @@ def test_scan_gradients_of_many_sequences(dtype):
     want, bound = (ref.scan_grad(**a, **kw, dy=dy, h0=h0, absolute=ab) for ab in (False, True))
     for n in ("dx", "ddt", "dBt", "dCt", "dz", "dh0"):
         close(got[n], want[n], bound[n], 2 * scan_steps(c, T), n)
+
+
+# ---- calls larger than 2^32 threads of one element each ---------------------
+
+def test_norm_of_very_many_rows():
+    """More groups of rows than 2^24 workgroups hold: they are walked."""
+    R, C, tail = (1 << 29) + 37, 8, 70
+    x = torch.ones(R, C, dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = rn(gen(92), tail, C, dtype=torch.bfloat16)
+    w = 1 + 0.1 * rn(gen(93), C)
+    y = layer.norm_forward(x, w, kind="rms")
+    assert torch.equal(y[-tail:], layer.norm_forward(x[-tail:].clone(), w, kind="rms"))
+    one = layer.norm_forward(x[:1].clone(), w, kind="rms")
+    assert bool((y[:-tail] == one).all())
+
+
+def test_conv_step_of_very_many_channels():
+    """2^32 elements of one token each: four to a thread."""
+    N, C, tail = (1 << 21) + 3, 2048, 5
+    g = gen(94)
+    st = torch.zeros(N, 3, C, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(N, C, dtype=torch.bfloat16, device="cuda")
+    st[-tail:], x[-tail:] = rn(g, tail, 3, C, dtype=torch.bfloat16), rn(g, tail, C, dtype=torch.bfloat16)
+    w, b = rn(g, C, 4), rn(g, C)
+    end = st[-tail:].clone()
+    y = layer.conv_step(st, x, w, b)
+    assert torch.equal(y[-tail:], layer.conv_step(end, x[-tail:].clone(), w, b)) and torch.equal(st[-tail:], end)
+    assert torch.equal(y[:1], layer.conv_step(torch.zeros_like(end[:1]), x[:1].clone(), w, b)) and torch.equal(y[N // 2], y[0])
+
+
+def test_scan_step_of_very_many_sequences():
+    B, C, N, tail = (1 << 20) + 3, 128, 4, 5
+    g = gen(95)
+    s, x, bc = torch.zeros(B, C, N).cuda(), torch.zeros(B, C).cuda(), torch.zeros(B, 1, N).cuda()
+    s[-tail:], x[-tail:], bc[-tail:] = rn(g, tail, C, N), rn(g, tail, C), rn(g, tail, 1, N)
+    A, end = -torch.rand(C, N, generator=g).cuda(), s[-tail:].clone()
+    y = layer.scan_step(s, x, x, A, bc, bc)
+    tok = [t[-tail:].clone() for t in (x, bc)]
+    assert torch.equal(y[-tail:], layer.scan_step(end, tok[0], tok[0], A, tok[1], tok[1])) and torch.equal(s[-tail:], end)
+    assert bool((s[:-tail] == 0).all()) and bool((y[:-tail] == 0).all())
+
+
+def test_scan_of_very_many_tokens():
+    """More tokens than a thread each for their B and C would allow."""
+    B, T, C, N = 64, (1 << 20) + 3, 8, 32
+    g = torch.Generator(device="cuda").manual_seed(96)
+    x = torch.randn(B, T, C, generator=g, device="cuda", dtype=torch.bfloat16)
+    bc = torch.randn(B, T, 1, N, generator=g, device="cuda", dtype=torch.bfloat16)
+    assert B * T * 2 * N > 1 << 32
+    A = -torch.rand(C, N, generator=g, device="cuda") - 0.5
+    y, h = layer.scan_forward(x, x, A, bc, bc)
+    near = slice(T - 4100, T)                # decays of at most exp(-0.5 * 0.31) a token: the rest is forgotten
+    for b in (0, B - 1):
+        yn, hn = layer.scan_forward(x[b:b + 1, near].contiguous(), x[b:b + 1, near].contiguous(), A,
+                                    bc[b:b + 1, near].contiguous(), bc[b:b + 1, near].contiguous())
+        # the same recurrence from another start of its segments: 600 tokens of fp32 roundings are remembered
+        assert float((h[b] - hn[0]).abs().max()) <= 1e-4 * float(h[b].abs().max())
+        assert float((y[b, -100:].float() - yn[0, -100:].float()).abs().max()) <= 2.0 ** -7 * float(yn[0, -100:].float().abs().max())
