@@ -1,0 +1,200 @@
+// gdr2_glr.h -- shared by the gated linear recurrence's forward and backward
+// kernels: the lane layout, the per-token terms and the segment plan.
+//
+// The recurrence h_t = a_t h_{t-1} + b_t is linear in the state, so a run of
+// tokens maps the state before it to the one after it by h -> P h + L (P the
+// product of its decays, L its end state from zero), and runs join:
+// (P2, L2) after (P1, L1) is (P2 P1, P2 L1 + L2).  A workgroup owns LR V
+// channels and walks a sequence in tiles:
+//
+//   sub-chunk  16 tokens of V adjacent channels of one lane.  LR lanes lie
+//              along the channels, so that a wave moves whole 128-byte lines (LR V
+//              elements a row), and 64 / LR sub-chunks side by side in time;
+//   tile       the sub-chunks of the 8 waves, kSubs of them.
+//
+// Each lane forms its decays and inputs once, in registers, and its (P, L);
+// through LDS it then finds the state its sub-chunk starts from, and walks its
+// tokens.  So every element is read once, its transcendentals are evaluated once, and
+// the state's chain is one multiply-add per sub-chunk, not per token.
+#pragma once
+
+#include "gdr2_block.h"
+#include "gdr2_scan.h"
+
+namespace gdr2 {
+
+constexpr int kGlrChunk = GDR2_GLR_CHUNK;     // tokens of a sub-chunk, and between recorded states
+constexpr int kGlrWaves = 8;
+
+template <int LR> struct GlrTile {
+    static constexpr int kGroups = 64 / LR;                     // sub-chunks of a wave
+    static constexpr int kSubs = kGlrWaves * kGroups;           // of a tile
+    static constexpr int kWaveTokens = kGroups * kGlrChunk;
+    static constexpr int kTokens = kSubs * kGlrChunk;
+};
+
+// Segments of 2^lg tokens, and channel blocks.
+struct GlrPlan {
+    Pieces seg;
+    int64_t blocks;    // of channels
+    int lr;            // lanes along the channels
+    bool split;        // sequences may have more than one segment
+};
+GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward);
+
+// Channels a lane holds: two where every row array is aligned to pairs.
+inline bool glr_pairs(const gdr2_glr_args& a)
+{
+    const int64_t e = a.dtype == GDR2_BF16 ? 2 : 4;
+    auto ok = [&](const void* p, int64_t ld) { return !p || (reinterpret_cast<uintptr_t>(p) % (2 * e) == 0 && ld % 2 == 0); };
+    return a.C % 2 == 0 && ok(a.x, a.x_stride) && ok(a.r, a.r_stride) && ok(a.i, a.i_stride);
+}
+
+// ---- rows of a sub-chunk ---------------------------------------------------
+// The V elements of every token as they lie in memory.
+template <typename T, int V> struct SubRows {
+    static constexpr int W = V * (int)sizeof(T) <= 4 ? 1 : 2;
+    uint32_t raw[kGlrChunk][W];
+
+    template <typename R> __device__ __forceinline__ void load(R rsrc, uint32_t off, uint32_t row_bytes)
+    {
+        typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k) {
+            const uint32_t at = off + k * row_bytes;
+            if constexpr (V * sizeof(T) == 2) {
+                raw[k][0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
+            } else if constexpr (W == 1) {
+                raw[k][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
+            } else {
+                const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0));
+                raw[k][0] = x[0];
+                raw[k][1] = x[1];
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int k, int v) const
+    {
+        if constexpr (sizeof(T) == 4)
+            return __builtin_bit_cast(float, raw[k][v]);
+        else
+            return __builtin_bit_cast(float, v ? raw[k][0] & 0xffff0000u : raw[k][0] << 16);
+    }
+    // Tokens past the sequence (from `left` on) as masked ones: a = 1, and the
+    // state passes them.
+    __device__ __forceinline__ void mask(int left)
+    {
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k)
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                raw[k][w] = k < left ? raw[k][w] : sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+    }
+};
+
+template <typename T, int V, typename R> __device__ __forceinline__ void store_token(R rsrc, uint32_t at, const float (&v)[V])
+{
+    typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+    if constexpr (V == 2 && sizeof(T) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b64(U2{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1])}, rsrc, at, 0, 0);
+    } else if constexpr (V == 2) {
+        typedef T Vec __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (Vec){(T)v[0], (T)v[1]}), rsrc, at, 0, 0);
+    } else if constexpr (sizeof(T) == 4) {
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), rsrc, at, 0, 0);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[0]), rsrc, at, 0, 0);
+    }
+}
+
+// One array's rows in memory, from the wave's first row of a tile on.
+struct WaveRows {
+    const char* base;
+    uint32_t row_bytes;
+    template <typename T> static __device__ __forceinline__ WaveRows at(const void* p, int64_t row, int64_t ld)
+    {
+        return {(const char*)((const T*)p + row * ld), (uint32_t)ld * (uint32_t)sizeof(T)};
+    }
+    // `left` rows from `row` rows behind the base
+    __device__ __forceinline__ auto buffer(int64_t row, int left) const
+    {
+        return __builtin_amdgcn_make_buffer_rsrc((void*)uniform((int64_t)(base + row * (int64_t)row_bytes)), (short)0,
+                                                 __builtin_amdgcn_readfirstlane((int)((uint32_t)left * row_bytes)), 0x00020000);
+    }
+};
+
+// ---- the terms of a token --------------------------------------------------
+// sr = s(r), a = exp(A s(r)) with A2 = A log2(e).
+__device__ __forceinline__ float glr_decay(float A2, float sr) { return fast_exp2(A2 * sr); }
+
+// sqrt(1 - a^2) = sqrt(-expm1(w)), w = 2 A s(r) <= 0.  Near w = 0 the
+// difference cancels, so -expm1(w) = -w (1 + w/2 + .. + w^5/720) there: at
+// |w| <= 1/4 the first term left out is w^6/5040 < 5e-8, and beyond it 1 - a^2 >= 0.22 has
+// lost two bits at most.
+__device__ __forceinline__ float glr_root(float A2, float sr, float a)
+{
+    const float w = 2.f * 0.693147181f * (A2 * sr);
+    float p = fmaf(w, 1.f / 720.f, 1.f / 120.f);
+    p = fmaf(p, w, 1.f / 24.f);
+    p = fmaf(p, w, 1.f / 6.f);
+    p = fmaf(p, w, 0.5f);
+    p = fmaf(p, w, 1.f) * -w;
+    return __builtin_amdgcn_sqrtf(w > -0.25f ? p : fmaf(-a, a, 1.f));
+}
+
+// Where this lane's channels and sub-chunk lie.
+template <int V, int LR> struct GlrLane {
+    int li, sub, wave;
+    int64_t c;
+    bool on;
+    __device__ __forceinline__ GlrLane(int64_t C, int64_t block)
+    {
+        const int lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        li = lane % LR;
+        sub = wave * GlrTile<LR>::kGroups + lane / LR;
+        c = block * (LR * V) + li * V;
+        on = c < C;
+    }
+    // offset in an array's rows from the wave's first one
+    template <typename T> __device__ __forceinline__ uint32_t offset(uint32_t row_bytes) const
+    {
+        return on ? (uint32_t)((threadIdx.x & 63) / LR) * kGlrChunk * row_bytes + (uint32_t)c * (uint32_t)sizeof(T) : kNowhere;
+    }
+};
+
+// This workgroup's segment: `n` tokens from token `t0` of the sequence on.
+struct Segment {
+    Piece q;
+    int64_t t0, n;
+};
+__device__ __forceinline__ Segment segment_of(const GlrPlan& plan, int64_t slot)
+{
+    Segment s;
+    s.q = uniform(piece_of(plan.seg, slot));
+    s.t0 = s.q.index << plan.seg.lg;
+    const int64_t rest = s.q.len - s.t0, L = (int64_t)1 << plan.seg.lg;
+    s.n = rest < L ? rest : L;
+    return s;
+}
+
+// Rows of 16 tokens before a sequence's first one in h_chunks.
+__device__ __forceinline__ int64_t chunk_row(const gdr2_glr_args& a, const Piece& q)
+{
+    return a.offsets ? q.row0 / kGlrChunk + q.seq : q.seq * ((a.T + kGlrChunk - 1) / kGlrChunk);
+}
+
+template <int V> __device__ __forceinline__ void load_channels(const float* p, float (&v)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        v[i] = p[i];
+}
+template <int V> __device__ __forceinline__ void store_channels(float* p, const float (&v)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        p[i] = v[i];
+}
+
+}  // namespace gdr2

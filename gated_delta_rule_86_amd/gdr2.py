@@ -62,8 +62,12 @@ EXPORTS = ("gdr2_forward_workspace_size", "gdr2_forward_chunked", "gdr2_decode_s
            "gdr2_conv_forward", "gdr2_conv_step", "gdr2_conv_backward_workspace_size", "gdr2_conv_backward",
            "gdr2_scan_chunk_count", "gdr2_scan_workspace_size", "gdr2_scan_forward", "gdr2_scan_step",
            "gdr2_scan_backward_workspace_size", "gdr2_scan_backward",
-           "gdr2_norm_forward", "gdr2_norm_backward_workspace_size", "gdr2_norm_backward")
-ABI_VERSION = 7
+           "gdr2_norm_forward", "gdr2_norm_backward_workspace_size", "gdr2_norm_backward",
+           "gdr2_pack_rows", "gdr2_unpack_rows",
+           "gdr2_add_norm_forward", "gdr2_add_norm_backward_workspace_size", "gdr2_add_norm_backward",
+           "gdr2_glr_chunk_count", "gdr2_glr_workspace_size", "gdr2_glr_forward", "gdr2_glr_step",
+           "gdr2_glr_backward_workspace_size", "gdr2_glr_backward")
+ABI_VERSION = 8
 NOALLOC_SCRATCH_BYTES = 64 << 20
 BWD_CHUNK = 64
 
@@ -108,8 +112,9 @@ def load_library(path: str = LIB_PATH):
         lib.gdr2_abi_version.argtypes = []
         if lib.gdr2_abi_version() != ABI_VERSION:
             raise RuntimeError("libgdr2.so ABI version mismatch")
-        from . import layer
+        from . import block, layer
         layer.declare(lib)
+        block.declare(lib)
         _lib = lib
         return lib
 

@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define GDR2_ABI_VERSION 7
+#define GDR2_ABI_VERSION 8
 
 typedef enum gdr2_status {
     GDR2_OK = 0,
@@ -570,6 +570,226 @@ gdr2_status gdr2_scan_backward(const gdr2_scan_bwd_args *args, void *stream);
 gdr2_status gdr2_norm_forward(const gdr2_norm_args *args, void *stream);
 size_t gdr2_norm_backward_workspace_size(const gdr2_norm_bwd_args *args);
 gdr2_status gdr2_norm_backward(const gdr2_norm_bwd_args *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The operators of a block around its mixing layers: the norm with the
+ * residual's addition, the gated linear recurrence (a mixing layer whose
+ * state is one number per channel), and rows in 8 bits, which these two write
+ * as activation checkpoints and read in their gradients.  The rules of the
+ * layer operators above hold for them too (rows, batches, parameters,
+ * gradients, sizes), with these additions:
+ *   Rows8     : rows of C columns in 8 bits are codes [R, C], one e4m3 number
+ *               (4 exponent bits, 3 mantissa bits, largest finite 448) per
+ *               element, and scales [R, ceil(C/32)], one byte b per 32 columns of a
+ *               row (the last block may be shorter) that stands for 2^(b-127).
+ *               An element's value is its code times its block's scale: the
+ *               layout of block-scaled matrix operands.  Both dense.
+ *   Rounding  : a block's scale is the smallest 2^e, e >= -127, with
+ *               448 2^e >= the largest finite magnitude in it, so that no finite value is
+ *               clipped; a code is the value over the scale, to nearest even.
+ *               NaN becomes a NaN code.  e4m3 has no infinity: one becomes a
+ *               NaN beside finite values, but a block without any finite
+ *               value takes e = 120 and the codes +-448, which read as
+ *               infinities again (a row masked with -inf, or with the
+ *               dtype's lowest value, stays one).
+ * ------------------------------------------------------------------------ */
+
+/* Columns that share a scale. */
+#define GDR2_ROWS8_BLOCK 32
+
+typedef struct gdr2_rows8 {
+    void *codes;          /* [R, C] bytes */
+    void *scales;         /* [R, ceil(C / 32)] bytes */
+} gdr2_rows8;
+
+/*
+ * Rows into 8 bits.
+ *   x [R, C] dtype, rows of x_stride elements     out: written
+ * Supported set: C >= 1, R >= 0; dtype F32 or BF16.
+ */
+typedef struct gdr2_pack_args {
+    int64_t R, C;
+    int64_t x_stride;
+    int32_t dtype;        /* gdr2_dtype */
+    int32_t reserved;     /* must be 0 */
+    const void *x;
+    gdr2_rows8 out;
+} gdr2_pack_args;
+
+/* Rows from 8 bits: y [R, C] dtype, dense, written (in fp32 the exact values;
+ * those past the type's range read as infinite). */
+typedef struct gdr2_unpack_args {
+    int64_t R, C;
+    int32_t dtype;        /* gdr2_dtype of y */
+    int32_t reserved;     /* must be 0 */
+    gdr2_rows8 rows;
+    void *y;
+} gdr2_unpack_args;
+
+/*
+ * Norm with the residual's addition, over R rows of C elements:
+ *     h = x + residual, rounded to the residual's type
+ *     n = (h - m) (mean((h - m)^2) + eps)^(-1/2) weight + bias
+ *     y = n,  y8 = n in 8 bits,  h8 = h in 8 bits
+ * with m the row's mean (LAYER) or 0 (RMS).  The norm is taken of h as it is
+ * stored, so that the gradients see the same rows.
+ *   x, residual [R, C]   dtype and res_dtype, rows of x_stride, res_stride
+ *                        elements; residual may be NULL (h = x; then res_dtype
+ *                        must be dtype)
+ *   weight, bias [C] fp32, may be NULL (1 and 0)
+ *   h    [R, C] res_dtype, dense, may be NULL; may be the same pointer as a
+ *        dense residual (res_stride == C): the stream is then updated in place
+ *   y    [R, C] dtype, dense, may be NULL
+ *   y8, h8  may be NULL (both pointers of one); at least one of h, y, y8, h8 is given
+ * The statistics and n are formed in 64 bits, so that codes do not depend on
+ * how a row is spread over lanes.
+ * Supported set: 1 <= C <= 16384, R >= 0; eps >= 0 and finite; dtype F32 or
+ * BF16; res_dtype the same or F32.
+ */
+typedef struct gdr2_add_norm_args {
+    int64_t R, C;
+    int64_t x_stride, res_stride;
+    int32_t dtype;        /* gdr2_dtype of x and y */
+    int32_t res_dtype;    /* gdr2_dtype of residual and h */
+    int32_t kind;         /* gdr2_norm_kind */
+    float eps;
+    const void *x, *residual;
+    const float *weight, *bias;
+    void *h, *y;
+    gdr2_rows8 y8, h8;
+} gdr2_add_norm_args;
+
+/*
+ * Gradients of the norm with the residual's addition, given dy (dL/dy) and
+ * optionally dh (dL/dh by the stream's other uses):
+ *     dresidual = dh + the norm's gradient with respect to h;  dx the same
+ *   h [R, C] res_dtype, dense, as the forward wrote it; or NULL, and h8: the
+ *     gradient is then that at the values the codes stand for
+ *   dy [R, C] dtype   dh [R, C] res_dtype, may be NULL      all dense
+ *   dresidual [R, C] res_dtype, may be the same pointer as dh
+ *   dx [R, C] dtype, may be NULL      at least one of dresidual and dx is given
+ *   dweight, dbias [C] fp32, may be NULL
+ * A gradient through y8 or h8 is taken as one through n or h.
+ * Supported set: as the forward's.
+ */
+typedef struct gdr2_add_norm_bwd_args {
+    int64_t R, C;
+    int32_t dtype;        /* gdr2_dtype of dy and dx */
+    int32_t res_dtype;    /* gdr2_dtype of h, dh and dresidual */
+    int32_t kind;         /* gdr2_norm_kind */
+    float eps;
+    const float *weight;
+    const void *h;
+    gdr2_rows8 h8;
+    const void *dy, *dh;
+    void *dresidual, *dx;
+    float *dweight, *dbias;
+    void *workspace;      /* device, >= gdr2_add_norm_backward_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_add_norm_bwd_args;
+
+/* Tokens between two recorded states of the gated linear recurrence. */
+#define GDR2_GLR_CHUNK 16
+
+/*
+ * Gated linear recurrence.  For every sequence and channel c, s the logistic
+ * sigmoid:
+ *     a_t = exp(A[c] s(r_t[c]))
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(i_t[c]) x_t[c],   y_t = h_t
+ * A token with a_t = 1 (r = -inf or the dtype's lowest value, as a mask sets
+ * it, or A = 0) leaves the state as it is; its x and i are not used, whatever they
+ * hold.  A <= 0 is expected (a positive A gives NaN, the root's value there).
+ *   x, r, i  [.., C]  dtype, rows of x_stride, r_stride, i_stride elements
+ *   A        [C] fp32
+ *   h0       [B, C] fp32, may be NULL (zero)
+ *   y        [.., C]  dtype, dense, written
+ *   h_out    [B, C] fp32, may be NULL: the state after each sequence; may be
+ *            the same pointer as h0
+ *   h_chunks [gdr2_glr_chunk_count(), C] fp32, may be NULL: the state before
+ *            the tokens 0, 16, 32, ... of each sequence, which the backward
+ *            reads.  Token 16*j of sequence s is recorded in row
+ *            s*ceil(T/16) + j, or with offsets offsets[s]/16 + s + j; other
+ *            rows are left as they were.
+ *   x8, r8, i8  the rows of x, r and i in 8 bits, as gdr2_pack_rows forms
+ *            them; all six pointers or none.  Rows of no sequence are left as they were.
+ * algo: AUTO, STAGED (one pass over each sequence) or SEGMENTED (sequences
+ * cut into segments that run in parallel: a span pass forms each segment's
+ * total decay and local end state, and the main pass chains those before its
+ * segment).  AUTO takes segments when one pass would leave much of the GPU idle.
+ * Supported set: C >= 1; rows at most 2^22 elements apart; dtype F32 or BF16; B, T >= 0.
+ */
+typedef struct gdr2_glr_args {
+    int64_t B, T, C;
+    int64_t x_stride, r_stride, i_stride;
+    int32_t dtype;        /* gdr2_dtype */
+    int32_t algo;         /* gdr2_algo: AUTO, STAGED or SEGMENTED */
+    const void *x, *r, *i;
+    const float *A, *h0;
+    const int64_t *offsets;
+    void *y;
+    float *h_out, *h_chunks;
+    gdr2_rows8 x8, r8, i8;
+    void *workspace;      /* device, >= gdr2_glr_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_glr_args;
+
+/*
+ * The recurrence for one token of each of N sequences:
+ *   state [N, C] fp32, read and overwritten in place
+ *   x, r, i [N, C] dtype, rows of x_stride, r_stride, i_stride elements (at
+ *   most 2^40)      y [N, C] dtype, written
+ */
+typedef struct gdr2_glr_step_args {
+    int64_t N, C;
+    int64_t x_stride, r_stride, i_stride;
+    int32_t dtype;        /* gdr2_dtype */
+    int32_t reserved;     /* must be 0 */
+    float *state;
+    const void *x, *r, *i;
+    const float *A;
+    void *y;
+} gdr2_glr_step_args;
+
+/*
+ * Gradients of the recurrence, given dy (dL/dy, dense) and optionally dh_out
+ * (dL/dh_out).  `f` holds the forward's arguments: sizes, dtype (of dy and the
+ * gradients too), A, offsets, algo, h_chunks as the forward wrote them (required),
+ * and either x, r, i, or, with these NULL, x8, r8, i8: the gradients are then
+ * those at the values the codes stand for, with the states formed again from
+ * the recorded one before every 16th token.  f's other fields are not read.
+ *   dx, dr, di [.., C] dtype, dense     dA [C] fp32     dh0 [B, C] fp32
+ * dh0 may be NULL, and may be the same pointer as dh_out.  Where a_t = 1 the
+ * root's own derivative, which has no value there, counts as 0.
+ */
+typedef struct gdr2_glr_bwd_args {
+    gdr2_glr_args f;
+    const void *dy;
+    const float *dh_out;
+    void *dx, *dr, *di;
+    float *dA, *dh0;
+    void *workspace;      /* device, >= gdr2_glr_backward_workspace_size() bytes */
+    size_t workspace_bytes;
+} gdr2_glr_bwd_args;
+
+/* Rows into 8 bits and back. */
+gdr2_status gdr2_pack_rows(const gdr2_pack_args *args, void *stream);
+gdr2_status gdr2_unpack_rows(const gdr2_unpack_args *args, void *stream);
+
+/* The norm with the residual's addition, and its gradients. */
+gdr2_status gdr2_add_norm_forward(const gdr2_add_norm_args *args, void *stream);
+size_t gdr2_add_norm_backward_workspace_size(const gdr2_add_norm_bwd_args *args);
+gdr2_status gdr2_add_norm_backward(const gdr2_add_norm_bwd_args *args, void *stream);
+
+/* The gated linear recurrence, its single-token step, its gradients.  The
+ * workspace queries (here and above) look at sizes, at whether an optional
+ * pointer is NULL, and at the current device's compute units; 0 when none is
+ * needed or the arguments are invalid or unsupported. */
+int64_t gdr2_glr_chunk_count(int64_t B, int64_t T, int packed);
+size_t gdr2_glr_workspace_size(const gdr2_glr_args *args);
+gdr2_status gdr2_glr_forward(const gdr2_glr_args *args, void *stream);
+gdr2_status gdr2_glr_step(const gdr2_glr_step_args *args, void *stream);
+size_t gdr2_glr_backward_workspace_size(const gdr2_glr_bwd_args *args);
+gdr2_status gdr2_glr_backward(const gdr2_glr_bwd_args *args, void *stream);
 
 /* Static text for a status code (never NULL). */
 const char *gdr2_status_string(gdr2_status status);
