@@ -47,16 +47,18 @@ __device__ __forceinline__ int block_exponent(int amax)
     const int e = ((amax + 0x1fffff) >> 23) - 135;
     return amax < 0 ? 120 : max(e, -127);
 }
-// 2^-e as a factor: a normal number for every e in -127 .. 120.
-__device__ __forceinline__ float inverse_scale(int e) { return __builtin_bit_cast(float, (uint32_t)(127 - e) << 23); }
+// A scale as the scaled conversions take it: the exponent field of an fp32
+// number, 0 for 2^-127.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
 
 // Two values over their block's scale as codes, in the low or high half of
-// `old`.  The product by a power of two is exact (below the smallest normal
-// number it may round, but such a value's code is 0), the conversion rounds to
+// `old` (v_cvt_scalef32_pk_fp8_*): the quotient is exact, the rounding to
 // nearest even, and an infinity becomes NaN.
-template <bool HIGH> __device__ __forceinline__ int codes2(float a, float b, float inv, int old)
+template <bool HIGH> __device__ __forceinline__ s16x2 codes2(float a, float b, float scale, s16x2 old)
 {
-    return __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, old, HIGH);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, a, b, scale, HIGH);
 }
 // For blocks without finite values: infinities as +-448, NaN as it is.
 __device__ __forceinline__ float clip_infinity(float v) { return __builtin_isinf(v) ? __builtin_copysignf(448.f, v) : v; }
@@ -66,7 +68,6 @@ template <int V> struct Codes {
     uint32_t w[V == 8 ? 2 : 1];
     __device__ __forceinline__ void pack(const float (&v)[V], int amax, int e)
     {
-        const float inv = inverse_scale(e);
         if (__builtin_expect(amax < 0, 0)) {
             float c[V];
 #pragma unroll
@@ -74,19 +75,21 @@ template <int V> struct Codes {
                 c[i] = clip_infinity(v[i]);
             set(c, 1.f);
         } else {
-            set(v, inv);
+            set(v, scale_of(e + 127));
         }
     }
-    __device__ __forceinline__ void set(const float (&v)[V], float inv)
+    __device__ __forceinline__ void set(const float (&v)[V], float scale)
     {
+        const s16x2 none = {0, 0};
         if constexpr (V == 8) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                w[h] = codes2<true>(v[4 * h + 2], v[4 * h + 3], inv, codes2<false>(v[4 * h], v[4 * h + 1], inv, 0));
+                w[h] = __builtin_bit_cast(uint32_t, codes2<true>(v[4 * h + 2], v[4 * h + 3], scale,
+                                                                codes2<false>(v[4 * h], v[4 * h + 1], scale, none)));
         } else if constexpr (V == 2) {
-            w[0] = codes2<false>(v[0], v[1], inv, 0);
+            w[0] = __builtin_bit_cast(uint32_t, codes2<false>(v[0], v[1], scale, none));
         } else {
-            w[0] = codes2<false>(v[0], 0.f, inv, 0);
+            w[0] = __builtin_bit_cast(uint32_t, codes2<false>(v[0], 0.f, scale, none));
         }
     }
     __device__ __forceinline__ void load(const uint8_t* p)
@@ -119,21 +122,22 @@ template <int V> struct Codes {
     // values at the scale byte s
     __device__ __forceinline__ void get(uint32_t s, float (&v)[V]) const
     {
-        const int e = (int)s - 127;
+        const float scale = scale_of(s);
         if constexpr (V == 8) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true);
-                v[4 * h] = __builtin_amdgcn_ldexpf(lo[0], e);
-                v[4 * h + 1] = __builtin_amdgcn_ldexpf(lo[1], e);
-                v[4 * h + 2] = __builtin_amdgcn_ldexpf(hi[0], e);
-                v[4 * h + 3] = __builtin_amdgcn_ldexpf(hi[1], e);
+                const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, false);
+                const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, true);
+                v[4 * h] = lo[0];
+                v[4 * h + 1] = lo[1];
+                v[4 * h + 2] = hi[0];
+                v[4 * h + 3] = hi[1];
             }
         } else {
-            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[0], false);
+            const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[0], scale, false);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                v[i] = __builtin_amdgcn_ldexpf(lo[i], e);
+                v[i] = lo[i];
         }
     }
 };

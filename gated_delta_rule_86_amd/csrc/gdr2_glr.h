@@ -42,43 +42,55 @@ struct GlrPlan {
 };
 GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward);
 
-// Channels a lane holds: two where every row array is aligned to pairs.
+// Whether a lane holds two channels: bf16 where every row array is aligned to
+// pairs.  (One of fp32 is as wide, and 64 lanes of them 256 bytes.)
 inline bool glr_pairs(const gdr2_glr_args& a)
 {
-    const int64_t e = a.dtype == GDR2_BF16 ? 2 : 4;
-    auto ok = [&](const void* p, int64_t ld) { return !p || (reinterpret_cast<uintptr_t>(p) % (2 * e) == 0 && ld % 2 == 0); };
-    return a.C % 2 == 0 && ok(a.x, a.x_stride) && ok(a.r, a.r_stride) && ok(a.i, a.i_stride);
+    auto ok = [&](const void* p, int64_t ld) { return !p || (reinterpret_cast<uintptr_t>(p) % 4 == 0 && ld % 2 == 0); };
+    return a.dtype == GDR2_BF16 && a.C % 2 == 0 && ok(a.x, a.x_stride) && ok(a.r, a.r_stride) && ok(a.i, a.i_stride);
 }
 
 // ---- rows of a sub-chunk ---------------------------------------------------
-// The V elements of every token as they lie in memory.
-template <typename T, int V> struct SubRows {
-    static constexpr int W = V * (int)sizeof(T) <= 4 ? 1 : 2;
-    uint32_t raw[kGlrChunk][W];
-
-    template <typename R> __device__ __forceinline__ void load(R rsrc, uint32_t off, uint32_t row_bytes)
-    {
-        typedef uint32_t U2 __attribute__((ext_vector_type(2)));
+// f(k, lane offset, scalar offset) for the 16 tokens, `off` and k row_bytes apart.
+// A descriptor's length is held against the lane offset alone.  So where some
+// of a wave's tokens do not exist, the row goes into that, and those read 0 or
+// write nothing; where all do (`full`), it goes into the scalar one, which costs
+// no vector operation and no register.  (The empty statement keeps the sums
+// where they are: as invariants of the tiles' loop they would fill the registers.)
+template <typename F> __device__ __forceinline__ void for_tokens(bool full, uint32_t off, uint32_t row_bytes, const F& f)
+{
+    if (full) {
 #pragma unroll
-        for (int k = 0; k < kGlrChunk; ++k) {
-            const uint32_t at = off + k * row_bytes;
-            if constexpr (V * sizeof(T) == 2) {
-                raw[k][0] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, 0, 0);
-            } else if constexpr (W == 1) {
-                raw[k][0] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, 0, 0);
-            } else {
-                const U2 x = __builtin_bit_cast(U2, __builtin_amdgcn_raw_buffer_load_b64(rsrc, at, 0, 0));
-                raw[k][0] = x[0];
-                raw[k][1] = x[1];
-            }
-        }
+        for (int k = 0; k < kGlrChunk; ++k)
+            f(k, off, k * row_bytes);
+    } else {
+        asm volatile("" : "+s"(row_bytes));
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k)
+            f(k, off + k * row_bytes, 0u);
+    }
+}
+
+// The V elements of every token as they lie in memory, a register each.
+template <typename T, int V> struct SubRows {
+    static_assert(V * sizeof(T) <= 4, "one register");
+    uint32_t raw[kGlrChunk];
+
+    template <typename R> __device__ __forceinline__ void load(R rsrc, uint32_t off, uint32_t row_bytes, bool full)
+    {
+        for_tokens(full, off, row_bytes, [&](int k, uint32_t at, uint32_t row) {
+            if constexpr (V * sizeof(T) == 2)
+                raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, row, 0);
+            else
+                raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, row, 0);
+        });
     }
     __device__ __forceinline__ float get(int k, int v) const
     {
         if constexpr (sizeof(T) == 4)
-            return __builtin_bit_cast(float, raw[k][v]);
+            return __builtin_bit_cast(float, raw[k]);
         else
-            return __builtin_bit_cast(float, v ? raw[k][0] & 0xffff0000u : raw[k][0] << 16);
+            return __builtin_bit_cast(float, v ? raw[k] & 0xffff0000u : raw[k] << 16);
     }
     // Tokens past the sequence (from `left` on) as masked ones: a = 1, and the
     // state passes them.
@@ -86,24 +98,19 @@ template <typename T, int V> struct SubRows {
     {
 #pragma unroll
         for (int k = 0; k < kGlrChunk; ++k)
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                raw[k][w] = k < left ? raw[k][w] : sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+            raw[k] = k < left ? raw[k] : sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
     }
 };
 
-template <typename T, int V, typename R> __device__ __forceinline__ void store_token(R rsrc, uint32_t at, const float (&v)[V])
+template <typename T, int V, typename R> __device__ __forceinline__ void store_token(R rsrc, uint32_t at, uint32_t row, const float (&v)[V])
 {
-    typedef uint32_t U2 __attribute__((ext_vector_type(2)));
-    if constexpr (V == 2 && sizeof(T) == 4) {
-        __builtin_amdgcn_raw_buffer_store_b64(U2{__builtin_bit_cast(uint32_t, v[0]), __builtin_bit_cast(uint32_t, v[1])}, rsrc, at, 0, 0);
-    } else if constexpr (V == 2) {
+    if constexpr (V == 2) {
         typedef T Vec __attribute__((ext_vector_type(2)));
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (Vec){(T)v[0], (T)v[1]}), rsrc, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (Vec){(T)v[0], (T)v[1]}), rsrc, at, row, 0);
     } else if constexpr (sizeof(T) == 4) {
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), rsrc, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), rsrc, at, row, 0);
     } else {
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[0]), rsrc, at, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[0]), rsrc, at, row, 0);
     }
 }
 
@@ -124,23 +131,24 @@ struct WaveRows {
 };
 
 // ---- the terms of a token --------------------------------------------------
-// sr = s(r), a = exp(A s(r)) with A2 = A log2(e).
-__device__ __forceinline__ float glr_decay(float A2, float sr) { return fast_exp2(A2 * sr); }
-
-// sqrt(1 - a^2) = sqrt(-expm1(w)), w = 2 A s(r) <= 0.  Near w = 0 the
-// difference cancels, so -expm1(w) = -w (1 + w/2 + .. + w^5/720) there: at
-// |w| <= 1/4 the first term left out is w^6/5040 < 5e-8, and beyond it 1 - a^2 >= 0.22 has
-// lost two bits at most.
-__device__ __forceinline__ float glr_root(float A2, float sr, float a)
+// q = sqrt(1 - a^2) = sqrt(-expm1(w)), w = 2 A s(r) = 2 ln 2 t with t = A2 s(r).
+// Near w = 0 the difference cancels, so -expm1(w) = -(w + w^2/2 + .. + w^5/120)
+// there, a polynomial in t: at |w| <= 1/8 the first term left out is w^5/720 <
+// 5e-8 of the value, and beyond it 1 - a^2 >= 0.117 has lost three bits at most.
+__device__ __forceinline__ float glr_root(float t, float a)
 {
-    const float w = 2.f * 0.693147181f * (A2 * sr);
-    float p = fmaf(w, 1.f / 720.f, 1.f / 120.f);
-    p = fmaf(p, w, 1.f / 24.f);
-    p = fmaf(p, w, 1.f / 6.f);
-    p = fmaf(p, w, 0.5f);
-    p = fmaf(p, w, 1.f) * -w;
-    return __builtin_amdgcn_sqrtf(w > -0.25f ? p : fmaf(-a, a, 1.f));
+    constexpr float c = 1.386294361f;
+    float p = fmaf(t, -c * c * c * c * c / 120.f, -c * c * c * c / 24.f);
+    p = fmaf(p, t, -c * c * c / 6.f);
+    p = fmaf(p, t, -c * c / 2.f);
+    p = fmaf(p, t, -c) * t;
+    return __builtin_amdgcn_sqrtf(__builtin_unpredictable(t > -0.125f / c) ? p : fmaf(-a, a, 1.f));
 }
+
+// 0 for a masked token (q == 0), whose x and i may be anything, NaN among them.
+// (Unpredictable, that is a select: a branch per element would split the block
+// it is scheduled in.)
+__device__ __forceinline__ float unless_masked(float q, float v) { return __builtin_unpredictable(q == 0.f) ? 0.f : v; }
 
 // Where this lane's channels and sub-chunk lie.
 template <int V, int LR> struct GlrLane {
@@ -160,6 +168,13 @@ template <int V, int LR> struct GlrLane {
     template <typename T> __device__ __forceinline__ uint32_t offset(uint32_t row_bytes) const
     {
         return on ? (uint32_t)((threadIdx.x & 63) / LR) * kGlrChunk * row_bytes + (uint32_t)c * (uint32_t)sizeof(T) : kNowhere;
+    }
+    // the same for the scale of the block its channels lie in, which the lanes
+    // past the row's end share with those before it
+    __device__ __forceinline__ uint32_t scale_offset(uint32_t row_bytes, int64_t C) const
+    {
+        const int64_t at = c / kRows8;
+        return at < scale_count(C) ? (uint32_t)((threadIdx.x & 63) / LR) * kGlrChunk * row_bytes + (uint32_t)at : kNowhere;
     }
 };
 

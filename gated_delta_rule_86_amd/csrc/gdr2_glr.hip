@@ -38,10 +38,9 @@ __device__ __forceinline__ SpanVec<V> form_terms(const Inputs<T, V>& in, const f
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float sr = sigmoid_f(in.r.get(k, v)), si = sigmoid_f(in.i.get(k, v));
-            const float at = glr_decay(A2[v], sr), q = glr_root(A2[v], sr, at);
+            const float u = A2[v] * sr, at = fast_exp2(u), q = glr_root(u, at);
             a[k][v] = at;
-            // a masked token's input may be anything, NaN among it
-            b[k][v] = q == 0.f ? 0.f : q * si * in.x.get(k, v);
+            b[k][v] = unless_masked(q, q * si * in.x.get(k, v));
             s.l[v] = fmaf(at, s.l[v], b[k][v]);
             s.p[v] *= at;
         }
@@ -74,35 +73,115 @@ template <typename T, int V, int LR> struct Walk {
         const int m = left(t);
         // no row past the segment is addressed, not even by a descriptor without bytes
         const int64_t at = m > 0 ? first(t) : 0;
-        in.r.load(r.buffer(at, m), orr, r.row_bytes);
-        in.x.load(x.buffer(at, m), ox, x.row_bytes);
-        in.i.load(i.buffer(at, m), oi, i.row_bytes);
+        const bool full = m == Tile::kWaveTokens;
+        in.r.load(r.buffer(at, m), orr, r.row_bytes, full);
+        in.x.load(x.buffer(at, m), ox, x.row_bytes, full);
+        in.i.load(i.buffer(at, m), oi, i.row_bytes, full);
     }
 };
 
-// The rows of one array of a sub-chunk in 8 bits.
-template <typename T, int V, int LR>
-__device__ __forceinline__ void put_codes(const gdr2_rows8& to, const SubRows<T, V>& rows, int64_t C, int64_t row, int left,
-                                          const GlrLane<V, LR>& lane)
+// ---- rows in 8 bits --------------------------------------------------------
+// The largest magnitudes of the 16 tokens over the 16 lanes of a block, lane k
+// of the block returning that of token k: each round hands half of the tokens to
+// the partner that keeps them.  Magnitudes are pairs of 16-bit integers that
+// order like the bf16 numbers they are the bits of.
+__device__ __forceinline__ int pair_max(int a, int b)
 {
-    constexpr int LPB = kRows8 / V;
-    const int64_t nb = scale_count(C);
+    return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(s16x2, a), __builtin_bit_cast(s16x2, b)));
+}
+template <int CTRL, int N> __device__ __forceinline__ void max_round(int (&m)[N], bool upper)
+{
 #pragma unroll
-    for (int k = 0; k < kGlrChunk; ++k) {
-        float v[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            v[j] = rows.get(k, j);
-        const int amax = block_max<V>(v, lane.on), e = block_exponent(amax);
-        Codes<V> codes;
-        codes.pack(v, amax, e);
-        if (lane.on && k < left) {
-            codes.store((uint8_t*)to.codes + (row + k) * C + lane.c);
-            if (lane.li % LPB == 0)
-                ((uint8_t*)to.scales)[(row + k) * nb + lane.c / kRows8] = (uint8_t)(e + 127);
-        }
+    for (int k = 0; k < N / 2; ++k) {
+        const int keep = upper ? m[k + N / 2] : m[k], give = upper ? m[k] : m[k + N / 2];
+        m[k] = pair_max(keep, __builtin_amdgcn_update_dpp(0, give, CTRL, 0xF, 0xF, true));
     }
 }
+__device__ __forceinline__ int token_max(const int (&in)[16])
+{
+    const int lane = threadIdx.x;
+    int m[16], n[8], o[4], p[2];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+        m[k] = in[k];
+    max_round<0x140>(m, lane & 8);       // lane 15 - i
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        n[k] = m[k];
+    max_round<0x141>(n, lane & 4);       // lane 7 - i of the eight
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = n[k];
+    max_round<0x4E>(o, lane & 2);        // lane i ^ 2
+    p[0] = o[0];
+    p[1] = o[1];
+    max_round<0xB1>(p, lane & 1);        // lane i ^ 1
+    const s16x2 v = __builtin_bit_cast(s16x2, p[0]);
+    return v[0] > v[1] ? v[0] : v[1];
+}
+
+// The rows of one array of a sub-chunk in 8 bits.
+template <typename T, int V> struct CodeRows {
+    WaveRows codes, scales;
+    uint32_t off, soff;
+    template <int LR> __device__ __forceinline__ CodeRows(const gdr2_rows8& to, int64_t row0, int64_t C, const GlrLane<V, LR>& lane)
+        : codes(WaveRows::at<uint8_t>(to.codes, row0, C)), scales(WaveRows::at<uint8_t>(to.scales, row0, scale_count(C))),
+          off(lane.template offset<uint8_t>(codes.row_bytes)), soff(lane.scale_offset(scales.row_bytes, C))
+    {
+    }
+    __device__ __forceinline__ void put(const SubRows<T, V>& rows, bool on, int64_t first, int left, bool full) const
+    {
+        const auto bc = codes.buffer(first, left), bs = scales.buffer(first, left);
+        const s16x2 none = {0, 0};
+        if constexpr (V == 2) {
+            // |v| + 0x80 is negative as a 16-bit integer for NaN and infinities, and above 0 otherwise
+            int m[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                m[k] = on ? __builtin_bit_cast(int, __builtin_bit_cast(s16x2, rows.raw[k] & 0x7fff7fffu) + (s16x2){0x80, 0x80}) : 0;
+            const int most = token_max(m);
+            const int e = block_exponent(most > 0 ? (most - 0x80) << 16 : -1);
+            __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e + 127), bs, soff + (threadIdx.x % 16) * scales.row_bytes, 0, 0);
+            const int scale = (e + 127) << 23;
+            uint32_t c[16];
+            if (__any(most <= 0 && on))
+                codes_of<true, 0>(rows, scale, most > 0, c);
+            else
+                codes_of<false, 0>(rows, scale, true, c);
+            for_tokens(full, off, codes.row_bytes, [&](int k, uint32_t at, uint32_t row) {
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)c[k], bc, at, row, 0);
+            });
+        } else {
+            for_tokens(full, off, codes.row_bytes, [&](int k, uint32_t at, uint32_t row) {
+                const float v[1] = {rows.get(k, 0)};
+                const int amax = block_max<1>(v, on), e = block_exponent(amax);
+                const float clipped = amax < 0 ? clip_infinity(v[0]) : v[0];
+                const s16x2 c = codes2<false>(clipped, 0.f, amax < 0 ? 1.f : scale_of(e + 127), none);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)c[0], bc, at, row, 0);
+                if (threadIdx.x % kRows8 == 0)
+                    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e + 127), bs, soff + k * scales.row_bytes, 0, 0);
+            });
+        }
+    }
+    // Token K's scale lies in lane K of the block.  ODD: some block of the wave is without numbers.
+    template <bool ODD, int K>
+    __device__ __forceinline__ void codes_of(const SubRows<T, V>& rows, int scale, bool number, uint32_t (&out)[16]) const
+    {
+        if constexpr (K < 16) {
+            typedef __bf16 Pair __attribute__((ext_vector_type(2)));
+            const s16x2 none = {0, 0};
+            const float s = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, scale, 0x150 + K, 0xF, 0xF, true));
+            s16x2 c = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(none, __builtin_bit_cast(Pair, rows.raw[K]), s, false);
+            if constexpr (ODD) {
+                const bool some = __builtin_amdgcn_update_dpp(0, (int)number, 0x150 + K, 0xF, 0xF, true);
+                const s16x2 clipped = codes2<false>(clip_infinity(rows.get(K, 0)), clip_infinity(rows.get(K, 1)), 1.f, none);
+                c = some ? c : clipped;
+            }
+            out[K] = __builtin_bit_cast(uint32_t, c);
+            codes_of<ODD, K + 1>(rows, scale, number, out);
+        }
+    }
+};
 
 // The state the segment starts from: h0 and the segments before it in turn,
 // eight of their (P, L) in flight.
@@ -159,6 +238,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
     const uint32_t oy = lane.template offset<T>(y.row_bytes);
     const int64_t chunk0 = a.h_chunks ? chunk_row(a, seg.q) + seg.t0 / kGlrChunk : 0;
 
+    const CodeRows<T, V> x8(a.x8, row0, a.C, lane), r8(a.r8, row0, a.C, lane), i8(a.i8, row0, a.C, lane);
+
     Inputs<T, V> next;
     walk.load(next, 0);
     int buf = 0;
@@ -166,11 +247,15 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
         Inputs<T, V> cur = next;
         walk.load(next, t + Tile::kTokens);
         const int left = walk.left(t), mine = left - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
-        const int64_t first = t + lane.sub * kGlrChunk;       // of this sub-chunk in the segment
         if constexpr (PACK) {
-            put_codes<T, V, LR>(a.x8, cur.x, a.C, row0 + first, mine, lane);
-            put_codes<T, V, LR>(a.r8, cur.r, a.C, row0 + first, mine, lane);
-            put_codes<T, V, LR>(a.i8, cur.i, a.C, row0 + first, mine, lane);
+            const int64_t at = left > 0 ? walk.first(t) : 0;
+            const bool full = left == Tile::kWaveTokens;
+            x8.put(cur.x, lane.on, at, left, full);
+            __builtin_amdgcn_sched_barrier(0);       // one array after the other: their registers
+            r8.put(cur.r, lane.on, at, left, full);
+            __builtin_amdgcn_sched_barrier(0);
+            i8.put(cur.i, lane.on, at, left, full);
+            __builtin_amdgcn_sched_barrier(0);
         }
         if (left < Tile::kWaveTokens)
             cur.r.mask(mine);
@@ -201,15 +286,14 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
         }
         if constexpr (!SPAN) {
             if (a.h_chunks && lane.on && mine > 0)
-                store_channels<V>(a.h_chunks + (chunk0 + first / kGlrChunk) * a.C + lane.c, start);
+                store_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, start);
             const auto out = y.buffer(left > 0 ? walk.first(t) : 0, left);
-#pragma unroll
-            for (int k = 0; k < kGlrChunk; ++k) {
+            for_tokens(left == Tile::kWaveTokens, oy, y.row_bytes, [&](int k, uint32_t off, uint32_t row) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     start[v] = fmaf(at[k][v], start[v], b[k][v]);
-                store_token<T, V>(out, oy + k * y.row_bytes, start);
-            }
+                store_token<T, V>(out, off, row, start);
+            });
         }
     }
     if (lane.sub != 0 || !lane.on)
@@ -241,8 +325,8 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const float A2 = exponent_scale(A[v]), sr = sigmoid_f(r[v]), si = sigmoid_f(i[v]);
-            const float at_ = glr_decay(A2, sr), q = glr_root(A2, sr, at_);
-            h[v] = fmaf(at_, h[v], q == 0.f ? 0.f : q * si * x[v]);
+            const float u = A2 * sr, a_t = fast_exp2(u), q = glr_root(u, a_t);
+            h[v] = fmaf(a_t, h[v], unless_masked(q, q * si * x[v]));
         }
         store_row<V>(a.state + n * a.C + c, h);
         store_row<V>((T*)a.y + n * a.C + c, h);
@@ -268,12 +352,10 @@ template <typename T, int V, int LR> hipError_t forward_lr(const gdr2_glr_args& 
     return hipGetLastError();
 }
 
-template <typename T> hipError_t forward_t(const gdr2_glr_args& a, hipStream_t stream)
+hipError_t forward_pairs(const gdr2_glr_args& a, hipStream_t stream)
 {
-    if (!glr_pairs(a))
-        return forward_lr<T, 1, 64>(a, glr_plan(a, 1, false), stream);
     const GlrPlan plan = glr_plan(a, 2, false);
-    return plan.lr == 32 ? forward_lr<T, 2, 32>(a, plan, stream) : forward_lr<T, 2, 16>(a, plan, stream);
+    return plan.lr == 32 ? forward_lr<bf16, 2, 32>(a, plan, stream) : forward_lr<bf16, 2, 16>(a, plan, stream);
 }
 
 template <typename T, int V> hipError_t step_v(const gdr2_glr_step_args& a, hipStream_t stream)
@@ -322,13 +404,16 @@ GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward)
 // The larger of the two widths' needs where the pointers decide between them.
 size_t glr_workspace_bytes(const gdr2_glr_args& a)
 {
-    const int64_t one = span_floats(a, glr_plan(a, 1, false)), two = a.C % 2 ? 0 : span_floats(a, glr_plan(a, 2, false));
+    const int64_t one = span_floats(a, glr_plan(a, 1, false)), two = a.C % 2 || a.dtype != GDR2_BF16 ? 0 : span_floats(a, glr_plan(a, 2, false));
     return (size_t)std::max(one, two) * sizeof(float);
 }
 
 hipError_t launch_glr_forward(const gdr2_glr_args& a, hipStream_t stream)
 {
-    return a.dtype == GDR2_BF16 ? forward_t<bf16>(a, stream) : forward_t<float>(a, stream);
+    if (glr_pairs(a))
+        return forward_pairs(a, stream);
+    const GlrPlan plan = glr_plan(a, 1, false);
+    return a.dtype == GDR2_BF16 ? forward_lr<bf16, 1, 64>(a, plan, stream) : forward_lr<float, 1, 64>(a, plan, stream);
 }
 
 hipError_t launch_glr_step(const gdr2_glr_step_args& a, hipStream_t stream)

@@ -28,23 +28,23 @@ template <int V> struct SubCodes {
     uint32_t scale[V == 1 ? kGlrChunk : 1];
 
     template <typename R, typename S>
-    __device__ __forceinline__ void load(R codes, uint32_t off, uint32_t row_bytes, S scales, uint32_t soff, uint32_t scale_bytes)
+    __device__ __forceinline__ void load(R codes, uint32_t off, uint32_t row_bytes, S scales, uint32_t soff, uint32_t scale_bytes,
+                                         bool full)
     {
-#pragma unroll
-        for (int k = 0; k < kGlrChunk; ++k) {
+        for_tokens(full, off, row_bytes, [&](int k, uint32_t at, uint32_t row) {
             if constexpr (V == 2)
-                raw[k] = __builtin_amdgcn_raw_buffer_load_b16(codes, off + k * row_bytes, 0, 0);
+                raw[k] = __builtin_amdgcn_raw_buffer_load_b16(codes, at, row, 0);
             else
-                raw[k] = __builtin_amdgcn_raw_buffer_load_b8(codes, off + k * row_bytes, 0, 0);
-        }
+                raw[k] = __builtin_amdgcn_raw_buffer_load_b8(codes, at, row, 0);
+        });
         if constexpr (V == 2) {
             // 16 lanes hold a block, as many as a sub-chunk has tokens
             static_assert(kRows8 / V == kGlrChunk, "one lane a token");
             scale[0] = __builtin_amdgcn_raw_buffer_load_b8(scales, soff + (threadIdx.x % kGlrChunk) * scale_bytes, 0, 0);
         } else {
-#pragma unroll
-            for (int k = 0; k < kGlrChunk; ++k)
-                scale[k] = __builtin_amdgcn_raw_buffer_load_b8(scales, soff + k * scale_bytes, 0, 0);
+            for_tokens(full, soff, scale_bytes, [&](int k, uint32_t at, uint32_t row) {
+                scale[k] = __builtin_amdgcn_raw_buffer_load_b8(scales, at, row, 0);
+            });
         }
     }
     template <int K> __device__ __forceinline__ void token(float (&v)[V]) const
@@ -102,18 +102,16 @@ struct Source {
         s.rows = WaveRows::at<uint8_t>(p.codes, row0, C);
         s.scales = WaveRows::at<uint8_t>(p.scales, row0, scale_count(C));
         s.off = lane.template offset<uint8_t>(s.rows.row_bytes);
-        // the block of this lane's channels, which exists where lane 0 of the block has one
-        const int64_t at = lane.c / kRows8;
-        s.soff = at < scale_count(C) ? (uint32_t)((threadIdx.x & 63) / LR) * kGlrChunk * s.scales.row_bytes + (uint32_t)at : kNowhere;
+        s.soff = lane.scale_offset(s.scales.row_bytes, C);
         return s;
     }
-    template <typename T, int V> __device__ __forceinline__ void load(SubRows<T, V>& to, int64_t at, int left) const
+    template <typename T, int V> __device__ __forceinline__ void load(SubRows<T, V>& to, int64_t at, int left, bool full) const
     {
-        to.load(rows.buffer(at, left), off, rows.row_bytes);
+        to.load(rows.buffer(at, left), off, rows.row_bytes, full);
     }
-    template <int V> __device__ __forceinline__ void load(SubCodes<V>& to, int64_t at, int left) const
+    template <int V> __device__ __forceinline__ void load(SubCodes<V>& to, int64_t at, int left, bool full) const
     {
-        to.load(rows.buffer(at, left), off, rows.row_bytes, scales.buffer(at, left), soff, scales.row_bytes);
+        to.load(rows.buffer(at, left), off, rows.row_bytes, scales.buffer(at, left), soff, scales.row_bytes, full);
     }
 };
 
@@ -165,6 +163,8 @@ __device__ __forceinline__ void reverse_fold(const float (*s_span)[LR][2 * V], c
             if constexpr (SPAN)
                 whole[v] *= pl[2 * v];
         }
+        if (j % 8 == 0)
+            __builtin_amdgcn_sched_barrier(0);       // eight reads in flight at most
     }
 }
 
@@ -206,8 +206,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
     auto fetch = [&](decltype(GradInputs<T, V, P8>::r)& r, SubRows<T, V>& dy, int64_t t) {
         const int m = rows.left(t);
         const int64_t at = m > 0 ? rows.first(t) : 0;
-        sr.load(r, at, m);
-        sd.load(dy, at, m);
+        sr.load(r, at, m, m == Tile::kWaveTokens);
+        sd.load(dy, at, m, m == Tile::kWaveTokens);
     };
     decltype(GradInputs<T, V, P8>::r) next_r;
     SubRows<T, V> next_dy;
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
             token_of<K>(r, rv);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                at[K][v] = K < mine ? glr_decay(A2[v], sigmoid_f(rv[v])) : 1.f;
+                at[K][v] = __builtin_unpredictable(K < mine) ? fast_exp2(A2[v] * sigmoid_f(rv[v])) : 1.f;
         });
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -289,48 +289,54 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
         }
         const Source sd = Source::of_rows<T, V, LR>(p.dy, row0, a.C, lane);
         const WaveRows ox = WaveRows::at<T>(p.dx, row0, a.C), orr = WaveRows::at<T>(p.dr, row0, a.C), oi = WaveRows::at<T>(p.di, row0, a.C);
+        const uint32_t off = lane.template offset<T>(ox.row_bytes);
         const int64_t chunk0 = chunk_row(a, seg.q) + seg.t0 / kGlrChunk;
         const int64_t L = (int64_t)1 << plan.seg.lg, count = plan.split ? (seg.q.len + L - 1) >> plan.seg.lg : 1;
         float lam[V], reach[V], unused[V];
         end_gradient<V>(p.dh_out, spans, seg.q, count, a.C, lane.c, lane.on, lam);
 
-        struct Fetched {
-            GradInputs<T, V, P8> in;
-            SubRows<T, V> dy;
-            float h[V];
-        } next;
+        // r, dy and the recorded state of the next tile are on their way through the second half of this one, x and i
+        // of this one through its first half
+        decltype(GradInputs<T, V, P8>::r) r;
+        SubRows<T, V> dy;
+        float h0[V];
         auto fetch = [&](int64_t t) {
             const int m = rows.left(t), mine = m - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
             const int64_t at = m > 0 ? rows.first(t) : 0;
-            sr.load(next.in.r, at, m);
-            sd.load(next.dy, at, m);
-            sx.load(next.in.x, at, m);
-            si.load(next.in.i, at, m);
+            sr.load(r, at, m, m == Tile::kWaveTokens);
+            sd.load(dy, at, m, m == Tile::kWaveTokens);
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                next.h[v] = 0.f;
+                h0[v] = 0.f;
             if (lane.on && mine > 0)
-                load_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, next.h);
+                load_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, h0);
         };
         const int64_t last = seg.n > 0 ? (seg.n - 1) / Tile::kTokens * Tile::kTokens : -1;
         if (last >= 0)
             fetch(last);
         int buf = 0;
         for (int64_t t = last; t >= 0; t -= Tile::kTokens, buf ^= 1) {
-            Fetched cur = next;
-            fetch(t - Tile::kTokens);
             const int left = rows.left(t), mine = left - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
+            const int64_t first = left > 0 ? rows.first(t) : 0;
+            decltype(GradInputs<T, V, P8>::x) x, i;
+            sx.load(x, first, left, left == Tile::kWaveTokens);
+            si.load(i, first, left, left == Tile::kWaveTokens);
             float at[kGlrChunk][V], sg[kGlrChunk][V], g[kGlrChunk][V], P[V], Lr[V];
             tokens_up([&](auto at_k) {
                 constexpr int K = decltype(at_k)::value;
                 float rv[V];
-                token_of<K>(cur.in.r, rv);
+                token_of<K>(r, rv);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    sg[K][v] = K < mine ? sigmoid_f(rv[v]) : 0.f;
-                    at[K][v] = glr_decay(A2[v], sg[K][v]);
-                }
+                for (int v = 0; v < V; ++v)
+                    sg[K][v] = sigmoid_f(rv[v]);
             });
+            if (left < Tile::kWaveTokens) {
+#pragma unroll
+                for (int k = 0; k < kGlrChunk; ++k)
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        sg[k][v] = k < mine ? sg[k][v] : 0.f;
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 P[v] = 1.f;
@@ -340,7 +346,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             for (int k = kGlrChunk - 1; k >= 0; --k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    Lr[v] = at[k][v] * (cur.dy.get(k, v) + Lr[v]);
+                    at[k][v] = fast_exp2(A2[v] * sg[k][v]);
+                    Lr[v] = at[k][v] * (dy.get(k, v) + Lr[v]);
                     P[v] *= at[k][v];
                 }
 #pragma unroll
@@ -350,39 +357,53 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             }
             lds_barrier();
             reverse_fold<V, LR, false>(s_span[buf], lane, lam, reach, unused);
+            float h[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                h[v] = h0[v];
 #pragma unroll
             for (int k = kGlrChunk - 1; k >= 0; --k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    g[k][v] = cur.dy.get(k, v) + reach[v];
+                    g[k][v] = dy.get(k, v) + reach[v];
                     reach[v] = at[k][v] * g[k][v];
                 }
-            const int64_t first = left > 0 ? rows.first(t) : 0;
+            __builtin_amdgcn_sched_barrier(0);
             const auto bx = ox.buffer(first, left), br = orr.buffer(first, left), bi = oi.buffer(first, left);
-            const uint32_t off = lane.template offset<T>(ox.row_bytes);
+            // a token's row in the lanes' or in the scalar offset, as for_tokens places it
+            const bool full = left == Tile::kWaveTokens;
+            uint32_t row_bytes = ox.row_bytes;
+            asm volatile("" : "+s"(row_bytes));
             tokens_up([&](auto at_k) {
                 constexpr int K = decltype(at_k)::value;
                 float xv[V], iv[V], dx[V], dr[V], di[V];
-                token_of<K>(cur.in.x, xv);
-                token_of<K>(cur.in.i, iv);
+                token_of<K>(x, xv);
+                token_of<K>(i, iv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float s = sg[K][v], e = at[K][v], q = glr_root(A2[v], s, e);
+                    const float s = sg[K][v], e = at[K][v], q = glr_root(A2[v] * s, e);
                     // a masked token's x and i have no part, whatever they hold
-                    const bool shut = q == 0.f;
-                    const float o = shut ? 0.f : sigmoid_f(iv[v]), x = shut ? 0.f : xv[v];
-                    const float ox_ = o * x, gq = g[K][v] * q;
+                    const float all = sigmoid_f(iv[v]), o = unless_masked(q, all), in = unless_masked(q, all * xv[v]);
+                    const float gq = g[K][v] * q;
                     dx[v] = gq * o;
-                    di[v] = gq * ox_ * (1.f - o);
-                    const float over = shut ? 0.f : e * e * __builtin_amdgcn_rcpf(q);
-                    const float du = g[K][v] * fmaf(e, cur.h[v], -ox_ * over);
+                    di[v] = gq * in * (1.f - o);
+                    // 1/q where q is 0: anything finite, for `in` is 0
+                    const float over = e * e * __builtin_amdgcn_rcpf(fmaxf(q, 1e-30f));
+                    const float du = g[K][v] * fmaf(e, h[v], -in * over);
                     dA[v] = fmaf(du, s, dA[v]);
-                    dr[v] = du * Av[v] * (s * (1.f - s));
-                    cur.h[v] = fmaf(e, cur.h[v], q * ox_);
+                    dr[v] = du * (Av[v] * fmaf(-s, s, s));
+                    h[v] = fmaf(e, h[v], q * in);
                 }
-                store_token<T, V>(bx, off + K * ox.row_bytes, dx);
-                store_token<T, V>(br, off + K * ox.row_bytes, dr);
-                store_token<T, V>(bi, off + K * ox.row_bytes, di);
+                const uint32_t row = K * row_bytes, lane_row = full ? off : off + row, all_row = full ? row : 0;
+                store_token<T, V>(bx, lane_row, all_row, dx);
+                store_token<T, V>(br, lane_row, all_row, dr);
+                store_token<T, V>(bi, lane_row, all_row, di);
+                // tokens are scheduled four at a time, and the next tile's loads take the registers of the first half:
+                // more in flight would not fit
+                if constexpr (K % 4 == 3)
+                    __builtin_amdgcn_sched_barrier(0);
+                if constexpr (K == kGlrChunk / 2 - 1)
+                    fetch(t - Tile::kTokens);
             });
         }
         if (p.dh0 && seg.q.index == 0 && lane.sub == 0 && lane.on)
@@ -428,12 +449,14 @@ hipError_t backward_lr(const gdr2_glr_bwd_args& p, const GlrPlan& plan, hipStrea
     return launch_column_sum(part, P, p.f.C, {p.dA, p.f.C}, {nullptr, 0}, {nullptr, 0}, stream);
 }
 
-template <typename T, bool P8> hipError_t backward_t(const gdr2_glr_bwd_args& p, hipStream_t stream)
+template <bool P8> hipError_t backward_p(const gdr2_glr_bwd_args& p, hipStream_t stream)
 {
-    if (P8 ? p.f.C % 2 != 0 : !glr_pairs(p.f))
-        return backward_lr<T, 1, 64, P8>(p, glr_plan(p.f, 1, true), stream);
-    const GlrPlan plan = glr_plan(p.f, 2, true);
-    return plan.lr == 32 ? backward_lr<T, 2, 32, P8>(p, plan, stream) : backward_lr<T, 2, 16, P8>(p, plan, stream);
+    if (glr_pairs(p.f)) {
+        const GlrPlan plan = glr_plan(p.f, 2, true);
+        return plan.lr == 32 ? backward_lr<bf16, 2, 32, P8>(p, plan, stream) : backward_lr<bf16, 2, 16, P8>(p, plan, stream);
+    }
+    const GlrPlan plan = glr_plan(p.f, 1, true);
+    return p.f.dtype == GDR2_BF16 ? backward_lr<bf16, 1, 64, P8>(p, plan, stream) : backward_lr<float, 1, 64, P8>(p, plan, stream);
 }
 
 }  // namespace
@@ -443,7 +466,7 @@ size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& p)
 {
     int64_t most = 0;
     for (int V : {1, 2}) {
-        if (p.f.C % V)
+        if (V == 2 && (p.f.C % 2 || p.f.dtype != GDR2_BF16))
             continue;
         const GlrPlan plan = glr_plan(p.f, V, true);
         most = std::max(most, span_floats(p.f, plan) + plan.seg.slots() * p.f.C);
@@ -453,16 +476,14 @@ size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& p)
 
 hipError_t launch_glr_backward(const gdr2_glr_bwd_args& p, hipStream_t stream)
 {
-    if (p.f.dtype == GDR2_BF16)
-        return p.f.x ? backward_t<bf16, false>(p, stream) : backward_t<bf16, true>(p, stream);
-    return p.f.x ? backward_t<float, false>(p, stream) : backward_t<float, true>(p, stream);
+    return p.f.x ? backward_p<false>(p, stream) : backward_p<true>(p, stream);
 }
 
 int64_t glr_launch_groups(const gdr2_glr_args& a, bool backward)
 {
     int64_t most = 0;
     for (int V : {1, 2}) {
-        if (a.C % V)
+        if (V == 2 && (a.C % 2 || a.dtype != GDR2_BF16))
             continue;
         const GlrPlan plan = glr_plan(a, V, backward);
         const double groups = (double)plan.seg.slots() * (double)plan.blocks * (kGlrWaves * 64 / 256);
