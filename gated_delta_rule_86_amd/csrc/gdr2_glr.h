@@ -51,39 +51,32 @@ inline bool glr_pairs(const gdr2_glr_args& a)
 }
 
 // ---- rows of a sub-chunk ---------------------------------------------------
-// f(k, lane offset, scalar offset) for the 16 tokens, `off` and k row_bytes apart.
-// A descriptor's length is held against the lane offset alone.  So where some
-// of a wave's tokens do not exist, the row goes into that, and those read 0 or
-// write nothing; where all do (`full`), it goes into the scalar one, which costs
-// no vector operation and no register.  (The empty statement keeps the sums
-// where they are: as invariants of the tiles' loop they would fill the registers.)
-template <typename F> __device__ __forceinline__ void for_tokens(bool full, uint32_t off, uint32_t row_bytes, const F& f)
-{
-    if (full) {
-#pragma unroll
-        for (int k = 0; k < kGlrChunk; ++k)
-            f(k, off, k * row_bytes);
-    } else {
-        asm volatile("" : "+s"(row_bytes));
-#pragma unroll
-        for (int k = 0; k < kGlrChunk; ++k)
-            f(k, off + k * row_bytes, 0u);
+// A sub-chunk's rows are addressed by one offset that goes on by a row per
+// token: formed from the token's number they would be invariants of the tiles'
+// loop, and fill the registers.  Tokens past the sequence lie past the
+// descriptor's end: they read 0 and write nothing.
+struct RowOffset {
+    uint32_t at, row_bytes;
+    __device__ __forceinline__ uint32_t next()
+    {
+        const uint32_t v = at;
+        at += row_bytes;
+        asm("" : "+v"(at));
+        return v;
     }
-}
+};
 
 // The V elements of every token as they lie in memory, a register each.
 template <typename T, int V> struct SubRows {
     static_assert(V * sizeof(T) <= 4, "one register");
     uint32_t raw[kGlrChunk];
 
-    template <typename R> __device__ __forceinline__ void load(R rsrc, uint32_t off, uint32_t row_bytes, bool full)
+    template <typename R> __device__ __forceinline__ void load(int k, R rsrc, RowOffset& at)
     {
-        for_tokens(full, off, row_bytes, [&](int k, uint32_t at, uint32_t row) {
-            if constexpr (V * sizeof(T) == 2)
-                raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at, row, 0);
-            else
-                raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, row, 0);
-        });
+        if constexpr (V * sizeof(T) == 2)
+            raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at.next(), 0, 0);
+        else
+            raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at.next(), 0, 0);
     }
     __device__ __forceinline__ float get(int k, int v) const
     {
@@ -102,15 +95,15 @@ template <typename T, int V> struct SubRows {
     }
 };
 
-template <typename T, int V, typename R> __device__ __forceinline__ void store_token(R rsrc, uint32_t at, uint32_t row, const float (&v)[V])
+template <typename T, int V, typename R> __device__ __forceinline__ void store_token(R rsrc, uint32_t at, const float (&v)[V])
 {
     if constexpr (V == 2) {
         typedef T Vec __attribute__((ext_vector_type(2)));
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (Vec){(T)v[0], (T)v[1]}), rsrc, at, row, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, (Vec){(T)v[0], (T)v[1]}), rsrc, at, 0, 0);
     } else if constexpr (sizeof(T) == 4) {
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), rsrc, at, row, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[0]), rsrc, at, 0, 0);
     } else {
-        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[0]), rsrc, at, row, 0);
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[0]), rsrc, at, 0, 0);
     }
 }
 

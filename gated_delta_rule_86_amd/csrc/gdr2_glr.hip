@@ -22,32 +22,7 @@ template <typename T, int V> struct Inputs {
     SubRows<T, V> x, r, i;
 };
 
-// (a, b) of a sub-chunk, and its (P, L).
-template <typename T, int V>
-__device__ __forceinline__ SpanVec<V> form_terms(const Inputs<T, V>& in, const float (&A2)[V], float (&a)[kGlrChunk][V],
-                                                 float (&b)[kGlrChunk][V])
-{
-    SpanVec<V> s;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        s.p[v] = 1.f;
-        s.l[v] = 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < kGlrChunk; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float sr = sigmoid_f(in.r.get(k, v)), si = sigmoid_f(in.i.get(k, v));
-            const float u = A2[v] * sr, at = fast_exp2(u), q = glr_root(u, at);
-            a[k][v] = at;
-            b[k][v] = unless_masked(q, q * si * in.x.get(k, v));
-            s.l[v] = fmaf(at, s.l[v], b[k][v]);
-            s.p[v] *= at;
-        }
-    return s;
-}
-
-// What a workgroup needs to walk the tiles of its segment.
+// The rows of x, r and i, from the segment's first one on.
 template <typename T, int V, int LR> struct Walk {
     typedef GlrTile<LR> Tile;
     WaveRows x, r, i;
@@ -68,17 +43,49 @@ template <typename T, int V, int LR> struct Walk {
         const int64_t m = n - first(t);
         return (int)(m < 0 ? 0 : m > Tile::kWaveTokens ? Tile::kWaveTokens : m);
     }
-    __device__ __forceinline__ void load(Inputs<T, V>& in, int64_t t) const
+    // f(buffers of r, x and i, offsets) of the tile at t
+    template <typename F> __device__ __forceinline__ void with_tile(int64_t t, const F& f) const
     {
         const int m = left(t);
         // no row past the segment is addressed, not even by a descriptor without bytes
         const int64_t at = m > 0 ? first(t) : 0;
-        const bool full = m == Tile::kWaveTokens;
-        in.r.load(r.buffer(at, m), orr, r.row_bytes, full);
-        in.x.load(x.buffer(at, m), ox, x.row_bytes, full);
-        in.i.load(i.buffer(at, m), oi, i.row_bytes, full);
+        f(r.buffer(at, m), x.buffer(at, m), i.buffer(at, m), RowOffset{orr, r.row_bytes}, RowOffset{ox, x.row_bytes},
+          RowOffset{oi, i.row_bytes});
     }
 };
+
+// (a, b) of a sub-chunk, and its (P, L).  Each token's registers are loaded
+// again, for the tile at `t`, as soon as its terms are formed: the loads run a whole tile
+// ahead of their use, and go out evenly over the tile.
+template <typename T, int V, int LR>
+__device__ __forceinline__ SpanVec<V> form_terms(Inputs<T, V>& in, const Walk<T, V, LR>& walk, int64_t t, const float (&A2)[V],
+                                                 float (&a)[kGlrChunk][V], float (&b)[kGlrChunk][V])
+{
+    SpanVec<V> s;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        s.p[v] = 1.f;
+        s.l[v] = 0.f;
+    }
+    walk.with_tile(t, [&](auto br, auto bx, auto bi, RowOffset atr, RowOffset atx, RowOffset ati) {
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float sr = sigmoid_f(in.r.get(k, v)), si = sigmoid_f(in.i.get(k, v));
+                const float u = A2[v] * sr, at = fast_exp2(u), q = glr_root(u, at);
+                a[k][v] = at;
+                b[k][v] = unless_masked(q, q * si * in.x.get(k, v));
+                s.l[v] = fmaf(at, s.l[v], b[k][v]);
+                s.p[v] *= at;
+            }
+            in.r.load(k, br, atr);
+            in.x.load(k, bx, atx);
+            in.i.load(k, bi, ati);
+        }
+    });
+    return s;
+}
 
 // ---- rows in 8 bits --------------------------------------------------------
 // The largest magnitudes of the 16 tokens over the 16 lanes of a block, lane k
@@ -129,9 +136,10 @@ template <typename T, int V> struct CodeRows {
           off(lane.template offset<uint8_t>(codes.row_bytes)), soff(lane.scale_offset(scales.row_bytes, C))
     {
     }
-    __device__ __forceinline__ void put(const SubRows<T, V>& rows, bool on, int64_t first, int left, bool full) const
+    __device__ __forceinline__ void put(const SubRows<T, V>& rows, bool on, int64_t first, int left) const
     {
         const auto bc = codes.buffer(first, left), bs = scales.buffer(first, left);
+        RowOffset at{off, codes.row_bytes};
         const s16x2 none = {0, 0};
         if constexpr (V == 2) {
             // |v| + 0x80 is negative as a 16-bit integer for NaN and infinities, and above 0 otherwise
@@ -148,19 +156,22 @@ template <typename T, int V> struct CodeRows {
                 codes_of<true, 0>(rows, scale, most > 0, c);
             else
                 codes_of<false, 0>(rows, scale, true, c);
-            for_tokens(full, off, codes.row_bytes, [&](int k, uint32_t at, uint32_t row) {
-                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)c[k], bc, at, row, 0);
-            });
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)c[k], bc, at.next(), 0, 0);
         } else {
-            for_tokens(full, off, codes.row_bytes, [&](int k, uint32_t at, uint32_t row) {
+            RowOffset sat{soff, scales.row_bytes};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
                 const float v[1] = {rows.get(k, 0)};
                 const int amax = block_max<1>(v, on), e = block_exponent(amax);
                 const float clipped = amax < 0 ? clip_infinity(v[0]) : v[0];
                 const s16x2 c = codes2<false>(clipped, 0.f, amax < 0 ? 1.f : scale_of(e + 127), none);
-                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)c[0], bc, at, row, 0);
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)c[0], bc, at.next(), 0, 0);
+                const uint32_t place = sat.next();
                 if (threadIdx.x % kRows8 == 0)
-                    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e + 127), bs, soff + k * scales.row_bytes, 0, 0);
-            });
+                    __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e + 127), bs, place, 0, 0);
+            }
         }
     }
     // Token K's scale lies in lane K of the block.  ODD: some block of the wave is without numbers.
@@ -240,27 +251,31 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
 
     const CodeRows<T, V> x8(a.x8, row0, a.C, lane), r8(a.r8, row0, a.C, lane), i8(a.i8, row0, a.C, lane);
 
-    Inputs<T, V> next;
-    walk.load(next, 0);
+    Inputs<T, V> in;
+    walk.with_tile(0, [&](auto br, auto bx, auto bi, RowOffset atr, RowOffset atx, RowOffset ati) {
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k) {
+            in.r.load(k, br, atr);
+            in.x.load(k, bx, atx);
+            in.i.load(k, bi, ati);
+        }
+    });
     int buf = 0;
     for (int64_t t = 0; t < seg.n; t += Tile::kTokens, buf ^= 1) {
-        Inputs<T, V> cur = next;
-        walk.load(next, t + Tile::kTokens);
         const int left = walk.left(t), mine = left - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
         if constexpr (PACK) {
             const int64_t at = left > 0 ? walk.first(t) : 0;
-            const bool full = left == Tile::kWaveTokens;
-            x8.put(cur.x, lane.on, at, left, full);
+            x8.put(in.x, lane.on, at, left);
             __builtin_amdgcn_sched_barrier(0);       // one array after the other: their registers
-            r8.put(cur.r, lane.on, at, left, full);
+            r8.put(in.r, lane.on, at, left);
             __builtin_amdgcn_sched_barrier(0);
-            i8.put(cur.i, lane.on, at, left, full);
+            i8.put(in.i, lane.on, at, left);
             __builtin_amdgcn_sched_barrier(0);
         }
         if (left < Tile::kWaveTokens)
-            cur.r.mask(mine);
+            in.r.mask(mine);
         float at[kGlrChunk][V], b[kGlrChunk][V];
-        const SpanVec<V> s = form_terms<T, V>(cur, A2, at, b);
+        const SpanVec<V> s = form_terms<T, V, LR>(in, walk, t + Tile::kTokens, A2, at, b);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             s_span[buf][lane.sub][lane.li][2 * v] = s.p[v];
@@ -288,12 +303,14 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
             if (a.h_chunks && lane.on && mine > 0)
                 store_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, start);
             const auto out = y.buffer(left > 0 ? walk.first(t) : 0, left);
-            for_tokens(left == Tile::kWaveTokens, oy, y.row_bytes, [&](int k, uint32_t off, uint32_t row) {
+            RowOffset to{oy, y.row_bytes};
+#pragma unroll
+            for (int k = 0; k < kGlrChunk; ++k) {
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     start[v] = fmaf(at[k][v], start[v], b[k][v]);
-                store_token<T, V>(out, off, row, start);
-            });
+                store_token<T, V>(out, to.next(), start);
+            }
         }
     }
     if (lane.sub != 0 || !lane.on)

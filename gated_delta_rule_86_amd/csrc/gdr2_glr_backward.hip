@@ -22,31 +22,11 @@ namespace gdr2 {
 namespace {
 
 // ---- rows in 8 bits --------------------------------------------------------
-// A sub-chunk's codes; lane k of a block's lanes holds the scale of token k.
+// A sub-chunk's codes; with two channels a lane, lane k of a block's 16 lanes
+// holds the scale of token k.
 template <int V> struct SubCodes {
     uint32_t raw[kGlrChunk];
     uint32_t scale[V == 1 ? kGlrChunk : 1];
-
-    template <typename R, typename S>
-    __device__ __forceinline__ void load(R codes, uint32_t off, uint32_t row_bytes, S scales, uint32_t soff, uint32_t scale_bytes,
-                                         bool full)
-    {
-        for_tokens(full, off, row_bytes, [&](int k, uint32_t at, uint32_t row) {
-            if constexpr (V == 2)
-                raw[k] = __builtin_amdgcn_raw_buffer_load_b16(codes, at, row, 0);
-            else
-                raw[k] = __builtin_amdgcn_raw_buffer_load_b8(codes, at, row, 0);
-        });
-        if constexpr (V == 2) {
-            // 16 lanes hold a block, as many as a sub-chunk has tokens
-            static_assert(kRows8 / V == kGlrChunk, "one lane a token");
-            scale[0] = __builtin_amdgcn_raw_buffer_load_b8(scales, soff + (threadIdx.x % kGlrChunk) * scale_bytes, 0, 0);
-        } else {
-            for_tokens(full, soff, scale_bytes, [&](int k, uint32_t at, uint32_t row) {
-                scale[k] = __builtin_amdgcn_raw_buffer_load_b8(scales, at, row, 0);
-            });
-        }
-    }
     template <int K> __device__ __forceinline__ void token(float (&v)[V]) const
     {
         Codes<V> c;
@@ -58,14 +38,6 @@ template <int V> struct SubCodes {
     }
 };
 
-// The sub-chunk's x, r and i, from rows or from codes.
-template <typename T, int V, bool P8> struct GradInputs;
-template <typename T, int V> struct GradInputs<T, V, false> {
-    SubRows<T, V> x, r, i;
-};
-template <typename T, int V> struct GradInputs<T, V, true> {
-    SubCodes<V> x, r, i;
-};
 template <int K, typename T, int V> __device__ __forceinline__ void token_of(const SubRows<T, V>& s, float (&v)[V])
 {
 #pragma unroll
@@ -83,37 +55,64 @@ template <int K = 0, typename F> __device__ __forceinline__ void tokens_up(const
     }
 }
 
-// Where an array's rows lie, for the wave's rows of a tile.
-struct Source {
+// One array's rows, from the segment's first one on.
+template <typename T, int V, bool P8> struct Source {
+    typedef SubRows<T, V> Tokens;
+    WaveRows rows;
+    uint32_t off;
+    template <int LR> __device__ __forceinline__ Source(const void* p, int64_t row0, int64_t ld, const GlrLane<V, LR>& lane)
+        : rows(WaveRows::at<T>(p, row0, ld)), off(lane.template offset<T>(rows.row_bytes))
+    {
+    }
+    template <int LR>
+    __device__ __forceinline__ Source(const void* p, const gdr2_rows8&, int64_t row0, int64_t ld, int64_t, const GlrLane<V, LR>& lane)
+        : Source(p, row0, ld, lane)
+    {
+    }
+    // The tokens of one tile, in turn: the wave's first one is `first`, `left` of them exist.
+    struct Reader {
+        __amdgpu_buffer_rsrc_t rsrc;
+        RowOffset at;
+        __device__ __forceinline__ void load(int k, Tokens& to) { to.load(k, rsrc, at); }
+    };
+    __device__ __forceinline__ Reader reader(int64_t first, int left) const { return {rows.buffer(first, left), {off, rows.row_bytes}}; }
+};
+template <typename T, int V> struct Source<T, V, true> {
+    typedef SubCodes<V> Tokens;
     WaveRows rows, scales;
     uint32_t off, soff;
-    template <typename T, int V, int LR>
-    static __device__ __forceinline__ Source of_rows(const void* p, int64_t row0, int64_t ld, const GlrLane<V, LR>& lane)
+    template <int LR>
+    __device__ __forceinline__ Source(const void*, const gdr2_rows8& p, int64_t row0, int64_t, int64_t C, const GlrLane<V, LR>& lane)
+        : rows(WaveRows::at<uint8_t>(p.codes, row0, C)), scales(WaveRows::at<uint8_t>(p.scales, row0, scale_count(C))),
+          off(lane.template offset<uint8_t>(rows.row_bytes)), soff(lane.scale_offset(scales.row_bytes, C))
     {
-        Source s{};
-        s.rows = WaveRows::at<T>(p, row0, ld);
-        s.off = lane.template offset<T>(s.rows.row_bytes);
-        return s;
     }
-    template <int V, int LR>
-    static __device__ __forceinline__ Source of_codes(const gdr2_rows8& p, int64_t row0, int64_t C, const GlrLane<V, LR>& lane)
+    struct Reader {
+        __amdgpu_buffer_rsrc_t codes, scales;
+        RowOffset at, scale_at;
+        __device__ __forceinline__ void load(int k, Tokens& to)
+        {
+            if constexpr (V == 2) {
+                to.raw[k] = __builtin_amdgcn_raw_buffer_load_b16(codes, at.next(), 0, 0);
+                // 16 lanes hold a block, as many as a sub-chunk has tokens; the last token's code is the last use
+                static_assert(kRows8 / V == kGlrChunk, "one lane a token");
+                if (k == kGlrChunk - 1)
+                    to.scale[0] = __builtin_amdgcn_raw_buffer_load_b8(scales, scale_at.at + (threadIdx.x % kGlrChunk) * scale_at.row_bytes, 0, 0);
+            } else {
+                to.raw[k] = __builtin_amdgcn_raw_buffer_load_b8(codes, at.next(), 0, 0);
+                to.scale[k] = __builtin_amdgcn_raw_buffer_load_b8(scales, scale_at.next(), 0, 0);
+            }
+        }
+    };
+    __device__ __forceinline__ Reader reader(int64_t first, int left) const
     {
-        Source s{};
-        s.rows = WaveRows::at<uint8_t>(p.codes, row0, C);
-        s.scales = WaveRows::at<uint8_t>(p.scales, row0, scale_count(C));
-        s.off = lane.template offset<uint8_t>(s.rows.row_bytes);
-        s.soff = lane.scale_offset(s.scales.row_bytes, C);
-        return s;
-    }
-    template <typename T, int V> __device__ __forceinline__ void load(SubRows<T, V>& to, int64_t at, int left, bool full) const
-    {
-        to.load(rows.buffer(at, left), off, rows.row_bytes, full);
-    }
-    template <int V> __device__ __forceinline__ void load(SubCodes<V>& to, int64_t at, int left, bool full) const
-    {
-        to.load(rows.buffer(at, left), off, rows.row_bytes, scales.buffer(at, left), soff, scales.row_bytes, full);
+        return {rows.buffer(first, left), scales.buffer(first, left), {off, rows.row_bytes}, {soff, scales.row_bytes}};
     }
 };
+
+// A value that is formed here, not where it is used: what it is formed from
+// gives its registers to the loads that follow.
+__device__ __forceinline__ void here(float& v) { asm volatile("" : "+v"(v)); }
 
 // The gradient that reaches the segment's end: dL/dh_out, and the segments
 // behind it in turn, the last one first.
@@ -178,6 +177,8 @@ template <int V, int LR> struct TileRows {
         const int64_t m = t < 0 ? 0 : n - first(t);
         return (int)(m < 0 ? 0 : m > W ? W : m);
     }
+    // the wave's first token, where it has one
+    __device__ __forceinline__ int64_t at(int64_t t) const { return left(t) > 0 ? first(t) : 0; }
 };
 
 // (P, L) of every segment but a sequence's first one.
@@ -194,8 +195,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
     const GlrLane<V, LR> lane(a.C, block);
     const int64_t row0 = seg.q.row0 + seg.t0;
     const TileRows<V, LR> rows{seg.n, lane.wave};
-    const Source sr = P8 ? Source::of_codes<V, LR>(a.r8, row0, a.C, lane) : Source::of_rows<T, V, LR>(a.r, row0, a.r_stride, lane);
-    const Source sd = Source::of_rows<T, V, LR>(p.dy, row0, a.C, lane);
+    const Source<T, V, P8> sr(a.r, a.r8, row0, a.r_stride, a.C, lane);
+    const Source<T, V, false> sd(p.dy, row0, a.C, lane);
     float A2[V], lam[V], whole[V], reach[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -203,21 +204,25 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
         lam[v] = 0.f;
         whole[v] = 1.f;
     }
-    auto fetch = [&](decltype(GradInputs<T, V, P8>::r)& r, SubRows<T, V>& dy, int64_t t) {
-        const int m = rows.left(t);
-        const int64_t at = m > 0 ? rows.first(t) : 0;
-        sr.load(r, at, m, m == Tile::kWaveTokens);
-        sd.load(dy, at, m, m == Tile::kWaveTokens);
-    };
-    decltype(GradInputs<T, V, P8>::r) next_r;
-    SubRows<T, V> next_dy;
+    typename Source<T, V, P8>::Tokens r;
+    SubRows<T, V> dy;
     const int64_t last = (seg.n - 1) / Tile::kTokens * Tile::kTokens;
-    fetch(next_r, next_dy, last);
+    {
+        const int m = rows.left(last);
+        auto nr = sr.reader(rows.at(last), m);
+        auto nd = sd.reader(rows.at(last), m);
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k) {
+            nr.load(k, r);
+            nd.load(k, dy);
+        }
+    }
     int buf = 0;
     for (int64_t t = last; t >= 0; t -= Tile::kTokens, buf ^= 1) {
-        const auto r = next_r;
-        const SubRows<T, V> dy = next_dy;
-        fetch(next_r, next_dy, t - Tile::kTokens);
+        // the next tile's tokens take the registers of this one's as these are used up
+        const int64_t ahead = t - Tile::kTokens;
+        auto nr = sr.reader(rows.at(ahead), rows.left(ahead));
+        auto nd = sd.reader(rows.at(ahead), rows.left(ahead));
         const int mine = rows.left(t) - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
         float at[kGlrChunk][V], P[V], L[V];
         tokens_up([&](auto at_k) {
@@ -227,6 +232,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 at[K][v] = __builtin_unpredictable(K < mine) ? fast_exp2(A2[v] * sigmoid_f(rv[v])) : 1.f;
+            nr.load(K, r);
         });
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -240,6 +246,9 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
                 L[v] = at[k][v] * (dy.get(k, v) + L[v]);
                 P[v] *= at[k][v];
             }
+#pragma unroll
+        for (int k = 0; k < kGlrChunk; ++k)
+            nd.load(k, dy);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             s_span[buf][lane.sub][lane.li][2 * v] = P[v];
@@ -277,17 +286,9 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
     if (seg.q.seq >= 0) {
         const int64_t row0 = seg.q.row0 + seg.t0;
         const TileRows<V, LR> rows{seg.n, lane.wave};
-        Source sx, sr, si;
-        if constexpr (P8) {
-            sx = Source::of_codes<V, LR>(a.x8, row0, a.C, lane);
-            sr = Source::of_codes<V, LR>(a.r8, row0, a.C, lane);
-            si = Source::of_codes<V, LR>(a.i8, row0, a.C, lane);
-        } else {
-            sx = Source::of_rows<T, V, LR>(a.x, row0, a.x_stride, lane);
-            sr = Source::of_rows<T, V, LR>(a.r, row0, a.r_stride, lane);
-            si = Source::of_rows<T, V, LR>(a.i, row0, a.i_stride, lane);
-        }
-        const Source sd = Source::of_rows<T, V, LR>(p.dy, row0, a.C, lane);
+        const Source<T, V, P8> sx(a.x, a.x8, row0, a.x_stride, a.C, lane), sr(a.r, a.r8, row0, a.r_stride, a.C, lane),
+            si(a.i, a.i8, row0, a.i_stride, a.C, lane);
+        const Source<T, V, false> sd(p.dy, row0, a.C, lane);
         const WaveRows ox = WaveRows::at<T>(p.dx, row0, a.C), orr = WaveRows::at<T>(p.dr, row0, a.C), oi = WaveRows::at<T>(p.di, row0, a.C);
         const uint32_t off = lane.template offset<T>(ox.row_bytes);
         const int64_t chunk0 = chunk_row(a, seg.q) + seg.t0 / kGlrChunk;
@@ -295,16 +296,13 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
         float lam[V], reach[V], unused[V];
         end_gradient<V>(p.dh_out, spans, seg.q, count, a.C, lane.c, lane.on, lam);
 
-        // r, dy and the recorded state of the next tile are on their way through the second half of this one, x and i
-        // of this one through its first half
-        decltype(GradInputs<T, V, P8>::r) r;
+        // the next tile's tokens take the registers of this one's as these are used up: every load runs most of a
+        // tile ahead of its use, and they go out evenly over the tile
+        typename Source<T, V, P8>::Tokens x, r, i;
         SubRows<T, V> dy;
         float h0[V];
-        auto fetch = [&](int64_t t) {
-            const int m = rows.left(t), mine = m - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
-            const int64_t at = m > 0 ? rows.first(t) : 0;
-            sr.load(r, at, m, m == Tile::kWaveTokens);
-            sd.load(dy, at, m, m == Tile::kWaveTokens);
+        auto load_state = [&](int64_t t) {
+            const int mine = rows.left(t) - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 h0[v] = 0.f;
@@ -312,24 +310,47 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                 load_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, h0);
         };
         const int64_t last = seg.n > 0 ? (seg.n - 1) / Tile::kTokens * Tile::kTokens : -1;
-        if (last >= 0)
-            fetch(last);
+        if (last >= 0) {
+            const int m = rows.left(last);
+            const int64_t first = rows.at(last);
+            auto nr = sr.reader(first, m), nx = sx.reader(first, m), ni = si.reader(first, m);
+            auto nd = sd.reader(first, m);
+#pragma unroll
+            for (int k = 0; k < kGlrChunk; ++k) {
+                nr.load(k, r);
+                nd.load(k, dy);
+            }
+#pragma unroll
+            for (int k = 0; k < kGlrChunk; ++k) {
+                nx.load(k, x);
+                ni.load(k, i);
+            }
+            load_state(last);
+        }
         int buf = 0;
         for (int64_t t = last; t >= 0; t -= Tile::kTokens, buf ^= 1) {
             const int left = rows.left(t), mine = left - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
-            const int64_t first = left > 0 ? rows.first(t) : 0;
-            decltype(GradInputs<T, V, P8>::x) x, i;
-            sx.load(x, first, left, left == Tile::kWaveTokens);
-            si.load(i, first, left, left == Tile::kWaveTokens);
+            const int64_t ahead = t - Tile::kTokens;
+            const int nleft = rows.left(ahead);
+            auto nr = sr.reader(rows.at(ahead), nleft), nx = sx.reader(rows.at(ahead), nleft), ni = si.reader(rows.at(ahead), nleft);
+            auto nd = sd.reader(rows.at(ahead), nleft);
             float at[kGlrChunk][V], sg[kGlrChunk][V], g[kGlrChunk][V], P[V], Lr[V];
             tokens_up([&](auto at_k) {
                 constexpr int K = decltype(at_k)::value;
                 float rv[V];
                 token_of<K>(r, rv);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < V; ++v) {
                     sg[K][v] = sigmoid_f(rv[v]);
+                    here(sg[K][v]);
+                }
             });
+            // (loads stay behind the uses of what was in their registers)
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < kGlrChunk; ++k)
+                nr.load(k, r);
+            __builtin_amdgcn_sched_barrier(0);
             if (left < Tile::kWaveTokens) {
 #pragma unroll
                 for (int k = 0; k < kGlrChunk; ++k)
@@ -367,13 +388,17 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                 for (int v = 0; v < V; ++v) {
                     g[k][v] = dy.get(k, v) + reach[v];
                     reach[v] = at[k][v] * g[k][v];
+                    here(g[k][v]);
                 }
             __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < kGlrChunk; ++k)
+                nd.load(k, dy);
+            load_state(ahead);
+            __builtin_amdgcn_sched_barrier(0);
+            const int64_t first = rows.at(t);
             const auto bx = ox.buffer(first, left), br = orr.buffer(first, left), bi = oi.buffer(first, left);
-            // a token's row in the lanes' or in the scalar offset, as for_tokens places it
-            const bool full = left == Tile::kWaveTokens;
-            uint32_t row_bytes = ox.row_bytes;
-            asm volatile("" : "+s"(row_bytes));
+            RowOffset to{off, ox.row_bytes};
             tokens_up([&](auto at_k) {
                 constexpr int K = decltype(at_k)::value;
                 float xv[V], iv[V], dx[V], dr[V], di[V];
@@ -394,16 +419,20 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                     dr[v] = du * (Av[v] * fmaf(-s, s, s));
                     h[v] = fmaf(e, h[v], q * in);
                 }
-                const uint32_t row = K * row_bytes, lane_row = full ? off : off + row, all_row = full ? row : 0;
-                store_token<T, V>(bx, lane_row, all_row, dx);
-                store_token<T, V>(br, lane_row, all_row, dr);
-                store_token<T, V>(bi, lane_row, all_row, di);
-                // tokens are scheduled four at a time, and the next tile's loads take the registers of the first half:
-                // more in flight would not fit
-                if constexpr (K % 4 == 3)
+                const uint32_t place = to.next();
+                store_token<T, V>(bx, place, dx);
+                store_token<T, V>(br, place, dr);
+                store_token<T, V>(bi, place, di);
+                // tokens are scheduled four at a time: more of them in flight would not fit the registers
+                if constexpr (K % 4 == 3) {
                     __builtin_amdgcn_sched_barrier(0);
-                if constexpr (K == kGlrChunk / 2 - 1)
-                    fetch(t - Tile::kTokens);
+#pragma unroll
+                    for (int k = K - 3; k <= K; ++k) {
+                        nx.load(k, x);
+                        ni.load(k, i);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             });
         }
         if (p.dh0 && seg.q.index == 0 && lane.sub == 0 && lane.on)
