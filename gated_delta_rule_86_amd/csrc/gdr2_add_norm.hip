@@ -10,13 +10,15 @@
 //   dweight = sum_rows dy xh,  dbias = sum_rows dy
 //
 // Memory bounds both.  A row is held in registers by a group of LPR lanes (16
-// to 1024), NV vectors of V elements each, read once.  Forwards the sums and n
+// to 1024), one or two vectors of eight elements each, read once; the next
+// row's loads are in flight while one is worked on.  Forwards the sums and n
 // are fp64: a code next to a rounding border is then the same however the row
 // is spread over lanes, and fp64 costs this chip's vector units what fp32
 // does.
 #include <algorithm>
 
 #include "gdr2_block.h"
+#include "gdr2_scan.h"
 
 namespace gdr2 {
 
@@ -54,24 +56,52 @@ template <int W> __device__ __forceinline__ double wave_sum(double v)
 }
 template <int W> __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<W>(v); }
 
-// Sum over the LPR lanes that hold one row; every lane gets it.
-template <int LPR, typename S> __device__ __forceinline__ S row_sum(S v, S* s_part)
-{
-    v = wave_sum<(LPR < 64 ? LPR : 64)>(v);
-    if constexpr (LPR > 64) {
-        __syncthreads();                       // the previous sum has been read
-        if ((threadIdx.x & 63) == 0)
-            s_part[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = s_part[0];
+// N sums over the LPR lanes that hold one row; every lane gets them.  Over
+// more than a wave they go through one of two places in turn: one barrier a
+// sum, for a place is written again behind the next one's.
+template <int LPR, typename S, int N> struct RowSums {
+    static constexpr int W = LPR > 64 ? LPR / 64 : 1;
+    typedef S Place[2][W][N];
+    Place* place;
+    int turn = 0;
+    __device__ __forceinline__ explicit RowSums(Place* p) : place(p) {}
+    template <int M> __device__ __forceinline__ void operator()(S (&v)[M])
+    {
+        static_assert(M <= N, "place");
 #pragma unroll
-        for (int k = 1; k < LPR / 64; ++k)
-            v += s_part[k];
+        for (int i = 0; i < M; ++i)
+            v[i] = wave_sum<(LPR < 64 ? LPR : 64)>(v[i]);
+        if constexpr (LPR > 64) {
+            if ((threadIdx.x & 63) == 0)
+#pragma unroll
+                for (int i = 0; i < M; ++i)
+                    (*place)[turn][threadIdx.x >> 6][i] = v[i];
+            lds_barrier();
+#pragma unroll
+            for (int i = 0; i < M; ++i) {
+                v[i] = (*place)[turn][0][i];
+#pragma unroll
+                for (int k = 1; k < W; ++k)
+                    v[i] += (*place)[turn][k][i];
+            }
+            turn ^= 1;
+        }
     }
-    return v;
-}
+};
 
 template <int LPR> constexpr int kThreads = LPR > 256 ? LPR : 256;
+// Whether the next row's loads fit the registers (a workgroup of 1024 has 128 a lane).
+template <int LPR, int NV> constexpr bool kAhead = LPR * NV < 2048;
+
+// x^(-1/2): the unit's estimate and two Newton steps, each doubling its bits.
+__device__ __forceinline__ double inverse_root(double x)
+{
+    double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        y = fma(y, fma(-0.5 * x * y, y, 0.5), y);
+    return y;
+}
 
 // The element's 64-bit value as fp32 bits for a rounding to fewer bits: the
 // leading 21 bits, and a last one that is set if any bit behind them is.  A
@@ -81,279 +111,289 @@ __device__ __forceinline__ uint32_t sticky_bits(double v)
     const uint32_t hi = (uint32_t)__double2hiint(v), lo = (uint32_t)__double2loint(v), mag = hi & 0x7fffffffu;
     const uint32_t bits = ((mag - (896u << 20)) << 3) | (lo != 0 ? 1u : 0u) | (hi & 0x80000000u);
     const bool normal = mag - (897u << 20) < (254u << 20);
-    return normal ? bits : __builtin_bit_cast(uint32_t, (float)v);
+    return __builtin_unpredictable(normal) ? bits : __builtin_bit_cast(uint32_t, (float)v);
 }
 
-template <typename T, int V, int NV> struct RowRegs {
-    RowPart<T, V> part[NV];
-    template <int LPR> __device__ __forceinline__ void load(const void* base, int64_t row, int64_t stride, int C, int lane, bool on)
+// A group's share of one row array.  TAIL: the row ends within a vector.
+// Otherwise lanes past its end read its last vector, and rows past the last one
+// the last one: no branch; what they hold goes into no sum and is not written.
+template <typename T, int NV, bool TAIL> struct RowRegs {
+    Row8<T> part[NV];
+    template <int LPR> __device__ __forceinline__ void load(const void* base, int64_t row, int64_t R, int64_t stride, int C, int lane)
     {
-        const T* p = (const T*)base + row * stride;
+        const T* p = (const T*)base + (row < R ? row : R - 1) * stride;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * V;
-            if (on && c < C)
-                part[j].load(p + c);
+            const int c = (j * LPR + lane) * 8;
+            if constexpr (TAIL)
+                part[j].load(p + c, C - c);
             else
-                part[j].zero();
+                part[j].load(p + min(c, C - 8));
         }
     }
 };
 
-template <int V> __device__ __forceinline__ void params(const float* p, float without, int c, bool in, float (&out)[V])
+// Weights or biases of a vector, n of whose elements exist.
+__device__ __forceinline__ void params(const float* p, float without, int c, int n, float (&out)[8])
 {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        out[v] = p && in ? p[c + v] : without;
+    for (int v = 0; v < 8; ++v)
+        out[v] = p && v < n ? p[c + v] : without;
 }
 
-// The lanes of a block (those past the row's end among them) write its V codes
-// each, the first of them the scale.
-template <int V>
-__device__ __forceinline__ void put_rows8(const gdr2_rows8& to, int64_t row, int C, int c, const float (&v)[V], bool in)
-{
-    const int64_t nb = scale_count(C);
-    const int amax = block_max<V>(v, in), e = block_exponent(amax);
-    Codes<V> k;
-    k.pack(v, amax, e);
-    if (in) {
-        k.store((uint8_t*)to.codes + row * C + c);
-        if (c % kRows8 == 0)
-            ((uint8_t*)to.scales)[row * nb + c / kRows8] = (uint8_t)(e + 127);
+// A vector's codes and its block's scale, for the lanes of a block together.
+struct Vector8 {
+    Codes8 codes;
+    int e;
+    __device__ __forceinline__ Vector8(const float (&v)[8], int n)
+    {
+        const int amax = block_max<8>(v, n);
+        e = block_exponent(amax);
+        codes.pack(v, amax, e);
     }
-}
+    __device__ __forceinline__ void store(const gdr2_rows8& to, int64_t row, int C, int64_t blocks, int c, int n) const
+    {
+        codes.store((uint8_t*)to.codes + row * C + c, n);
+        if (c % kRows8 == 0)
+            ((uint8_t*)to.scales)[row * blocks + c / kRows8] = (uint8_t)(e + 127);
+    }
+};
 
 // ---- forward ---------------------------------------------------------------
-template <typename TX, typename TR, int V, int LPR, int NV>
+template <typename TX, typename TR, int LPR, int NV, bool TAIL>
 __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_add_norm_args a)
 {
-    __shared__ double s_part[LPR > 64 ? LPR / 64 : 1];
+    typedef RowSums<LPR, double, 1> Sums;
+    __shared__ typename Sums::Place s_part;
+    Sums sums(&s_part);
     constexpr int RPB = kThreads<LPR> / LPR;
-    constexpr bool HOLD = LPR < 1024;          // parameters and the next row's loads in registers
     const int lane = threadIdx.x % LPR, C = (int)a.C;
-    const int64_t step = (int64_t)gridDim.x * RPB;
+    const int64_t step = (int64_t)gridDim.x * RPB, blocks = scale_count(C);
     const double inv = 1.0 / (double)C;
-    float w[HOLD ? NV : 1][V], b[HOLD ? NV : 1][V];
-    if constexpr (HOLD) {
+    float w[NV][8];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * V;
-            params<V>(a.weight, 1.f, c, c < C, w[j]);
-            params<V>(a.bias, 0.f, c, c < C, b[j]);
-        }
-    }
+    for (int j = 0; j < NV; ++j)
+        params(a.weight, 1.f, (j * LPR + lane) * 8, C - (j * LPR + lane) * 8, w[j]);
     int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-    RowRegs<TX, V, NV> nx;
-    RowRegs<TR, V, NV> nr;
+    RowRegs<TX, NV, TAIL> nx;
+    RowRegs<TR, NV, TAIL> nr;
     auto fetch = [&](int64_t r) {
-        nx.template load<LPR>(a.x, r, a.x_stride, C, lane, r < a.R);
+        nx.template load<LPR>(a.x, r, a.R, a.x_stride, C, lane);
         if (a.residual)
-            nr.template load<LPR>(a.residual, r, a.res_stride, C, lane, r < a.R);
+            nr.template load<LPR>(a.residual, r, a.R, a.res_stride, C, lane);
     };
-    if constexpr (HOLD)
+    if constexpr (kAhead<LPR, NV>)
         fetch(row);
-    // every lane of a workgroup goes as often: rows past the last one are zero, and not written
+    // every lane of a workgroup goes as often
     for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.R; first += step, row += step) {
-        if constexpr (!HOLD)
+        if constexpr (!kAhead<LPR, NV>)
             fetch(row);
-        const bool on = row < a.R;
-        float h[NV][V];
+        float h[NV][8];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             nx.part[j].get(h[j]);
             if (a.residual) {
-                float r[V];
+                float r[8];
                 nr.part[j].get(r);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < 8; ++v)
                     h[j][v] = to_f32(from_f32<TR>(h[j][v] + r[v]));
             }
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                here(h[j][v]);
         }
-        if constexpr (HOLD)
+        if constexpr (kAhead<LPR, NV>)
             fetch(row + step);
         double mean = 0.0;
         if (a.kind == GDR2_NORM_LAYER) {
-            double s = 0.0;
+            double s[1] = {0.0};
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) {
+                const int n = C - (j * LPR + lane) * 8;
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    s += (double)h[j][v];
-            mean = row_sum<LPR>(s, s_part) * inv;
-        }
-        double ss = 0.0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool in = (j * LPR + lane) * V < C;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const double d = in ? (double)h[j][v] - mean : 0.0;
-                ss = fma(d, d, ss);
+                for (int v = 0; v < 8; ++v)
+                    s[0] += (double)(v < n ? h[j][v] : 0.f);
             }
+            sums(s);
+            mean = s[0] * inv;
         }
-        const double rstd = 1.0 / sqrt(row_sum<LPR>(ss, s_part) * inv + (double)a.eps);
+        double ss[1] = {0.0};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * V;
-            const bool in = on && c < C;
-            if (a.h && in)
-                RowPart<TR, V>::store((TR*)a.h + row * C + c, h[j]);
-            if (a.h8.codes)
-                put_rows8<V>(a.h8, row, C, c, h[j], in);
+            const int n = C - (j * LPR + lane) * 8;
+            double part = 0.0;
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const double d = (double)h[j][v] - mean;
+                part = TAIL && v >= n ? part : fma(d, d, part);
+            }
+            ss[0] += n > 0 ? part : 0.0;
+        }
+        sums(ss);
+        const double rstd = inverse_root(ss[0] * inv + (double)a.eps);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * LPR + lane) * 8, n = row < a.R ? C - c : 0;
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                here(h[j][v]);
+            if (a.h && n > 0)
+                Row8<TR>::store((TR*)a.h + row * C + c, h[j], n);
+            if (a.h8.codes) {
+                const Vector8 k(h[j], n);
+                if (n > 0)
+                    k.store(a.h8, row, C, blocks, c, n);
+            }
             if (!a.y && !a.y8.codes)
                 continue;
-            float wj[V], bj[V], n[V], n8[V];
-            if constexpr (!HOLD) {
-                params<V>(a.weight, 1.f, c, c < C, wj);
-                params<V>(a.bias, 0.f, c, c < C, bj);
-            }
+            float b[8] = {}, y[8], y8[8];
+            if (a.bias)
+                params(a.bias, 0.f, c, C - c, b);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const double t = fma(((double)h[j][v] - mean) * rstd, (double)(HOLD ? w[HOLD ? j : 0][v] : wj[v]),
-                                     (double)(HOLD ? b[HOLD ? j : 0][v] : bj[v]));
-                n[v] = (float)t;
-                n8[v] = __builtin_bit_cast(float, sticky_bits(t));
+            for (int v = 0; v < 8; ++v) {
+                here(w[j][v]);
+                const double t = fma(((double)h[j][v] - mean) * rstd, (double)w[j][v], (double)b[v]);
+                y[v] = (float)t;
+                y8[v] = __builtin_bit_cast(float, sticky_bits(t));
             }
-            if (a.y && in)
-                RowPart<TX, V>::store((TX*)a.y + row * C + c, n);
-            if (a.y8.codes)
-                put_rows8<V>(a.y8, row, C, c, n8, in);
+            if (a.y && n > 0)
+                Row8<TX>::store((TX*)a.y + row * C + c, y, n);
+            if (a.y8.codes) {
+                const Vector8 k(y8, n);
+                if (n > 0)
+                    k.store(a.y8, row, C, blocks, c, n);
+            }
         }
     }
 }
 
 // ---- gradients -------------------------------------------------------------
 // The stream's rows as they are, or in 8 bits.
-template <typename TR, bool P8, int V, int NV> struct StreamRegs {
-    RowRegs<TR, V, NV> rows;
-    template <int LPR> __device__ __forceinline__ void load(const gdr2_add_norm_bwd_args& a, int64_t row, int lane, bool on)
+template <typename TR, bool P8, int NV, bool TAIL> struct StreamRegs {
+    RowRegs<TR, NV, TAIL> rows;
+    template <int LPR> __device__ __forceinline__ void load(const gdr2_add_norm_bwd_args& a, int64_t row, int lane)
     {
-        rows.template load<LPR>(a.h, row, a.C, (int)a.C, lane, on);
+        rows.template load<LPR>(a.h, row, a.R, a.C, (int)a.C, lane);
     }
-    __device__ __forceinline__ void get(int j, float (&v)[V]) const { rows.part[j].get(v); }
+    __device__ __forceinline__ void get(int j, float (&v)[8]) const { rows.part[j].get(v); }
 };
-template <typename TR, int V, int NV> struct StreamRegs<TR, true, V, NV> {
-    Codes<V> codes[NV];
+template <typename TR, int NV, bool TAIL> struct StreamRegs<TR, true, NV, TAIL> {
+    Codes8 codes[NV];
     uint32_t scale[NV];
-    template <int LPR> __device__ __forceinline__ void load(const gdr2_add_norm_bwd_args& a, int64_t row, int lane, bool on)
+    template <int LPR> __device__ __forceinline__ void load(const gdr2_add_norm_bwd_args& a, int64_t row, int lane)
     {
-        const int64_t nb = scale_count(a.C);
+        const int64_t from = row < a.R ? row : a.R - 1, nb = scale_count(a.C);
+        const int C = (int)a.C;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * V;
-            codes[j].zero();
-            scale[j] = 127;
-            if (on && c < (int)a.C) {
-                codes[j].load((const uint8_t*)a.h8.codes + row * a.C + c);
-                scale[j] = ((const uint8_t*)a.h8.scales)[row * nb + c / kRows8];
-            }
+            const int own = (j * LPR + lane) * 8, c = TAIL ? min(own, C - 1) : min(own, C - 8);
+            codes[j].load((const uint8_t*)a.h8.codes + from * C + c, TAIL ? C - own : 8);
+            scale[j] = ((const uint8_t*)a.h8.scales)[from * nb + c / kRows8];
         }
     }
-    __device__ __forceinline__ void get(int j, float (&v)[V]) const { codes[j].get(scale[j], v); }
+    __device__ __forceinline__ void get(int j, float (&v)[8]) const { codes[j].get(scale[j], v); }
 };
 
 // A group's sums of dweight and dbias stay in registers, are added over the
 // workgroup's groups in LDS (in group order), and leave as one row [2][C] of
 // partial sums.
-template <typename TX, typename TR, bool P8, int V, int LPR, int NV>
+template <typename TX, typename TR, bool P8, int LPR, int NV, bool TAIL>
 __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_add_norm_bwd_args a, float* part)
 {
-    __shared__ float s_part[LPR > 64 ? LPR / 64 : 1];
+    typedef RowSums<LPR, float, 3> Sums;
+    __shared__ typename Sums::Place s_part;
+    Sums sums(&s_part);
     constexpr int RPB = kThreads<LPR> / LPR;
-    __shared__ float s_red[RPB > 1 ? 256 * NV * V : 1];
+    __shared__ float s_red[RPB > 1 ? 256 * NV * 8 : 1];
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, C = (int)a.C;
     const int64_t step = (int64_t)gridDim.x * RPB;
     const float inv = 1.f / (float)C;
-    constexpr bool HOLD = LPR < 1024;          // the next row's loads in registers
-    float dw[NV][V] = {}, db[NV][V] = {};
+    float dw[NV][8] = {}, db[NV][8] = {}, w[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        params(a.weight, 1.f, (j * LPR + lane) * 8, C - (j * LPR + lane) * 8, w[j]);
     int64_t row = (int64_t)blockIdx.x * RPB + grp;
-    StreamRegs<TR, P8, V, NV> nh;
-    RowRegs<TX, V, NV> nd;
+    StreamRegs<TR, P8, NV, TAIL> nh;
+    RowRegs<TX, NV, TAIL> nd;
     auto fetch = [&](int64_t r) {
-        nh.template load<LPR>(a, r, lane, r < a.R);
-        nd.template load<LPR>(a.dy, r, C, C, lane, r < a.R);
+        nh.template load<LPR>(a, r, lane);
+        nd.template load<LPR>(a.dy, r, a.R, C, C, lane);
     };
-    if constexpr (HOLD)
+    if constexpr (kAhead<LPR, NV>)
         fetch(row);
     for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.R; first += step, row += step) {
-        if constexpr (!HOLD)
+        if constexpr (!kAhead<LPR, NV>)
             fetch(row);
-        const bool on = row < a.R;
-        float x[NV][V], g[NV][V];
-        RowRegs<TR, V, NV> dh;
+        float x[NV][8], g[NV][8];
+        RowRegs<TR, NV, TAIL> dh;
         if (a.dh)
-            dh.template load<LPR>(a.dh, row, C, C, lane, on);
+            dh.template load<LPR>(a.dh, row, a.R, C, C, lane);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             nh.get(j, x[j]);
             nd.part[j].get(g[j]);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                here(x[j][v]);
+                here(g[j][v]);
+            }
         }
-        if constexpr (HOLD)
+        if constexpr (kAhead<LPR, NV>)
             fetch(row + step);
-        float mean = 0.f, ss = 0.f;
+        float mean = 0.f;
         if (a.kind == GDR2_NORM_LAYER) {
-            float s = 0.f;
+            float s[1] = {0.f};
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) {
+                const int n = C - (j * LPR + lane) * 8;
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    s += x[j][v];
-            mean = row_sum<LPR>(s, s_part) * inv;
+                for (int v = 0; v < 8; ++v)
+                    s[0] += v < n ? x[j][v] : 0.f;
+            }
+            sums(s);
+            mean = s[0] * inv;
         }
+        // sum d^2, sum v d and, for the layer norm, sum v, in one go: xh = r d
+        float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool in = (j * LPR + lane) * V < C;
+            // elements and rows that are not there add nothing, whatever they hold
+            const int n = row < a.R ? C - (j * LPR + lane) * 8 : 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                x[j][v] = in ? x[j][v] - mean : 0.f;
-                ss = fmaf(x[j][v], x[j][v], ss);
+            for (int v = 0; v < 8; ++v) {
+                const bool in = TAIL ? v < n : n > 0;
+                const float d = in ? x[j][v] - mean : 0.f;
+                x[j][v] = d;
+                g[j][v] = in ? g[j][v] : 0.f;
+                s[0] = fmaf(d, d, s[0]);
+                s[1] = fmaf(g[j][v] * w[j][v], d, s[1]);
+                s[2] = fmaf(g[j][v], w[j][v], s[2]);
             }
         }
-        const float rstd = 1.f / sqrtf(row_sum<LPR>(ss, s_part) * inv + a.eps);
-        float s1 = 0.f, s2 = 0.f;
+        sums(s);
+        const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
+        const float m1 = a.kind == GDR2_NORM_LAYER ? s[2] * inv : 0.f, m2 = rstd * s[1] * inv;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * V;
-            float w[V];
-            params<V>(a.weight, 1.f, c, c < C, w);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float xh = x[j][v] * rstd;
-                // a row past the last one has dy = 0, but its xh may be NaN (eps = 0)
-                if (on) {
-                    dw[j][v] = fmaf(g[j][v], xh, dw[j][v]);
-                    db[j][v] += g[j][v];
-                }
-                const float e = g[j][v] * w[v];
-                s1 += e;
-                s2 = fmaf(e, xh, s2);
-                x[j][v] = xh;
-                g[j][v] = e;
-            }
-        }
-        if (a.kind == GDR2_NORM_LAYER)
-            s1 = row_sum<LPR>(s1, s_part) * inv;
-        else
-            s1 = 0.f;
-        s2 = row_sum<LPR>(s2, s_part) * inv;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * LPR + lane) * V;
-            if (!on || c >= C)
-                continue;
-            float o[V], more[V];
+            const int c = (j * LPR + lane) * 8, n = row < a.R ? C - c : 0;
+            float o[8], more[8] = {};
             if (a.dh)
                 dh.part[j].get(more);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                o[v] = rstd * (g[j][v] - s1 - x[j][v] * s2);
-                if (a.dh)
-                    o[v] += more[v];
+            for (int v = 0; v < 8; ++v) {
+                // (a row that is not there has d = 0, and may have an infinite r)
+                const float xh = n > 0 ? x[j][v] * rstd : 0.f;
+                dw[j][v] = fmaf(g[j][v], xh, dw[j][v]);
+                db[j][v] += g[j][v];
+                o[v] = fmaf(rstd, fmaf(g[j][v], w[j][v], -m1) - xh * m2, more[v]);
             }
+            if (n <= 0)
+                continue;
             if (a.dresidual)
-                RowPart<TR, V>::store((TR*)a.dresidual + row * C + c, o);
+                Row8<TR>::store((TR*)a.dresidual + row * C + c, o, n);
             if (a.dx)
-                RowPart<TX, V>::store((TX*)a.dx + row * C + c, o);
+                Row8<TX>::store((TX*)a.dx + row * C + c, o, n);
         }
     }
     if (!part)
@@ -364,23 +404,23 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_a
         if constexpr (RPB == 1) {
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-                if ((j * LPR + lane) * V < C)
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        to[half * C + (j * LPR + lane) * V + v] = half ? db[j][v] : dw[j][v];
+                for (int v = 0; v < 8; ++v)
+                    if ((j * LPR + lane) * 8 + v < C)
+                        to[half * C + (j * LPR + lane) * 8 + v] = half ? db[j][v] : dw[j][v];
         } else {
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    s_red[grp * (LPR * NV * V) + (j * LPR + lane) * V + v] = half ? db[j][v] : dw[j][v];
+                for (int v = 0; v < 8; ++v)
+                    s_red[grp * (LPR * NV * 8) + (j * LPR + lane) * 8 + v] = half ? db[j][v] : dw[j][v];
             __syncthreads();
             for (int c = threadIdx.x; c < C; c += 256) {
                 float s = 0.f;
 #pragma unroll
                 for (int r = 0; r < RPB; ++r)
-                    s += s_red[r * (LPR * NV * V) + c];
+                    s += s_red[r * (LPR * NV * 8) + c];
                 to[half * C + c] = s;
             }
         }
@@ -388,27 +428,23 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_a
 }
 
 // ---- variants --------------------------------------------------------------
-// The narrowest group of lanes whose registers hold the row: 16 lanes of one
-// vector, a wave with up to 32 elements a lane, workgroups of 256 (32 elements
-// forwards, 16 backwards, where a lane also holds dy, dweight and dbias) and
-// 1024 lanes (16).
+// The narrowest group of lanes whose registers hold the row with at most two
+// vectors each: part of a wave, a wave, a workgroup of 256, one of 1024.  (Four
+// vectors a lane take 256 registers, one wave a SIMD: 32768 rows of 2048 with an
+// 8-bit output in 153 us.)
 struct Shape {
     int lpr, nv;
 };
+constexpr int kLanes[] = {16, 64, 256, 1024};
 
-Shape shape_of(int64_t C, int V, bool backward)
+Shape shape_of(int64_t C)
 {
-    const int64_t nvec = ceil_div(C, V);
-    if (V == 8 && nvec <= 16)
-        return {16, 1};
-    const int wave = (backward ? 16 : 32) / V, group = (backward ? 16 : 32) / V;
-    for (int nv = 1; nv <= wave; nv *= 2)
-        if (nvec <= 64 * nv)
-            return {64, nv};
-    for (int nv = wave / 2; nv <= group; nv *= 2)
-        if (nvec <= 256 * nv)
-            return {256, nv};
-    return {1024, 16 / V};
+    const int64_t vectors = ceil_div(C, 8);
+    for (int lpr : kLanes)
+        for (int nv = 1; nv <= (lpr == 16 ? 1 : 2); ++nv)
+            if (vectors <= lpr * nv)
+                return {lpr, nv};
+    return {0, 0};           // refused before
 }
 
 #define GDR2_ADD_NORM_CASE(L, N)                                                                 \
@@ -417,93 +453,66 @@ Shape shape_of(int64_t C, int V, bool backward)
         return hipGetLastError();                                                                \
     }
 
-// Exactly the shapes shape_of can return.
-template <int V, bool BACKWARD, typename F> hipError_t dispatch(const Shape& s, const F& f)
+template <typename F> hipError_t dispatch(const Shape& s, const F& f)
 {
-    GDR2_ADD_NORM_CASE(64, 1) GDR2_ADD_NORM_CASE(64, 2)
-    if constexpr (V == 8) {
-        GDR2_ADD_NORM_CASE(16, 1) GDR2_ADD_NORM_CASE(256, 2) GDR2_ADD_NORM_CASE(1024, 2)
-        if constexpr (BACKWARD) {
-            GDR2_ADD_NORM_CASE(256, 1)
-        } else {
-            GDR2_ADD_NORM_CASE(64, 4) GDR2_ADD_NORM_CASE(256, 4)
-        }
-    } else {
-        GDR2_ADD_NORM_CASE(64, 4) GDR2_ADD_NORM_CASE(64, 8) GDR2_ADD_NORM_CASE(64, 16) GDR2_ADD_NORM_CASE(256, 16)
-        GDR2_ADD_NORM_CASE(1024, 16)
-        if constexpr (BACKWARD) {
-            GDR2_ADD_NORM_CASE(256, 8)
-        } else {
-            GDR2_ADD_NORM_CASE(64, 32) GDR2_ADD_NORM_CASE(256, 32)
-        }
-    }
+    GDR2_ADD_NORM_CASE(16, 1) GDR2_ADD_NORM_CASE(64, 1) GDR2_ADD_NORM_CASE(64, 2) GDR2_ADD_NORM_CASE(256, 1)
+    GDR2_ADD_NORM_CASE(256, 2) GDR2_ADD_NORM_CASE(1024, 1) GDR2_ADD_NORM_CASE(1024, 2)
     return hipErrorInvalidValue;
 }
 
-template <typename TX, typename TR, int V> struct ForwardLaunch {
+template <typename TX, typename TR> struct ForwardLaunch {
     const gdr2_add_norm_args& a;
     hipStream_t stream;
     template <int L, int N> void operator()() const
     {
-        // eight workgroups of 256 per compute unit, then the rows are walked
+        // eight workgroups of 256 per compute unit (as many waves in larger ones), then the rows are walked
         constexpr int RPB = kThreads<L> / L;
         const dim3 grid((unsigned)std::min(ceil_div(a.R, RPB), (int64_t)device_cu_count() * 2048 / kThreads<L>));
-        hipLaunchKernelGGL((add_norm_forward_kernel<TX, TR, V, L, N>), grid, dim3(kThreads<L>), 0, stream, a);
+        if (a.C % 8)
+            hipLaunchKernelGGL((add_norm_forward_kernel<TX, TR, L, N, true>), grid, dim3(kThreads<L>), 0, stream, a);
+        else
+            hipLaunchKernelGGL((add_norm_forward_kernel<TX, TR, L, N, false>), grid, dim3(kThreads<L>), 0, stream, a);
     }
 };
 
-template <typename TX, typename TR, bool P8, int V> struct BackwardLaunch {
+template <typename TX, typename TR, bool P8> struct BackwardLaunch {
     const gdr2_add_norm_bwd_args& a;
     float* part;
     int64_t groups;
     hipStream_t stream;
     template <int L, int N> void operator()() const
     {
-        hipLaunchKernelGGL((add_norm_backward_kernel<TX, TR, P8, V, L, N>), dim3((unsigned)groups), dim3(kThreads<L>), 0, stream,
-                           a, part);
+        const dim3 grid((unsigned)groups);
+        if (a.C % 8)
+            hipLaunchKernelGGL((add_norm_backward_kernel<TX, TR, P8, L, N, true>), grid, dim3(kThreads<L>), 0, stream, a, part);
+        else
+            hipLaunchKernelGGL((add_norm_backward_kernel<TX, TR, P8, L, N, false>), grid, dim3(kThreads<L>), 0, stream, a, part);
     }
 };
 
-template <typename TX, typename TR> hipError_t forward_t(const gdr2_add_norm_args& a, hipStream_t stream)
-{
-    const bool wide = rows_in_eights(a.x, a.x_stride, a.C, a.dtype) &&
-                      (!a.residual || rows_in_eights(a.residual, a.res_stride, a.C, a.res_dtype));
-    if (wide)
-        return dispatch<8, false>(shape_of(a.C, 8, false), ForwardLaunch<TX, TR, 8>{a, stream});
-    return dispatch<1, false>(shape_of(a.C, 1, false), ForwardLaunch<TX, TR, 1>{a, stream});
-}
-
-int width_of(const gdr2_add_norm_bwd_args& a) { return a.C % 8 == 0 ? 8 : 1; }
-
-// Workgroups of the gradients: two of 256 threads per compute unit (as many
-// waves in larger ones), fewer when there are fewer rows.
+// Workgroups of the gradients: four of 256 threads per compute unit (as many
+// waves in larger ones), fewer when there are fewer rows.  Each leaves a row of
+// partial sums.
 int64_t backward_groups(const gdr2_add_norm_bwd_args& a)
 {
-    const Shape s = shape_of(a.C, width_of(a), true);
-    const int64_t most = s.lpr > 256 ? device_cu_count() : (int64_t)device_cu_count() * 2;
-    return std::min(ceil_div(a.R, std::max(1, 256 / s.lpr)), most);
-}
-
-template <typename TX, typename TR, bool P8> hipError_t backward_t(const gdr2_add_norm_bwd_args& a, float* part, int64_t P, hipStream_t stream)
-{
-    const int V = width_of(a);
-    const Shape s = shape_of(a.C, V, true);
-    return V == 8 ? dispatch<8, true>(s, BackwardLaunch<TX, TR, P8, 8>{a, part, P, stream})
-                  : dispatch<1, true>(s, BackwardLaunch<TX, TR, P8, 1>{a, part, P, stream});
+    const Shape s = shape_of(a.C);
+    return std::min(ceil_div(a.R, std::max(1, 256 / s.lpr)), (int64_t)device_cu_count() * 1024 / std::max(256, s.lpr));
 }
 
 template <typename TX, typename TR> hipError_t backward_p(const gdr2_add_norm_bwd_args& a, float* part, int64_t P, hipStream_t stream)
 {
-    return a.h ? backward_t<TX, TR, false>(a, part, P, stream) : backward_t<TX, TR, true>(a, part, P, stream);
+    return a.h ? dispatch(shape_of(a.C), BackwardLaunch<TX, TR, false>{a, part, P, stream})
+               : dispatch(shape_of(a.C), BackwardLaunch<TX, TR, true>{a, part, P, stream});
 }
 
 }  // namespace
 
 hipError_t launch_add_norm_forward(const gdr2_add_norm_args& a, hipStream_t stream)
 {
+    const Shape s = shape_of(a.C);
     if (a.dtype == GDR2_F32)
-        return forward_t<float, float>(a, stream);
-    return a.res_dtype == GDR2_F32 ? forward_t<bf16, float>(a, stream) : forward_t<bf16, bf16>(a, stream);
+        return dispatch(s, ForwardLaunch<float, float>{a, stream});
+    return a.res_dtype == GDR2_F32 ? dispatch(s, ForwardLaunch<bf16, float>{a, stream}) : dispatch(s, ForwardLaunch<bf16, bf16>{a, stream});
 }
 
 size_t add_norm_backward_workspace_bytes(const gdr2_add_norm_bwd_args& a)

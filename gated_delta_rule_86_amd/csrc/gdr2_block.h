@@ -27,6 +27,11 @@ size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& a);
 // Workgroups, counted as of 256 threads, of a call's largest launch.
 int64_t glr_launch_groups(const gdr2_glr_args& a, bool backward);
 
+// A value that is formed here: not earlier, as an invariant of a loop whose
+// registers it would fill, and not later, where it is used: what it is formed
+// from gives its registers to the loads that follow.
+__device__ __forceinline__ void here(float& v) { asm volatile("" : "+v"(v)); }
+
 // ---- rows in 8 bits --------------------------------------------------------
 constexpr int kRows8 = GDR2_ROWS8_BLOCK;
 
@@ -63,121 +68,131 @@ template <bool HIGH> __device__ __forceinline__ s16x2 codes2(float a, float b, f
 // For blocks without finite values: infinities as +-448, NaN as it is.
 __device__ __forceinline__ float clip_infinity(float v) { return __builtin_isinf(v) ? __builtin_copysignf(448.f, v) : v; }
 
-// V codes (V = 1: in the low byte; V = 8: two words) of a block with exponent e.
-template <int V> struct Codes {
-    uint32_t w[V == 8 ? 2 : 1];
-    __device__ __forceinline__ void pack(const float (&v)[V], int amax, int e)
-    {
-        if (__builtin_expect(amax < 0, 0)) {
-            float c[V];
+// V = 1 or 2 values of codes in the low bytes of w, at the scale byte s.
+template <int V> __device__ __forceinline__ void values_of(uint32_t w, uint32_t s, float (&v)[V])
+{
+    const auto x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale_of(s), false);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                c[i] = clip_infinity(v[i]);
-            set(c, 1.f);
-        } else {
-            set(v, scale_of(e + 127));
-        }
-    }
-    __device__ __forceinline__ void set(const float (&v)[V], float scale)
-    {
-        const s16x2 none = {0, 0};
-        if constexpr (V == 8) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                w[h] = __builtin_bit_cast(uint32_t, codes2<true>(v[4 * h + 2], v[4 * h + 3], scale,
-                                                                codes2<false>(v[4 * h], v[4 * h + 1], scale, none)));
-        } else if constexpr (V == 2) {
-            w[0] = __builtin_bit_cast(uint32_t, codes2<false>(v[0], v[1], scale, none));
-        } else {
-            w[0] = __builtin_bit_cast(uint32_t, codes2<false>(v[0], 0.f, scale, none));
-        }
-    }
-    __device__ __forceinline__ void load(const uint8_t* p)
-    {
-        if constexpr (V == 8) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            w[0] = x.x;
-            w[1] = x.y;
-        } else if constexpr (V == 2) {
-            w[0] = *reinterpret_cast<const uint16_t*>(p);
-        } else {
-            w[0] = *p;
-        }
-    }
-    __device__ __forceinline__ void store(uint8_t* p) const
-    {
-        if constexpr (V == 8)
-            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-        else if constexpr (V == 2)
-            *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
-        else
-            *p = (uint8_t)w[0];
-    }
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (uint32_t& x : w)
-            x = 0;
-    }
-    // values at the scale byte s
-    __device__ __forceinline__ void get(uint32_t s, float (&v)[V]) const
-    {
-        const float scale = scale_of(s);
-        if constexpr (V == 8) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, false);
-                const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, true);
-                v[4 * h] = lo[0];
-                v[4 * h + 1] = lo[1];
-                v[4 * h + 2] = hi[0];
-                v[4 * h + 3] = hi[1];
-            }
-        } else {
-            const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[0], scale, false);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                v[i] = lo[i];
-        }
-    }
-};
+    for (int i = 0; i < V; ++i)
+        v[i] = x[i];
+}
 
-// V consecutive elements as they lie in memory.  Eight fp32 go as two accesses
-// of 16 bytes, which is all the alignment their rows are asked for.
-template <typename T, int V> struct RowPart {
-    static constexpr int N = V == 8 ? 8 * (int)sizeof(T) / 16 : 1, W = V / N;
-    typedef Raw<T, W> Part;
-    typename Part::Type raw[N];
+// ---- eight consecutive elements of a row -----------------------------------
+// One or two accesses of 16 bytes (of 8 for codes) that need the alignment of
+// an element only, so rows of any width and spacing go this way.  n elements
+// of the eight exist: where fewer do, they go one by one.
+template <typename T> struct Row8 {
+    static constexpr int N = sizeof(T) == 2 ? 1 : 2, W = 8 / N;
+    typedef T Part __attribute__((ext_vector_type(W), aligned(sizeof(T))));
+    typedef T Vec __attribute__((ext_vector_type(W)));
+    Vec raw[N];
     __device__ __forceinline__ void load(const T* p)
     {
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            raw[j] = Part::load(p + j * W);
+            raw[j] = *reinterpret_cast<const Part*>(p + j * W);
     }
-    __device__ __forceinline__ void zero()
+    __device__ __forceinline__ void load(const T* p, int n)
+    {
+        if (n >= 8) {
+            load(p);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                raw[i / W][i % W] = i < n ? p[i] : (T)0.f;
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
     {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            raw[j] = Part::zero();
+        for (int i = 0; i < 8; ++i)
+            v[i] = (float)raw[i / W][i % W];
     }
-    __device__ __forceinline__ void get(float (&v)[V]) const
+    static __device__ __forceinline__ void store(T* p, const float (&v)[8], int n)
     {
+        if (n >= 8) {
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            Part::get(raw[j], v + j * W);
-    }
-    static __device__ __forceinline__ void store(T* p, const float (&v)[V])
-    {
+            for (int j = 0; j < N; ++j) {
+                Vec x;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            store_row<W>(p + j * W, v + j * W);
+                for (int i = 0; i < W; ++i)
+                    x[i] = (T)v[j * W + i];
+                *reinterpret_cast<Part*>(p + j * W) = x;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n)
+                    p[i] = (T)v[i];
+        }
     }
 };
-// Whether RowPart<T, 8> can read rows of `width` elements, `stride` apart.
-inline bool rows_in_eights(const void* p, int64_t stride, int64_t width, int32_t dtype)
-{
-    return width % 8 == 0 && rows_aligned(p, stride, width, dtype == GDR2_BF16 ? 2 : 4, dtype == GDR2_BF16 ? 8 : 4);
-}
+
+struct Codes8 {
+    typedef uint32_t Part __attribute__((ext_vector_type(2), aligned(1)));
+    uint32_t w[2];
+    __device__ __forceinline__ void set(const float (&v)[8], float scale)
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            w[h] = __builtin_bit_cast(uint32_t, codes2<true>(v[4 * h + 2], v[4 * h + 3], scale,
+                                                            codes2<false>(v[4 * h], v[4 * h + 1], scale, s16x2{0, 0})));
+    }
+    // of a block with this largest magnitude and exponent
+    __device__ __forceinline__ void pack(const float (&v)[8], int amax, int e)
+    {
+        set(v, scale_of(e + 127));
+        // (asked of the wave: a branch per lane would be taken apart into masks)
+        if (__builtin_expect(__any(amax < 0), 0)) {
+            Codes8 k;
+            float c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = clip_infinity(v[i]);
+            k.set(c, 1.f);
+            w[0] = amax < 0 ? k.w[0] : w[0];
+            w[1] = amax < 0 ? k.w[1] : w[1];
+        }
+    }
+    __device__ __forceinline__ void load(const uint8_t* p, int n)
+    {
+        if (n >= 8) {
+            const Part x = *reinterpret_cast<const Part*>(p);
+            w[0] = x[0];
+            w[1] = x[1];
+        } else {
+            w[0] = w[1] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n)
+                    w[i / 4] |= (uint32_t)p[i] << (8 * (i % 4));
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* p, int n) const
+    {
+        if (n >= 8) {
+            *reinterpret_cast<Part*>(p) = Part{w[0], w[1]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n)
+                    p[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+        }
+    }
+    __device__ __forceinline__ void get(uint32_t s, float (&v)[8]) const
+    {
+        const float scale = scale_of(s);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const auto lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, false);
+            const auto hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w[h], scale, true);
+            v[4 * h] = lo[0];
+            v[4 * h + 1] = lo[1];
+            v[4 * h + 2] = hi[0];
+            v[4 * h + 3] = hi[1];
+        }
+    }
+};
 
 // Largest of the values of aligned groups of W lanes, in every lane.
 template <int W> __device__ __forceinline__ int lanes_max(int v)
@@ -195,14 +210,17 @@ template <int W> __device__ __forceinline__ int lanes_max(int v)
     return v;
 }
 
-// Largest finite magnitude of the V values of each lane of a block's lanes.
-template <int V> __device__ __forceinline__ int block_max(const float (&v)[V], bool in)
+// Largest finite magnitude of a block whose lanes hold V values each, the first
+// n of which exist.
+template <int V> __device__ __forceinline__ int block_max(const float (&v)[V], int n)
 {
     int m = -1;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        m = max(m, finite_bits(__builtin_bit_cast(uint32_t, v[i])));
-    return lanes_max<kRows8 / V>(in ? m : -1);
+    for (int i = 0; i < V; ++i) {
+        const int x = finite_bits(__builtin_bit_cast(uint32_t, v[i]));
+        m = max(m, i < n ? x : -1);
+    }
+    return lanes_max<kRows8 / V>(m);
 }
 
 __host__ __device__ inline int64_t scale_count(int64_t C) { return (C + kRows8 - 1) / kRows8; }

@@ -24,7 +24,7 @@
 namespace gdr2 {
 
 constexpr int kGlrChunk = GDR2_GLR_CHUNK;     // tokens of a sub-chunk, and between recorded states
-constexpr int kGlrWaves = 8;
+constexpr int kGlrWaves = 8;     // of a workgroup
 
 template <int LR> struct GlrTile {
     static constexpr int kGroups = 64 / LR;                     // sub-chunks of a wave
@@ -66,6 +66,8 @@ struct RowOffset {
     }
 };
 
+constexpr int kOnce = 2;     // cache policy of loads: read once (nt), 8x4096x2048 131 -> 127 us
+
 // The V elements of every token as they lie in memory, a register each.
 template <typename T, int V> struct SubRows {
     static_assert(V * sizeof(T) <= 4, "one register");
@@ -74,9 +76,9 @@ template <typename T, int V> struct SubRows {
     template <typename R> __device__ __forceinline__ void load(int k, R rsrc, RowOffset& at)
     {
         if constexpr (V * sizeof(T) == 2)
-            raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at.next(), 0, 0);
+            raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at.next(), 0, kOnce);
         else
-            raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at.next(), 0, 0);
+            raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at.next(), 0, kOnce);
     }
     __device__ __forceinline__ float get(int k, int v) const
     {
@@ -143,6 +145,15 @@ __device__ __forceinline__ float glr_root(float t, float a)
 // it is scheduled in.)
 __device__ __forceinline__ float unless_masked(float q, float v) { return __builtin_unpredictable(q == 0.f) ? 0.f : v; }
 
+// The workgroup's number.  Workgroups go to the eight XCDs in turn; numbered so,
+// an XCD owns a range of neighbouring channel blocks, and its cache sees whole
+// rows: every eighth block of 128 bytes would fall into a few of its channels.
+__device__ __forceinline__ uint32_t block_id()
+{
+    const uint32_t n = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
+    return xcd * n + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+}
+
 // Where this lane's channels and sub-chunk lie.
 template <int V, int LR> struct GlrLane {
     int li, sub, wave;
@@ -153,7 +164,7 @@ template <int V, int LR> struct GlrLane {
         const int lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         li = lane % LR;
-        sub = wave * GlrTile<LR>::kGroups + lane / LR;
+        sub = wave * (64 / LR) + lane / LR;
         c = block * (LR * V) + li * V;
         on = c < C;
     }

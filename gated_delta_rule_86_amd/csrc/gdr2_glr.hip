@@ -24,7 +24,7 @@ template <typename T, int V> struct Inputs {
 
 // The rows of x, r and i, from the segment's first one on.
 template <typename T, int V, int LR> struct Walk {
-    typedef GlrTile<LR> Tile;
+    static constexpr int kWaveTokens = 64 / LR * kGlrChunk;
     WaveRows x, r, i;
     uint32_t ox, orr, oi;
     int64_t n;          // tokens of the segment
@@ -37,11 +37,11 @@ template <typename T, int V, int LR> struct Walk {
     {
     }
     // first token of this wave in the tile at `t`, and how many of its tokens exist
-    __device__ __forceinline__ int64_t first(int64_t t) const { return t + wave * Tile::kWaveTokens; }
+    __device__ __forceinline__ int64_t first(int64_t t) const { return t + wave * kWaveTokens; }
     __device__ __forceinline__ int left(int64_t t) const
     {
         const int64_t m = n - first(t);
-        return (int)(m < 0 ? 0 : m > Tile::kWaveTokens ? Tile::kWaveTokens : m);
+        return (int)(m < 0 ? 0 : m > kWaveTokens ? kWaveTokens : m);
     }
     // f(buffers of r, x and i, offsets) of the tile at t
     template <typename F> __device__ __forceinline__ void with_tile(int64_t t, const F& f) const
@@ -76,11 +76,11 @@ __device__ __forceinline__ SpanVec<V> form_terms(Inputs<T, V>& in, const Walk<T,
                 const float u = A2[v] * sr, at = fast_exp2(u), q = glr_root(u, at);
                 a[k][v] = at;
                 b[k][v] = unless_masked(q, q * si * in.x.get(k, v));
+                here(b[k][v]);
                 s.l[v] = fmaf(at, s.l[v], b[k][v]);
                 s.p[v] *= at;
             }
             in.r.load(k, br, atr);
-            in.x.load(k, bx, atx);
             in.i.load(k, bi, ati);
         }
     });
@@ -164,7 +164,7 @@ template <typename T, int V> struct CodeRows {
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const float v[1] = {rows.get(k, 0)};
-                const int amax = block_max<1>(v, on), e = block_exponent(amax);
+                const int amax = block_max<1>(v, on ? 1 : 0), e = block_exponent(amax);
                 const float clipped = amax < 0 ? clip_infinity(v[0]) : v[0];
                 const s16x2 c = codes2<false>(clipped, 0.f, amax < 0 ? 1.f : scale_of(e + 127), none);
                 __builtin_amdgcn_raw_buffer_store_b8((uint8_t)c[0], bc, at.next(), 0, 0);
@@ -225,11 +225,12 @@ __device__ __forceinline__ void start_state(const float* h0, const float* spans,
 
 // SPAN: (P, L) of every segment but a sequence's last one, nothing else.
 template <typename T, int V, int LR, bool PACK, bool SPAN>
-__global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_args a, GlrPlan plan, float* spans)
+__global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kernel(gdr2_glr_args a, GlrPlan plan, float* spans)
 {
     typedef GlrTile<LR> Tile;
     __shared__ float s_span[2][Tile::kSubs][LR][2 * V];
-    const int64_t slot = blockIdx.x / plan.blocks, block = blockIdx.x - slot * plan.blocks;
+    const uint32_t id = block_id();
+    const int64_t slot = id / plan.blocks, block = id - slot * plan.blocks;
     const Segment seg = segment_of(plan, slot);
     if (seg.q.seq < 0 || (SPAN && seg.t0 + seg.n >= seg.q.len))
         return;
@@ -298,6 +299,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
                 if constexpr (SPAN)
                     whole[v] *= pl[2 * v];
             }
+            if (j % 4 == 3)
+                __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!SPAN) {
             if (a.h_chunks && lane.on && mine > 0)
@@ -312,6 +315,11 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_forward_kernel(gdr2_glr_ar
                 store_token<T, V>(out, to.next(), start);
             }
         }
+        walk.with_tile(t + Tile::kTokens, [&](auto, auto bx, auto, RowOffset, RowOffset atx, RowOffset) {
+#pragma unroll
+            for (int k = 0; k < kGlrChunk; ++k)
+                in.x.load(k, bx, atx);
+        });
     }
     if (lane.sub != 0 || !lane.on)
         return;

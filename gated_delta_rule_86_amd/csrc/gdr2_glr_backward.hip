@@ -29,12 +29,10 @@ template <int V> struct SubCodes {
     uint32_t scale[V == 1 ? kGlrChunk : 1];
     template <int K> __device__ __forceinline__ void token(float (&v)[V]) const
     {
-        Codes<V> c;
-        c.w[0] = raw[K];
         if constexpr (V == 2)
-            c.get(__builtin_amdgcn_update_dpp(0, scale[0], 0x150 + K, 0xF, 0xF, true), v);   // row_newbcast
+            values_of<V>(raw[K], __builtin_amdgcn_update_dpp(0, scale[0], 0x150 + K, 0xF, 0xF, true), v);   // row_newbcast
         else
-            c.get(scale[K], v);
+            values_of<V>(raw[K], scale[K], v);
     }
 };
 
@@ -110,10 +108,6 @@ template <typename T, int V> struct Source<T, V, true> {
     }
 };
 
-// A value that is formed here, not where it is used: what it is formed from
-// gives its registers to the loads that follow.
-__device__ __forceinline__ void here(float& v) { asm volatile("" : "+v"(v)); }
-
 // The gradient that reaches the segment's end: dL/dh_out, and the segments
 // behind it in turn, the last one first.
 template <int V>
@@ -188,7 +182,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_
     typedef GlrTile<LR> Tile;
     __shared__ float s_span[2][Tile::kSubs][LR][2 * V];
     const gdr2_glr_args& a = p.f;
-    const int64_t slot = blockIdx.x / plan.blocks, block = blockIdx.x - slot * plan.blocks;
+    const uint32_t id = block_id();
+    const int64_t slot = id / plan.blocks, block = id - slot * plan.blocks;
     const Segment seg = segment_of(plan, slot);
     if (seg.q.seq < 0 || seg.q.index == 0)
         return;
@@ -273,7 +268,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
     typedef GlrTile<LR> Tile;
     __shared__ float s_span[2][Tile::kSubs][LR][2 * V];
     const gdr2_glr_args& a = p.f;
-    const int64_t slot = blockIdx.x / plan.blocks, block = blockIdx.x - slot * plan.blocks;
+    const uint32_t id = block_id();
+    const int64_t slot = id / plan.blocks, block = id - slot * plan.blocks;
     const Segment seg = segment_of(plan, slot);
     const GlrLane<V, LR> lane(a.C, block);
     float dA[V], A2[V], Av[V];

@@ -3,9 +3,8 @@
 //
 //   e = min { e >= -127 : max_block |v| <= 448 2^e },  code = e4m3(v 2^-e)
 //
-// Memory bounds both: 3 bytes an element of bf16 rows, and two operations on
-// the matrix of a block's lanes.  A lane holds 8 columns, four lanes a block
-// (one column and 32 lanes where rows are not whole, aligned vectors).
+// Memory bounds both: 3 bytes an element of bf16 rows.  A lane holds 8 columns,
+// four lanes a block.
 #include <algorithm>
 
 #include "gdr2_block.h"
@@ -26,87 +25,76 @@ __device__ __forceinline__ Place place_of(int64_t at, int64_t per, bool one_row)
     const int64_t row = (at | per) >> 32 ? at / per : (int64_t)((uint32_t)at / (uint32_t)per);
     return {row, at - row * per};
 }
+__device__ __forceinline__ int left_of(int64_t C, int64_t c) { return C - c >= 8 ? 8 : (int)(C - c); }
 
-template <typename T, int V> __global__ __launch_bounds__(256) void pack_kernel(gdr2_pack_args a, int64_t items)
+template <typename T> __global__ __launch_bounds__(256) void pack_kernel(gdr2_pack_args a, int64_t items)
 {
-    constexpr int LPB = kRows8 / V;
-    const int64_t nb = scale_count(a.C), per = nb * LPB, step = (int64_t)gridDim.x * 256;
+    const int64_t nb = scale_count(a.C), step = (int64_t)gridDim.x * 256;
     for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < items; at += step) {
-        const Place p = place_of(at, per, a.R == 1);
-        const int64_t c = p.item * V;
-        const bool in = c < a.C;
-        RowPart<T, V> raw;
-        if (in)
-            raw.load((const T*)a.x + p.row * a.x_stride + c);
-        else
-            raw.zero();
-        float v[V];
+        const Place p = place_of(at, nb * 4, a.R == 1);
+        const int64_t c = p.item * 8;
+        const int n = left_of(a.C, c);
+        Row8<T> raw;
+        raw.load((const T*)a.x + p.row * a.x_stride + c, n);
+        float v[8];
         raw.get(v);
-        const int amax = block_max<V>(v, in), e = block_exponent(amax);
-        Codes<V> k;
+        const int amax = block_max<8>(v, n), e = block_exponent(amax);
+        Codes8 k;
         k.pack(v, amax, e);
-        if (in)
-            k.store((uint8_t*)a.out.codes + p.row * a.C + c);
-        if (p.item % LPB == 0)
-            ((uint8_t*)a.out.scales)[p.row * nb + p.item / LPB] = (uint8_t)(e + 127);
+        k.store((uint8_t*)a.out.codes + p.row * a.C + c, n);
+        if (p.item % 4 == 0)
+            ((uint8_t*)a.out.scales)[p.row * nb + p.item / 4] = (uint8_t)(e + 127);
     }
 }
 
-template <typename T, int V> __global__ __launch_bounds__(256) void unpack_kernel(gdr2_unpack_args a, int64_t items)
+template <typename T> __global__ __launch_bounds__(256) void unpack_kernel(gdr2_unpack_args a, int64_t items)
 {
-    const int64_t nb = scale_count(a.C), per = (a.C + V - 1) / V, step = (int64_t)gridDim.x * 256;
+    const int64_t nb = scale_count(a.C), per = (a.C + 7) / 8, step = (int64_t)gridDim.x * 256;
     for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < items; at += step) {
         const Place p = place_of(at, per, a.R == 1);
-        const int64_t c = p.item * V;
-        Codes<V> k;
-        k.load((const uint8_t*)a.rows.codes + p.row * a.C + c);
-        float v[V];
+        const int64_t c = p.item * 8;
+        const int n = left_of(a.C, c);
+        Codes8 k;
+        k.load((const uint8_t*)a.rows.codes + p.row * a.C + c, n);
+        float v[8];
         k.get(((const uint8_t*)a.rows.scales)[p.row * nb + c / kRows8], v);
-        RowPart<T, V>::store((T*)a.y + p.row * a.C + c, v);
+        Row8<T>::store((T*)a.y + p.row * a.C + c, v, n);
     }
 }
 
 // Eight workgroups per compute unit, then the items are walked.
 unsigned grid_of(int64_t items) { return (unsigned)std::min(ceil_div(items, 256), (int64_t)device_cu_count() * 8); }
 
-template <typename T, int V> hipError_t pack_v(gdr2_pack_args a, hipStream_t stream)
+}  // namespace
+
+hipError_t launch_pack(const gdr2_pack_args& args, hipStream_t stream)
 {
+    gdr2_pack_args a = args;
     if (a.x_stride == a.C && a.C % kRows8 == 0) {
         a.C *= a.R;
         a.R = 1;
     }
-    const int64_t items = a.R * scale_count(a.C) * (kRows8 / V);
-    hipLaunchKernelGGL((pack_kernel<T, V>), dim3(grid_of(items)), dim3(256), 0, stream, a, items);
+    const int64_t items = a.R * scale_count(a.C) * 4;
+    if (a.dtype == GDR2_BF16)
+        hipLaunchKernelGGL((pack_kernel<bf16>), dim3(grid_of(items)), dim3(256), 0, stream, a, items);
+    else
+        hipLaunchKernelGGL((pack_kernel<float>), dim3(grid_of(items)), dim3(256), 0, stream, a, items);
     return hipGetLastError();
 }
 
-template <typename T, int V> hipError_t unpack_v(gdr2_unpack_args a, hipStream_t stream)
+hipError_t launch_unpack(const gdr2_unpack_args& args, hipStream_t stream)
 {
+    gdr2_unpack_args a = args;
     if (a.C % kRows8 == 0) {
         a.C *= a.R;
         a.R = 1;
     }
-    const int64_t items = a.R * ceil_div(a.C, V);
-    hipLaunchKernelGGL((unpack_kernel<T, V>), dim3(grid_of(items)), dim3(256), 0, stream, a, items);
-    return hipGetLastError();
-}
-
-}  // namespace
-
-hipError_t launch_pack(const gdr2_pack_args& a, hipStream_t stream)
-{
-    const bool bf = a.dtype == GDR2_BF16, wide = rows_in_eights(a.x, a.x_stride, a.C, a.dtype);
-    if (bf)
-        return wide ? pack_v<bf16, 8>(a, stream) : pack_v<bf16, 1>(a, stream);
-    return wide ? pack_v<float, 8>(a, stream) : pack_v<float, 1>(a, stream);
-}
-
-hipError_t launch_unpack(const gdr2_unpack_args& a, hipStream_t stream)
-{
-    const bool wide = a.C % 8 == 0;
+    const int64_t items = a.R * ceil_div(a.C, 8);
     if (a.dtype == GDR2_BF16)
-        return wide ? unpack_v<bf16, 8>(a, stream) : unpack_v<bf16, 1>(a, stream);
-    return wide ? unpack_v<float, 8>(a, stream) : unpack_v<float, 1>(a, stream);
+        hipLaunchKernelGGL((unpack_kernel<bf16>), dim3(grid_of(items)), dim3(256), 0, stream, a, items);
+    else
+        hipLaunchKernelGGL((unpack_kernel<float>), dim3(grid_of(items)), dim3(256), 0, stream, a, items);
+    return hipGetLastError();
 }
 
 }  // namespace gdr2
