@@ -16,6 +16,11 @@
 // through LDS it then finds the state its sub-chunk starts from, and walks its
 // tokens.  So every element is read once, its transcendentals are evaluated once, and
 // the state's chain is one multiply-add per sub-chunk, not per token.
+//
+// Where sequences are too few to fill the chip so, every tile is a workgroup of
+// its own (a chain): it hands its (P, L) on through device memory, finds the
+// state it starts from by the (P, L) of the tiles before it, back to one whose
+// state is there, and hands on the state behind it.  Elements are still read once.
 #pragma once
 
 #include "gdr2_block.h"
@@ -33,14 +38,34 @@ template <int LR> struct GlrTile {
     static constexpr int kTokens = kSubs * kGlrChunk;
 };
 
-// Segments of 2^lg tokens, and channel blocks.
+// What tiles hand on, in device memory.  A map is (P, L), a state (h, 1); each is
+// one 64-bit word, so that it is there whole or not at all.
+struct GlrChain {
+    uint32_t* tickets;     // one for each channel block, 128 bytes apart
+    uint64_t* maps;        // [slots][C]
+    uint64_t* states;      // [slots][C]
+};
+constexpr int kTicketWords = 32;
+constexpr uint32_t kNoMap = 0xbf800000u;     // P = -1, which no product of exponentials is
+
+// How a call's workgroups are laid out: pieces of whole sequences (or, chained,
+// of one tile), and channel blocks.
 struct GlrPlan {
     Pieces seg;
     int64_t blocks;    // of channels
-    int lr;            // lanes along the channels
-    bool split;        // sequences may have more than one segment
+    bool chained;
+    int64_t chain_words() const { return chained ? blocks * (kTicketWords / 2) + 2 * seg.slots() * C : 0; }
+    int64_t C;
+    GlrChain chain(void* workspace) const
+    {
+        uint64_t* w = (uint64_t*)workspace;
+        uint64_t* maps = w + blocks * (kTicketWords / 2);
+        return {(uint32_t*)w, maps, maps + seg.slots() * C};
+    }
 };
-GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward);
+GlrPlan glr_plan(const gdr2_glr_args& a, int V);
+// Empties a chain.
+hipError_t launch_glr_chain_reset(const GlrPlan& plan, void* workspace, hipStream_t stream);
 
 // Whether a lane holds two channels: bf16 where every row array is aligned to
 // pairs.  (One of fp32 is as wide, and 64 lanes of them 256 bytes.)
@@ -145,13 +170,118 @@ __device__ __forceinline__ float glr_root(float t, float a)
 // it is scheduled in.)
 __device__ __forceinline__ float unless_masked(float q, float v) { return __builtin_unpredictable(q == 0.f) ? 0.f : v; }
 
-// The workgroup's number.  Workgroups go to the eight XCDs in turn; numbered so,
-// an XCD owns a range of neighbouring channel blocks, and its cache sees whole
-// rows: every eighth block of 128 bytes would fall into a few of its channels.
-__device__ __forceinline__ uint32_t block_id()
+// This workgroup's slot and channel block.
+struct GlrWork {
+    int64_t slot, block;
+};
+// One pass: workgroups go to the eight XCDs in turn; numbered so, an XCD owns a
+// range of neighbouring channel blocks, and its cache sees whole rows: every
+// eighth block of 128 bytes would fall into a few of its channels.
+__device__ __forceinline__ GlrWork one_pass_work(const GlrPlan& plan)
 {
     const uint32_t n = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
-    return xcd * n + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+    const uint32_t id = xcd * n + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+    const int64_t slot = id / plan.blocks;
+    return {slot, id - slot * plan.blocks};
+}
+// Chained: tiles are taken in the order of their tickets, so that the tiles one
+// waits for are taken by workgroups that run already, and wait only for such
+// themselves.
+__device__ __forceinline__ GlrWork chained_work(const GlrPlan& plan, const GlrChain& chain, bool reverse)
+{
+    __shared__ uint32_t s_ticket;
+    const int64_t block = blockIdx.x % (uint32_t)plan.blocks;
+    if (threadIdx.x == 0)
+        s_ticket = atomicAdd(chain.tickets + block * kTicketWords, 1u);
+    __syncthreads();
+    const int64_t ticket = uniform((int64_t)s_ticket);
+    return {reverse ? plan.seg.slots() - 1 - ticket : ticket, block};
+}
+
+__device__ __forceinline__ void hand_on(uint64_t* to, uint32_t low, uint32_t high)
+{
+    __hip_atomic_store(to, (uint64_t)high << 32 | low, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t handed(const uint64_t* from)
+{
+    return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The state of channel c behind the `count` > 0 tiles before `slot` (in steps of
+// `step`): the nearest one that is there, and the maps from it on.  Maps are
+// applied one by one, as the tile whose state it is applied those before it, so
+// the result does not depend on which state was found.  Every slot's state is
+// handed on in the end, whatever the offsets say, so the wait ends.
+__device__ __forceinline__ float state_behind(const GlrChain& chain, int64_t slot, int step, int64_t count, int64_t C, uint32_t c)
+{
+    constexpr int kBack = 4;      // tiles looked at together: their words are a round trip away
+    for (;;) {
+        uint64_t maps[kBack], states[kBack];
+#pragma unroll
+        for (int u = 0; u < kBack; ++u) {
+            maps[u] = kNoMap;
+            states[u] = 0;
+            if (u < count) {
+                const int64_t row = (slot + (int64_t)step * (u + 1)) * C;     // the same for all lanes
+                maps[u] = handed(chain.maps + row + c);
+                states[u] = handed(chain.states + row + c);
+            }
+        }
+        int found = kBack;
+        bool open = true;
+#pragma unroll
+        for (int u = 0; u < kBack; ++u) {
+            const bool state = (uint32_t)(states[u] >> 32) != 0;
+            if (open && state)
+                found = u;
+            open = open && !state && (uint32_t)maps[u] != kNoMap;
+        }
+        if (found < kBack) {
+            float h = 0.f;
+#pragma unroll
+            for (int u = kBack - 1; u >= 0; --u) {
+                const float P = __builtin_bit_cast(float, (uint32_t)maps[u]), L = __builtin_bit_cast(float, (uint32_t)(maps[u] >> 32));
+                if (u == found)
+                    h = __builtin_bit_cast(float, (uint32_t)states[u]);
+                else if (u < found)
+                    h = fmaf(P, h, L);
+            }
+            return h;
+        }
+        __builtin_amdgcn_s_sleep(1);
+    }
+}
+
+// By the first wave, a lane a channel: the tile's map from its sub-chunks', in
+// the order FIRST, FIRST + STEP, .., then the state it starts from, then the one behind it.
+// `begin`: the state where the tile is its sequence's first in this direction.
+template <int V, int LR, int STEP>
+__device__ __forceinline__ float chain_state(const GlrChain& chain, const float (*s_span)[LR][2 * V], int64_t slot, int64_t before,
+                                             int64_t C, int64_t c, const float* begin)
+{
+    constexpr int N = GlrTile<LR>::kSubs;
+    const int lane = threadIdx.x, li = lane / V, v = lane % V;
+    float P = 1.f, L = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < N; ++k) {
+        const int j = STEP > 0 ? k : N - 1 - k;
+        const float p = s_span[j][li][2 * v], l = s_span[j][li][2 * v + 1];
+        L = fmaf(p, L, l);
+        P *= p;
+    }
+    if (c >= C)
+        return 0.f;
+    hand_on(chain.maps + slot * C + c, __builtin_bit_cast(uint32_t, P), __builtin_bit_cast(uint32_t, L));
+    const float h = before > 0 ? state_behind(chain, slot, -STEP, before, C, (uint32_t)c) : begin ? begin[c] : 0.f;
+    hand_on(chain.states + slot * C + c, __builtin_bit_cast(uint32_t, fmaf(P, h, L)), 1u);
+    return h;
+}
+// What an idle slot hands on: nothing changes.
+__device__ __forceinline__ void chain_idle(const GlrChain& chain, int64_t slot, int64_t C, int64_t c)
+{
+    if (threadIdx.x < 64 && c < C) {
+        hand_on(chain.maps + slot * C + c, __builtin_bit_cast(uint32_t, 1.f), 0u);
+        hand_on(chain.states + slot * C + c, 0u, 1u);
+    }
 }
 
 // Where this lane's channels and sub-chunk lie.

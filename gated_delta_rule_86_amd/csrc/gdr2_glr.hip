@@ -54,10 +54,10 @@ template <typename T, int V, int LR> struct Walk {
     }
 };
 
-// (a, b) of a sub-chunk, and its (P, L).  Each token's registers are loaded
-// again, for the tile at `t`, as soon as its terms are formed: the loads run a whole tile
-// ahead of their use, and go out evenly over the tile.
-template <typename T, int V, int LR>
+// (a, b) of a sub-chunk, and its (P, L).  AHEAD: the registers of r and i are
+// loaded again, for the tile at `t`, as soon as a token's terms are formed: the loads run a
+// tile ahead of their use, and go out evenly over the tile.
+template <bool AHEAD, typename T, int V, int LR>
 __device__ __forceinline__ SpanVec<V> form_terms(Inputs<T, V>& in, const Walk<T, V, LR>& walk, int64_t t, const float (&A2)[V],
                                                  float (&a)[kGlrChunk][V], float (&b)[kGlrChunk][V])
 {
@@ -80,8 +80,10 @@ __device__ __forceinline__ SpanVec<V> form_terms(Inputs<T, V>& in, const Walk<T,
                 s.l[v] = fmaf(at, s.l[v], b[k][v]);
                 s.p[v] *= at;
             }
-            in.r.load(k, br, atr);
-            in.i.load(k, bi, ati);
+            if constexpr (AHEAD) {
+                in.r.load(k, br, atr);
+                in.i.load(k, bi, ati);
+            }
         }
     });
     return s;
@@ -194,62 +196,34 @@ template <typename T, int V> struct CodeRows {
     }
 };
 
-// The state the segment starts from: h0 and the segments before it in turn,
-// eight of their (P, L) in flight.
-template <int V>
-__device__ __forceinline__ void start_state(const float* h0, const float* spans, const Piece& q, int64_t C, int64_t c, bool on,
-                                            float (&h)[V])
-{
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        h[v] = 0.f;
-    if (!on)
-        return;
-    if (h0)
-        load_channels<V>(h0 + q.seq * C + c, h);
-    const float* s = spans + (q.first * C + c) * 2;
-    for (int64_t j = 0; j < q.index; j += kFoldAhead) {
-        float pl[kFoldAhead][2 * V];
-#pragma unroll
-        for (int u = 0; u < kFoldAhead; ++u)
-            if (j + u < q.index)
-                load_channels<2 * V>(s + (j + u) * C * 2, pl[u]);
-#pragma unroll
-        for (int u = 0; u < kFoldAhead; ++u)
-            if (j + u < q.index)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    h[v] = fmaf(pl[u][2 * v], h[v], pl[u][2 * v + 1]);
-    }
-}
-
-// SPAN: (P, L) of every segment but a sequence's last one, nothing else.
-template <typename T, int V, int LR, bool PACK, bool SPAN>
-__global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kernel(gdr2_glr_args a, GlrPlan plan, float* spans)
+template <typename T, int V, int LR, bool PACK, bool CHAINED>
+__global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kernel(gdr2_glr_args a, GlrPlan plan, GlrChain chain)
 {
     typedef GlrTile<LR> Tile;
-    __shared__ float s_span[2][Tile::kSubs][LR][2 * V];
-    const uint32_t id = block_id();
-    const int64_t slot = id / plan.blocks, block = id - slot * plan.blocks;
-    const Segment seg = segment_of(plan, slot);
-    if (seg.q.seq < 0 || (SPAN && seg.t0 + seg.n >= seg.q.len))
+    __shared__ float s_span[CHAINED ? 1 : 2][Tile::kSubs][LR][2 * V];
+    __shared__ float s_state[CHAINED ? LR * V : 1];
+    const GlrWork work = CHAINED ? chained_work(plan, chain, false) : one_pass_work(plan);
+    const Segment seg = segment_of(plan, work.slot);
+    const int64_t c64 = work.block * (LR * V) + threadIdx.x;       // the first wave's channels, one a lane
+    if (seg.q.seq < 0) {
+        if constexpr (CHAINED)
+            chain_idle(chain, work.slot, a.C, c64);
         return;
-    const GlrLane<V, LR> lane(a.C, block);
+    }
+    const GlrLane<V, LR> lane(a.C, work.block);
     const int64_t row0 = seg.q.row0 + seg.t0;
     const Walk<T, V, LR> walk(a, row0, seg.n, lane);
-    float A2[V], h[V], whole[V];
+    float A2[V], h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         A2[v] = lane.on ? exponent_scale(a.A[lane.c + v]) : 0.f;
         h[v] = 0.f;
-        whole[v] = 1.f;
     }
-    if constexpr (!SPAN)
-        start_state<V>(a.h0, spans, seg.q, a.C, lane.c, lane.on, h);
+    if (!CHAINED && a.h0 && lane.on)
+        load_channels<V>(a.h0 + seg.q.seq * a.C + lane.c, h);
     const WaveRows y = WaveRows::at<T>(a.y, row0, a.C);
     const uint32_t oy = lane.template offset<T>(y.row_bytes);
     const int64_t chunk0 = a.h_chunks ? chunk_row(a, seg.q) + seg.t0 / kGlrChunk : 0;
-
     const CodeRows<T, V> x8(a.x8, row0, a.C, lane), r8(a.r8, row0, a.C, lane), i8(a.i8, row0, a.C, lane);
 
     Inputs<T, V> in;
@@ -262,7 +236,8 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
         }
     });
     int buf = 0;
-    for (int64_t t = 0; t < seg.n; t += Tile::kTokens, buf ^= 1) {
+    // a tile of an empty sequence hands on what it is handed
+    for (int64_t t = 0; CHAINED || t < seg.n; t += Tile::kTokens) {
         const int left = walk.left(t), mine = left - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
         if constexpr (PACK) {
             const int64_t at = left > 0 ? walk.first(t) : 0;
@@ -276,7 +251,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
         if (left < Tile::kWaveTokens)
             in.r.mask(mine);
         float at[kGlrChunk][V], b[kGlrChunk][V];
-        const SpanVec<V> s = form_terms<T, V, LR>(in, walk, t + Tile::kTokens, A2, at, b);
+        const SpanVec<V> s = form_terms<!CHAINED, T, V, LR>(in, walk, t + Tile::kTokens, A2, at, b);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             s_span[buf][lane.sub][lane.li][2 * v] = s.p[v];
@@ -285,6 +260,15 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
         // one barrier a tile: a buffer is written again two tiles on, when every wave has passed
         // the barrier between, and so read it
         lds_barrier();
+        if constexpr (CHAINED) {
+            if (lane.wave == 0)
+                s_state[threadIdx.x] = chain_state<V, LR, 1>(chain, s_span[0], work.slot, seg.q.index, a.C, c64,
+                                                             a.h0 ? a.h0 + seg.q.seq * a.C : nullptr);
+            lds_barrier();
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                h[v] = s_state[lane.li * V + v];
+        }
         float start[V];
 #pragma unroll
         for (int j = 0; j < Tile::kSubs; ++j) {
@@ -296,42 +280,44 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
             for (int v = 0; v < V; ++v) {
                 start[v] = j == lane.sub || j == 0 ? h[v] : start[v];
                 h[v] = fmaf(pl[2 * v], h[v], pl[2 * v + 1]);
-                if constexpr (SPAN)
-                    whole[v] *= pl[2 * v];
             }
             if (j % 4 == 3)
                 __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!SPAN) {
-            if (a.h_chunks && lane.on && mine > 0)
-                store_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, start);
-            const auto out = y.buffer(left > 0 ? walk.first(t) : 0, left);
-            RowOffset to{oy, y.row_bytes};
+        if (a.h_chunks && lane.on && mine > 0)
+            store_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, start);
+        const auto out = y.buffer(left > 0 ? walk.first(t) : 0, left);
+        RowOffset to{oy, y.row_bytes};
 #pragma unroll
-            for (int k = 0; k < kGlrChunk; ++k) {
+        for (int k = 0; k < kGlrChunk; ++k) {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    start[v] = fmaf(at[k][v], start[v], b[k][v]);
-                store_token<T, V>(out, to.next(), start);
-            }
+            for (int v = 0; v < V; ++v)
+                start[v] = fmaf(at[k][v], start[v], b[k][v]);
+            store_token<T, V>(out, to.next(), start);
         }
-        walk.with_tile(t + Tile::kTokens, [&](auto, auto bx, auto, RowOffset, RowOffset atx, RowOffset) {
+        if constexpr (!CHAINED) {
+            walk.with_tile(t + Tile::kTokens, [&](auto, auto bx, auto, RowOffset, RowOffset atx, RowOffset) {
 #pragma unroll
-            for (int k = 0; k < kGlrChunk; ++k)
-                in.x.load(k, bx, atx);
-        });
+                for (int k = 0; k < kGlrChunk; ++k)
+                    in.x.load(k, bx, atx);
+            });
+            buf ^= 1;
+        } else {
+            break;
+        }
     }
-    if (lane.sub != 0 || !lane.on)
-        return;
-    if constexpr (SPAN) {
-        float* to = spans + (slot * a.C + lane.c) * 2;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            to[2 * v] = whole[v];
-            to[2 * v + 1] = h[v];
-        }
-    } else if (a.h_out && seg.t0 + seg.n == seg.q.len) {
+    if (a.h_out && lane.sub == 0 && lane.on && seg.t0 + seg.n == seg.q.len)
         store_channels<V>(a.h_out + seg.q.seq * a.C + lane.c, h);
+}
+
+__global__ __launch_bounds__(256) void glr_chain_reset_kernel(GlrChain chain, int64_t tickets, int64_t words)
+{
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < words; at += step) {
+        chain.maps[at] = kNoMap;
+        chain.states[at] = 0;
+        if (at < tickets)
+            chain.tickets[at * kTicketWords] = 0;
     }
 }
 
@@ -358,29 +344,27 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
     }
 }
 
-int64_t span_floats(const gdr2_glr_args& a, const GlrPlan& p) { return p.split ? p.seg.slots() * a.C * 2 : 0; }
-
-template <typename T, int V, int LR> hipError_t forward_lr(const gdr2_glr_args& a, const GlrPlan& plan, hipStream_t stream)
+template <typename T, int V, int LR> hipError_t forward_lr(const gdr2_glr_args& a, hipStream_t stream)
 {
+    const GlrPlan plan = glr_plan(a, V);
     const dim3 grid((unsigned)(plan.seg.slots() * plan.blocks)), threads(64 * kGlrWaves);
-    float* spans = (float*)a.workspace;
-    if (plan.split) {
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, false, true>), grid, threads, 0, stream, a, plan, spans);
-        const hipError_t e = hipGetLastError();
+    GlrChain chain = {};
+    if (plan.chained) {
+        const hipError_t e = launch_glr_chain_reset(plan, a.workspace, stream);
         if (e != hipSuccess)
             return e;
+        chain = plan.chain(a.workspace);
     }
-    if (a.x8.codes)
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, true, false>), grid, threads, 0, stream, a, plan, spans);
+    const bool pack = a.x8.codes;
+    if (plan.chained && pack)
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, true, true>), grid, threads, 0, stream, a, plan, chain);
+    else if (plan.chained)
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, false, true>), grid, threads, 0, stream, a, plan, chain);
+    else if (pack)
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, true, false>), grid, threads, 0, stream, a, plan, chain);
     else
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, false, false>), grid, threads, 0, stream, a, plan, spans);
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, false, false>), grid, threads, 0, stream, a, plan, chain);
     return hipGetLastError();
-}
-
-hipError_t forward_pairs(const gdr2_glr_args& a, hipStream_t stream)
-{
-    const GlrPlan plan = glr_plan(a, 2, false);
-    return plan.lr == 32 ? forward_lr<bf16, 2, 32>(a, plan, stream) : forward_lr<bf16, 2, 16>(a, plan, stream);
 }
 
 template <typename T, int V> hipError_t step_v(const gdr2_glr_step_args& a, hipStream_t stream)
@@ -394,51 +378,45 @@ template <typename T, int V> hipError_t step_v(const gdr2_glr_step_args& a, hipS
 
 }  // namespace
 
-// One workgroup walks a sequence when that gives at least three workgroups for
-// four compute units, with half as many channels each where that makes the
-// difference.  Otherwise sequences are cut into segments, for two workgroups a
-// compute unit.
-GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward)
+// One workgroup walks a sequence where that fills the chip: workgroups in
+// whole rounds of the compute units, or nearly.  Otherwise tiles are chained, and so are
+// packed sequences, whose lengths are not known here.
+GlrPlan glr_plan(const gdr2_glr_args& a, int V)
 {
-    GlrPlan p{{a.offsets, a.B, a.T, 40}, 0, V == 2 ? 32 : 64, false};
-    const int64_t units = device_cu_count(), B = std::max(a.B, (int64_t)1);
-    auto blocks = [&](int lr) { return ceil_div(a.C, (int64_t)lr * V); };
-    auto enough = [&](int lr) { return B * blocks(lr) * 4 >= units * 3; };
-    bool split = a.algo == GDR2_ALGO_SEGMENTED;
-    if (a.algo != GDR2_ALGO_SEGMENTED && !enough(p.lr)) {
-        if (V == 2)
-            p.lr = 16;
-        split = a.algo == GDR2_ALGO_AUTO && !enough(p.lr);
-        if (split && V == 2)
-            p.lr = 32;
-    }
-    p.blocks = blocks(p.lr);
-    if (split) {
-        // a dense sequence has T tokens; a packed one has T / B on average
-        const int64_t tokens = a.offsets ? a.T : B * a.T, want = ceil_div(units * 2, p.blocks);
-        int lg = a.algo == GDR2_ALGO_SEGMENTED ? 7 : 9;
-        while (lg < 40 && (tokens >> lg) > want)
-            ++lg;
-        p.split = a.offsets ? (a.T >> lg) > 0 : a.T > ((int64_t)1 << lg);
-        if (p.split)
-            p.seg.lg = lg;
-    }
+    constexpr int kPairLg = 8, kOneLg = 7;
+    static_assert(GlrTile<32>::kTokens == 1 << kPairLg && GlrTile<64>::kTokens == 1 << kOneLg, "tiles");
+    const int lg = V == 2 ? kPairLg : kOneLg;
+    GlrPlan p{{a.offsets, a.B, a.T, 40}, ceil_div(a.C, (int64_t)64), false, a.C};
+    const int64_t units = device_cu_count(), groups = std::max(a.B, (int64_t)1) * p.blocks, rounds = ceil_div(groups, units);
+    const bool fills = groups * 4 >= rounds * units * 3;
+    const bool wanted = a.algo == GDR2_ALGO_SEGMENTED || (a.algo == GDR2_ALGO_AUTO && (a.offsets || !fills));
+    // (a packed sequence may have all of the rows)
+    p.chained = wanted && a.T > ((int64_t)1 << lg);
+    if (p.chained)
+        p.seg.lg = lg;
     return p;
+}
+
+hipError_t launch_glr_chain_reset(const GlrPlan& plan, void* workspace, hipStream_t stream)
+{
+    const int64_t words = plan.seg.slots() * plan.C;
+    const dim3 grid((unsigned)std::min(ceil_div(words, 256), (int64_t)device_cu_count() * 8));
+    hipLaunchKernelGGL(glr_chain_reset_kernel, grid, dim3(256), 0, stream, plan.chain(workspace), plan.blocks, words);
+    return hipGetLastError();
 }
 
 // The larger of the two widths' needs where the pointers decide between them.
 size_t glr_workspace_bytes(const gdr2_glr_args& a)
 {
-    const int64_t one = span_floats(a, glr_plan(a, 1, false)), two = a.C % 2 || a.dtype != GDR2_BF16 ? 0 : span_floats(a, glr_plan(a, 2, false));
-    return (size_t)std::max(one, two) * sizeof(float);
+    const int64_t one = glr_plan(a, 1).chain_words(), two = glr_plan(a, 2).chain_words();
+    return a.B > 0 ? (size_t)std::max(one, two) * 8 : 0;
 }
 
 hipError_t launch_glr_forward(const gdr2_glr_args& a, hipStream_t stream)
 {
     if (glr_pairs(a))
-        return forward_pairs(a, stream);
-    const GlrPlan plan = glr_plan(a, 1, false);
-    return a.dtype == GDR2_BF16 ? forward_lr<bf16, 1, 64>(a, plan, stream) : forward_lr<float, 1, 64>(a, plan, stream);
+        return forward_lr<bf16, 2, 32>(a, stream);
+    return a.dtype == GDR2_BF16 ? forward_lr<bf16, 1, 64>(a, stream) : forward_lr<float, 1, 64>(a, stream);
 }
 
 hipError_t launch_glr_step(const gdr2_glr_step_args& a, hipStream_t stream)

@@ -108,40 +108,11 @@ template <typename T, int V> struct Source<T, V, true> {
     }
 };
 
-// The gradient that reaches the segment's end: dL/dh_out, and the segments
-// behind it in turn, the last one first.
-template <int V>
-__device__ __forceinline__ void end_gradient(const float* dh_out, const float* spans, const Piece& q, int64_t count, int64_t C,
-                                             int64_t c, bool on, float (&lam)[V])
-{
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        lam[v] = 0.f;
-    if (!on)
-        return;
-    if (dh_out)
-        load_channels<V>(dh_out + q.seq * C + c, lam);
-    const float* s = spans + (q.first * C + c) * 2;
-    for (int64_t j = count - 1; j > q.index; j -= kFoldAhead) {
-        float pl[kFoldAhead][2 * V];
-#pragma unroll
-        for (int u = 0; u < kFoldAhead; ++u)
-            if (j - u > q.index)
-                load_channels<2 * V>(s + (j - u) * C * 2, pl[u]);
-#pragma unroll
-        for (int u = 0; u < kFoldAhead; ++u)
-            if (j - u > q.index)
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    lam[v] = fmaf(pl[u][2 * v], lam[v], pl[u][2 * v + 1]);
-    }
-}
-
 // A sub-chunk's (P, L) through LDS: the gradient that reaches this lane's
 // sub-chunk from behind, and in `lam` the one that leaves the tile.
-template <int V, int LR, bool SPAN>
+template <int V, int LR>
 __device__ __forceinline__ void reverse_fold(const float (*s_span)[LR][2 * V], const GlrLane<V, LR>& lane, float (&lam)[V],
-                                             float (&reach)[V], float (&whole)[V])
+                                             float (&reach)[V])
 {
 #pragma unroll
     for (int j = GlrTile<LR>::kSubs - 1; j >= 0; --j) {
@@ -153,8 +124,6 @@ __device__ __forceinline__ void reverse_fold(const float (*s_span)[LR][2 * V], c
         for (int v = 0; v < V; ++v) {
             reach[v] = j == lane.sub || j == GlrTile<LR>::kSubs - 1 ? lam[v] : reach[v];
             lam[v] = fmaf(pl[2 * v], lam[v], pl[2 * v + 1]);
-            if constexpr (SPAN)
-                whole[v] *= pl[2 * v];
         }
         if (j % 8 == 0)
             __builtin_amdgcn_sched_barrier(0);       // eight reads in flight at most
@@ -175,103 +144,19 @@ template <int V, int LR> struct TileRows {
     __device__ __forceinline__ int64_t at(int64_t t) const { return left(t) > 0 ? first(t) : 0; }
 };
 
-// (P, L) of every segment but a sequence's first one.
-template <typename T, int V, int LR, bool P8>
-__global__ __launch_bounds__(64 * kGlrWaves) void glr_span_backward_kernel(gdr2_glr_bwd_args p, GlrPlan plan, float* spans)
+template <typename T, int V, int LR, bool P8, bool CHAINED>
+__global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_bwd_args p, GlrPlan plan, GlrChain chain, float* part)
 {
     typedef GlrTile<LR> Tile;
-    __shared__ float s_span[2][Tile::kSubs][LR][2 * V];
+    __shared__ float s_span[CHAINED ? 1 : 2][Tile::kSubs][LR][2 * V];
+    __shared__ float s_state[CHAINED ? LR * V : 1];
     const gdr2_glr_args& a = p.f;
-    const uint32_t id = block_id();
-    const int64_t slot = id / plan.blocks, block = id - slot * plan.blocks;
-    const Segment seg = segment_of(plan, slot);
-    if (seg.q.seq < 0 || seg.q.index == 0)
-        return;
-    const GlrLane<V, LR> lane(a.C, block);
-    const int64_t row0 = seg.q.row0 + seg.t0;
-    const TileRows<V, LR> rows{seg.n, lane.wave};
-    const Source<T, V, P8> sr(a.r, a.r8, row0, a.r_stride, a.C, lane);
-    const Source<T, V, false> sd(p.dy, row0, a.C, lane);
-    float A2[V], lam[V], whole[V], reach[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        A2[v] = lane.on ? exponent_scale(a.A[lane.c + v]) : 0.f;
-        lam[v] = 0.f;
-        whole[v] = 1.f;
-    }
-    typename Source<T, V, P8>::Tokens r;
-    SubRows<T, V> dy;
-    const int64_t last = (seg.n - 1) / Tile::kTokens * Tile::kTokens;
-    {
-        const int m = rows.left(last);
-        auto nr = sr.reader(rows.at(last), m);
-        auto nd = sd.reader(rows.at(last), m);
-#pragma unroll
-        for (int k = 0; k < kGlrChunk; ++k) {
-            nr.load(k, r);
-            nd.load(k, dy);
-        }
-    }
-    int buf = 0;
-    for (int64_t t = last; t >= 0; t -= Tile::kTokens, buf ^= 1) {
-        // the next tile's tokens take the registers of this one's as these are used up
-        const int64_t ahead = t - Tile::kTokens;
-        auto nr = sr.reader(rows.at(ahead), rows.left(ahead));
-        auto nd = sd.reader(rows.at(ahead), rows.left(ahead));
-        const int mine = rows.left(t) - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
-        float at[kGlrChunk][V], P[V], L[V];
-        tokens_up([&](auto at_k) {
-                constexpr int K = decltype(at_k)::value;
-            float rv[V];
-            token_of<K>(r, rv);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                at[K][v] = __builtin_unpredictable(K < mine) ? fast_exp2(A2[v] * sigmoid_f(rv[v])) : 1.f;
-            nr.load(K, r);
-        });
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            P[v] = 1.f;
-            L[v] = 0.f;
-        }
-#pragma unroll
-        for (int k = kGlrChunk - 1; k >= 0; --k)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                L[v] = at[k][v] * (dy.get(k, v) + L[v]);
-                P[v] *= at[k][v];
-            }
-#pragma unroll
-        for (int k = 0; k < kGlrChunk; ++k)
-            nd.load(k, dy);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s_span[buf][lane.sub][lane.li][2 * v] = P[v];
-            s_span[buf][lane.sub][lane.li][2 * v + 1] = L[v];
-        }
-        lds_barrier();
-        reverse_fold<V, LR, true>(s_span[buf], lane, lam, reach, whole);
-    }
-    if (lane.sub != 0 || !lane.on)
-        return;
-    float* to = spans + (slot * a.C + lane.c) * 2;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        to[2 * v] = whole[v];
-        to[2 * v + 1] = lam[v];
-    }
-}
-
-template <typename T, int V, int LR, bool P8>
-__global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_bwd_args p, GlrPlan plan, const float* spans, float* part)
-{
-    typedef GlrTile<LR> Tile;
-    __shared__ float s_span[2][Tile::kSubs][LR][2 * V];
-    const gdr2_glr_args& a = p.f;
-    const uint32_t id = block_id();
-    const int64_t slot = id / plan.blocks, block = id - slot * plan.blocks;
-    const Segment seg = segment_of(plan, slot);
-    const GlrLane<V, LR> lane(a.C, block);
+    const GlrWork work = CHAINED ? chained_work(plan, chain, true) : one_pass_work(plan);
+    const Segment seg = segment_of(plan, work.slot);
+    const GlrLane<V, LR> lane(a.C, work.block);
+    const int64_t c64 = work.block * (LR * V) + threadIdx.x;       // the first wave's channels, one a lane
+    if (CHAINED && seg.q.seq < 0)
+        chain_idle(chain, work.slot, a.C, c64);
     float dA[V], A2[V], Av[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -288,9 +173,14 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
         const WaveRows ox = WaveRows::at<T>(p.dx, row0, a.C), orr = WaveRows::at<T>(p.dr, row0, a.C), oi = WaveRows::at<T>(p.di, row0, a.C);
         const uint32_t off = lane.template offset<T>(ox.row_bytes);
         const int64_t chunk0 = chunk_row(a, seg.q) + seg.t0 / kGlrChunk;
-        const int64_t L = (int64_t)1 << plan.seg.lg, count = plan.split ? (seg.q.len + L - 1) >> plan.seg.lg : 1;
-        float lam[V], reach[V], unused[V];
-        end_gradient<V>(p.dh_out, spans, seg.q, count, a.C, lane.c, lane.on, lam);
+        // tiles behind this one
+        const int64_t L = (int64_t)1 << plan.seg.lg, count = (seg.q.len + L - 1) >> plan.seg.lg, behind = count > 0 ? count - 1 - seg.q.index : 0;
+        float lam[V], reach[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            lam[v] = 0.f;
+        if (!CHAINED && p.dh_out && lane.on)
+            load_channels<V>(p.dh_out + seg.q.seq * a.C + lane.c, lam);
 
         // the next tile's tokens take the registers of this one's as these are used up: every load runs most of a
         // tile ahead of its use, and they go out evenly over the tile
@@ -305,7 +195,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             if (lane.on && mine > 0)
                 load_channels<V>(a.h_chunks + (chunk0 + t / kGlrChunk + lane.sub) * a.C + lane.c, h0);
         };
-        const int64_t last = seg.n > 0 ? (seg.n - 1) / Tile::kTokens * Tile::kTokens : -1;
+        // a tile of an empty sequence hands on what it is handed
+        const int64_t last = seg.n > 0 ? (seg.n - 1) / Tile::kTokens * Tile::kTokens : CHAINED ? 0 : -1;
         if (last >= 0) {
             const int m = rows.left(last);
             const int64_t first = rows.at(last);
@@ -324,7 +215,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             load_state(last);
         }
         int buf = 0;
-        for (int64_t t = last; t >= 0; t -= Tile::kTokens, buf ^= 1) {
+        for (int64_t t = last; CHAINED || t >= 0; t -= Tile::kTokens) {
             const int left = rows.left(t), mine = left - (lane.sub - lane.wave * Tile::kGroups) * kGlrChunk;
             const int64_t ahead = t - Tile::kTokens;
             const int nleft = rows.left(ahead);
@@ -343,9 +234,11 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             });
             // (loads stay behind the uses of what was in their registers)
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!CHAINED) {
 #pragma unroll
-            for (int k = 0; k < kGlrChunk; ++k)
-                nr.load(k, r);
+                for (int k = 0; k < kGlrChunk; ++k)
+                    nr.load(k, r);
+            }
             __builtin_amdgcn_sched_barrier(0);
             if (left < Tile::kWaveTokens) {
 #pragma unroll
@@ -373,7 +266,16 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                 s_span[buf][lane.sub][lane.li][2 * v + 1] = Lr[v];
             }
             lds_barrier();
-            reverse_fold<V, LR, false>(s_span[buf], lane, lam, reach, unused);
+            if constexpr (CHAINED) {
+                if (lane.wave == 0)
+                    s_state[threadIdx.x] = chain_state<V, LR, -1>(chain, s_span[0], work.slot, behind, a.C, c64,
+                                                                  p.dh_out ? p.dh_out + seg.q.seq * a.C : nullptr);
+                lds_barrier();
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    lam[v] = s_state[lane.li * V + v];
+            }
+            reverse_fold<V, LR>(s_span[buf], lane, lam, reach);
             float h[V];
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -387,10 +289,12 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                     here(g[k][v]);
                 }
             __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!CHAINED) {
 #pragma unroll
-            for (int k = 0; k < kGlrChunk; ++k)
-                nd.load(k, dy);
-            load_state(ahead);
+                for (int k = 0; k < kGlrChunk; ++k)
+                    nd.load(k, dy);
+                load_state(ahead);
+            }
             __builtin_amdgcn_sched_barrier(0);
             const int64_t first = rows.at(t);
             const auto bx = ox.buffer(first, left), br = orr.buffer(first, left), bi = oi.buffer(first, left);
@@ -422,14 +326,19 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                 // tokens are scheduled four at a time: more of them in flight would not fit the registers
                 if constexpr (K % 4 == 3) {
                     __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (!CHAINED) {
 #pragma unroll
-                    for (int k = K - 3; k <= K; ++k) {
-                        nx.load(k, x);
-                        ni.load(k, i);
+                        for (int k = K - 3; k <= K; ++k) {
+                            nx.load(k, x);
+                            ni.load(k, i);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
                 }
             });
+            if constexpr (CHAINED)
+                break;
+            buf ^= 1;
         }
         if (p.dh0 && seg.q.index == 0 && lane.sub == 0 && lane.on)
             store_channels<V>(p.dh0 + seg.q.seq * a.C + lane.c, lam);
@@ -446,27 +355,25 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 dA[v] += s_sum[j][lane.li][v];
-        store_channels<V>(part + slot * a.C + lane.c, dA);
+        store_channels<V>(part + work.slot * a.C + lane.c, dA);
     }
 }
 
-int64_t span_floats(const gdr2_glr_args& a, const GlrPlan& p) { return p.split ? p.seg.slots() * a.C * 2 : 0; }
-
-template <typename T, int V, int LR, bool P8>
-hipError_t backward_lr(const gdr2_glr_bwd_args& p, const GlrPlan& plan, hipStream_t stream)
+template <typename T, int V, int LR, bool P8> hipError_t backward_lr(const gdr2_glr_bwd_args& p, hipStream_t stream)
 {
+    const GlrPlan plan = glr_plan(p.f, V);
     const dim3 grid((unsigned)(plan.seg.slots() * plan.blocks)), threads(64 * kGlrWaves);
-    float* spans = (float*)p.workspace;
-    float* part = spans + span_floats(p.f, plan);
+    float* part = (float*)((uint64_t*)p.workspace + plan.chain_words());
     const int64_t P = p.f.B > 0 ? plan.seg.slots() : 0;
     if (P > 0) {
-        if (plan.split) {
-            hipLaunchKernelGGL((glr_span_backward_kernel<T, V, LR, P8>), grid, threads, 0, stream, p, plan, spans);
-            const hipError_t e = hipGetLastError();
+        if (plan.chained) {
+            const hipError_t e = launch_glr_chain_reset(plan, p.workspace, stream);
             if (e != hipSuccess)
                 return e;
+            hipLaunchKernelGGL((glr_backward_kernel<T, V, LR, P8, true>), grid, threads, 0, stream, p, plan, plan.chain(p.workspace), part);
+        } else {
+            hipLaunchKernelGGL((glr_backward_kernel<T, V, LR, P8, false>), grid, threads, 0, stream, p, plan, GlrChain{}, part);
         }
-        hipLaunchKernelGGL((glr_backward_kernel<T, V, LR, P8>), grid, threads, 0, stream, p, plan, spans, part);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -476,12 +383,9 @@ hipError_t backward_lr(const gdr2_glr_bwd_args& p, const GlrPlan& plan, hipStrea
 
 template <bool P8> hipError_t backward_p(const gdr2_glr_bwd_args& p, hipStream_t stream)
 {
-    if (glr_pairs(p.f)) {
-        const GlrPlan plan = glr_plan(p.f, 2, true);
-        return plan.lr == 32 ? backward_lr<bf16, 2, 32, P8>(p, plan, stream) : backward_lr<bf16, 2, 16, P8>(p, plan, stream);
-    }
-    const GlrPlan plan = glr_plan(p.f, 1, true);
-    return p.f.dtype == GDR2_BF16 ? backward_lr<bf16, 1, 64, P8>(p, plan, stream) : backward_lr<float, 1, 64, P8>(p, plan, stream);
+    if (glr_pairs(p.f))
+        return backward_lr<bf16, 2, 32, P8>(p, stream);
+    return p.f.dtype == GDR2_BF16 ? backward_lr<bf16, 1, 64, P8>(p, stream) : backward_lr<float, 1, 64, P8>(p, stream);
 }
 
 }  // namespace
@@ -491,12 +395,10 @@ size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& p)
 {
     int64_t most = 0;
     for (int V : {1, 2}) {
-        if (V == 2 && (p.f.C % 2 || p.f.dtype != GDR2_BF16))
-            continue;
-        const GlrPlan plan = glr_plan(p.f, V, true);
-        most = std::max(most, span_floats(p.f, plan) + plan.seg.slots() * p.f.C);
+        const GlrPlan plan = glr_plan(p.f, V);
+        most = std::max(most, plan.chain_words() * 8 + plan.seg.slots() * p.f.C * 4);
     }
-    return p.f.B > 0 ? (size_t)most * sizeof(float) : 0;
+    return p.f.B > 0 ? (size_t)most : 0;
 }
 
 hipError_t launch_glr_backward(const gdr2_glr_bwd_args& p, hipStream_t stream)
@@ -504,13 +406,11 @@ hipError_t launch_glr_backward(const gdr2_glr_bwd_args& p, hipStream_t stream)
     return p.f.x ? backward_p<false>(p, stream) : backward_p<true>(p, stream);
 }
 
-int64_t glr_launch_groups(const gdr2_glr_args& a, bool backward)
+int64_t glr_launch_groups(const gdr2_glr_args& a)
 {
     int64_t most = 0;
     for (int V : {1, 2}) {
-        if (V == 2 && (a.C % 2 || a.dtype != GDR2_BF16))
-            continue;
-        const GlrPlan plan = glr_plan(a, V, backward);
+        const GlrPlan plan = glr_plan(a, V);
         const double groups = (double)plan.seg.slots() * (double)plan.blocks * (kGlrWaves * 64 / 256);
         most = groups >= (double)kMaxGroups ? kMaxGroups : std::max(most, (int64_t)groups);
     }
