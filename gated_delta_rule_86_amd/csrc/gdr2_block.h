@@ -25,7 +25,7 @@ hipError_t launch_glr_backward(const gdr2_glr_bwd_args& a, hipStream_t stream);
 size_t glr_workspace_bytes(const gdr2_glr_args& a);
 size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& a);
 // Workgroups, counted as of 256 threads, of a call's largest launch.
-int64_t glr_launch_groups(const gdr2_glr_args& a);
+int64_t glr_launch_groups(const gdr2_glr_args& a, bool backward);
 
 // A value that is formed here: not earlier, as an invariant of a loop whose
 // registers it would fill, and not later, where it is used: what it is formed

@@ -135,7 +135,7 @@ gdr2_status validate(const gdr2_add_norm_bwd_args* a)
 // ---- gated linear recurrence -----------------------------------------------
 
 // `rows`: x, r and i are there, with their strides.
-gdr2_status check_glr(const gdr2_glr_args& a, bool rows)
+gdr2_status check_glr(const gdr2_glr_args& a, bool backward, bool rows)
 {
     if (a.B < 0 || a.T < 0)
         return set_error(GDR2_ERR_INVALID_ARG, "B, T must be >= 0");
@@ -160,7 +160,7 @@ gdr2_status check_glr(const gdr2_glr_args& a, bool rows)
             return set_error(GDR2_ERR_UNSUPPORTED, "%s: rows may be at most 2^22 elements apart", s.name);
     }
     const int64_t n = a.offsets ? a.T : mul(a.B, a.T);
-    if (a.B > ((int64_t)1 << 31) || a.T > ((int64_t)1 << 40) || n > ((int64_t)1 << 40) || glr_launch_groups(a) >= kMaxGroups)
+    if (a.B > ((int64_t)1 << 31) || a.T > ((int64_t)1 << 40) || n > ((int64_t)1 << 40) || glr_launch_groups(a, backward) >= kMaxGroups)
         return too_many();
     return GDR2_OK;
 }
@@ -193,7 +193,7 @@ gdr2_status validate(const gdr2_glr_args* a)
 {
     if (!a)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    GDR2_TRY(check_glr(*a, true));
+    GDR2_TRY(check_glr(*a, false, true));
     const size_t need = glr_workspace_bytes(*a);
     GDR2_TRY(check_workspace(a->workspace, a->workspace_bytes, need));
     const int64_t st = mul(a->B, a->C);
@@ -238,7 +238,7 @@ gdr2_status check_sizes(const gdr2_glr_bwd_args* p)
 {
     if (!p)
         return set_error(GDR2_ERR_INVALID_ARG, "args is NULL");
-    return check_glr(p->f, !glr_packed(p->f));
+    return check_glr(p->f, true, !glr_packed(p->f));
 }
 
 gdr2_status validate(const gdr2_glr_bwd_args* p)
@@ -314,7 +314,7 @@ int64_t gdr2_glr_chunk_count(int64_t B, int64_t T, int packed)
 
 size_t gdr2_glr_workspace_size(const gdr2_glr_args* a)
 {
-    return a && check_glr(*a, true) == GDR2_OK ? gdr2::glr_workspace_bytes(*a) : 0;
+    return a && check_glr(*a, false, true) == GDR2_OK ? gdr2::glr_workspace_bytes(*a) : 0;
 }
 
 gdr2_status gdr2_glr_forward(const gdr2_glr_args* a, void* stream)

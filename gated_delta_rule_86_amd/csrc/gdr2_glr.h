@@ -10,7 +10,7 @@
 //   sub-chunk  16 tokens of V adjacent channels of one lane.  LR lanes lie
 //              along the channels, so that a wave moves whole 128-byte lines (LR V
 //              elements a row), and 64 / LR sub-chunks side by side in time;
-//   tile       the sub-chunks of the 8 waves, kSubs of them.
+//   tile       the sub-chunks of the workgroup's waves, kSubs of them.
 //
 // Each lane forms its decays and inputs once, in registers, and its (P, L);
 // through LDS it then finds the state its sub-chunk starts from, and walks its
@@ -29,11 +29,10 @@
 namespace gdr2 {
 
 constexpr int kGlrChunk = GDR2_GLR_CHUNK;     // tokens of a sub-chunk, and between recorded states
-constexpr int kGlrWaves = 8;     // of a workgroup
-
-template <int LR> struct GlrTile {
+// NW: waves of a workgroup.
+template <int LR, int NW> struct GlrTile {
     static constexpr int kGroups = 64 / LR;                     // sub-chunks of a wave
-    static constexpr int kSubs = kGlrWaves * kGroups;           // of a tile
+    static constexpr int kSubs = NW * kGroups;           // of a tile
     static constexpr int kWaveTokens = kGroups * kGlrChunk;
     static constexpr int kTokens = kSubs * kGlrChunk;
 };
@@ -63,7 +62,10 @@ struct GlrPlan {
         return {(uint32_t*)w, maps, maps + seg.slots() * C};
     }
 };
-GlrPlan glr_plan(const gdr2_glr_args& a, int V);
+// Waves of a workgroup.  One pass: two on each SIMD.  Chained tiles: as many for
+// the forward, fewer for the gradients, which take more registers: three workgroups a compute unit.
+constexpr int kGlrWaves = 8, kChainedBackwardWaves = 4;
+GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward);
 // Empties a chain.
 hipError_t launch_glr_chain_reset(const GlrPlan& plan, void* workspace, hipStream_t stream);
 
@@ -251,15 +253,14 @@ __device__ __forceinline__ float state_behind(const GlrChain& chain, int64_t slo
     }
 }
 
-// By the first wave, a lane a channel: the tile's map from its sub-chunks', in
+// By the first wave, a lane a channel: the tile's map from its N sub-chunks', in
 // the order FIRST, FIRST + STEP, .., then the state it starts from, then the one behind it.
 // `begin`: the state where the tile is its sequence's first in this direction.
-template <int V, int LR, int STEP>
+template <int V, int LR, int N, int STEP>
 __device__ __forceinline__ float chain_state(const GlrChain& chain, const float (*s_span)[LR][2 * V], int64_t slot, int64_t before,
                                              int64_t C, int64_t c, const float* begin)
 {
-    constexpr int N = GlrTile<LR>::kSubs;
-    const int lane = threadIdx.x, li = lane / V, v = lane % V;
+    const int li = threadIdx.x / V, v = threadIdx.x % V;
     float P = 1.f, L = 0.f;
 #pragma unroll 4
     for (int k = 0; k < N; ++k) {

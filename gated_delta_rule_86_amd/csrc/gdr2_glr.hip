@@ -199,7 +199,7 @@ template <typename T, int V> struct CodeRows {
 template <typename T, int V, int LR, bool PACK, bool CHAINED>
 __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kernel(gdr2_glr_args a, GlrPlan plan, GlrChain chain)
 {
-    typedef GlrTile<LR> Tile;
+    typedef GlrTile<LR, kGlrWaves> Tile;
     __shared__ float s_span[CHAINED ? 1 : 2][Tile::kSubs][LR][2 * V];
     __shared__ float s_state[CHAINED ? LR * V : 1];
     const GlrWork work = CHAINED ? chained_work(plan, chain, false) : one_pass_work(plan);
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
         lds_barrier();
         if constexpr (CHAINED) {
             if (lane.wave == 0)
-                s_state[threadIdx.x] = chain_state<V, LR, 1>(chain, s_span[0], work.slot, seg.q.index, a.C, c64,
+                s_state[threadIdx.x] = chain_state<V, LR, Tile::kSubs, 1>(chain, s_span[0], work.slot, seg.q.index, a.C, c64,
                                                              a.h0 ? a.h0 + seg.q.seq * a.C : nullptr);
             lds_barrier();
 #pragma unroll
@@ -346,7 +346,7 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
 
 template <typename T, int V, int LR> hipError_t forward_lr(const gdr2_glr_args& a, hipStream_t stream)
 {
-    const GlrPlan plan = glr_plan(a, V);
+    const GlrPlan plan = glr_plan(a, V, false);
     const dim3 grid((unsigned)(plan.seg.slots() * plan.blocks)), threads(64 * kGlrWaves);
     GlrChain chain = {};
     if (plan.chained) {
@@ -381,11 +381,12 @@ template <typename T, int V> hipError_t step_v(const gdr2_glr_step_args& a, hipS
 // One workgroup walks a sequence where that fills the chip: workgroups in
 // whole rounds of the compute units, or nearly.  Otherwise tiles are chained, and so are
 // packed sequences, whose lengths are not known here.
-GlrPlan glr_plan(const gdr2_glr_args& a, int V)
+GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward)
 {
-    constexpr int kPairLg = 8, kOneLg = 7;
-    static_assert(GlrTile<32>::kTokens == 1 << kPairLg && GlrTile<64>::kTokens == 1 << kOneLg, "tiles");
-    const int lg = V == 2 ? kPairLg : kOneLg;
+    // a chained tile: 16 tokens of 32 or 64 lanes along the channels
+    int lg = V == 2 ? 5 : 4;
+    for (int waves = backward ? kChainedBackwardWaves : kGlrWaves; waves > 1; waves /= 2)
+        ++lg;
     GlrPlan p{{a.offsets, a.B, a.T, 40}, ceil_div(a.C, (int64_t)64), false, a.C};
     const int64_t units = device_cu_count(), groups = std::max(a.B, (int64_t)1) * p.blocks, rounds = ceil_div(groups, units);
     const bool fills = groups * 4 >= rounds * units * 3;
@@ -408,7 +409,7 @@ hipError_t launch_glr_chain_reset(const GlrPlan& plan, void* workspace, hipStrea
 // The larger of the two widths' needs where the pointers decide between them.
 size_t glr_workspace_bytes(const gdr2_glr_args& a)
 {
-    const int64_t one = glr_plan(a, 1).chain_words(), two = glr_plan(a, 2).chain_words();
+    const int64_t one = glr_plan(a, 1, false).chain_words(), two = glr_plan(a, 2, false).chain_words();
     return a.B > 0 ? (size_t)std::max(one, two) * 8 : 0;
 }
 

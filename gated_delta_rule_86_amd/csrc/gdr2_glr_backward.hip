@@ -110,19 +110,19 @@ template <typename T, int V> struct Source<T, V, true> {
 
 // A sub-chunk's (P, L) through LDS: the gradient that reaches this lane's
 // sub-chunk from behind, and in `lam` the one that leaves the tile.
-template <int V, int LR>
+template <int V, int LR, int N>
 __device__ __forceinline__ void reverse_fold(const float (*s_span)[LR][2 * V], const GlrLane<V, LR>& lane, float (&lam)[V],
                                              float (&reach)[V])
 {
 #pragma unroll
-    for (int j = GlrTile<LR>::kSubs - 1; j >= 0; --j) {
+    for (int j = N - 1; j >= 0; --j) {
         float pl[2 * V];
 #pragma unroll
         for (int v = 0; v < 2 * V; ++v)
             pl[v] = s_span[j][lane.li][v];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            reach[v] = j == lane.sub || j == GlrTile<LR>::kSubs - 1 ? lam[v] : reach[v];
+            reach[v] = j == lane.sub || j == N - 1 ? lam[v] : reach[v];
             lam[v] = fmaf(pl[2 * v], lam[v], pl[2 * v + 1]);
         }
         if (j % 8 == 0)
@@ -130,13 +130,12 @@ __device__ __forceinline__ void reverse_fold(const float (*s_span)[LR][2 * V], c
     }
 }
 
-template <int V, int LR> struct TileRows {
+template <int W> struct TileRows {
     int64_t n;
     int wave;
-    __device__ __forceinline__ int64_t first(int64_t t) const { return t + wave * GlrTile<LR>::kWaveTokens; }
+    __device__ __forceinline__ int64_t first(int64_t t) const { return t + wave * W; }
     __device__ __forceinline__ int left(int64_t t) const
     {
-        constexpr int W = GlrTile<LR>::kWaveTokens;
         const int64_t m = t < 0 ? 0 : n - first(t);
         return (int)(m < 0 ? 0 : m > W ? W : m);
     }
@@ -144,10 +143,12 @@ template <int V, int LR> struct TileRows {
     __device__ __forceinline__ int64_t at(int64_t t) const { return left(t) > 0 ? first(t) : 0; }
 };
 
+template <bool CHAINED> constexpr int kWaves = CHAINED ? kChainedBackwardWaves : kGlrWaves;
+
 template <typename T, int V, int LR, bool P8, bool CHAINED>
-__global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_bwd_args p, GlrPlan plan, GlrChain chain, float* part)
+__global__ __launch_bounds__(64 * kWaves<CHAINED>, CHAINED ? 3 : 2) void glr_backward_kernel(gdr2_glr_bwd_args p, GlrPlan plan, GlrChain chain, float* part)
 {
-    typedef GlrTile<LR> Tile;
+    typedef GlrTile<LR, kWaves<CHAINED>> Tile;
     __shared__ float s_span[CHAINED ? 1 : 2][Tile::kSubs][LR][2 * V];
     __shared__ float s_state[CHAINED ? LR * V : 1];
     const gdr2_glr_args& a = p.f;
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
     }
     if (seg.q.seq >= 0) {
         const int64_t row0 = seg.q.row0 + seg.t0;
-        const TileRows<V, LR> rows{seg.n, lane.wave};
+        const TileRows<Tile::kWaveTokens> rows{seg.n, lane.wave};
         const Source<T, V, P8> sx(a.x, a.x8, row0, a.x_stride, a.C, lane), sr(a.r, a.r8, row0, a.r_stride, a.C, lane),
             si(a.i, a.i8, row0, a.i_stride, a.C, lane);
         const Source<T, V, false> sd(p.dy, row0, a.C, lane);
@@ -221,7 +222,10 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             const int nleft = rows.left(ahead);
             auto nr = sr.reader(rows.at(ahead), nleft), nx = sx.reader(rows.at(ahead), nleft), ni = si.reader(rows.at(ahead), nleft);
             auto nd = sd.reader(rows.at(ahead), nleft);
-            float at[kGlrChunk][V], sg[kGlrChunk][V], g[kGlrChunk][V], P[V], Lr[V];
+            // Chained, only s(r) is kept from here to the gradients, not a: the exponential is evaluated again where it
+            // is used, which costs less than the registers (three waves a SIMD instead of two).
+            float sg[kGlrChunk][V], at[CHAINED ? 1 : kGlrChunk][V], g[kGlrChunk][V], P[V], Lr[V];
+            auto decay = [&](int k, int v) { return CHAINED ? fast_exp2(A2[v] * sg[k][v]) : at[CHAINED ? 0 : k][v]; };
             tokens_up([&](auto at_k) {
                 constexpr int K = decltype(at_k)::value;
                 float rv[V];
@@ -256,9 +260,13 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             for (int k = kGlrChunk - 1; k >= 0; --k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    at[k][v] = fast_exp2(A2[v] * sg[k][v]);
-                    Lr[v] = at[k][v] * (dy.get(k, v) + Lr[v]);
-                    P[v] *= at[k][v];
+                    const float e = fast_exp2(A2[v] * sg[k][v]);
+                    Lr[v] = e * (dy.get(k, v) + Lr[v]);
+                    P[v] *= e;
+                    if constexpr (CHAINED)
+                        here(sg[k][v]);
+                    else
+                        at[k][v] = e;
                 }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -268,14 +276,14 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
             lds_barrier();
             if constexpr (CHAINED) {
                 if (lane.wave == 0)
-                    s_state[threadIdx.x] = chain_state<V, LR, -1>(chain, s_span[0], work.slot, behind, a.C, c64,
+                    s_state[threadIdx.x] = chain_state<V, LR, Tile::kSubs, -1>(chain, s_span[0], work.slot, behind, a.C, c64,
                                                                   p.dh_out ? p.dh_out + seg.q.seq * a.C : nullptr);
                 lds_barrier();
 #pragma unroll
                 for (int v = 0; v < V; ++v)
                     lam[v] = s_state[lane.li * V + v];
             }
-            reverse_fold<V, LR>(s_span[buf], lane, lam, reach);
+            reverse_fold<V, LR, Tile::kSubs>(s_span[buf], lane, lam, reach);
             float h[V];
 #pragma unroll
             for (int v = 0; v < V; ++v)
@@ -285,8 +293,10 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     g[k][v] = dy.get(k, v) + reach[v];
-                    reach[v] = at[k][v] * g[k][v];
+                    reach[v] = decay(k, v) * g[k][v];
                     here(g[k][v]);
+                    if constexpr (CHAINED)
+                        here(sg[k][v]);
                 }
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (!CHAINED) {
@@ -306,7 +316,7 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
                 token_of<K>(i, iv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float s = sg[K][v], e = at[K][v], q = glr_root(A2[v] * s, e);
+                    const float s = sg[K][v], e = decay(K, v), q = glr_root(A2[v] * s, e);
                     // a masked token's x and i have no part, whatever they hold
                     const float all = sigmoid_f(iv[v]), o = unless_masked(q, all), in = unless_masked(q, all * xv[v]);
                     const float gq = g[K][v] * q;
@@ -361,8 +371,8 @@ __global__ __launch_bounds__(64 * kGlrWaves) void glr_backward_kernel(gdr2_glr_b
 
 template <typename T, int V, int LR, bool P8> hipError_t backward_lr(const gdr2_glr_bwd_args& p, hipStream_t stream)
 {
-    const GlrPlan plan = glr_plan(p.f, V);
-    const dim3 grid((unsigned)(plan.seg.slots() * plan.blocks)), threads(64 * kGlrWaves);
+    const GlrPlan plan = glr_plan(p.f, V, true);
+    const dim3 grid((unsigned)(plan.seg.slots() * plan.blocks)), threads(64 * (plan.chained ? kWaves<true> : kWaves<false>));
     float* part = (float*)((uint64_t*)p.workspace + plan.chain_words());
     const int64_t P = p.f.B > 0 ? plan.seg.slots() : 0;
     if (P > 0) {
@@ -395,7 +405,7 @@ size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& p)
 {
     int64_t most = 0;
     for (int V : {1, 2}) {
-        const GlrPlan plan = glr_plan(p.f, V);
+        const GlrPlan plan = glr_plan(p.f, V, true);
         most = std::max(most, plan.chain_words() * 8 + plan.seg.slots() * p.f.C * 4);
     }
     return p.f.B > 0 ? (size_t)most : 0;
@@ -406,12 +416,13 @@ hipError_t launch_glr_backward(const gdr2_glr_bwd_args& p, hipStream_t stream)
     return p.f.x ? backward_p<false>(p, stream) : backward_p<true>(p, stream);
 }
 
-int64_t glr_launch_groups(const gdr2_glr_args& a)
+int64_t glr_launch_groups(const gdr2_glr_args& a, bool backward)
 {
     int64_t most = 0;
     for (int V : {1, 2}) {
-        const GlrPlan plan = glr_plan(a, V);
-        const double groups = (double)plan.seg.slots() * (double)plan.blocks * (kGlrWaves * 64 / 256);
+        const GlrPlan plan = glr_plan(a, V, backward);
+        const int waves = plan.chained && backward ? kChainedBackwardWaves : kGlrWaves;
+        const double groups = (double)plan.seg.slots() * (double)plan.blocks * (waves * 64 / 256);
         most = groups >= (double)kMaxGroups ? kMaxGroups : std::max(most, (int64_t)groups);
     }
     return most;
