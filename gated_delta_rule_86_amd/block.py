@@ -120,8 +120,9 @@ def _scale_shape(shape):
     return (*shape[:-1], -(-shape[-1] // ROWS8_BLOCK))
 
 
-def _empty_rows8(shape, dev) -> Rows8:
-    return Rows8(torch.empty(shape, dtype=CODES, device=dev), torch.empty(_scale_shape(shape), dtype=SCALES, device=dev))
+def _new_rows8(x) -> Rows8:
+    """Memory for rows like ``x`` in 8 bits."""
+    return Rows8(x.new_empty(x.shape, dtype=CODES), x.new_empty(_scale_shape(x.shape), dtype=SCALES))
 
 
 def _check_rows8(p, name: str, shape):
@@ -150,7 +151,7 @@ def pack_rows(x, out=None) -> Rows8:
     codes, scales = (None, None) if out is None else out
     _on(x.device, (codes, scales), (x,), "out.codes out.scales x")
     if out is None:
-        out = _empty_rows8(tuple(x.shape), x.device)
+        out = _new_rows8(x)
     _call("gdr2_pack_rows", PackArgs(x.numel() // C, C, ld, _dtype_code(x), 0, x.data_ptr(), _rows8_args(out)), x.device)
     return Rows8(*out)
 
@@ -204,46 +205,42 @@ def add_norm_forward(x, residual=None, weight=None, bias=None, eps: float = 1e-5
     them into; h may be written over a contiguous residual."""
     R, C, stream = check_add_norm_shapes(x, residual, weight, bias)
     code = _mode(KINDS, kind, "kind")
-    shape, dev, out = x.shape, x.device, out or {}
-    for n in (*want, *out):
+    for n in want:
         if n not in ADD_NORM_OUTPUTS:
             raise ValueError(f"unknown output {n!r} ({', '.join(ADD_NORM_OUTPUTS)})")
-        if n in out and n not in want:
-            raise ValueError(f"out: {n!r} is not in want")
-    got = dict.fromkeys(ADD_NORM_OUTPUTS)
+    shape, dev = x.shape, x.device
     ldx = _row_stride(x, "x", x.dim() - 1, C)
     ldr = 0 if residual is None else _row_stride(residual, "residual", x.dim() - 1, C)
-    if out:
-        for n, t in out.items():
-            if n in ("y8", "h8"):
-                _check_rows8(t, f"out[{n!r}]", tuple(shape))
-                _on(dev, tuple(t), (), f"{n}.codes {n}.scales")
-                got[n] = Rows8(*t)
-            else:
-                _req_shape(t, f"out[{n!r}]", stream if n == "h" else x.dtype, tuple(shape))
-                _on(dev, (t,), (), n)
-                got[n] = t
-    _on(dev, (weight, bias), (x, residual), "weight bias x residual")
-    ptrs = []
-    for n in ADD_NORM_OUTPUTS:
-        t = got[n]
-        if t is None and n in want:
-            if n == "h":
-                t = torch.empty(shape, dtype=stream, device=dev)
-            elif n == "y":
-                t = torch.empty(shape, dtype=x.dtype, device=dev)
-            else:
-                t = _empty_rows8(shape, dev)
-            got[n] = t
-        if n in ("h", "y"):
-            ptrs.append(0 if t is None else t.data_ptr())
-        else:
-            ptrs += (0, 0) if t is None else (t.codes.data_ptr(), t.scales.data_ptr())
+    h, y, y8, h8 = _add_norm_out(out, want, tuple(shape), x.dtype, stream) if out else (None,) * 4
+    _on(dev, (weight, bias, h, y, *(y8 or (None, None)), *(h8 or (None, None))) if out else (weight, bias), (x, residual),
+        "weight bias h y y8.codes y8.scales h8.codes h8.scales x residual" if out else "weight bias x residual")
+    if h is None and "h" in want:
+        h = x.new_empty(shape, dtype=stream)
+    if y is None and "y" in want:
+        y = x.new_empty(shape)
+    if y8 is None and "y8" in want:
+        y8 = _new_rows8(x)
+    if h8 is None and "h8" in want:
+        h8 = _new_rows8(x)
     _call("gdr2_add_norm_forward", _ADD_NORM.pack(
         R, C, ldx, ldr, _dtype_code(x), gdr2.F32 if stream is torch.float32 else gdr2.BF16, code, eps, x.data_ptr(),
         0 if residual is None else residual.data_ptr(), 0 if weight is None else weight.data_ptr(),
-        0 if bias is None else bias.data_ptr(), *ptrs), dev)
-    return got
+        0 if bias is None else bias.data_ptr(), 0 if h is None else h.data_ptr(), 0 if y is None else y.data_ptr(),
+        *((0, 0) if y8 is None else (y8[0].data_ptr(), y8[1].data_ptr())),
+        *((0, 0) if h8 is None else (h8[0].data_ptr(), h8[1].data_ptr()))), dev)
+    return {"h": h, "y": y, "y8": y8, "h8": h8}
+
+
+def _add_norm_out(out, want, shape, dtype, stream):
+    """The outputs the caller gives, of the right types and shapes: h, y, y8, h8, None for the others."""
+    for n, t in out.items():
+        if n not in ADD_NORM_OUTPUTS or n not in want:
+            raise ValueError(f"out: {n!r} is not in want")
+        if n in ("y8", "h8"):
+            _check_rows8(t, f"out[{n!r}]", shape)
+        else:
+            _req_shape(t, f"out[{n!r}]", stream if n == "h" else dtype, shape)
+    return (out.get("h"), out.get("y"), *(Rows8(*out[n]) if n in out else None for n in ("y8", "h8")))
 
 
 def add_norm_backward(h, dy, dh=None, weight=None, bias=None, eps: float = 1e-5, kind: str = "rms", residual_dtype=None,
@@ -365,7 +362,7 @@ def glr_forward(x, r, i, A, h0=None, offsets=None, out=None, h_out=None, final_s
     if ck is None and (chunk_states or checkpoint):
         ck = A.new_empty((glr_chunk_count(B, T, offsets is not None), C))
     if saved is None and checkpoint:
-        saved = tuple(_empty_rows8(shape, dev) for _ in range(3))
+        saved = tuple(_new_rows8(x) for _ in range(3))
     a = GlrArgs(B, T, C, _row_stride(x, "x", lead, C), _row_stride(r, "r", lead, C), _row_stride(i, "i", lead, C), _dtype_code(x),
                 algo, x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _ptr(h0), _ptr(offsets), out.data_ptr(), _ptr(h_out),
                 _ptr(ck), *(_rows8_args(p) for p in saved or (None, None, None)))

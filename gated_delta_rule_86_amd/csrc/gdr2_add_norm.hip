@@ -138,7 +138,12 @@ __device__ __forceinline__ void params(const float* p, float without, int c, int
 {
 #pragma unroll
     for (int v = 0; v < 8; ++v)
-        out[v] = p && v < n ? p[c + v] : without;
+        out[v] = without;
+    if (p && n > 0) {
+        Row8<float> r;
+        r.load(p + c, n);
+        r.get(out);
+    }
 }
 
 // A vector's codes and its block's scale, for the lanes of a block together.
@@ -490,13 +495,15 @@ template <typename TX, typename TR, bool P8> struct BackwardLaunch {
     }
 };
 
-// Workgroups of the gradients: four of 256 threads per compute unit (as many
-// waves in larger ones), fewer when there are fewer rows.  Each leaves a row of
-// partial sums.
+// Workgroups of the gradients, each of which leaves a row of partial sums: of
+// 256 threads three per compute unit, two where a lane holds two vectors (32768 rows of 2048: two
+// 111 us, three 108, four 115; 16384 of 4096: 110, 117, 127), of 1024 one;
+// fewer when there are fewer rows.
 int64_t backward_groups(const gdr2_add_norm_bwd_args& a)
 {
     const Shape s = shape_of(a.C);
-    return std::min(ceil_div(a.R, std::max(1, 256 / s.lpr)), (int64_t)device_cu_count() * 1024 / std::max(256, s.lpr));
+    const int64_t per_unit = s.lpr > 256 ? 1 : s.nv == 2 ? 2 : 3;
+    return std::min(ceil_div(a.R, std::max(1, 256 / s.lpr)), device_cu_count() * per_unit);
 }
 
 template <typename TX, typename TR> hipError_t backward_p(const gdr2_add_norm_bwd_args& a, float* part, int64_t P, hipStream_t stream)
