@@ -176,13 +176,17 @@ __device__ __forceinline__ float unless_masked(float q, float v) { return __buil
 struct GlrWork {
     int64_t slot, block;
 };
-// One pass: workgroups go to the eight XCDs in turn; numbered so, an XCD owns a
-// range of neighbouring channel blocks, and its cache sees whole rows: every
+// Workgroups go to the eight XCDs in turn; numbered so, an XCD owns a range of
+// neighbouring channel blocks, and its cache sees whole rows: every
 // eighth block of 128 bytes would fall into a few of its channels.
+__device__ __forceinline__ uint32_t xcd_ranges(uint32_t at, uint32_t count)
+{
+    const uint32_t n = count / 8, rest = count % 8, xcd = at % 8;
+    return xcd * n + (xcd < rest ? xcd : rest) + at / 8;
+}
 __device__ __forceinline__ GlrWork one_pass_work(const GlrPlan& plan)
 {
-    const uint32_t n = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
-    const uint32_t id = xcd * n + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
+    const uint32_t id = xcd_ranges(blockIdx.x, gridDim.x);
     const int64_t slot = id / plan.blocks;
     return {slot, id - slot * plan.blocks};
 }
@@ -192,7 +196,7 @@ __device__ __forceinline__ GlrWork one_pass_work(const GlrPlan& plan)
 __device__ __forceinline__ GlrWork chained_work(const GlrPlan& plan, const GlrChain& chain, bool reverse)
 {
     __shared__ uint32_t s_ticket;
-    const int64_t block = blockIdx.x % (uint32_t)plan.blocks;
+    const int64_t block = xcd_ranges(blockIdx.x % (uint32_t)plan.blocks, (uint32_t)plan.blocks);
     if (threadIdx.x == 0)
         s_ticket = atomicAdd(chain.tickets + block * kTicketWords, 1u);
     __syncthreads();
