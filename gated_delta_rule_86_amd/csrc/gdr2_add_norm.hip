@@ -44,28 +44,31 @@ __device__ __forceinline__ double swap_sum32(double v)
     const auto hi = __builtin_amdgcn_permlane32_swap(__double2hiint(v), __double2hiint(v), false, false);
     return __hiloint2double(hi[0], lo[0]) + __hiloint2double(hi[1], lo[1]);
 }
+// Sum over aligned groups of W lanes.
 template <int W> __device__ __forceinline__ double wave_sum(double v)
 {
+    static_assert(W == 4 || W == 16 || W == 64, "lanes");
     v += dpp_move<0xB1>(v);
     v += dpp_move<0x4E>(v);
-    v += dpp_move<0x141>(v);
-    v += dpp_move<0x140>(v);
+    if constexpr (W >= 16) {
+        v += dpp_move<0x141>(v);
+        v += dpp_move<0x140>(v);
+    }
     if constexpr (W >= 64)
         v = swap_sum32(swap_sum16(v));
     return v;
 }
-template <int W> __device__ __forceinline__ float wave_sum(float v) { return lanes_sum<W>(v); }
 
 // N sums over the LPR lanes that hold one row; every lane gets them.  Over
 // more than a wave they go through one of two places in turn: one barrier a
 // sum, for a place is written again behind the next one's.
-template <int LPR, typename S, int N> struct RowSums {
+template <int LPR, int N> struct RowSums {
     static constexpr int W = LPR > 64 ? LPR / 64 : 1;
-    typedef S Place[2][W][N];
+    typedef double Place[2][W][N];
     Place* place;
     int turn = 0;
     __device__ __forceinline__ explicit RowSums(Place* p) : place(p) {}
-    template <int M> __device__ __forceinline__ void operator()(S (&v)[M])
+    template <int M> __device__ __forceinline__ void operator()(double (&v)[M])
     {
         static_assert(M <= N, "place");
 #pragma unroll
@@ -78,29 +81,29 @@ template <int LPR, typename S, int N> struct RowSums {
                     (*place)[turn][threadIdx.x >> 6][i] = v[i];
             lds_barrier();
 #pragma unroll
-            for (int i = 0; i < M; ++i) {
-                v[i] = (*place)[turn][0][i];
-#pragma unroll
-                for (int k = 1; k < W; ++k)
-                    v[i] += (*place)[turn][k][i];
-            }
+            for (int i = 0; i < M; ++i)
+                v[i] = wave_sum<W>((*place)[turn][threadIdx.x % W][i]);
             turn ^= 1;
         }
     }
 };
 
 template <int LPR> constexpr int kThreads = LPR > 256 ? LPR : 256;
-// Whether the next row's loads fit the registers (a workgroup of 1024 has 128 a lane).
-template <int LPR, int NV> constexpr bool kAhead = LPR * NV < 2048;
+// Whether the next row's loads, and the weights, fit the registers (a workgroup
+// of 1024 has 128 a lane); elsewhere both are loaded where they are used, the
+// vectors one after the other.
+template <int LPR, int NV> constexpr bool kRoomy = LPR * NV < 2048;
 
-// x^(-1/2): the unit's estimate and two Newton steps, each doubling its bits.
-__device__ __forceinline__ double inverse_root(double x)
+// x^(-1/2): the unit's estimate and STEPS Newton steps, each doubling its 14 bits or more;
+// infinite for 0 and 0 for infinity (the steps would make NaN of both).
+template <int STEPS> __device__ __forceinline__ double inverse_root(double x)
 {
-    double y = __builtin_amdgcn_rsq(x);
+    const double first = __builtin_amdgcn_rsq(x);
+    double y = first;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < STEPS; ++i)
         y = fma(y, fma(-0.5 * x * y, y, 0.5), y);
-    return y;
+    return x > 0.0 && x < __builtin_inf() ? y : first;
 }
 
 // The element's 64-bit value as fp32 bits for a rounding to fewer bits: the
@@ -146,6 +149,31 @@ __device__ __forceinline__ void params(const float* p, float without, int c, int
     }
 }
 
+// A lane's weights: held, or loaded for each row.
+template <int LPR, int NV> struct Weights {
+    const float* p;
+    int lane, C;
+    float held[kRoomy<LPR, NV> ? NV : 1][8];
+    __device__ __forceinline__ Weights(const float* p_, int lane_, int C_) : p(p_), lane(lane_), C(C_)
+    {
+        if constexpr (kRoomy<LPR, NV>)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                load(j, held[j]);
+    }
+    __device__ __forceinline__ void load(int j, float (&w)[8]) const { params(p, 1.f, (j * LPR + lane) * 8, C - (j * LPR + lane) * 8, w); }
+    __device__ __forceinline__ void get(int j, float (&w)[8]) const
+    {
+        if constexpr (kRoomy<LPR, NV>) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                w[v] = held[j][v];
+        } else {
+            load(j, w);
+        }
+    }
+};
+
 // A vector's codes and its block's scale, for the lanes of a block together.
 struct Vector8 {
     Codes8 codes;
@@ -168,17 +196,14 @@ struct Vector8 {
 template <typename TX, typename TR, int LPR, int NV, bool TAIL>
 __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_add_norm_args a)
 {
-    typedef RowSums<LPR, double, 1> Sums;
+    typedef RowSums<LPR, 1> Sums;
     __shared__ typename Sums::Place s_part;
     Sums sums(&s_part);
     constexpr int RPB = kThreads<LPR> / LPR;
     const int lane = threadIdx.x % LPR, C = (int)a.C;
     const int64_t step = (int64_t)gridDim.x * RPB, blocks = scale_count(C);
     const double inv = 1.0 / (double)C;
-    float w[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        params(a.weight, 1.f, (j * LPR + lane) * 8, C - (j * LPR + lane) * 8, w[j]);
+    Weights<LPR, NV> weights(a.weight, lane, C);
     int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
     RowRegs<TX, NV, TAIL> nx;
     RowRegs<TR, NV, TAIL> nr;
@@ -187,11 +212,11 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_ad
         if (a.residual)
             nr.template load<LPR>(a.residual, r, a.R, a.res_stride, C, lane);
     };
-    if constexpr (kAhead<LPR, NV>)
+    if constexpr (kRoomy<LPR, NV>)
         fetch(row);
     // every lane of a workgroup goes as often
     for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.R; first += step, row += step) {
-        if constexpr (!kAhead<LPR, NV>)
+        if constexpr (!kRoomy<LPR, NV>)
             fetch(row);
         float h[NV][8];
 #pragma unroll
@@ -208,7 +233,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_ad
             for (int v = 0; v < 8; ++v)
                 here(h[j][v]);
         }
-        if constexpr (kAhead<LPR, NV>)
+        if constexpr (kRoomy<LPR, NV>)
             fetch(row + step);
         double mean = 0.0;
         if (a.kind == GDR2_NORM_LAYER) {
@@ -236,7 +261,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_ad
             ss[0] += n > 0 ? part : 0.0;
         }
         sums(ss);
-        const double rstd = inverse_root(ss[0] * inv + (double)a.eps);
+        const double rstd = inverse_root<2>(ss[0] * inv + (double)a.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + lane) * 8, n = row < a.R ? C - c : 0;
@@ -252,13 +277,14 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_ad
             }
             if (!a.y && !a.y8.codes)
                 continue;
-            float b[8] = {}, y[8], y8[8];
+            float w[8], b[8] = {}, y[8], y8[8];
+            weights.get(j, w);
             if (a.bias)
                 params(a.bias, 0.f, c, C - c, b);
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
-                here(w[j][v]);
-                const double t = fma(((double)h[j][v] - mean) * rstd, (double)w[j][v], (double)b[v]);
+                here(w[v]);
+                const double t = fma(((double)h[j][v] - mean) * rstd, (double)w[v], (double)b[v]);
                 y[v] = (float)t;
                 y8[v] = __builtin_bit_cast(float, sticky_bits(t));
             }
@@ -269,6 +295,8 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_ad
                 if (n > 0)
                     k.store(a.y8, row, C, blocks, c, n);
             }
+            if constexpr (!kRoomy<LPR, NV>)
+                __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
@@ -306,18 +334,16 @@ template <typename TR, int NV, bool TAIL> struct StreamRegs<TR, true, NV, TAIL> 
 template <typename TX, typename TR, bool P8, int LPR, int NV, bool TAIL>
 __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_add_norm_bwd_args a, float* part)
 {
-    typedef RowSums<LPR, float, 3> Sums;
+    typedef RowSums<LPR, 3> Sums;
     __shared__ typename Sums::Place s_part;
     Sums sums(&s_part);
     constexpr int RPB = kThreads<LPR> / LPR;
     __shared__ float s_red[RPB > 1 ? 256 * NV * 8 : 1];
     const int lane = threadIdx.x % LPR, grp = threadIdx.x / LPR, C = (int)a.C;
     const int64_t step = (int64_t)gridDim.x * RPB;
-    const float inv = 1.f / (float)C;
-    float dw[NV][8] = {}, db[NV][8] = {}, w[NV][8];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        params(a.weight, 1.f, (j * LPR + lane) * 8, C - (j * LPR + lane) * 8, w[j]);
+    const double inv = 1.0 / (double)C;
+    float dw[NV][8] = {}, db[NV][8] = {};
+    Weights<LPR, NV> weights(a.weight, lane, C);
     int64_t row = (int64_t)blockIdx.x * RPB + grp;
     StreamRegs<TR, P8, NV, TAIL> nh;
     RowRegs<TX, NV, TAIL> nd;
@@ -325,14 +351,14 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_a
         nh.template load<LPR>(a, r, lane);
         nd.template load<LPR>(a.dy, r, a.R, C, C, lane);
     };
-    if constexpr (kAhead<LPR, NV>)
+    if constexpr (kRoomy<LPR, NV>)
         fetch(row);
     for (int64_t first = (int64_t)blockIdx.x * RPB; first < a.R; first += step, row += step) {
-        if constexpr (!kAhead<LPR, NV>)
+        if constexpr (!kRoomy<LPR, NV>)
             fetch(row);
         float x[NV][8], g[NV][8];
         RowRegs<TR, NV, TAIL> dh;
-        if (a.dh)
+        if (kRoomy<LPR, NV> && a.dh)
             dh.template load<LPR>(a.dh, row, a.R, C, C, lane);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -344,45 +370,63 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_a
                 here(g[j][v]);
             }
         }
-        if constexpr (kAhead<LPR, NV>)
+        if constexpr (kRoomy<LPR, NV>)
             fetch(row + step);
-        float mean = 0.f;
+        double mean = 0.0;
         if (a.kind == GDR2_NORM_LAYER) {
-            float s[1] = {0.f};
+            double s[1] = {0.0};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int n = C - (j * LPR + lane) * 8;
 #pragma unroll
                 for (int v = 0; v < 8; ++v)
-                    s[0] += v < n ? x[j][v] : 0.f;
+                    s[0] += (double)(v < n ? x[j][v] : 0.f);
             }
             sums(s);
             mean = s[0] * inv;
         }
         // sum d^2, sum v d and, for the layer norm, sum v, in one go: xh = r d
-        float s[3] = {0.f, 0.f, 0.f};
+        double s[3] = {0.0, 0.0, 0.0};
+        float sv = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             // elements and rows that are not there add nothing, whatever they hold
             const int n = row < a.R ? C - (j * LPR + lane) * 8 : 0;
+            float w[8];
+            weights.get(j, w);
 #pragma unroll
             for (int v = 0; v < 8; ++v) {
                 const bool in = TAIL ? v < n : n > 0;
-                const float d = in ? x[j][v] - mean : 0.f;
+                const float d = in ? (float)((double)x[j][v] - mean) : 0.f;
                 x[j][v] = d;
                 g[j][v] = in ? g[j][v] : 0.f;
-                s[0] = fmaf(d, d, s[0]);
-                s[1] = fmaf(g[j][v] * w[j][v], d, s[1]);
-                s[2] = fmaf(g[j][v], w[j][v], s[2]);
+                const float gw = g[j][v] * w[v];
+                s[0] = fma((double)d, (double)d, s[0]);
+                s[1] = fma((double)gw, (double)d, s[1]);
+                sv += gw;
             }
+            if constexpr (!kRoomy<LPR, NV>)
+                __builtin_amdgcn_sched_barrier(0);
         }
-        sums(s);
-        const float rstd = 1.f / sqrtf(s[0] * inv + a.eps);
-        const float m1 = a.kind == GDR2_NORM_LAYER ? s[2] * inv : 0.f, m2 = rstd * s[1] * inv;
+        if (a.kind == GDR2_NORM_LAYER) {
+            s[2] = (double)sv;
+            sums(s);
+        } else {
+            double two[2] = {s[0], s[1]};
+            sums(two);
+            s[0] = two[0];
+            s[1] = two[1];
+        }
+        const double root = inverse_root<1>(s[0] * inv + (double)a.eps);
+        const float rstd = (float)root;
+        const float m1 = a.kind == GDR2_NORM_LAYER ? (float)(s[2] * inv) : 0.f, m2 = (float)(root * s[1] * inv);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + lane) * 8, n = row < a.R ? C - c : 0;
-            float o[8], more[8] = {};
+            float w[8], o[8], more[8] = {};
+            weights.get(j, w);
+            if (!kRoomy<LPR, NV> && a.dh)
+                dh.template load<LPR>(a.dh, row, a.R, C, C, lane);
             if (a.dh)
                 dh.part[j].get(more);
 #pragma unroll
@@ -391,14 +435,14 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_a
                 const float xh = n > 0 ? x[j][v] * rstd : 0.f;
                 dw[j][v] = fmaf(g[j][v], xh, dw[j][v]);
                 db[j][v] += g[j][v];
-                o[v] = fmaf(rstd, fmaf(g[j][v], w[j][v], -m1) - xh * m2, more[v]);
+                o[v] = fmaf(rstd, fmaf(g[j][v], w[v], -m1) - xh * m2, more[v]);
             }
-            if (n <= 0)
-                continue;
-            if (a.dresidual)
+            if (n > 0 && a.dresidual)
                 Row8<TR>::store((TR*)a.dresidual + row * C + c, o, n);
-            if (a.dx)
+            if (n > 0 && a.dx)
                 Row8<TX>::store((TX*)a.dx + row * C + c, o, n);
+            if constexpr (!kRoomy<LPR, NV>)
+                __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!part)

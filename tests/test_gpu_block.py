@@ -248,6 +248,28 @@ def test_add_norm_rows_without_numbers():
                *ref.pack(ref.norm(ref.add(x[[0, 3, 5]], None), None, b, 1e-5, "rms"))[:2])
 
 
+@pytest.mark.parametrize("C", [64, 99, 2048, 9000])
+@pytest.mark.parametrize("types", TYPES, ids=["-".join(t) for t in TYPES])
+def test_add_norm_ends_of_the_stream(types, C):
+    """Streams whose squares pass fp32's range on either side keep their norm
+    and its gradients; under an infinity the rms norm of the others is the bias."""
+    g = gen(44)
+    x, dy, w, b = rn(g, 5, C, dtype=DT[types[0]]), rn(g, 5, C, dtype=DT[types[0]]), rn(g, C), rn(g, C)
+    res = torch.zeros(5, C, dtype=DT[types[1]]).cuda()
+    x[0], x[1], x[2] = x[0] * 2.0 ** 100, x[1] * 2.0 ** 120, x[2] * 2.0 ** -90
+    for kind in ("rms", "layer"):
+        o = block.add_norm_forward(x, res, w, b, 0.0, kind, want=("h", "y", "h8"))
+        check_y(o["y"], ref.norm(ref.add(x, res), w, b, 0.0, kind))
+        got = block.add_norm_backward(o["h"], dy, None, w, b, 0.0, kind)
+        want, bound = ref.norm_grad(o["h"].cpu().double(), dy, None, w, 0.0, kind)
+        norm_grad_close(got, want, bound, 5, C, DT[types[1]], DT[types[0]])
+    x[3, 5] = math.inf
+    y = block.add_norm_forward(x, res, w, b)["y"][3].cpu()
+    want = b.cpu().to(y.dtype)
+    want[5] = math.nan
+    assert torch.equal(y.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
 def norm_grad_close(got, want, bound, R, C, stream, rows, name=""):
     # the row's sums: C / 8 elements in sequence, then lanes; dx passes three of them
     close(got["dresidual"], want["dresidual"], bound["dresidual"], 96 + C / 4, name + "dresidual")
