@@ -11,10 +11,14 @@
 //
 // Memory bounds both.  A row is held in registers by a group of LPR lanes (16
 // to 1024), one or two vectors of eight elements each, read once; the next
-// row's loads are in flight while one is worked on.  Forwards the sums and n
-// are fp64: a code next to a rounding border is then the same however the row
-// is spread over lanes, and fp64 costs this chip's vector units what fp32
-// does.
+// row's loads are in flight while one is worked on.  A row's sums are fp64
+// (squares of fp32 numbers pass fp32's range), and forwards so is n: a code next
+// to a rounding border is then the same however the row is spread over lanes.
+// An fp64 operation costs this chip's vector units what one of fp32 does:
+// forwards that is hidden, in the gradients the sums' longer way over the lanes
+// is 4 us of 111 (32768 rows of 2048).  There the forward with h and y takes
+// 113 us (4.7 TB/s; a large copy 5.15), with h and an 8-bit y 105, the gradients
+// 111 (4.8 TB/s), from rows in 8 bits 104; 1 row 15 us, all of it the call.
 #include <algorithm>
 
 #include "gdr2_block.h"
@@ -91,17 +95,18 @@ template <int LPR, int N> struct RowSums {
 template <int LPR> constexpr int kThreads = LPR > 256 ? LPR : 256;
 // Whether the next row's loads, and the weights, fit the registers (a workgroup
 // of 1024 has 128 a lane); elsewhere both are loaded where they are used, the
-// vectors one after the other.
+// vectors one after the other (4096 rows of 16384, gradients: held, with spills,
+// 231 us, loaded again 141).
 template <int LPR, int NV> constexpr bool kRoomy = LPR * NV < 2048;
 
-// x^(-1/2): the unit's estimate and STEPS Newton steps, each doubling its 14 bits or more;
+// x^(-1/2): the unit's estimate and two Newton steps, each doubling its bits;
 // infinite for 0 and 0 for infinity (the steps would make NaN of both).
-template <int STEPS> __device__ __forceinline__ double inverse_root(double x)
+__device__ __forceinline__ double inverse_root(double x)
 {
     const double first = __builtin_amdgcn_rsq(x);
     double y = first;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i)
+    for (int i = 0; i < 2; ++i)
         y = fma(y, fma(-0.5 * x * y, y, 0.5), y);
     return x > 0.0 && x < __builtin_inf() ? y : first;
 }
@@ -261,7 +266,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_forward_kernel(gdr2_ad
             ss[0] += n > 0 ? part : 0.0;
         }
         sums(ss);
-        const double rstd = inverse_root<2>(ss[0] * inv + (double)a.eps);
+        const double rstd = inverse_root(ss[0] * inv + (double)a.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int c = (j * LPR + lane) * 8, n = row < a.R ? C - c : 0;
@@ -417,7 +422,7 @@ __global__ __launch_bounds__(kThreads<LPR>) void add_norm_backward_kernel(gdr2_a
             s[0] = two[0];
             s[1] = two[1];
         }
-        const double root = inverse_root<1>(s[0] * inv + (double)a.eps);
+        const double root = inverse_root(s[0] * inv + (double)a.eps);
         const float rstd = (float)root;
         const float m1 = a.kind == GDR2_NORM_LAYER ? (float)(s[2] * inv) : 0.f, m2 = (float)(root * s[1] * inv);
 #pragma unroll
@@ -540,9 +545,9 @@ template <typename TX, typename TR, bool P8> struct BackwardLaunch {
 };
 
 // Workgroups of the gradients, each of which leaves a row of partial sums: of
-// 256 threads three per compute unit, two where a lane holds two vectors (32768 rows of 2048: two
-// 111 us, three 108, four 115; 16384 of 4096: 110, 117, 127), of 1024 one;
-// fewer when there are fewer rows.
+// 256 threads three per compute unit, two where a lane holds two vectors (32768
+// rows of 2048: two 120 us, three 111, four 116; 16384 of 4096: two 111, three
+// 117, four 127), of 1024 one; fewer when there are fewer rows.
 int64_t backward_groups(const gdr2_add_norm_bwd_args& a)
 {
     const Shape s = shape_of(a.C);

@@ -379,8 +379,20 @@ template <typename T, int V> hipError_t step_v(const gdr2_glr_step_args& a, hipS
 }  // namespace
 
 // One workgroup walks a sequence where that fills the chip: workgroups in
-// whole rounds of the compute units, or nearly.  Otherwise tiles are chained, and so are
-// packed sequences, whose lengths are not known here.
+// whole rounds of the compute units, or nearly (us, one pass and chained, bf16: forward
+// 8x4096x2048 112 and 126, 4x4096x2048 93 and 72, 1x32768x2048 673 and 126).
+// Otherwise tiles are chained, and so are packed sequences, whose lengths are
+// not known here.
+// Chained are also the two passes with many registers or much arithmetic, the
+// gradients from rows as they are and the forward that writes rows in 8 bits,
+// where arrays are larger than half of the last cache and blocks of channels
+// are whole lines of wide rows: workgroups that start whenever another ends
+// overlap better with memory than ones that go in step.  Gradients: 8x4096x2048
+// 253 and 230, 4x4096x4096 241 and 207, 16x4096x1024 237 and 231, fp32
+// 8x2048x2048 212 and 190; 8-bit rows: 221 and 203, 213 and 197, 215 and 202,
+// 171 and 154.  On the other sides: 8x2048x2048 111 and 119, 32x4096x512 236
+// and 244, 15x3001x1002 161 and 216; 93 and 103, 208 and 211, 140 and 202.
+// (From rows in 8 bits one pass stays ahead: 8x4096x2048 187 and 230.)
 GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward)
 {
     // a chained tile: 16 tokens of 32 or 64 lanes along the channels
@@ -390,7 +402,10 @@ GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward)
     GlrPlan p{{a.offsets, a.B, a.T, 40}, ceil_div(a.C, (int64_t)64), false, a.C};
     const int64_t units = device_cu_count(), groups = std::max(a.B, (int64_t)1) * p.blocks, rounds = ceil_div(groups, units);
     const bool fills = groups * 4 >= rounds * units * 3;
-    const bool wanted = a.algo == GDR2_ALGO_SEGMENTED || (a.algo == GDR2_ALGO_AUTO && (a.offsets || !fills));
+    const int64_t row_bytes = a.C * (a.dtype == GDR2_BF16 ? 2 : 4);
+    const bool heavy = (backward ? a.x != nullptr : a.x8.codes != nullptr) && a.C >= 1024 && row_bytes % 128 == 0 &&
+                       (double)a.B * (double)a.T * (double)row_bytes >= 128.0 * (1 << 20);
+    const bool wanted = a.algo == GDR2_ALGO_SEGMENTED || (a.algo == GDR2_ALGO_AUTO && (a.offsets || !fills || heavy));
     // (a packed sequence may have all of the rows)
     p.chained = wanted && a.T > ((int64_t)1 << lg);
     if (p.chained)

@@ -400,14 +400,17 @@ template <bool P8> hipError_t backward_p(const gdr2_glr_bwd_args& p, hipStream_t
 
 }  // namespace
 
-// The larger of the two widths' needs where the pointers decide between them.
+// The largest of the needs that the pointers decide between.
 size_t glr_backward_workspace_bytes(const gdr2_glr_bwd_args& p)
 {
     int64_t most = 0;
-    for (int V : {1, 2}) {
-        const GlrPlan plan = glr_plan(p.f, V, true);
-        most = std::max(most, plan.chain_words() * 8 + plan.seg.slots() * p.f.C * 4);
-    }
+    for (int V : {1, 2})
+        for (const void* x : {(const void*)nullptr, (const void*)&p}) {       // none or any
+            gdr2_glr_args f = p.f;
+            f.x = x;
+            const GlrPlan plan = glr_plan(f, V, true);
+            most = std::max(most, plan.chain_words() * 8 + plan.seg.slots() * p.f.C * 4);
+        }
     return p.f.B > 0 ? (size_t)most : 0;
 }
 
