@@ -683,3 +683,91 @@ def test_training_step_of_a_block(eight):
         # fp32 throughout: some hundred roundings of 2^-24 over 150 tokens' memory.  A code is off by 2^-4 of its value
         # at most, 2.6 % on average; a gradient has up to four such factors.
         assert err < (0.1 if eight else 1e-4), (k, err)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("is_packed", [False, True])
+def test_glr_long_chains(is_packed, dtype):
+    """Tiles chained over dozens of others, alike in every run; also in one pass."""
+    g = gen(64)
+    C, T = 70, 6000
+    offsets = torch.tensor([0, 0, 3, 5403, 5403, 5404, 6000, 6000]).cuda() if is_packed else None
+    B, lead = (7, (T,)) if is_packed else (1, (1, T))
+    x, r, i, dy = (rn(g, *lead, C, dtype=DT[dtype]).clamp(-5, 5) for _ in range(4))
+    A, h0, dh = -torch.rand(C, generator=g).cuda(), rn(g, B, C), rn(g, B, C)
+    A[0] = 0.0
+    wy, by, wh, bh, _ = ref.glr(x, r, i, A, h0, offsets)
+    want, bound = ref.glr_grad(x, r, i, A, dy, h0, offsets, dh)
+    for algo in ("segmented", "staged"):
+        first = None
+        for _ in range(4):
+            y, h, ck = block.glr_forward(x, r, i, A, h0, offsets, chunk_states=True, algo=algo)
+            got = block.glr_backward(x, r, i, A, dy, ck, offsets, dh, algo=algo)
+            now = [y, h, *got.values()]
+            assert first is None or all(torch.equal(a, b) for a, b in zip(first, now))
+            first = now
+        close(y, wy, by, 64, "y")
+        close(h, wh, bh, 64, "h")
+        check_glr_grads(got, want, bound, slice(None), T)
+
+
+def test_glr_of_the_training_shape():
+    """8 x 4096 x 2048: the channels are independent, a few of them are checked."""
+    g = torch.Generator(device="cuda").manual_seed(65)
+    B, T, C = 8, 4096, 2048
+    x, r, i, dy = (torch.randn(B, T, C, device="cuda", generator=g).to(torch.bfloat16) for _ in range(4))
+    A = -torch.rand(C, device="cuda", generator=g)
+    pick = torch.tensor([0, 63, 64, 2047]).cuda()
+    few = [t[..., pick].contiguous() for t in (x, r, i)]
+    wy, by, wh, bh, _ = ref.glr(*few, A[pick])
+    want, bound = ref.glr_grad(*few, A[pick], dy[..., pick], None, None, None)
+    y, h, ck, saved = block.glr_forward(x, r, i, A, checkpoint=True)
+    plain, last, ck1 = block.glr_forward(x, r, i, A, chunk_states=True)
+    for a, b in ((y, h), (plain, last)):
+        close(a[..., pick], wy, by, 64, "y")
+        close(b[..., pick], wh, bh, 64, "h")
+    for p, t in zip(saved, (x, r, i)):
+        assert all(torch.equal(u.view(torch.uint8), v.view(torch.uint8)) for u, v in zip(p, block.pack_rows(t)))
+    for states in (ck, ck1):
+        got = block.glr_backward(x, r, i, A, dy, states)
+        got = {n: t[..., pick] for n, t in got.items()}
+        check_glr_grads(got, want, bound, slice(None), B * T)
+
+
+def test_workspaces_of_the_callers_own():
+    """One workspace for calls in turn, larger than needed and full of anything."""
+    g = gen(66)
+    x, r, i, dy = (rn(g, 2, 1500, 66, dtype=torch.bfloat16) for _ in range(4))
+    A, w = -torch.rand(66, generator=g).cuda(), rn(g, 66)
+    y, h, ck = block.glr_forward(x, r, i, A, chunk_states=True, algo="segmented")
+    want = block.glr_backward(x, r, i, A, dy, ck, algo="segmented")
+    nw = block.add_norm_backward(x, dy, None, w)
+    space = torch.full((1 << 22,), 0xC0, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        y1, h1, ck1 = block.glr_forward(x, r, i, A, chunk_states=True, algo="segmented", workspace=space)
+        got = block.glr_backward(x, r, i, A, dy, ck1, algo="segmented", workspace=space)
+        nb = block.add_norm_backward(x, dy, None, w, workspace=space)
+        assert torch.equal(y, y1) and torch.equal(h, h1) and torch.equal(ck, ck1)
+        assert all(torch.equal(got[n], want[n]) for n in want)
+        assert all(torch.equal(nb[n], nw[n]) for n in ("dx", "dweight"))
+
+
+@pytest.mark.parametrize("algo", ["staged", "segmented"])
+def test_glr_bad_offsets_stay_inside(algo):
+    """Offsets out of range or descending are clamped on the device: the calls
+    return and write only their outputs' rows."""
+    g = gen(67)
+    T, C = 600, 34
+    x, r, i, dy = (rn(g, T, C, dtype=torch.bfloat16) for _ in range(4))
+    A, nck = -torch.rand(C, generator=g).cuda(), block.glr_chunk_count(2, T, True)
+    for offs in ([-5, 300, 900], [400, 10, 500], [0, 1 << 60, -(1 << 60)], [600, 600, 600], [700, 700, 700], [0, 599, 300]):
+        o = torch.tensor(offs, dtype=torch.int64).cuda()
+        y, h, ck = Guarded(x.shape, x.dtype), Guarded((2, C), torch.float32), Guarded((nck, C), torch.float32)
+        saved = [Guarded8((T, C)) for _ in range(3)]
+        block.glr_forward(x, r, i, A, None, o, out=y.t, h_out=h.t, chunk_states=ck.t, checkpoint=[s.t for s in saved], algo=algo)
+        grads = {n: Guarded(x.shape, x.dtype) for n in ("dx", "dr", "di")}
+        grads.update(dA=Guarded((C,), torch.float32), dh0=Guarded((2, C), torch.float32))
+        block.glr_backward(x, r, i, A, dy, torch.zeros_like(ck.t), o, algo=algo, out={n: t.t for n, t in grads.items()})
+        torch.cuda.synchronize()
+        for n, b in (("y", y), ("h", h), ("chunks", ck), *enumerate(saved), *grads.items()):
+            b.check(n)
