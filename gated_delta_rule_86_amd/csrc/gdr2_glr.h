@@ -9,7 +9,8 @@
 //
 //   sub-chunk  16 tokens of V adjacent channels of one lane.  LR lanes lie
 //              along the channels, so that a wave moves whole 128-byte lines (LR V
-//              elements a row), and 64 / LR sub-chunks side by side in time;
+//              elements a row; with halves of them 8x4096x2048 takes 156 us, not
+//              112), and 64 / LR sub-chunks side by side in time;
 //   tile       the sub-chunks of the workgroup's waves, kSubs of them.
 //
 // Each lane forms its decays and inputs once, in registers, and its (P, L);
@@ -63,7 +64,8 @@ struct GlrPlan {
     }
 };
 // Waves of a workgroup.  One pass: two on each SIMD.  Chained tiles: as many for
-// the forward, fewer for the gradients, which take more registers: three workgroups a compute unit.
+// the forward, fewer for the gradients, which take more registers: three
+// workgroups a compute unit (4x4096x2048 from 8 bits: eight waves 143 us, four 126).
 constexpr int kGlrWaves = 8, kChainedBackwardWaves = 4;
 GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward);
 // Empties a chain.
@@ -220,6 +222,7 @@ __device__ __forceinline__ uint64_t handed(const uint64_t* from)
 __device__ __forceinline__ float state_behind(const GlrChain& chain, int64_t slot, int step, int64_t count, int64_t C, uint32_t c)
 {
     constexpr int kBack = 4;      // tiles looked at together: their words are a round trip away
+                                  // (gradients 4x4096x2048: 2 and 4 alike, 8 fills the registers, 122 -> 149 us)
     for (;;) {
         uint64_t maps[kBack], states[kBack];
 #pragma unroll

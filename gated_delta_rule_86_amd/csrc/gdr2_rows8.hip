@@ -3,8 +3,10 @@
 //
 //   e = min { e >= -127 : max_block |v| <= 448 2^e },  code = e4m3(v 2^-e)
 //
-// Memory bounds both: 3 bytes an element of bf16 rows.  A lane holds 8 columns,
-// four lanes a block.
+// Memory bounds both: 3 bytes an element of bf16 rows.  A lane holds 8 columns
+// (one access of 16 bytes), four lanes a block.  32768 rows of 2048 bf16 in 42 us
+// and 32 us back, 4.9 and 6.3 TB/s (a large copy 5.15); a slice of 10007 rows of
+// 1003 fp32, whose vectors begin at any element, in 10 and 11 us.
 #include <algorithm>
 
 #include "gdr2_block.h"

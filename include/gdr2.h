@@ -713,9 +713,10 @@ typedef struct gdr2_add_norm_bwd_args {
  *   x8, r8, i8  the rows of x, r and i in 8 bits, as gdr2_pack_rows forms
  *            them; all six pointers or none.  Rows of no sequence are left as they were.
  * algo: AUTO, STAGED (one pass over each sequence) or SEGMENTED (sequences
- * cut into segments that run in parallel: a span pass forms each segment's
- * total decay and local end state, and the main pass chains those before its
- * segment).  AUTO takes segments when one pass would leave much of the GPU idle.
+ * cut into tiles that run in parallel, each handing its total decay and its end
+ * state on to the next through the workspace, which one call uses at a time).
+ * AUTO takes tiles when one pass would leave much of the GPU idle, for packed
+ * batches, and for some large arrays; results differ by roundings.
  * Supported set: C >= 1; rows at most 2^22 elements apart; dtype F32 or BF16; B, T >= 0.
  */
 typedef struct gdr2_glr_args {
