@@ -19,9 +19,9 @@ from typing import NamedTuple
 import torch
 
 from . import gdr2
-from .gdr2 import _c_i32, _c_i64, _dtype_code, _ptr, _req_shape, _vp, load_library
-from .layer import (KINDS, SCAN_ALGOS, _call, _empty, _grad_buffers, _mode, _offsets, _on, _packed, _row_stride, _rows_dtype,
-                    _with_workspace)
+from .gdr2 import _c_i32, _c_i64, _check, _dtype_code, _req_shape, _vp, load_library
+from .layer import (KINDS, SCAN_ALGOS, _call, _empty, _grad_buffers, _mode, _offsets, _on, _packed, _raw_stream, _row_stride,
+                    _rows_dtype)
 
 ROWS8_BLOCK = 32
 GLR_CHUNK = 16
@@ -92,11 +92,18 @@ ENTRIES = {"gdr2_pack_rows": PackArgs, "gdr2_unpack_rows": UnpackArgs, "gdr2_add
 SIZES = {"gdr2_add_norm_backward_workspace_size": AddNormBwdArgs, "gdr2_glr_workspace_size": GlrArgs,
          "gdr2_glr_backward_workspace_size": GlrBwdArgs}
 
-# The calls for single tokens are all host time: their argument structs are
-# packed in one go, and handed over as bytes.
+# Calls on few rows are all host time: the argument structs are packed in one
+# go, and handed over as bytes.  (Those with a workspace up to its two fields.)
 _GLR_STEP = struct.Struct("@5q2i6P")
 _ADD_NORM = struct.Struct("@4q3if10P")
+_ADD_NORM_BWD = struct.Struct("@2q3if10P")
+_GLR = struct.Struct("@6q2i15P")
+_GLR_BWD = struct.Struct("@6q2i16PN7P")
+_WORKSPACE = struct.Struct("@PN")
+_NO_WORKSPACE = bytes(_WORKSPACE.size)
 assert _GLR_STEP.size == ctypes.sizeof(GlrStepArgs) and _ADD_NORM.size == ctypes.sizeof(AddNormArgs)
+assert all(s.size + _WORKSPACE.size == ctypes.sizeof(a)
+           for s, a in ((_ADD_NORM_BWD, AddNormBwdArgs), (_GLR, GlrArgs), (_GLR_BWD, GlrBwdArgs)))
 
 
 def declare(lib):
@@ -109,9 +116,39 @@ def declare(lib):
     for name, args in SIZES.items():
         f = getattr(lib, name)
         f.restype, f.argtypes = _size, [ctypes.POINTER(args)]
+        f = _packed[name] = lib[name]
+        f.restype, f.argtypes = _size, [ctypes.c_char_p]
     lib.gdr2_glr_chunk_count.restype = _c_i64
     lib.gdr2_glr_chunk_count.argtypes = [_c_i64, _c_i64, ctypes.c_int]
     return lib
+
+
+def _call_with_workspace(entry: str, size: str, body: bytes, workspace, like):
+    """Calls an entry point with its arguments packed up to the workspace's, on
+    the current stream of the device of ``like``.  The workspace's size depends
+    on the device's compute units, so it is asked for with that device current."""
+    index = like.device.index
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _call_with_workspace(entry, size, body, workspace, like)
+    lib = load_library()
+    if workspace is None:
+        need = _packed[size](body + _NO_WORKSPACE)
+        if need > 0:
+            workspace = like.new_empty(need, dtype=torch.uint8)
+    tail = _NO_WORKSPACE
+    if workspace is not None:
+        tail = _WORKSPACE.pack(workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    status = _packed[entry](body + tail, _raw_stream(index))
+    if status:
+        _check(lib, status)
+
+
+def _new_grads(out, like, **want):
+    """``layer._grad_buffers``; where the caller gives none, fresh memory beside ``like``."""
+    if out:
+        return _grad_buffers(out, like.device, **want)
+    return {n: None if s is None else like.new_empty(s[1], dtype=s[0]) for n, s in want.items()}
 
 
 # ---- rows in 8 bits --------------------------------------------------------
@@ -135,6 +172,15 @@ def _check_rows8(p, name: str, shape):
 
 def _rows8_args(p) -> Rows8Args:
     return Rows8Args() if p is None else Rows8Args(p[0].data_ptr(), p[1].data_ptr())
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _addrs8(rows8):
+    """Pointers of several rows in 8 bits, codes and scales in turn."""
+    return [t.data_ptr() for p in rows8 for t in p]
 
 
 def pack_rows(x, out=None) -> Rows8:
@@ -224,10 +270,8 @@ def add_norm_forward(x, residual=None, weight=None, bias=None, eps: float = 1e-5
         h8 = _new_rows8(x)
     _call("gdr2_add_norm_forward", _ADD_NORM.pack(
         R, C, ldx, ldr, _dtype_code(x), gdr2.F32 if stream is torch.float32 else gdr2.BF16, code, eps, x.data_ptr(),
-        0 if residual is None else residual.data_ptr(), 0 if weight is None else weight.data_ptr(),
-        0 if bias is None else bias.data_ptr(), 0 if h is None else h.data_ptr(), 0 if y is None else y.data_ptr(),
-        *((0, 0) if y8 is None else (y8[0].data_ptr(), y8[1].data_ptr())),
-        *((0, 0) if h8 is None else (h8[0].data_ptr(), h8[1].data_ptr()))), dev)
+        _addr(residual), _addr(weight), _addr(bias), _addr(h), _addr(y), *((0, 0) if y8 is None else _addrs8((y8,))),
+        *((0, 0) if h8 is None else _addrs8((h8,)))), dev)
     return {"h": h, "y": y, "y8": y8, "h8": h8}
 
 
@@ -275,13 +319,13 @@ def add_norm_backward(h, dy, dh=None, weight=None, bias=None, eps: float = 1e-5,
     code = _mode(KINDS, kind, "kind")
     _on(dev, (*(h if packed else (h, None)), dy, dh, weight, bias, workspace), (), "h h.scales dy dh weight bias workspace")
     param = (torch.float32, (C,))
-    g = _grad_buffers(out, dev, dresidual=(stream, shape), dx=None if stream is dy.dtype else (dy.dtype, shape),
+    g = _new_grads(out, dy, dresidual=(stream, shape), dx=None if stream is dy.dtype else (dy.dtype, shape),
                       dweight=None if weight is None else param, dbias=None if bias is None else param)
-    a = AddNormBwdArgs(dy.numel() // C, C, _dtype_code(dy), gdr2.F32 if stream is torch.float32 else gdr2.BF16, code, eps,
-                       _ptr(weight), None if packed else h.data_ptr(), _rows8_args(h if packed else None), dy.data_ptr(), _ptr(dh),
-                       g["dresidual"].data_ptr(), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]))
-    workspace = _with_workspace("gdr2_add_norm_backward_workspace_size", a, workspace, dev)
-    _call("gdr2_add_norm_backward", a, dev)
+    body = _ADD_NORM_BWD.pack(
+        dy.numel() // C, C, _dtype_code(dy), gdr2.F32 if stream is torch.float32 else gdr2.BF16, code, eps, _addr(weight),
+        *((0, *_addrs8((h,))) if packed else (h.data_ptr(), 0, 0)), dy.data_ptr(), _addr(dh), g["dresidual"].data_ptr(),
+        _addr(g["dx"]), _addr(g["dweight"]), _addr(g["dbias"]))
+    _call_with_workspace("gdr2_add_norm_backward", "gdr2_add_norm_backward_workspace_size", body, workspace, dy)
     if g["dx"] is None:
         g["dx"] = g["dresidual"]
     return g
@@ -321,6 +365,13 @@ def glr_chunk_count(B: int, T: int, packed: bool = False) -> int:
     return int(load_library().gdr2_glr_chunk_count(B, T, int(packed)))
 
 
+def _chunk_rows(B: int, T: int, offsets) -> int:
+    """glr_chunk_count of a call's sequences."""
+    if B <= 0:
+        return 0
+    return B * -(-T // GLR_CHUNK) if offsets is None else T // GLR_CHUNK + B
+
+
 def glr_forward(x, r, i, A, h0=None, offsets=None, out=None, h_out=None, final_state: bool = True, chunk_states=None,
                 checkpoint=False, algo: str = "auto", workspace=None):
     """Gated linear recurrence.  x, r, i [B,T,C] (packed [T,C]); A float32 [C]
@@ -344,7 +395,7 @@ def glr_forward(x, r, i, A, h0=None, offsets=None, out=None, h_out=None, final_s
         _req_shape(out, "out", x.dtype, shape)
     ck = chunk_states if isinstance(chunk_states, torch.Tensor) else None
     if ck is not None:
-        _req_shape(ck, "chunk_states", torch.float32, (glr_chunk_count(B, T, offsets is not None), C))
+        _req_shape(ck, "chunk_states", torch.float32, (_chunk_rows(B, T, offsets), C))
     saved = None
     if isinstance(checkpoint, (tuple, list)):
         if len(checkpoint) != 3:
@@ -360,14 +411,13 @@ def glr_forward(x, r, i, A, h0=None, offsets=None, out=None, h_out=None, final_s
     if h_out is None and final_state:
         h_out = A.new_empty((B, C))
     if ck is None and (chunk_states or checkpoint):
-        ck = A.new_empty((glr_chunk_count(B, T, offsets is not None), C))
+        ck = A.new_empty((_chunk_rows(B, T, offsets), C))
     if saved is None and checkpoint:
         saved = tuple(_new_rows8(x) for _ in range(3))
-    a = GlrArgs(B, T, C, _row_stride(x, "x", lead, C), _row_stride(r, "r", lead, C), _row_stride(i, "i", lead, C), _dtype_code(x),
-                algo, x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _ptr(h0), _ptr(offsets), out.data_ptr(), _ptr(h_out),
-                _ptr(ck), *(_rows8_args(p) for p in saved or (None, None, None)))
-    workspace = _with_workspace("gdr2_glr_workspace_size", a, workspace, dev)
-    _call("gdr2_glr_forward", a, dev)
+    body = _GLR.pack(B, T, C, _row_stride(x, "x", lead, C), _row_stride(r, "r", lead, C), _row_stride(i, "i", lead, C),
+                     _dtype_code(x), algo, x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _addr(h0), _addr(offsets),
+                     out.data_ptr(), _addr(h_out), _addr(ck), *(_addrs8(saved) if saved else (0,) * 6))
+    _call_with_workspace("gdr2_glr_forward", "gdr2_glr_workspace_size", body, workspace, x)
     if saved is not None:
         return out, h_out, ck, saved
     return (out, h_out) if ck is None else (out, h_out, ck)
@@ -407,7 +457,7 @@ def glr_backward(x, r, i, A, dy, h_chunks, offsets=None, dh_out=None, want_dh0: 
     B, T, C, shape, packed = check_glr_shapes(x, r, i, A, offsets)
     _rows_dtype(dy)
     _req_shape(dy, "dy", None if packed else x.dtype, shape)
-    _req_shape(h_chunks, "h_chunks", torch.float32, (glr_chunk_count(B, T, offsets is not None), C))
+    _req_shape(h_chunks, "h_chunks", torch.float32, (_chunk_rows(B, T, offsets), C))
     if dh_out is not None:
         _req_shape(dh_out, "dh_out", torch.float32, (B, C))
     algo = _mode(GLR_ALGOS, algo, "algo")
@@ -415,17 +465,16 @@ def glr_backward(x, r, i, A, dy, h_chunks, offsets=None, dh_out=None, want_dh0: 
     dense = (*x, *r, *i) if packed else (None,) * 6
     _on(dev, (A, offsets, dy, h_chunks, dh_out, workspace, *dense), () if packed else (x, r, i),
         "A offsets dy h_chunks dh_out workspace x x.scales r r.scales i i.scales x r i")
-    f = GlrArgs(B, T, C, 0, 0, 0, _dtype_code(dy), algo)
-    f.A, f.offsets, f.h_chunks = A.data_ptr(), _ptr(offsets), h_chunks.data_ptr()
-    if packed:
-        f.x8, f.r8, f.i8 = _rows8_args(x), _rows8_args(r), _rows8_args(i)
-    else:
-        f.x_stride, f.r_stride, f.i_stride = _row_stride(x, "x", lead, C), _row_stride(r, "r", lead, C), _row_stride(i, "i", lead, C)
-        f.x, f.r, f.i = x.data_ptr(), r.data_ptr(), i.data_ptr()
     rows = (dy.dtype, shape)
-    g = _grad_buffers(out, dev, dx=rows, dr=rows, di=rows, dA=(torch.float32, (C,)),
+    g = _new_grads(out, dy, dx=rows, dr=rows, di=rows, dA=(torch.float32, (C,)),
                       dh0=(torch.float32, (B, C)) if want_dh0 else None)
-    a = GlrBwdArgs(f, dy.data_ptr(), _ptr(dh_out), *(_ptr(g[n]) for n in ("dx", "dr", "di", "dA", "dh0")))
-    workspace = _with_workspace("gdr2_glr_backward_workspace_size", a, workspace, dev)
-    _call("gdr2_glr_backward", a, dev)
+    if packed:
+        strides, given = (0, 0, 0), (0, 0, 0)
+    else:
+        strides = _row_stride(x, "x", lead, C), _row_stride(r, "r", lead, C), _row_stride(i, "i", lead, C)
+        given = x.data_ptr(), r.data_ptr(), i.data_ptr()
+    body = _GLR_BWD.pack(B, T, C, *strides, _dtype_code(dy), algo, *given, A.data_ptr(), 0, _addr(offsets), 0, 0, h_chunks.data_ptr(),
+                         *(_addrs8((x, r, i)) if packed else (0,) * 6), 0, 0, dy.data_ptr(), _addr(dh_out), g["dx"].data_ptr(),
+                         g["dr"].data_ptr(), g["di"].data_ptr(), g["dA"].data_ptr(), _addr(g["dh0"]))
+    _call_with_workspace("gdr2_glr_backward", "gdr2_glr_backward_workspace_size", body, workspace, dy)
     return g
