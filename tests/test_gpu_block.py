@@ -771,3 +771,71 @@ def test_glr_bad_offsets_stay_inside(algo):
         torch.cuda.synchronize()
         for n, b in (("y", y), ("h", h), ("chunks", ck), *enumerate(saved), *grads.items()):
             b.check(n)
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_rows_far_apart():
+    """Rows whose byte offsets pass 32 bits: slices of wide rows against their copies."""
+    g = torch.Generator(device="cuda").manual_seed(68)
+    R, C, wide = 40001, 70, 1 << 16
+    far = torch.empty(R, wide, dtype=torch.bfloat16, device="cuda")[:, 6:6 + C]       # 5.2 GB
+    far.copy_(torch.randn(R, C, device="cuda", generator=g))
+    near, A, w = far.contiguous(), -torch.rand(C, device="cuda", generator=g), torch.rand(C, device="cuda", generator=g)
+    assert all(same(u, v) for u, v in zip(block.pack_rows(far), block.pack_rows(near)))
+    got, want = (block.add_norm_forward(t, t, w, want=("h", "y", "y8")) for t in (far, near))
+    assert same(got["h"], want["h"]) and same(got["y"], want["y"]) and same(got["y8"].codes, want["y8"].codes)
+    for algo in ("staged", "segmented"):
+        fwd = [block.glr_forward(t[None], t[None], t[None], A, checkpoint=True, algo=algo) for t in (far, near)]
+        assert all(same(u, v) for u, v in zip(fwd[0][:3], fwd[1][:3]))
+        assert all(same(u, v) for p, q in zip(fwd[0][3], fwd[1][3]) for u, v in zip(p, q))
+        grad = [block.glr_backward(t[None], t[None], t[None], A, near[None], f[2], algo=algo) for t, f in zip((far, near), fwd)]
+        assert all(same(grad[0][n], grad[1][n]) for n in grad[0])
+    st = [torch.zeros(R, C, device="cuda") for _ in range(2)]
+    y = [block.glr_step(s, t, t, t, A) for s, t in zip(st, (far, near))]
+    assert same(*y) and same(*st)
+
+
+def test_arrays_past_4_gib():
+    """Dense arrays of more than 2^32 elements: their last rows against the same rows by themselves."""
+    g = torch.Generator(device="cuda").manual_seed(69)
+    R, C, tail = (1 << 22) + 35, 1024, 8192
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)        # 8.6 GB
+    A, w = -torch.rand(C, device="cuda", generator=g) - 0.01, torch.rand(C, device="cuda", generator=g)
+    last = x[-tail:].contiguous()
+    p, q = block.pack_rows(x), block.pack_rows(last)
+    assert same(p.codes[-tail:], q.codes) and same(p.scales[-tail:], q.scales)
+    back = block.unpack_rows(p)
+    assert same(back[-tail:], block.unpack_rows(q))
+    del back, p
+    o, part = block.add_norm_forward(x, x, w, want=("h", "y8")), block.add_norm_forward(last, last, w, want=("h", "y8"))
+    assert same(o["h"][-tail:], part["h"]) and same(o["y8"].codes[-tail:], part["y8"].codes)
+    dx = block.add_norm_backward(o["h"], x, None, w)["dx"]
+    assert same(dx[-tail:], block.add_norm_backward(part["h"], last, None, w)["dx"])
+    del o, dx
+    cut = R // 16 * 16 - tail                                    # of a recorded state
+    rows = R - cut
+    y, h, ck = block.glr_forward(x[None], x[None], x[None], A, chunk_states=True)
+    few = [x[cut:, :6].contiguous()[None]] * 3
+    start = ck[cut // 16, :6][None].contiguous()
+    wy, by, wh, bh, _ = ref.glr(*few, A[:6], start)
+    close(y[:, cut:, :6], wy, by, 64, "y")
+    close(h[:, :6], wh, bh, 64, "h")
+    got = block.glr_backward(x[None], x[None], x[None], A, x[None], ck)
+    want, bound = ref.glr_grad(*few, A[:6], few[0], start, None, None)
+    for n in ("dx", "dr", "di"):
+        close(got[n][:, cut:, :6], want[n], bound[n], 192, n)
+    assert rows > tail
+
+
+def test_gradients_of_nothing():
+    z = torch.zeros(0, 5, 34, device="cuda")
+    A = -torch.ones(34, device="cuda")
+    got = block.glr_backward(z, z, z, A, z, torch.zeros(0, 34, device="cuda"))
+    assert torch.equal(got["dA"], torch.zeros_like(A)) and got["dx"].shape == z.shape and got["dh0"].shape == (0, 34)
+    e = torch.zeros(3, 0, 34, device="cuda")
+    h = torch.randn(3, 34, device="cuda")
+    got = block.glr_backward(e, e, e, A, e, torch.zeros(0, 34, device="cuda"), dh_out=h)
+    assert torch.equal(got["dA"], torch.zeros_like(A)) and torch.equal(got["dh0"], h)
