@@ -95,19 +95,30 @@ struct RowOffset {
     }
 };
 
-constexpr int kOnce = 2;     // cache policy of loads: read once (nt), 8x4096x2048 131 -> 127 us
+// Cache policy of loads: read once (nt) where rows are whole lines, forwards
+// 8x4096x2048 127 -> 112 us.  Where they are not, two workgroups share the lines
+// at their blocks' ends, and the cache should keep them: forwards fp32
+// 5x3001x1003 67 -> 62 us, bf16 49 -> 44, 15x3001x1002 90 -> 83, with 8-bit rows 8x3001x2050 220 -> 197.
+// (Gradients gain nothing by it on the whole, fp32 5x3001x1003 121 -> 131, 16x3001x1003 458 -> 399.)
+constexpr int kOnce = 2, kKeep = 0;
+inline bool glr_whole_lines(const gdr2_glr_args& a)
+{
+    const int64_t e = a.dtype == GDR2_BF16 ? 2 : 4;
+    auto ok = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 128 == 0 && ld * e % 128 == 0; };
+    return ok(a.x, a.x_stride) && ok(a.r, a.r_stride) && ok(a.i, a.i_stride);
+}
 
 // The V elements of every token as they lie in memory, a register each.
 template <typename T, int V> struct SubRows {
     static_assert(V * sizeof(T) <= 4, "one register");
     uint32_t raw[kGlrChunk];
 
-    template <typename R> __device__ __forceinline__ void load(int k, R rsrc, RowOffset& at)
+    template <int POLICY = kOnce, typename R> __device__ __forceinline__ void load(int k, R rsrc, RowOffset& at)
     {
         if constexpr (V * sizeof(T) == 2)
-            raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at.next(), 0, kOnce);
+            raw[k] = __builtin_amdgcn_raw_buffer_load_b16(rsrc, at.next(), 0, POLICY);
         else
-            raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at.next(), 0, kOnce);
+            raw[k] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at.next(), 0, POLICY);
     }
     __device__ __forceinline__ float get(int k, int v) const
     {

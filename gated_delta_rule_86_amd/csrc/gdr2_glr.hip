@@ -62,7 +62,7 @@ template <typename T, int V, int LR> struct Walk {
 // (a, b) of a sub-chunk, and its (P, L).  AHEAD: the registers of r and i are
 // loaded again, for the tile at `t`, as soon as a token's terms are formed: the loads run a
 // tile ahead of their use, and go out evenly over the tile.
-template <bool AHEAD, typename T, int V, int LR>
+template <bool AHEAD, int POLICY, typename T, int V, int LR>
 __device__ __forceinline__ SpanVec<V> form_terms(Inputs<T, V>& in, const Walk<T, V, LR>& walk, int64_t t, const float (&A2)[V],
                                                  float (&a)[kGlrChunk][V], float (&b)[kGlrChunk][V])
 {
@@ -86,8 +86,8 @@ __device__ __forceinline__ SpanVec<V> form_terms(Inputs<T, V>& in, const Walk<T,
                 s.p[v] *= at;
             }
             if constexpr (AHEAD) {
-                in.r.load(k, br, atr);
-                in.i.load(k, bi, ati);
+                in.r.template load<POLICY>(k, br, atr);
+                in.i.template load<POLICY>(k, bi, ati);
             }
         }
     });
@@ -201,7 +201,7 @@ template <typename T, int V> struct CodeRows {
     }
 };
 
-template <typename T, int V, int LR, bool PACK, bool CHAINED>
+template <typename T, int V, int LR, int POLICY, bool PACK, bool CHAINED>
 __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kernel(gdr2_glr_args a, GlrPlan plan, GlrChain chain)
 {
     typedef GlrTile<LR, kGlrWaves> Tile;
@@ -235,9 +235,9 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
     walk.with_tile(0, [&](auto br, auto bx, auto bi, RowOffset atr, RowOffset atx, RowOffset ati) {
 #pragma unroll
         for (int k = 0; k < kGlrChunk; ++k) {
-            in.r.load(k, br, atr);
-            in.x.load(k, bx, atx);
-            in.i.load(k, bi, ati);
+            in.r.template load<POLICY>(k, br, atr);
+            in.x.template load<POLICY>(k, bx, atx);
+            in.i.template load<POLICY>(k, bi, ati);
         }
     });
     int buf = 0;
@@ -256,7 +256,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
         if (left < Tile::kWaveTokens)
             in.r.mask(mine);
         float at[kGlrChunk][V], b[kGlrChunk][V];
-        const SpanVec<V> s = form_terms<!CHAINED, T, V, LR>(in, walk, t + Tile::kTokens, A2, at, b);
+        const SpanVec<V> s = form_terms<!CHAINED, POLICY, T, V, LR>(in, walk, t + Tile::kTokens, A2, at, b);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             s_span[buf][lane.sub][lane.li][2 * v] = s.p[v];
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, PACK ? 2 : 4) void glr_forward_kern
             walk.with_tile(t + Tile::kTokens, [&](auto, auto bx, auto, RowOffset, RowOffset atx, RowOffset) {
 #pragma unroll
                 for (int k = 0; k < kGlrChunk; ++k)
-                    in.x.load(k, bx, atx);
+                    in.x.template load<POLICY>(k, bx, atx);
             });
             buf ^= 1;
         } else {
@@ -349,7 +349,7 @@ template <typename T, int V> __global__ __launch_bounds__(256) void glr_step_ker
     }
 }
 
-template <typename T, int V, int LR> hipError_t forward_lr(const gdr2_glr_args& a, hipStream_t stream)
+template <typename T, int V, int LR, int POLICY> hipError_t forward_lr(const gdr2_glr_args& a, hipStream_t stream)
 {
     const GlrPlan plan = glr_plan(a, V, false);
     const dim3 grid((unsigned)(plan.seg.slots() * plan.blocks)), threads(64 * kGlrWaves);
@@ -362,13 +362,13 @@ template <typename T, int V, int LR> hipError_t forward_lr(const gdr2_glr_args& 
     }
     const bool pack = a.x8.codes;
     if (plan.chained && pack)
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, true, true>), grid, threads, 0, stream, a, plan, chain);
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, POLICY, true, true>), grid, threads, 0, stream, a, plan, chain);
     else if (plan.chained)
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, false, true>), grid, threads, 0, stream, a, plan, chain);
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, POLICY, false, true>), grid, threads, 0, stream, a, plan, chain);
     else if (pack)
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, true, false>), grid, threads, 0, stream, a, plan, chain);
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, POLICY, true, false>), grid, threads, 0, stream, a, plan, chain);
     else
-        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, false, false>), grid, threads, 0, stream, a, plan, chain);
+        hipLaunchKernelGGL((glr_forward_kernel<T, V, LR, POLICY, false, false>), grid, threads, 0, stream, a, plan, chain);
     return hipGetLastError();
 }
 
@@ -435,9 +435,12 @@ size_t glr_workspace_bytes(const gdr2_glr_args& a)
 
 hipError_t launch_glr_forward(const gdr2_glr_args& a, hipStream_t stream)
 {
+    const bool lines = glr_whole_lines(a);
     if (glr_pairs(a))
-        return forward_lr<bf16, 2, 32>(a, stream);
-    return a.dtype == GDR2_BF16 ? forward_lr<bf16, 1, 64>(a, stream) : forward_lr<float, 1, 64>(a, stream);
+        return lines ? forward_lr<bf16, 2, 32, kOnce>(a, stream) : forward_lr<bf16, 2, 32, kKeep>(a, stream);
+    if (a.dtype == GDR2_BF16)
+        return forward_lr<bf16, 1, 64, kKeep>(a, stream);      // rows at odd elements
+    return lines ? forward_lr<float, 1, 64, kOnce>(a, stream) : forward_lr<float, 1, 64, kKeep>(a, stream);
 }
 
 hipError_t launch_glr_step(const gdr2_glr_step_args& a, hipStream_t stream)
