@@ -159,7 +159,9 @@ template <typename T, int V> struct CodeRows {
             __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e + 127), bs, soff + (threadIdx.x % 16) * scales.row_bytes, 0, 0);
             const int scale = (e + 127) << 23;
             uint32_t c[16];
-            if (__any(most <= 0 && on))
+            // asked for every block of the row: a lane's token is another's than its channels, so that in the
+            // last block lanes past the row's end have tokens too
+            if (__any(most <= 0 && soff < kNowhere))
                 codes_of<true, 0>(rows, scale, most > 0, c);
             else
                 codes_of<false, 0>(rows, scale, true, c);
