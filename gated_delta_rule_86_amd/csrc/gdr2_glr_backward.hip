@@ -12,10 +12,10 @@
 // runs forwards over the sequence.
 //
 // 14 bytes an element of bf16 rows (11.1 from rows in 8 bits) and 0.25 of
-// recorded states, 56 vector operations (64).  8x4096x2048 in chained tiles 221
+// recorded states, 60 vector operations (68).  8x4096x2048 in chained tiles 221
 // us (4.3 TB/s; a large copy 5.15): seven streams at a time, the vector units
 // busy for half of it.  From 8 bits 4x4096x2048 113 us (3.4 TB/s), where loads
-// wait for 40 % of the waves' time: 149 registers leave three of them a SIMD.
+// wait for 40 % of the waves' time: 161 registers leave three of them a SIMD.
 #include <algorithm>
 #include <type_traits>
 
@@ -47,6 +47,20 @@ template <int K, typename T, int V> __device__ __forceinline__ void token_of(con
         v[j] = s.get(K, j);
 }
 template <int K, int V> __device__ __forceinline__ void token_of(const SubCodes<V>& s, float (&v)[V]) { s.template token<K>(v); }
+
+// A gate as it is kept between the passes: the smaller of s and 1 - s, with the
+// sign of r.  The slope s (1 - s) of an open gate is then as exact as that of a
+// closed one; from s alone it lost 1 % at r = 12 and all from 17 on.  The logistic
+// comes back as the fraction of -v, -v or 1 - v (at most 1 - 2^-24): one operation,
+// and no register more.  r goes in as at most 87, for 0 has the fraction 0;
+// -inf gives 0.  (The minimum of a NaN is NaN.)
+__device__ __forceinline__ float kept_gate(float r)
+{
+    const float m = __builtin_elementwise_minimum(r, 87.f), e = fast_exp2(-kLog2e * fabsf(m));
+    return copysignf(e * __builtin_amdgcn_rcpf(1.f + e), m);
+}
+__device__ __forceinline__ float gate_of(float kept) { return __builtin_amdgcn_fractf(-kept); }
+__device__ __forceinline__ float gate_slope(float kept) { return fmaf(-kept, kept, fabsf(kept)); }
 
 // f(0) .. f(15), the token's number a constant (DPP's broadcast lane is an immediate)
 template <int K = 0, typename F> __device__ __forceinline__ void tokens_up(const F& f)
@@ -226,17 +240,16 @@ __global__ __launch_bounds__(64 * kWaves<CHAINED>, CHAINED ? 3 : 2) void glr_bac
             const int nleft = rows.left(ahead);
             auto nr = sr.reader(rows.at(ahead), nleft), nx = sx.reader(rows.at(ahead), nleft), ni = si.reader(rows.at(ahead), nleft);
             auto nd = sd.reader(rows.at(ahead), nleft);
-            // Chained, only s(r) is kept from here to the gradients, not a: the exponential is evaluated again where it
-            // is used, which costs less than the registers (three waves a SIMD instead of two).
-            float sg[kGlrChunk][V], at[CHAINED ? 1 : kGlrChunk][V], g[kGlrChunk][V], P[V], Lr[V];
-            auto decay = [&](int k, int v) { return CHAINED ? fast_exp2(A2[v] * sg[k][v]) : at[CHAINED ? 0 : k][v]; };
+            // Chained, only the gate s(r) is kept from here to the gradients' recurrence, not a: the exponential is
+            // evaluated again there, which costs less than the registers (three waves a SIMD instead of two).
+            float sg[kGlrChunk][V], at[kGlrChunk][V], g[kGlrChunk][V], P[V], Lr[V];
             tokens_up([&](auto at_k) {
                 constexpr int K = decltype(at_k)::value;
                 float rv[V];
                 token_of<K>(r, rv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    sg[K][v] = sigmoid_f(rv[v]);
+                    sg[K][v] = kept_gate(rv[v]);
                     here(sg[K][v]);
                 }
             });
@@ -264,12 +277,13 @@ __global__ __launch_bounds__(64 * kWaves<CHAINED>, CHAINED ? 3 : 2) void glr_bac
             for (int k = kGlrChunk - 1; k >= 0; --k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float e = fast_exp2(A2[v] * sg[k][v]);
+                    const float e = fast_exp2(A2[v] * gate_of(sg[k][v]));
                     Lr[v] = e * (dy.get(k, v) + Lr[v]);
                     P[v] *= e;
-                    if constexpr (CHAINED)
+                    // the gate's value is formed again where it is used (one pass has the registers to hold half of them)
+                    if (CHAINED || k >= kGlrChunk / 2)
                         here(sg[k][v]);
-                    else
+                    if constexpr (!CHAINED)
                         at[k][v] = e;
                 }
 #pragma unroll
@@ -296,8 +310,10 @@ __global__ __launch_bounds__(64 * kWaves<CHAINED>, CHAINED ? 3 : 2) void glr_bac
             for (int k = kGlrChunk - 1; k >= 0; --k)
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
+                    if constexpr (CHAINED)
+                        at[k][v] = fast_exp2(A2[v] * gate_of(sg[k][v]));
                     g[k][v] = dy.get(k, v) + reach[v];
-                    reach[v] = decay(k, v) * g[k][v];
+                    reach[v] = at[k][v] * g[k][v];
                     here(g[k][v]);
                     if constexpr (CHAINED)
                         here(sg[k][v]);
@@ -320,17 +336,20 @@ __global__ __launch_bounds__(64 * kWaves<CHAINED>, CHAINED ? 3 : 2) void glr_bac
                 token_of<K>(i, iv);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const float s = sg[K][v], e = decay(K, v), q = glr_root(A2[v] * s, e);
+                    const float s = gate_of(sg[K][v]), e = at[K][v], q = glr_root(A2[v] * s, e);
                     // a masked token's x and i have no part, whatever they hold
-                    const float all = sigmoid_f(iv[v]), o = unless_masked(q, all), in = unless_masked(q, all * xv[v]);
+                    const float ei = fast_exp2(-kLog2e * iv[v]), all = __builtin_amdgcn_rcpf(1.f + ei);
+                    const float o = unless_masked(q, all), in = unless_masked(q, all * xv[v]);
                     const float gq = g[K][v] * q;
                     dx[v] = gq * o;
-                    di[v] = gq * in * (1.f - o);
-                    // 1/q where q is 0: anything finite, for `in` is 0
-                    const float over = e * e * __builtin_amdgcn_rcpf(fmaxf(q, 1e-30f));
-                    const float du = g[K][v] * fmaf(e, h[v], -in * over);
+                    // s(i) (1 - s(i)) as s(i)^2 e^-i: the difference would cancel where the gate is open.  (Where the
+                    // exponential is infinite, or i a masked NaN, `in` is 0.)
+                    di[v] = in * fminf(ei, __FLT_MAX__) * dx[v];
+                    // a/q where q is 0: anything finite, for `in` is 0
+                    const float over = e * __builtin_amdgcn_rcpf(fmaxf(q, 1e-30f));
+                    const float du = g[K][v] * e * fmaf(-in, over, h[v]);
                     dA[v] = fmaf(du, s, dA[v]);
-                    dr[v] = du * (Av[v] * fmaf(-s, s, s));
+                    dr[v] = du * (Av[v] * gate_slope(sg[K][v]));
                     h[v] = fmaf(e, h[v], q * in);
                 }
                 const uint32_t place = to.next();

@@ -8,6 +8,7 @@ import torch
 
 from gated_delta_rule_86_amd import block
 from tests import block_reference as ref
+from tests.layer_reference import close
 from tests.test_gpu_block import check_glr_grads
 from tests.test_gpu_layer import DT, gen, rn
 
@@ -79,3 +80,56 @@ def test_gradients_from_8_bits_of_masked_tokens(C, dtype):
         want, bound = ref.glr_grad(*values, A, dy, h0, None, dh, states)
         check_glr_grads(got, want, bound, slice(None), B * T)
         assert all(bool((got[n][off] == 0).all()) for n in ("dx", "dr", "di"))
+
+
+# ---- recurrence: gates far from 1/2 ----------------------------------------
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("C", [64, 33])
+@pytest.mark.parametrize("eight", [False, True])
+def test_gradients_of_open_and_closed_gates(eight, C, dtype):
+    """Logits of -24 to 24: the slope s (1 - s) keeps its digits where 1 - s
+    cancels.  A logit of l is 2 l + 5 roundings in its logistic and in one less it
+    (the exponent's product, then as for the logits of 5 that 192 stands for): 4
+    factors of a gradient, 19 more units of l, 2 roundings each, 152 more."""
+    g = gen(73)
+    B, T = 2, 300
+    x, dy = rn(g, B, T, C, dtype=DT[dtype]), rn(g, B, T, C, dtype=DT[dtype])
+    r, i = ((torch.rand(B, T, C, generator=g) * 48 - 24).to(DT[dtype]).cuda() for _ in range(2))
+    A, h0, dh = -torch.rand(C, generator=g).cuda(), rn(g, B, C), rn(g, B, C)
+    for algo in ("staged", "segmented"):
+        _, _, ck, saved = block.glr_forward(x, r, i, A, h0, checkpoint=True, algo=algo)
+        got = block.glr_backward(*(saved if eight else (x, r, i)), A, dy, ck, dh_out=dh, algo=algo)
+        values = [block.unpack_rows(p, torch.float32) for p in saved] if eight else [x, r, i]
+        states = [[(s, s.abs()) for s in ck[b * 19:(b + 1) * 19].cpu().double()] for b in range(B)] if eight else None
+        want, bound = ref.glr_grad(*values, A, dy, h0, None, dh, states)
+        sr, si = (torch.sigmoid(-t.cpu().double()) for t in values[1:])          # 1 - s
+        for n, slope in (("dx", 1), ("dr", sr), ("di", si)):
+            close(got[n], want[n], bound[n] * slope, 192 + 152, f"{algo} {n}")
+        close(got["dA"], want["dA"], bound["dA"], 192 + 152 + B * T, "dA")
+        close(got["dh0"], want["dh0"], bound["dh0"], 192 + 152, "dh0")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_gradients_of_gates_at_their_ends(dtype):
+    """Logits of +-inf, of the types' ends and past the exponential's range:
+    finite gradients, 0 (below every normal number) by the logit; a NaN in r or
+    i of an open token stays one, and only where it is."""
+    g = gen(74)
+    x, dy = rn(g, 2, 40, 8, dtype=DT[dtype]), rn(g, 2, 40, 8, dtype=DT[dtype])
+    r, i = rn(g, 2, 40, 8, dtype=DT[dtype]), rn(g, 2, 40, 8, dtype=DT[dtype])
+    fi = torch.finfo(DT[dtype])
+    ends = torch.tensor([math.inf, -math.inf, fi.max, fi.min, 200.0, -200.0, 87.5, 95.0]).to(DT[dtype]).cuda()
+    r[0, 4], r[1, 9], i[0, 20], i[1, 4] = ends, ends, ends, ends
+    A = -torch.rand(8, generator=g).cuda() - 0.1
+    _, _, ck = block.glr_forward(x, r, i, A, chunk_states=True)
+    got = block.glr_backward(x, r, i, A, dy, ck)
+    want, bound = ref.glr_grad(x, r, i, A, dy)
+    for n in ("dx", "dr", "di", "dA", "dh0"):
+        close(got[n], want[n], bound[n], 192 + 152, n)
+    assert bool((got["dr"][0, 4].abs() < 1e-34).all()) and bool((got["di"][0, 20].abs() < 1e-34).all())
+    r[0, 30, 2], i[1, 30, 3] = math.nan, math.nan
+    got = block.glr_backward(x, r, i, A, dy, ck)
+    assert bool(torch.isnan(got["dr"][0, 30, 2])) and bool(torch.isnan(got["di"][1, 30, 3]))
+    others = [c for c in range(8) if c != 2]
+    assert bool(torch.isfinite(got["dr"][0][:, others]).all()) and bool(torch.isfinite(got["dr"][1][:, [0, 1, 2, 4, 5, 6, 7]]).all())
