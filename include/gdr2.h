@@ -581,7 +581,8 @@ gdr2_status gdr2_norm_backward(const gdr2_norm_bwd_args *args, void *stream);
  *   Rows8     : rows of C columns in 8 bits are codes [R, C], one e4m3 number
  *               (4 exponent bits, 3 mantissa bits, largest finite 448) per
  *               element, and scales [R, ceil(C/32)], one byte b per 32 columns of a
- *               row (the last block may be shorter) that stands for 2^(b-127).
+ *               row (the last block may be shorter) that stands for 2^(b-127)
+ *               (255, which no rounding gives, for NaN).
  *               An element's value is its code times its block's scale: the
  *               layout of block-scaled matrix operands.  Both dense.
  *   Rounding  : a block's scale is the smallest 2^e, e >= -127, with
@@ -670,6 +671,8 @@ typedef struct gdr2_add_norm_args {
  *   dx [R, C] dtype, may be NULL      at least one of dresidual and dx is given
  *   dweight, dbias [C] fp32, may be NULL
  * A gradient through y8 or h8 is taken as one through n or h.
+ * The root enters the gradients in fp32: without eps, rows whose root mean
+ * square is below 2^-127 (subnormal streams) have no finite ones.
  * Supported set: as the forward's.
  */
 typedef struct gdr2_add_norm_bwd_args {

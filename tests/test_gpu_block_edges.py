@@ -133,3 +133,88 @@ def test_gradients_of_gates_at_their_ends(dtype):
     assert bool(torch.isnan(got["dr"][0, 30, 2])) and bool(torch.isnan(got["di"][1, 30, 3]))
     others = [c for c in range(8) if c != 2]
     assert bool(torch.isfinite(got["dr"][0][:, others]).all()) and bool(torch.isfinite(got["dr"][1][:, [0, 1, 2, 4, 5, 6, 7]]).all())
+
+
+# ---- sizes and shapes ------------------------------------------------------
+
+def test_recurrence_in_8_bits_past_4_gib():
+    """More than 2^32 elements: the last rows' codes, scales and gradients are
+    those of these rows by themselves (tiles begin at the same rows); the norm's
+    8-bit output likewise."""
+    g = torch.Generator(device="cuda").manual_seed(75)
+    R, C, tail = (1 << 22) + 35, 1024, 8192
+    cut = (R - tail) // 128 * 128                                    # of a tile
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)        # 8.6 GB
+    A, w = -torch.rand(C, device="cuda", generator=g) - 0.01, torch.rand(C, device="cuda", generator=g)
+    last = x[cut:].contiguous()
+    x[-3:], last[-3:] = -math.inf, -math.inf                         # masked, as r
+    _, _, ck, saved = block.glr_forward(x[None], x[None], x[None], A, checkpoint=True, algo="segmented")
+    want = block.pack_rows(last)
+    for n, p in zip("xri", saved):
+        same_rows8(block.Rows8(p.codes[0, cut:], p.scales[0, cut:]), want, n)
+    few = [block.Rows8(p.codes[:, cut:].contiguous(), p.scales[:, cut:].contiguous()) for p in saved]
+    part = block.glr_backward(*few, A, last[None].nan_to_num(neginf=0.0), ck[cut // 16:].contiguous(), algo="segmented")
+    x[-3:] = 0.0
+    got = block.glr_backward(*saved, A, x[None], ck, algo="segmented")
+    for n in ("dx", "dr", "di"):
+        assert torch.equal(got[n][:, cut:], part[n]) and not bool(got[n][:, -3:].any()), n
+    del got, saved, ck
+    o, p = (block.add_norm_forward(t, None, w, want=("y8",))["y8"] for t in (x[:, :], last.nan_to_num(neginf=0.0)))
+    same_rows8(block.Rows8(o.codes[cut:], o.scales[cut:]), p, "y8")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_every_code_at_every_scale(dtype):
+    """Exact in fp32; scale byte 255 is the type's NaN."""
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 8)
+    got = block.unpack_rows(block.Rows8(codes.cuda().view(block.CODES), scales.cuda().view(block.SCALES)), DT[dtype]).cpu()
+    want = codes.view(block.CODES).double() * torch.exp2(scales[:, :1].double() - 127)
+    want[255] = math.nan
+    want = want.float().to(DT[dtype])
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    keep = ~torch.isnan(want)
+    assert torch.equal(got[keep], want[keep])
+
+
+def test_rows_without_leading_dimensions():
+    g = gen(76)
+    x, res, dy, w = rn(g, 70), rn(g, 70), rn(g, 70), rn(g, 70)
+    o, many = block.add_norm_forward(x, res, w, want=("h", "y", "h8")), block.add_norm_forward(x[None], res[None], w, want=("h", "y", "h8"))
+    assert torch.equal(o["h"], many["h"][0]) and torch.equal(o["y"], many["y"][0])
+    same_rows8(block.pack_rows(o["h"]), o["h8"], "h8")
+    assert torch.equal(block.unpack_rows(o["h8"]), block.unpack_rows(many["h8"])[0])
+    a, b = block.add_norm_backward(o["h"], dy, None, w), block.add_norm_backward(many["h"], dy[None], None, w)
+    assert torch.equal(a["dx"], b["dx"][0]) and torch.equal(a["dweight"], b["dweight"])
+
+
+def test_mixed_stream_in_place():
+    """bf16 rows on an fp32 stream that is updated in place, forwards and backwards."""
+    g = gen(77)
+    x, dy = rn(g, 9, 136, dtype=torch.bfloat16), rn(g, 9, 136, dtype=torch.bfloat16)
+    res, dh, w = rn(g, 9, 136), rn(g, 9, 136), rn(g, 136)
+    want = block.add_norm_forward(x, res, w)
+    stream = res.clone()
+    got = block.add_norm_forward(x, stream, w, out={"h": stream})
+    assert torch.equal(stream, want["h"]) and torch.equal(got["y"], want["y"])
+    grads = block.add_norm_backward(stream, dy, dh, w)
+    into = dh.clone()
+    same = block.add_norm_backward(stream, dy, into, w, out={"dresidual": into})
+    assert torch.equal(into, grads["dresidual"]) and torch.equal(same["dx"], grads["dx"]) and torch.equal(same["dweight"], grads["dweight"])
+
+
+@pytest.mark.parametrize("B,T", [(0, 0), (0, 40), (3, 0)])
+def test_packed_batches_of_nothing(B, T):
+    """No sequences, or sequences without rows: states pass, dA is 0, rows of no
+    sequence are left as they were."""
+    g = gen(78)
+    offsets = torch.zeros(B + 1, dtype=torch.int64).cuda()
+    x, r, i, dy = (rn(g, T, 34) for _ in range(4))
+    A, h0 = -torch.ones(34).cuda(), rn(g, B, 34)
+    rows = {n: torch.full((T, 34), 5.0, device="cuda") for n in ("y", "dx", "dr", "di")}
+    _, h, ck, saved = block.glr_forward(x, r, i, A, h0, offsets, out=rows["y"], checkpoint=True)
+    assert torch.equal(h, h0) and ck.shape == (block.glr_chunk_count(B, T, True), 34)
+    for src in ((x, r, i), saved):
+        got = block.glr_backward(*src, A, dy, ck, offsets, h0, out={n: rows[n] for n in ("dx", "dr", "di")})
+        assert torch.equal(got["dh0"], h0) and torch.equal(got["dA"], torch.zeros_like(A))
+    assert all(bool((t == 5).all()) for t in rows.values())
