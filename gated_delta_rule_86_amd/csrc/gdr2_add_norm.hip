@@ -95,8 +95,8 @@ template <int LPR, int N> struct RowSums {
 template <int LPR> constexpr int kThreads = LPR > 256 ? LPR : 256;
 // Whether the next row's loads, and the weights, fit the registers (a workgroup
 // of 1024 has 128 a lane); elsewhere both are loaded where they are used, the
-// vectors one after the other (4096 rows of 16384, gradients: held, with spills,
-// 231 us, loaded again 141).
+// vectors one after the other (4096 rows of 16384, gradients: held, with many spills,
+// 231 us, loaded again, with 2 to 15 registers spilled, 141).
 template <int LPR, int NV> constexpr bool kRoomy = LPR * NV < 2048;
 
 // x^(-1/2): the unit's estimate and two Newton steps, each doubling its bits;

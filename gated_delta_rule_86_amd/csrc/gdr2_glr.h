@@ -99,8 +99,8 @@ struct RowOffset {
 // 8x4096x2048 127 -> 112 us.  Where they are not, two workgroups share the lines
 // at their blocks' ends, and the cache should keep them: forwards fp32
 // 5x3001x1003 67 -> 62 us, bf16 49 -> 44, 15x3001x1002 90 -> 83, with 8-bit rows 8x3001x2050 220 -> 197.
-// (Gradients gain nothing by it on the whole: fp32 16x3001x1003 363 -> 304,
-// 32x1000x500 87 -> 101, chained 5x3001x1003 121 -> 131.)
+// (Gradients have one policy: with the other fp32 16x3001x1003 363 -> 304, but
+// 32x1000x500 87 -> 101, chained 5x3001x1003 121 -> 131.  What divides them is open.)
 constexpr int kOnce = 2, kKeep = 0;
 inline bool glr_whole_lines(const gdr2_glr_args& a)
 {

@@ -9,6 +9,7 @@
 // the inputs in 8 bits makes that 11.3 bytes and 57 operations: 4x4096x2048
 // 99 us (3.8 TB/s), both at half of what they could be by themselves, because a
 // tile loads, computes and stores in turn and 116 registers leave four waves a SIMD.
+// (The one-pass variant of two channels a lane holds 128 registers and two spilled ones.)
 // gdr2_glr.h describes the layout.
 #include <algorithm>
 
@@ -395,11 +396,11 @@ template <typename T, int V> hipError_t step_v(const gdr2_glr_step_args& a, hipS
 // where arrays are larger than half of the last cache and blocks of channels
 // are whole lines of wide rows: workgroups that start whenever another ends
 // overlap better with memory than ones that go in step.  Gradients: 8x4096x2048
-// 253 and 230, 4x4096x4096 241 and 207, 16x4096x1024 237 and 231, fp32
-// 8x2048x2048 212 and 190; 8-bit rows: 221 and 203, 213 and 197, 215 and 202,
-// 171 and 154.  On the other sides: 8x2048x2048 111 and 119, 32x4096x512 236
-// and 244, 15x3001x1002 161 and 216; 93 and 103, 208 and 211, 140 and 202.
-// (From rows in 8 bits one pass stays ahead: 8x4096x2048 187 and 230.)
+// 248 and 232, 4x4096x4096 235 and 210, 16x4096x1024 229 and 228, fp32
+// 8x2048x2048 211 and 191; 8-bit rows: 221 and 203, 213 and 197, 215 and 202,
+// 171 and 154.  On the other sides: 8x2048x2048 105 and 121, 32x4096x512 231
+// and 246, 15x3001x1002 161 and 215; 93 and 103, 208 and 211, 140 and 202.
+// (From rows in 8 bits one pass stays ahead: 8x4096x2048 192 and 234.)
 GlrPlan glr_plan(const gdr2_glr_args& a, int V, bool backward)
 {
     // a chained tile: 16 tokens of 32 or 64 lanes along the channels

@@ -12,10 +12,11 @@
 // runs forwards over the sequence.
 //
 // 14 bytes an element of bf16 rows (11.1 from rows in 8 bits) and 0.25 of
-// recorded states, 60 vector operations (68).  8x4096x2048 in chained tiles 221
-// us (4.3 TB/s; a large copy 5.15): seven streams at a time, the vector units
-// busy for half of it.  From 8 bits 4x4096x2048 113 us (3.4 TB/s), where loads
-// wait for 40 % of the waves' time: 161 registers leave three of them a SIMD.
+// recorded states, 60 vector operations in one pass, 66 in chained tiles (68 from 8
+// bits).  8x4096x2048 in chained tiles 224 us (4.3 TB/s; a large copy 5.15): seven
+// streams at a time, the vector units busy for 56 % of it.  From 8 bits 4x4096x2048
+// 116 us (3.3 TB/s), where waves wait for data for 37 % of their time: 161
+// registers leave three of them a SIMD.
 #include <algorithm>
 #include <type_traits>
 
